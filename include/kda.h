@@ -337,6 +337,161 @@ kda_status kda_gdn_decode_step_pooled(const void *q, const void *k, const void *
                                       int32_t dk, int32_t dv, int32_t dtype, void *o,
                                       void *stream);
 
+/*
+ * Latent attention: the full-attention layers that hybrid models interleave
+ * with KDA layers (the lineage essay's and the explainer's 3 : 1 hybrid).
+ * Keys and values of all H heads come from one latent vector per token (512
+ * values) and one position key per token (64 values) that the heads share.
+ * Per head h, with c_j the latent and r_j the position key of token j:
+ *
+ *     k_jh = [ c_j W_K,h (128 values) ; r_j (64) ],   v_jh = c_j W_V,h (128)
+ *     s_ij = scale q_ih . k_jh,   o_ih = sum_j softmax_j(s_ij) v_jh
+ *
+ * Three operators, for the two forms that give the same result:
+ *   - kda_mla_append puts each token's [c ; r] into a paged cache and applies
+ *     the position rotation to r (and to the queries' position parts) on the
+ *     way;
+ *   - kda_mla_prefill is the expanded form, for prompts: k and v of every head
+ *     have been multiplied out;
+ *   - kda_mla_decode is the absorbed form, for single tokens: W_K has been
+ *     multiplied into the query (q W_K^T, 512 values) and W_V is applied to the
+ *     output afterwards, so that the kernel reads only the latent cache:
+ *         s_j = scale q . [c_j ; r_j],   o = sum_j softmax_j(s_j) c_j.
+ * The products with W_K and W_V are the caller's (plain matrix products).
+ *
+ * Conventions in addition to those at the top of this file
+ *   - dtype is that of every tensor that is not stated to be float32 or int32.
+ *   - The cache is [n_pages, page, 576]: a row is the latent (512) followed by
+ *     the position key (64); page is 16, 32, 64 or 128 tokens.  Cache slot s
+ *     is row s % page of page s / page.
+ *   - Scores, softmax statistics and sums are float32.  bf16 weights of the
+ *     softmax are rounded to bf16 where they meet the bf16 values; the
+ *     normalisation uses the float32 sum.
+ *   - lse is the natural logarithm of the sum of exp(s), float32; it lets a
+ *     caller merge results over parts of the keys.  A query that sees no key
+ *     gets o = 0 and lse = -inf.
+ *   - Inputs that a query can see are finite.  What it cannot see by length
+ *     or by sequence (cache rows behind a length, other sequences' tokens)
+ *     may hold anything, infinities and NaN included.
+ */
+
+/*
+ * kda_mla_append -- write T tokens to the paged latent cache, rotating their
+ * position keys and (optionally) their queries' position parts.
+ *
+ *   c          [T, 512]      latents; row stride c_stride elements
+ *   k_r        [T, 64]       position keys; row stride k_r_stride
+ *   slots      [T]           int32, cache slot of each token; a value outside
+ *                            [0, n_pages * page) leaves the cache untouched
+ *                            (padding tokens); the others must be distinct
+ *   positions  [T]           int32, row of `rope` per token, clamped into
+ *                            [0, max_pos); NULL when rope is
+ *   rope       [max_pos, 64] float32: cosines of the 32 pairs' angles, then
+ *                            their sines; NULL: no rotation (layers without
+ *                            position rotation)
+ *   interleaved  pairs are (2i, 2i + 1) if nonzero, else (i, i + 32)
+ *   cache      [n_pages, page, 576]  written at `slots`
+ *   k_out      [T, 64]       rotated position keys, row stride k_out_stride,
+ *                            or NULL; may be k_r itself
+ *   q_r        [T, H, 64]    the queries' position parts, or NULL; element
+ *                            strides q_token_stride and q_head_stride
+ *   q_out      [T, H, 64]    rotated, with its own strides; NULL exactly when
+ *                            q_r is; may be q_r itself (same strides)
+ *
+ * (a, b) -> (a cos - b sin, a sin + b cos) in float32, rounded once.  Strides
+ * are multiples of 16 bytes (so that views of a projection's output can be
+ * passed as they are).  T = 0 is a valid no-op.  Outputs must not overlap
+ * inputs otherwise.
+ */
+kda_status kda_mla_append(const void *c, int64_t c_stride, const void *k_r,
+                          int64_t k_r_stride, const int32_t *slots,
+                          const int32_t *positions, const float *rope,
+                          int32_t max_pos, int32_t interleaved, int64_t T,
+                          void *cache, int32_t n_pages, int32_t page,
+                          int32_t latent, int32_t rope_dim, int32_t dtype,
+                          void *k_out, int64_t k_out_stride, const void *q_r,
+                          int64_t q_token_stride, int64_t q_head_stride,
+                          int32_t H, void *q_out, int64_t qo_token_stride,
+                          int64_t qo_head_stride, void *stream);
+
+/*
+ * kda_mla_prefill -- the expanded form over a packed batch of N sequences.
+ *
+ *   q          [Tq, H, 192]  queries: 128 values that meet the latent's key,
+ *                            then the 64 that meet the position key (rotated)
+ *   kv         [Tk, H, 256]  the latents multiplied out: key (128), value (128)
+ *   k_r        [Tk, 64]      position keys (rotated), shared by the heads
+ *   cu_q, cu_k [N + 1]       int32 device offsets of the sequences' queries
+ *                            and keys, as cu_seqlens of kda_prefill_chunked
+ *                            (clamped into [0, Tq] and [0, Tk])
+ *   scale      finite factor of the scores
+ *   causal     if nonzero, the queries are the last of the keys' tokens: query
+ *              i of nq sees key j of nk when j <= i + nk - nq (none when that
+ *              is negative); else every query sees all nk keys
+ *   o          [Tq, H, 128]  outputs (written)
+ *   lse        [Tq, H]       float32 (written), or NULL
+ *   workspace  device scratch of kda_mla_prefill_workspace_size(N, Tq, H,
+ *              dtype) bytes, 16-byte aligned; may be NULL when that is 0
+ *
+ * bf16 runs on the tensor cores, fp32 on the CUDA cores.  Calls that share a
+ * workspace must not overlap on the GPU.  Tokens outside every [cu_q[n],
+ * cu_q[n + 1]) are not written.
+ */
+kda_status kda_mla_prefill(const void *q, const void *kv, const void *k_r,
+                           const int32_t *cu_q, const int32_t *cu_k, int32_t N,
+                           int64_t Tq, int64_t Tk, int32_t H, int32_t nope,
+                           int32_t rope_dim, int32_t dv, int32_t dtype,
+                           float scale, int32_t causal, void *o, float *lse,
+                           void *workspace, uint64_t workspace_bytes,
+                           void *stream);
+
+/* Bytes of workspace kda_mla_prefill needs (0: none).  Host arithmetic. */
+uint64_t kda_mla_prefill_workspace_size(int32_t N, int64_t Tq, int32_t H,
+                                        int32_t dtype);
+
+/*
+ * kda_mla_decode -- the absorbed form: one query token for each of B
+ * sequences over the paged latent cache.
+ *
+ *   q          [B, H, 576]   queries: 512 values that meet the latent (W_K
+ *                            multiplied in), then the 64 position values
+ *   cache      [n_pages, page, 576]
+ *   table      [B, max_pages] int32: page of tokens page*i .. page*i + page-1
+ *                            of sequence b; a value outside [0, n_pages) hides
+ *                            those tokens
+ *   seq_lens   [B]           int32, tokens cached per sequence (the new one
+ *                            included), clamped into [0, max_pages * page]
+ *   scale      finite factor of the scores (that of the expanded form)
+ *   o          [B, H, 512]   outputs over the latents (written)
+ *   lse        [B, H]        float32 (written), or NULL
+ *   workspace  device scratch of kda_mla_decode_workspace_size(B, H, dtype)
+ *              bytes, 16-byte aligned; its contents on entry do not matter
+ *
+ * Neither the table nor the lengths are read on the host.  The tokens of all
+ * sequences are shared out evenly over the SMs, whatever the lengths; a
+ * sequence that several SMs worked on is joined by a second kernel.  Results
+ * do not depend on timing: equal inputs give equal bits.  B = 0 is a valid
+ * no-op.  Calls that share a workspace must not overlap on the GPU.
+ */
+kda_status kda_mla_decode(const void *q, const void *cache, const int32_t *table,
+                          const int32_t *seq_lens, int32_t B, int32_t H,
+                          int32_t n_pages, int32_t page, int32_t max_pages,
+                          int32_t latent, int32_t rope_dim, int32_t dtype,
+                          float scale, void *o, float *lse, void *workspace,
+                          uint64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace kda_mla_decode needs.  Host arithmetic. */
+uint64_t kda_mla_decode_workspace_size(int32_t B, int32_t H, int32_t dtype);
+
+/*
+ * kda_prefill_check for kda_mla_prefill and kda_mla_decode: synchronise
+ * `stream` and report the device-side status of the last call that used
+ * `workspace` (KDA_ERR_TIMEOUT: a bounded wait gave up and outputs are
+ * incomplete).  A NULL workspace (a call that needed none) reports the
+ * stream's status only.
+ */
+kda_status kda_mla_check(const void *workspace, void *stream);
+
 /* Human-readable name of a status code (static storage; never NULL). */
 const char *kda_status_string(int32_t status);
 

@@ -83,6 +83,24 @@ def load() -> ctypes.CDLL:
         lib.kda_decode_step_pooled.restype = ctypes.c_int
         lib.kda_gdn_decode_step_pooled.argtypes = lib.kda_decode_step_pooled.argtypes
         lib.kda_gdn_decode_step_pooled.restype = ctypes.c_int
+        f32 = ctypes.c_float
+        lib.kda_mla_append.argtypes = [
+            vp, i64, vp, i64, vp, vp, vp, i32, i32, i64, vp, i32, i32, i32, i32, i32, vp, i64,
+            vp, i64, i64, i32, vp, i64, i64, vp]
+        lib.kda_mla_append.restype = ctypes.c_int
+        lib.kda_mla_prefill.argtypes = [
+            vp, vp, vp, vp, vp, i32, i64, i64, i32, i32, i32, i32, i32, f32, i32, vp, vp, vp,
+            u64, vp]
+        lib.kda_mla_prefill.restype = ctypes.c_int
+        lib.kda_mla_prefill_workspace_size.argtypes = [i32, i64, i32, i32]
+        lib.kda_mla_prefill_workspace_size.restype = u64
+        lib.kda_mla_decode.argtypes = [
+            vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, f32, vp, vp, vp, u64, vp]
+        lib.kda_mla_decode.restype = ctypes.c_int
+        lib.kda_mla_decode_workspace_size.argtypes = [i32, i32, i32]
+        lib.kda_mla_decode_workspace_size.restype = u64
+        lib.kda_mla_check.argtypes = [vp, vp]
+        lib.kda_mla_check.restype = ctypes.c_int
         lib.kda_status_string.argtypes = [i32]
         lib.kda_status_string.restype = ctypes.c_char_p
         lib.kda_abi_version.argtypes = []
@@ -409,3 +427,203 @@ def kda_gdn_decode_step_pooled(q, k, v, g, beta, S_pool, slots, *, o=None, strea
     in kda.h): as ``kda_decode_step_pooled`` with g [B, H] fp32."""
     return _decode_pooled("kda_gdn_decode_step_pooled", lambda B, H, dk: (B, H), q, k, v, g,
                           beta, S_pool, slots, o, stream)
+
+
+MLA_LATENT, MLA_ROPE, MLA_NOPE, MLA_DV = 512, 64, 128, 128
+
+
+def _check_rows(name, t, dtype, shape):
+    """A CUDA tensor whose last dimension is contiguous (the others may be
+    strided: views of a projection's output)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor (the KDA kernels run on the GPU only)" % name)
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.numel() and t.stride(-1) != 1:
+        raise ValueError("%s must be contiguous along its last dimension" % name)
+
+
+def kda_mla_append(c, k_r, slots, cache, *, positions=None, rope=None, interleaved=False,
+                   k_out=None, q_r=None, q_out=None, stream=None):
+    """Tokens into the paged latent cache (``kda_mla_append`` in kda.h).
+
+    c [T, 512] latents and k_r [T, 64] position keys (bf16 or fp32, rows may
+    be strided); slots [T] int32; cache [n_pages, page, 576].  With ``rope``
+    [max_pos, 64] fp32 (cosines, then sines) and ``positions`` [T] int32 the
+    position keys are rotated on the way.  ``k_out`` [T, 64] also receives
+    them; ``q_r`` [T, H, 64] (strided) is rotated into ``q_out`` (allocated if
+    omitted).  Returns q_out (None without q_r).
+    """
+    if not isinstance(c, torch.Tensor):
+        raise TypeError("c must be a torch.Tensor")
+    if c.dtype not in _DTYPE_CODE:
+        raise ValueError("c must be bfloat16 or float32")
+    T = c.shape[0]
+    _check_rows("c", c, c.dtype, (T, MLA_LATENT))
+    _check_rows("k_r", k_r, c.dtype, (T, MLA_ROPE))
+    _check_cuda("slots", slots, torch.int32, (T,))
+    _check_cuda("cache", cache, c.dtype)
+    if cache.dim() != 3 or cache.shape[2] != MLA_LATENT + MLA_ROPE:
+        raise ValueError("cache must have shape [n_pages, page, %d]" % (MLA_LATENT + MLA_ROPE))
+    max_pos = 0
+    if (rope is None) != (positions is None):
+        raise ValueError("positions and rope go together")
+    if rope is not None:
+        _check_cuda("positions", positions, torch.int32, (T,))
+        _check_cuda("rope", rope, torch.float32)
+        if rope.dim() != 2 or rope.shape[1] != MLA_ROPE:
+            raise ValueError("rope must have shape [max_pos, %d]" % MLA_ROPE)
+        max_pos = rope.shape[0]
+    if k_out is not None:
+        _check_rows("k_out", k_out, c.dtype, (T, MLA_ROPE))
+    H, qs, os_ = 0, (0, 0), (0, 0)
+    if q_r is not None:
+        if not isinstance(q_r, torch.Tensor) or q_r.dim() != 3:
+            raise ValueError("q_r must be a tensor of shape [T, H, %d]" % MLA_ROPE)
+        H = q_r.shape[1]
+        _check_rows("q_r", q_r, c.dtype, (T, H, MLA_ROPE))
+        if q_out is None:
+            q_out = torch.empty((T, H, MLA_ROPE), dtype=c.dtype, device=c.device)
+        _check_rows("q_out", q_out, c.dtype, (T, H, MLA_ROPE))
+        qs, os_ = q_r.stride()[:2], q_out.stride()[:2]
+    elif q_out is not None:
+        raise ValueError("q_out needs q_r")
+    _same_device(c.device, k_r=k_r, slots=slots, cache=cache, positions=positions, rope=rope,
+                 k_out=k_out, q_r=q_r, q_out=q_out)
+    with torch.cuda.device(c.device):
+        st = load().kda_mla_append(
+            _ptr(c), c.stride(0), _ptr(k_r), k_r.stride(0), _ptr(slots), _ptr(positions),
+            _ptr(rope), max_pos, int(bool(interleaved)), T, _ptr(cache), cache.shape[0],
+            cache.shape[1], MLA_LATENT, MLA_ROPE, _DTYPE_CODE[c.dtype], _ptr(k_out),
+            0 if k_out is None else k_out.stride(0), _ptr(q_r), qs[0], qs[1], H, _ptr(q_out),
+            os_[0], os_[1], _stream(stream, c.device))
+    if st != KDA_OK:
+        raise KdaError("kda_mla_append", st)
+    return q_out
+
+
+def kda_mla_prefill_workspace_size(N, Tq, H, dtype) -> int:
+    """Workspace bytes ``kda_mla_prefill`` needs (0: none)."""
+    code = _DTYPE_CODE[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
+    return int(load().kda_mla_prefill_workspace_size(N, Tq, H, code))
+
+
+def kda_mla_decode_workspace_size(B, H, dtype) -> int:
+    """Workspace bytes ``kda_mla_decode`` needs."""
+    code = _DTYPE_CODE[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
+    return int(load().kda_mla_decode_workspace_size(B, H, code))
+
+
+def kda_mla_check(workspace, stream=None) -> int:
+    """Synchronise the stream and return the device status of the last
+    latent-attention call that used ``workspace``."""
+    dev = None if workspace is None else workspace.device
+    with torch.cuda.device(dev):
+        return int(load().kda_mla_check(_ptr(workspace), _stream(stream, dev)))
+
+
+def _scale(scale):
+    return (MLA_NOPE + MLA_ROPE) ** -0.5 if scale is None else float(scale)
+
+
+def _workspace(workspace, need, device):
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    _check_cuda("workspace", workspace, torch.uint8)
+    return workspace
+
+
+def kda_mla_prefill(q, kv, k_r, cu_q, cu_k, *, scale=None, causal=True, o=None, lse=None,
+                    workspace=None, stream=None):
+    """Expanded latent attention over packed prompts (``kda_mla_prefill`` in kda.h).
+
+    q [Tq, H, 192], kv [Tk, H, 256] (key, then value, of each head), k_r
+    [Tk, 64] shared position keys, all bf16 or fp32; cu_q, cu_k [N+1] int32 on
+    the device.  ``scale`` defaults to 192 ** -0.5.  With ``causal`` the
+    queries are the last tokens of their sequence's keys.  Returns
+    (o [Tq, H, 128], lse [Tq, H] fp32).
+    """
+    _check_cuda("q", q)
+    if q.dtype not in _DTYPE_CODE:
+        raise ValueError("q must be bfloat16 or float32")
+    if q.dim() != 3:
+        raise ValueError("q must have shape [Tq, H, %d]" % (MLA_NOPE + MLA_ROPE))
+    Tq, H = q.shape[:2]
+    _check_cuda("q", q, None, (Tq, H, MLA_NOPE + MLA_ROPE))
+    _check_cuda("kv", kv, q.dtype)
+    Tk = kv.shape[0]
+    _check_cuda("kv", kv, None, (Tk, H, MLA_NOPE + MLA_DV))
+    _check_cuda("k_r", k_r, q.dtype, (Tk, MLA_ROPE))
+    _check_cuda("cu_q", cu_q, torch.int32)
+    N = cu_q.shape[0] - 1
+    _check_cuda("cu_k", cu_k, torch.int32, (N + 1,))
+    if o is None:
+        o = torch.empty((Tq, H, MLA_DV), dtype=q.dtype, device=q.device)
+    else:
+        _check_cuda("o", o, q.dtype, (Tq, H, MLA_DV))
+    if lse is None:
+        lse = torch.empty((Tq, H), dtype=torch.float32, device=q.device)
+    else:
+        _check_cuda("lse", lse, torch.float32, (Tq, H))
+    workspace = _workspace(workspace, kda_mla_prefill_workspace_size(N, Tq, H, q.dtype), q.device)
+    _same_device(q.device, kv=kv, k_r=k_r, cu_q=cu_q, cu_k=cu_k, o=o, lse=lse,
+                 workspace=workspace)
+    with torch.cuda.device(q.device):
+        st = load().kda_mla_prefill(
+            _ptr(q), _ptr(kv), _ptr(k_r), _ptr(cu_q), _ptr(cu_k), N, Tq, Tk, H, MLA_NOPE,
+            MLA_ROPE, MLA_DV, _DTYPE_CODE[q.dtype], _scale(scale), int(bool(causal)), _ptr(o),
+            _ptr(lse), _ptr(workspace), 0 if workspace is None else workspace.numel(),
+            _stream(stream, q.device))
+    if st != KDA_OK:
+        raise KdaError("kda_mla_prefill", st)
+    return o, lse
+
+
+def kda_mla_decode(q, cache, table, seq_lens, *, scale=None, o=None, lse=None, workspace=None,
+                   stream=None):
+    """Absorbed latent attention of one token per sequence over the paged
+    cache (``kda_mla_decode`` in kda.h).
+
+    q [B, H, 576] (W_K multiplied in), cache [n_pages, page, 576], both bf16
+    or fp32; table [B, max_pages] and seq_lens [B] int32 on the device.
+    ``scale`` defaults to 192 ** -0.5, that of the expanded heads.  Returns
+    (o [B, H, 512], lse [B, H] fp32).
+    """
+    _check_cuda("q", q)
+    if q.dtype not in _DTYPE_CODE:
+        raise ValueError("q must be bfloat16 or float32")
+    if q.dim() != 3:
+        raise ValueError("q must have shape [B, H, %d]" % (MLA_LATENT + MLA_ROPE))
+    B, H = q.shape[:2]
+    _check_cuda("q", q, None, (B, H, MLA_LATENT + MLA_ROPE))
+    _check_cuda("cache", cache, q.dtype)
+    if cache.dim() != 3 or cache.shape[2] != MLA_LATENT + MLA_ROPE:
+        raise ValueError("cache must have shape [n_pages, page, %d]" % (MLA_LATENT + MLA_ROPE))
+    _check_cuda("table", table, torch.int32)
+    if table.dim() != 2 or table.shape[0] != B:
+        raise ValueError("table must have shape [%d, max_pages]" % B)
+    _check_cuda("seq_lens", seq_lens, torch.int32, (B,))
+    if o is None:
+        o = torch.empty((B, H, MLA_LATENT), dtype=q.dtype, device=q.device)
+    else:
+        _check_cuda("o", o, q.dtype, (B, H, MLA_LATENT))
+    if lse is None:
+        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+    else:
+        _check_cuda("lse", lse, torch.float32, (B, H))
+    workspace = _workspace(workspace, kda_mla_decode_workspace_size(B, H, q.dtype), q.device)
+    _same_device(q.device, cache=cache, table=table, seq_lens=seq_lens, o=o, lse=lse,
+                 workspace=workspace)
+    with torch.cuda.device(q.device):
+        st = load().kda_mla_decode(
+            _ptr(q), _ptr(cache), _ptr(table), _ptr(seq_lens), B, H, cache.shape[0],
+            cache.shape[1], table.shape[1], MLA_LATENT, MLA_ROPE, _DTYPE_CODE[q.dtype],
+            _scale(scale), _ptr(o), _ptr(lse), _ptr(workspace),
+            0 if workspace is None else workspace.numel(), _stream(stream, q.device))
+    if st != KDA_OK:
+        raise KdaError("kda_mla_decode", st)
+    return o, lse

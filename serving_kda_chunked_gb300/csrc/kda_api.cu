@@ -1,13 +1,16 @@
 // kda_api.cu -- the C ABI: host-side validation and dispatch (see kda.h).
 #include "../../include/kda.h"
 #include "kda_internal.cuh"
+#include "kda_mla.cuh"
 
 #include <initializer_list>
+#include <math.h>
 
 namespace {
 
 inline bool aligned16(const void *p) { return p == nullptr || ((uintptr_t)p & 15u) == 0; }
 inline bool aligned4(const void *p) { return p == nullptr || ((uintptr_t)p & 3u) == 0; }
+inline bool page_ok(int32_t page) { return page == 16 || page == 32 || page == 64 || page == 128; }
 inline bool head_ok(int32_t dk, int32_t dv) { return dk == dv && (dk == 64 || dk == 128); }
 
 kda_status cuda_status(cudaError_t e) {
@@ -281,6 +284,120 @@ kda_status kda_gdn_decode_step_pooled(const void *q, const void *k, const void *
                        stream);
 }
 
+kda_status kda_mla_append(const void *c, int64_t c_stride, const void *k_r, int64_t k_r_stride,
+                          const int32_t *slots, const int32_t *positions, const float *rope,
+                          int32_t max_pos, int32_t interleaved, int64_t T, void *cache,
+                          int32_t n_pages, int32_t page, int32_t latent, int32_t rope_dim,
+                          int32_t dtype, void *k_out, int64_t k_out_stride, const void *q_r,
+                          int64_t q_token_stride, int64_t q_head_stride, int32_t H, void *q_out,
+                          int64_t qo_token_stride, int64_t qo_head_stride, void *stream) {
+    if (T < 0 || n_pages <= 0 || page <= 0 || latent <= 0 || rope_dim <= 0 || H < 0)
+        return KDA_ERR_INVALID_ARG;
+    if (dtype != KDA_BF16 && dtype != KDA_FP32) return KDA_ERR_INVALID_ARG;
+    if (latent != kda::mla::LATENT || rope_dim != kda::mla::ROPE || !page_ok(page) ||
+        T > 0x7fffffffLL || (int64_t)n_pages * page > 0x7fffffffLL)
+        return KDA_ERR_UNSUPPORTED;
+    if (T == 0) return KDA_OK;
+    if (!c || !k_r || !slots || !cache || (q_r == nullptr) != (q_out == nullptr) || (q_r && H == 0))
+        return KDA_ERR_INVALID_ARG;
+    if (rope && (!positions || max_pos <= 0)) return KDA_ERR_INVALID_ARG;
+    if (!aligned16(c) || !aligned16(k_r) || !aligned4(slots) || !aligned4(positions) ||
+        !aligned16(rope) || !aligned16(cache) || !aligned16(k_out) || !aligned16(q_r) ||
+        !aligned16(q_out))
+        return KDA_ERR_INVALID_ARG;
+    const int64_t piece = dtype == KDA_BF16 ? 8 : 4;       // elements of 16 bytes
+    for (int64_t x : {c_stride, k_r_stride, k_out ? k_out_stride : 0, q_r ? q_token_stride : 0,
+                      q_r ? q_head_stride : 0, q_r ? qo_token_stride : 0, q_r ? qo_head_stride : 0})
+        if (x < 0 || x % piece != 0) return KDA_ERR_INVALID_ARG;
+    const kda_status dst = check_device_ptrs({c, k_r, slots, positions, rope, cache, k_out, q_r, q_out});
+    if (dst != KDA_OK) return dst;
+    kda::mla::AppendArgs a;
+    a.c = c; a.k_r = k_r; a.q_r = q_r; a.cache = cache; a.k_out = k_out; a.q_out = q_out;
+    a.slots = slots; a.positions = positions; a.rope = rope;
+    a.c_stride = c_stride; a.k_r_stride = k_r_stride; a.k_out_stride = k_out_stride;
+    a.q_token_stride = q_token_stride; a.q_head_stride = q_head_stride;
+    a.qo_token_stride = qo_token_stride; a.qo_head_stride = qo_head_stride;
+    a.T = T; a.n_slots = (int64_t)n_pages * page;
+    a.max_pos = max_pos; a.interleaved = interleaved; a.H = H; a.dtype = dtype;
+    return cuda_status(kda::mla::launch_append(a, (cudaStream_t)stream));
+}
+
+uint64_t kda_mla_prefill_workspace_size(int32_t N, int64_t Tq, int32_t H, int32_t dtype) {
+    (void)N; (void)Tq; (void)H; (void)dtype;
+    return 0;
+}
+
+kda_status kda_mla_prefill(const void *q, const void *kv, const void *k_r, const int32_t *cu_q,
+                           const int32_t *cu_k, int32_t N, int64_t Tq, int64_t Tk, int32_t H,
+                           int32_t nope, int32_t rope_dim, int32_t dv, int32_t dtype, float scale,
+                           int32_t causal, void *o, float *lse, void *workspace,
+                           uint64_t workspace_bytes, void *stream) {
+    if (N < 0 || Tq < 0 || Tk < 0 || H <= 0 || nope <= 0 || rope_dim <= 0 || dv <= 0)
+        return KDA_ERR_INVALID_ARG;
+    if (dtype != KDA_BF16 && dtype != KDA_FP32) return KDA_ERR_INVALID_ARG;
+    if (!isfinite(scale)) return KDA_ERR_INVALID_ARG;
+    if (nope != kda::mla::NOPE || rope_dim != kda::mla::ROPE || dv != kda::mla::DV)
+        return KDA_ERR_UNSUPPORTED;
+    if (N == 0) return Tq == 0 && Tk == 0 ? KDA_OK : KDA_ERR_INVALID_ARG;
+    if (Tq > 0x7fffffffLL || Tk > 0x7fffffffLL) return KDA_ERR_INVALID_ARG;   // offsets are int32
+    if (!cu_q || !cu_k) return KDA_ERR_INVALID_ARG;
+    if (Tq == 0) return KDA_OK;
+    if (!q || !o || (Tk > 0 && (!kv || !k_r))) return KDA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(kv) || !aligned16(k_r) || !aligned16(o) || !aligned4(lse) ||
+        !aligned4(cu_q) || !aligned4(cu_k))
+        return KDA_ERR_INVALID_ARG;
+    const uint64_t need = kda_mla_prefill_workspace_size(N, Tq, H, dtype);
+    if (need && (!workspace || workspace_bytes < need || !aligned16(workspace)))
+        return KDA_ERR_INVALID_ARG;
+    if (H > 65535 || (Tq / 64 + N) * (int64_t)H > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
+    const kda_status dst = check_device_ptrs({q, kv, k_r, cu_q, cu_k, o, lse, need ? workspace : nullptr});
+    if (dst != KDA_OK) return dst;
+    kda::mla::PrefillArgs a;
+    a.q = q; a.kv = kv; a.k_r = k_r; a.cu_q = cu_q; a.cu_k = cu_k; a.o = o; a.lse = lse;
+    a.ws = workspace; a.Tq = Tq; a.Tk = Tk; a.N = N; a.H = H; a.dtype = dtype;
+    a.causal = causal; a.scale = scale;
+    return cuda_status(kda::mla::launch_prefill_simt(a, (cudaStream_t)stream));
+}
+
+uint64_t kda_mla_decode_workspace_size(int32_t B, int32_t H, int32_t dtype) {
+    if (B <= 0 || H <= 0 || (dtype != KDA_BF16 && dtype != KDA_FP32)) return 0;
+    return kda::mla::decode_simt_workspace_bytes(B, H);
+}
+
+kda_status kda_mla_decode(const void *q, const void *cache, const int32_t *table,
+                          const int32_t *seq_lens, int32_t B, int32_t H, int32_t n_pages,
+                          int32_t page, int32_t max_pages, int32_t latent, int32_t rope_dim,
+                          int32_t dtype, float scale, void *o, float *lse, void *workspace,
+                          uint64_t workspace_bytes, void *stream) {
+    if (B < 0 || H <= 0 || n_pages <= 0 || page <= 0 || max_pages < 0 || latent <= 0 || rope_dim <= 0)
+        return KDA_ERR_INVALID_ARG;
+    if (dtype != KDA_BF16 && dtype != KDA_FP32) return KDA_ERR_INVALID_ARG;
+    if (!isfinite(scale)) return KDA_ERR_INVALID_ARG;
+    if (latent != kda::mla::LATENT || rope_dim != kda::mla::ROPE || !page_ok(page) ||
+        B > 65535 || H > 65535 || (int64_t)n_pages * page > 0x7fffffffLL ||
+        (int64_t)max_pages * page > 0x7fffffffLL)
+        return KDA_ERR_UNSUPPORTED;
+    if (B == 0) return KDA_OK;
+    if (!q || !cache || (max_pages > 0 && !table) || !seq_lens || !o) return KDA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(cache) || !aligned4(table) || !aligned4(seq_lens) ||
+        !aligned16(o) || !aligned4(lse))
+        return KDA_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < kda_mla_decode_workspace_size(B, H, dtype) ||
+        !aligned16(workspace))
+        return KDA_ERR_INVALID_ARG;
+    const kda_status dst = check_device_ptrs({q, cache, table, seq_lens, o, lse, workspace});
+    if (dst != KDA_OK) return dst;
+    kda::mla::DecodeArgs a;
+    a.q = q; a.cache = cache; a.table = table; a.seq_lens = seq_lens; a.o = o; a.lse = lse;
+    a.ws = workspace; a.B = B; a.H = H; a.n_pages = n_pages; a.page = page;
+    a.max_pages = max_pages; a.dtype = dtype; a.scale = scale;
+    return cuda_status(kda::mla::launch_decode_simt(a, (cudaStream_t)stream));
+}
+
+kda_status kda_mla_check(const void *workspace, void *stream) {
+    return kda_prefill_check(workspace, stream);
+}
+
 const char *kda_status_string(int32_t status) {
     switch (status) {
     case KDA_OK: return "KDA_OK";
@@ -294,6 +411,6 @@ const char *kda_status_string(int32_t status) {
     }
 }
 
-int32_t kda_abi_version(void) { return (2 << 16) | 4; }
+int32_t kda_abi_version(void) { return (2 << 16) | 5; }
 
 }  // extern "C"
