@@ -361,7 +361,8 @@ kda_status kda_mla_prefill(const void *q, const void *kv, const void *k_r, const
 
 uint64_t kda_mla_decode_workspace_size(int32_t B, int32_t H, int32_t dtype) {
     if (B <= 0 || H <= 0 || (dtype != KDA_BF16 && dtype != KDA_FP32)) return 0;
-    return kda::mla::decode_simt_workspace_bytes(B, H);
+    return dtype == KDA_BF16 ? kda::mla::decode_tc_workspace_bytes(H)
+                             : kda::mla::decode_simt_workspace_bytes(B, H);
 }
 
 kda_status kda_mla_decode(const void *q, const void *cache, const int32_t *table,
@@ -391,7 +392,8 @@ kda_status kda_mla_decode(const void *q, const void *cache, const int32_t *table
     a.q = q; a.cache = cache; a.table = table; a.seq_lens = seq_lens; a.o = o; a.lse = lse;
     a.ws = workspace; a.B = B; a.H = H; a.n_pages = n_pages; a.page = page;
     a.max_pages = max_pages; a.dtype = dtype; a.scale = scale;
-    return cuda_status(kda::mla::launch_decode_simt(a, (cudaStream_t)stream));
+    return cuda_status(dtype == KDA_BF16 ? kda::mla::launch_decode_tc(a, (cudaStream_t)stream)
+                                         : kda::mla::launch_decode_simt(a, (cudaStream_t)stream));
 }
 
 kda_status kda_mla_check(const void *workspace, void *stream) {

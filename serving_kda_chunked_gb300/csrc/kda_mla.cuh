@@ -46,6 +46,8 @@ cudaError_t launch_append(const AppendArgs &a, cudaStream_t st);
 cudaError_t launch_prefill_simt(const PrefillArgs &a, cudaStream_t st);
 cudaError_t launch_decode_simt(const DecodeArgs &a, cudaStream_t st);
 uint64_t decode_simt_workspace_bytes(int32_t B, int32_t H);
+cudaError_t launch_decode_tc(const DecodeArgs &a, cudaStream_t st);
+uint64_t decode_tc_workspace_bytes(int32_t H);
 
 // Queries [bos, eos) of sequence n and its keys, from clamped offsets.
 struct SeqSpan { int64_t q0, k0; int nq, nk; };

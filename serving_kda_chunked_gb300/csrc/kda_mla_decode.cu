@@ -1,0 +1,741 @@
+// kda_mla_decode.cu -- absorbed latent attention of single tokens over the
+// paged bf16 cache, on the tensor cores (kda_mla_decode in kda.h).
+//
+// Per sequence, with the H queries q_h (576 values) and n cached rows c_j:
+//   s_jh = scale q_h . c_j,  p_jh = exp(s_jh - m_h),  o_h = sum_j p_jh c_j[:512] / sum_j p_jh
+//
+// What bounds it: the cache is read once (1152 bytes a token) for 2176 H
+// operations a token, 60 per byte at H = 32, a fifth of what the tensor cores
+// do in that time: HBM.  So a tile of 64 tokens is brought to shared memory
+// once and serves as the keys and as the values.
+//
+// Both products are transposed: S^T [64 tokens x N heads] = C Q^T and
+// O^T [512 x N heads] = C^T P, so that the tokens or latent channels are the
+// M rows of an MMA and the N columns are just the heads there are (16, 32 or
+// 64 a CTA).  With the heads as M rows, 32 heads would waste half or more of
+// every MMA, and 64 x 512 outputs would leave no tensor memory for the scores.
+//
+// Shared memory: two stages of 64 tokens x 576 (73,728 bytes each), the
+// queries, P.  A stage is laid out [8 groups of 8 tokens][9 chunks of 64
+// channels][8 tokens][128 bytes], 128-byte swizzled: one TMA box brings a
+// whole page piece, and both the K-major (scores) and the MN-major (output)
+// descriptors see uniform strides.
+//
+// Work split: the tiles of all sequences, laid end to end, are cut into equal
+// contiguous shares, one per CTA, by arithmetic that every CTA repeats from
+// the lengths; a sequence cut by a boundary leaves unnormalised partial
+// results that join_kernel adds up in a fixed order.
+//
+// Warps 0-3: softmax and epilogue; warp 4: MMA issue; warp 5: loads.
+#include "kda_mla_tc.cuh"
+
+#include <math_constants.h>
+#include <mutex>
+
+namespace kda {
+namespace mla {
+namespace {
+
+constexpr int TOK = 64, CHUNKS = ROW / 64;                  // tokens a tile, 128-byte chunks a row
+constexpr uint32_t GROUP = CHUNKS * 1024;                   // 8 tokens
+constexpr uint32_t STAGE = 8 * GROUP;
+constexpr int THREADS = 192, W_MMA = 4, W_LOAD = 5;
+constexpr int MAX_CTAS = 160;                               // per launch, up to one wave
+constexpr float RESCALE = 8.f;                              // see the softmax below
+constexpr uint32_t WS_STATUS = 256;                         // workspace: header | status | meta | ...
+
+template <int N> struct Smem {
+    static constexpr uint32_t Q = 2 * STAGE, P = Q + CHUNKS * N * 128, RED = P + N * 128,
+                              COL = RED + 2 * 4 * N * 4, MISC = COL + 2 * N * 4, BYTES = MISC + 256;
+};
+static_assert(Smem<64>::BYTES <= 232448, "shared memory");
+
+// What the CTA with share c of C starts in: sequence b, whose tiles are
+// [t0, t1) of all T; b < 0 marks an idle CTA.
+struct Meta { int64_t t0, t1, T; int32_t b, C; };
+
+struct DecParams {
+    CUtensorMap tm_c, tm_q;
+    const int32_t *table, *seq_lens;
+    __nv_bfloat16 *o;
+    float *lse;
+    int32_t *status;           // one word per CTA
+    Meta *meta;                // per CTA
+    float *part, *stat;        // two slots per CTA: [N][512], and [N][2] (maximum, sum)
+    int32_t B, H, n_pages, page, max_pages, groups;
+    float scale_log2;
+    int32_t force_timeout;
+};
+
+__device__ __forceinline__ int64_t seq_len(const DecParams &p, int b) {
+    const int64_t cap = (int64_t)p.max_pages * p.page, n = p.seq_lens[b];
+    return n < 0 ? 0 : (n > cap ? cap : n);
+}
+__device__ __forceinline__ int64_t tiles_of(int64_t len) { return (len + TOK - 1) / TOK; }
+__device__ __forceinline__ int64_t share_start(int64_t T, int c, int C) { return T * c / C; }
+
+// S^T accumulator (M = 64) of this warp's 16 tokens: register 4 i + 2 r + j is
+// token lane / 4 + 8 r, head 8 i + 2 (lane % 4) + j.
+template <int N> __device__ __forceinline__ void ld_scores(uint32_t a, float (&v)[N / 2]);
+template <> __device__ __forceinline__ void ld_scores<16>(uint32_t a, float (&v)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+                   "=f"(v[6]), "=f"(v[7]) : "r"(a) : "memory");
+}
+template <> __device__ __forceinline__ void ld_scores<32>(uint32_t a, float (&v)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+                   "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]),
+                   "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]) : "r"(a) : "memory");
+}
+template <> __device__ __forceinline__ void ld_scores<64>(uint32_t a, float (&v)[32]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+                   "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]),
+                   "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]),
+                   "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+                   "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]),
+                   "=f"(v[30]), "=f"(v[31]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t a, const float (&v)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+                 "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+                 :: "r"(a), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]),
+                    "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]),
+                    "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]) : "memory");
+}
+__device__ __forceinline__ uint32_t pack_bf(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+template <int N>
+__global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constant__ DecParams p) {
+    using L = Smem<N>;
+    constexpr int V = N / 4;                                // heads a softmax thread looks at
+    constexpr uint32_t TCOLS = N == 64 ? 512 : 256;
+    constexpr uint32_t S_COL = 0, O_COL = 2 * N;            // S^T twice, O^T in 4 blocks of 128 channels
+    extern __shared__ __align__(1024) uint8_t sm[];
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::MISC);   // [2] stage loaded
+    uint64_t *empty = full + 2;                             // [2] stage read
+    uint64_t *s_full = full + 4;                            // [2] S^T ready
+    uint64_t *p_full = full + 6, *o_full = full + 7;        // P written; its O^T product done
+    uint64_t *q_full = full + 8, *q_empty = full + 9, *o_empty = full + 10, *drain = full + 11;
+    uint64_t *vmask = full + 12;                            // [2] tokens of the stage that are seen
+    int64_t *s_t0 = reinterpret_cast<int64_t *>(full + 14);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(full + 16);
+    volatile int *fail = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    int *s_b = reinterpret_cast<int *>(tmem_slot + 2);
+    int64_t *scan = reinterpret_cast<int64_t *>(full + 20);  // [6] warp sums
+    float *red = reinterpret_cast<float *>(sm + L::RED);    // [2][4 warps][N]
+    float *col_a = reinterpret_cast<float *>(sm + L::COL);  // [N]
+    float *col_b = col_a + N;                               // [N]
+
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int group = blockIdx.x % p.groups, c = blockIdx.x / p.groups;
+    const int C0 = gridDim.x / p.groups;
+    const int h0 = group * N, nh = min(N, p.H - h0);
+
+    if (tid == 0) {
+        for (int i = 0; i < 12; ++i) mbar_init(&full[i], i == 6 || i == 10 ? 4 : 1);
+        mbar_fence_init();
+        *fail = 0;
+        *s_b = -1;
+    }
+    if (warp == W_MMA) tmem_alloc<TCOLS>(tmem_slot);
+    if (warp == W_LOAD && lane == 0) { prefetch_map(&p.tm_c); prefetch_map(&p.tm_q); }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // tiles of all sequences, and where this CTA's share starts
+    const int per = (p.B + THREADS - 1) / THREADS;
+    const int b_lo = min(p.B, tid * per), b_hi = min(p.B, b_lo + per);
+    int64_t mine = 0;
+    for (int b = b_lo; b < b_hi; ++b) mine += tiles_of(seq_len(p, b));
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) scan[warp] = incl;
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    int64_t T = 0, excl = incl - mine;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) excl += scan[w];
+        T += scan[w];
+    }
+    const int C = (int)(T < C0 ? T : C0);
+    const bool busy = c < C;
+    const int64_t g0 = busy ? share_start(T, c, C) : 0, g1 = busy ? share_start(T, c + 1, C) : 0;
+    if (busy && excl <= g0 && g0 < excl + mine) {
+        int64_t at = excl;
+        int b = b_lo;
+        for (;; ++b) {
+            const int64_t n = tiles_of(seq_len(p, b));
+            if (g0 < at + n) {
+                Meta m;
+                m.t0 = at; m.t1 = at + n; m.T = T; m.b = b; m.C = C;
+                p.meta[blockIdx.x] = m;
+                break;
+            }
+            at += n;
+        }
+        *s_t0 = at;
+        *s_b = b;
+    }
+    if (!busy && tid == 0) p.meta[blockIdx.x].b = -1;
+    // sequences with nothing cached
+    for (int b = c; b < p.B; b += C0) {
+        if (seq_len(p, b) > 0) continue;
+        const int64_t at = (int64_t)b * p.H + h0;
+        for (int e = tid; e < nh * (LATENT / 8); e += THREADS)
+            *reinterpret_cast<uint4 *>(p.o + at * LATENT + 8 * e) = make_uint4(0, 0, 0, 0);
+        if (p.lse && tid < nh) p.lse[at + tid] = -CUDART_INF_F;
+    }
+    __syncthreads();
+    const uint32_t tmem = warp_uniform(*tmem_slot);
+    const uint32_t smb = warp_uniform(smem_addr(sm));
+    const int b0 = *s_b;
+    const int64_t t00 = *s_t0;
+    const bool forced = p.force_timeout && busy;
+    if (forced) {      // test build only: a wait that nothing ends, before any copy or MMA
+        if (tid == 0 && !mbar_wait(drain, 0, 64)) *fail = FAIL_TIMEOUT;
+        __syncthreads();
+    }
+
+    // The share as segments: (sequence, its first tile here, one past its last
+    // tile here).  Every role walks them with the same arithmetic.
+    struct Walk { int b; int64_t at, len, lo, hi; };       // `at`: the sequence's first tile of all
+    auto open = [&](Walk &w, int b, int64_t at, int64_t g) {
+        w.len = seq_len(p, b);
+        w.b = b; w.at = at;
+        w.lo = g - at;
+        const int64_t n = tiles_of(w.len);
+        w.hi = g1 - at < n ? g1 - at : n;
+    };
+    auto next = [&](Walk &w) -> bool {                      // the next sequence with tiles in the share
+        int64_t at = w.at + tiles_of(w.len);
+        if (at >= g1) return false;
+        int b = w.b + 1;
+        while (b < p.B && seq_len(p, b) == 0) ++b;
+        if (b >= p.B) return false;                         // lengths changed under the kernel
+        open(w, b, at, at);
+        return true;
+    };
+
+    if (busy && !forced) {
+        Walk w;
+        open(w, b0, t00, g0);
+        if (warp == W_LOAD) {
+            // ---- loads: the table is read 32 entries at a time ----
+            const int piece = min(p.page, TOK), per_tile = TOK / piece;    // tokens a box, boxes a tile
+            const uint32_t box_bytes = (uint32_t)piece * ROW * 2;
+            const int64_t rows8 = (int64_t)p.n_pages * p.page / 8;         // out of range: zeros arrive
+            uint32_t k = 0;                                                // tiles asked for
+            int seg = 0;                                                   // queries asked for
+            bool ok = true;
+            do {
+                if (seg > 0) ok = wait_or_fail(q_empty, (seg - 1) & 1, fail);
+                if (!ok) break;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(q_full, CHUNKS * N * 128);
+                    tma4(smb + L::Q, &p.tm_q, 0, h0, 0, w.b, q_full);
+                }
+                __syncwarp();
+                ++seg;
+                const int32_t *tab = p.table + (int64_t)w.b * p.max_pages;
+                const int batch = 32 / per_tile;                           // tiles per table read
+                int mypage = -1;
+                for (int64_t i = w.lo; i < w.hi; ++i, ++k) {
+                    const int r = (int)((i - w.lo) % batch);
+                    if (r == 0) {
+                        const int64_t t = i * TOK + (int64_t)lane * piece;
+                        mypage = t < w.len ? tab[t / p.page] : -1;
+                        if (mypage < 0 || mypage >= p.n_pages) mypage = -1;
+                    }
+                    const int st = k & 1;
+                    if (k >= 2) ok = wait_or_fail(&empty[st], ((k >> 1) & 1) ^ 1, fail);
+                    if (!ok) break;
+                    uint64_t mask = 0;
+                    int pg[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        pg[j] = __shfl_sync(0xffffffffu, mypage, (r * per_tile + j) & 31);
+                        if (j < per_tile && pg[j] >= 0)
+                            mask |= (piece == 64 ? ~0ull : (1ull << piece) - 1) << (j * piece);
+                    }
+                    const int64_t left = w.len - i * TOK;
+                    if (left < TOK) mask &= (1ull << left) - 1;
+                    if (elect_one()) {
+                        vmask[st] = mask;
+                        mbar_arrive_expect_tx(&full[st], STAGE);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (j < per_tile) {
+                                const int64_t in_page = (i * TOK + j * piece) % p.page;
+                                const int64_t g8 = pg[j] < 0 ? rows8 : ((int64_t)pg[j] * p.page + in_page) / 8;
+                                tma4(smb + st * STAGE + j * box_bytes, &p.tm_c, 0, 0, 0, (int)g8, &full[st]);
+                            }
+                    }
+                    __syncwarp();
+                }
+            } while (ok && next(w));
+            if (!ok) {           // let what is in flight land before the CTA ends
+                for (uint32_t j = k >= 2 ? k - 2 : 0; j < k; ++j) mbar_wait(&full[j & 1], (j >> 1) & 1);
+                if (seg > 0) mbar_wait(q_full, (seg - 1) & 1);
+            }
+        } else if (warp == W_MMA) {
+            // ---- MMA issue: S^T of tile i, then O^T of tile i - 1 ----
+            constexpr uint32_t id_s = idesc(64, N, FMT_BF16, FMT_BF16, 0, 0);
+            constexpr uint32_t id_o = idesc(128, N, FMT_BF16, FMT_BF16, 1, 0);
+            const uint64_t dq = sdesc_k_sw128(smb + L::Q);
+            const uint64_t dp = sdesc_k_sw128(smb + L::P);
+            uint32_t k = 0;                                 // tiles whose S^T has been issued
+            int seg = 0;
+            bool ok = true;
+            auto out = [&](uint32_t j, bool first) {        // O^T of tile j
+                ok = ok && wait_or_fail(p_full, j & 1, fail);
+                if (first && seg > 0) ok = ok && wait_or_fail(o_empty, (seg - 1) & 1, fail);
+                if (!ok) return;
+                fence_after_sync();
+                const uint64_t dv = sdesc(warp_uniform(smb + (j & 1) * STAGE), 1024, GROUP, LAYOUT_SW128);
+                if (elect_one()) {
+#pragma unroll
+                    for (int mb = 0; mb < 4; ++mb)
+#pragma unroll
+                        for (int s = 0; s < TOK / 16; ++s)
+                            mma_f16(tmem + O_COL + mb * N, sdesc_add(dv, mb * 2048 + s * 2 * GROUP),
+                                    sdesc_add(dp, s * 32), id_o, !(first && s == 0));
+                    mma_commit(&empty[j & 1]);
+                    mma_commit(o_full);
+                }
+                __syncwarp();
+            };
+            do {
+                ok = wait_or_fail(q_full, seg & 1, fail);
+                for (int64_t i = w.lo; ok && i < w.hi; ++i, ++k) {
+                    const int st = k & 1;
+                    ok = wait_or_fail(&full[st], (k >> 1) & 1, fail);
+                    if (!ok) break;
+                    fence_after_sync();
+                    const uint64_t dc = sdesc(warp_uniform(smb + st * STAGE), 16, GROUP, LAYOUT_SW128);
+                    const uint32_t d_s = warp_uniform(tmem + S_COL + st * N);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int s = 0; s < ROW / 16; ++s)
+                            mma_f16(d_s, sdesc_add(dc, (s >> 2) * 1024 + (s & 3) * 32),
+                                    sdesc_add(dq, (s >> 2) * (N * 128) + (s & 3) * 32), id_s, s > 0);
+                        mma_commit(&s_full[st]);
+                        if (i == w.hi - 1) mma_commit(q_empty);
+                    }
+                    __syncwarp();
+                    if (i > w.lo) out(k - 1, i - 1 == w.lo);
+                }
+                if (ok) out(k - 1, w.hi - 1 == w.lo);
+                ++seg;
+            } while (ok && next(w));
+            if (!ok) {           // MMAs in flight end before tensor memory is freed
+                if (elect_one()) mma_commit(drain);
+                __syncwarp();
+                mbar_wait(drain, 0);
+            }
+        } else {
+            // ---- softmax and epilogue ----
+            // A warp whose wait failed stays in step with the others (their barriers
+            // count all 128 threads) until the next bar_or tells all of them.
+            uint32_t k = 0;
+            bool ok = true, stop = false;
+            const int row = 16 * warp + (lane >> 2);        // this thread's tokens: row, row + 8
+            do {
+                float m[V], l[V];                           // heads 8 (v / 2) + 2 (lane % 4) + v % 2
+#pragma unroll
+                for (int v = 0; v < V; ++v) { m[v] = -CUDART_INF_F; l[v] = 0.f; }
+                for (int64_t i = w.lo; i < w.hi; ++i, ++k) {
+                    const int st = k & 1;
+                    ok = wait_or_fail(&full[st], (k >> 1) & 1, fail);        // for vmask
+                    ok = ok && wait_or_fail(&s_full[st], (k >> 1) & 1, fail);
+                    fence_after_sync();
+                    float x[N / 2];
+                    ld_scores<N>(tmem_at(tmem, warp, S_COL + st * N), x);
+                    const uint64_t vm = vmask[st];
+                    tmem_wait_ld();
+                    reg_fence(x);
+                    const bool see0 = vm >> row & 1, see1 = vm >> (row + 8) & 1;
+#pragma unroll
+                    for (int e = 0; e < N / 2; ++e)
+                        x[e] = (e & 2 ? see1 : see0) ? x[e] * p.scale_log2 : -CUDART_INF_F;
+                    if (vm != ~0ull) {
+                        // rows that are not seen hold anything: zero them as values
+                        const int t = tid >> 1;
+                        if (!(vm >> t & 1)) {
+                            uint8_t *r = sm + st * STAGE + (t >> 3) * GROUP + (t & 7) * 128 + (tid & 1) * 4096;
+#pragma unroll
+                            for (int ch = 0; ch < 4; ++ch)
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    *reinterpret_cast<uint4 *>(r + ch * 1024 + e * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    // maximum over the warp's 16 tokens: each exchange halves the
+                    // heads a lane keeps, lane bits 4, 3, 2 choosing bits of v
+                    float t[V];
+#pragma unroll
+                    for (int v = 0; v < V; ++v) t[v] = fmaxf(x[(v >> 1) * 4 + (v & 1)], x[(v >> 1) * 4 + 2 + (v & 1)]);
+                    int keep = 0;
+                    constexpr int LAST = V >= 8 ? V / 8 : 1;
+#pragma unroll
+                    for (int bit = 16, half = V / 2; bit >= 4; bit >>= 1, half >>= 1) {
+                        if (half >= 1) {
+                            const bool up = lane & bit;
+#pragma unroll
+                            for (int v = 0; v < V / 2; ++v)
+                                if (v < half) {
+                                    const float give = up ? t[v] : t[v + half], have = up ? t[v + half] : t[v];
+                                    t[v] = fmaxf(have, __shfl_xor_sync(0xffffffffu, give, bit));
+                                }
+                            keep += up ? half : 0;
+                        } else {
+                            t[0] = fmaxf(t[0], __shfl_xor_sync(0xffffffffu, t[0], bit));
+                        }
+                    }
+                    float *rd = red + (k & 1) * 4 * N;
+#pragma unroll
+                    for (int v = 0; v < LAST; ++v) {
+                        const int at = keep + v;
+                        rd[warp * N + (at >> 1) * 8 + 2 * (lane & 3) + (at & 1)] = t[v];
+                    }
+                    stop = bar_or(1, 128, !ok);
+                    if (stop) break;
+                    bool grow = false;
+                    float mx[V];
+#pragma unroll
+                    for (int v = 0; v < V; v += 2) {
+                        const int at = (v >> 1) * 8 + 2 * (lane & 3);
+                        float2 y = *reinterpret_cast<const float2 *>(rd + at);
+#pragma unroll
+                        for (int q = 1; q < 4; ++q) {
+                            const float2 z = *reinterpret_cast<const float2 *>(rd + q * N + at);
+                            y.x = fmaxf(y.x, z.x); y.y = fmaxf(y.y, z.y);
+                        }
+                        mx[v] = y.x; mx[v + 1] = y.y;
+                        grow |= y.x > m[v] + RESCALE || y.y > m[v + 1] + RESCALE;
+                    }
+                    // The reference maximum is raised only when a score exceeds it by
+                    // more than 2^8: until then weights stay below 2^8, which float32
+                    // sums and bf16 weights hold as well as ones below 1, and the
+                    // output in tensor memory need not be rescaled.  All warps see
+                    // the same maxima and decide alike.
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const bool scale_o = i > w.lo;
+#pragma unroll
+                        for (int v = 0; v < V; ++v) {
+                            const float to = fmaxf(m[v], mx[v]);
+                            const float f = to == -CUDART_INF_F ? 1.f : ex2(m[v] - to);
+                            l[v] *= f;
+                            m[v] = to;
+                            if (warp == 0 && lane < 4) col_a[(v >> 1) * 8 + 2 * lane + (v & 1)] = f;
+                        }
+                        if (scale_o) {
+                            ok = wait_or_fail(o_full, (k - 1) & 1, fail);
+                            bar_sync(1, 128);               // col_a
+                            fence_after_sync();
+                            for (int cb = 0; cb < 4 * N; cb += 16) {
+                                float y[16];
+                                tmem_ld16(tmem_at(tmem, warp, O_COL + cb), y);
+                                tmem_wait_ld();
+                                reg_fence(y);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) y[e] *= col_a[(cb + e) % N];
+                                tmem_st16(tmem_at(tmem, warp, O_COL + cb), y);
+                            }
+                            tmem_wait_st();
+                        }
+                    }
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        const float ref = m[v] == -CUDART_INF_F ? 0.f : m[v];
+                        float &a = x[(v >> 1) * 4 + (v & 1)], &d = x[(v >> 1) * 4 + 2 + (v & 1)];
+                        a = ex2(a - ref);
+                        d = ex2(d - ref);
+                        l[v] += a + d;
+                    }
+                    // P [head][token] bf16, K-major: the previous product must have read it
+                    if (k > 0) ok = ok && wait_or_fail(o_full, (k - 1) & 1, fail);
+#pragma unroll
+                    for (int e = 0; e < N / 8; e += 2) {
+                        const uint32_t head = 8 * (e + (lane >> 4)) + (lane & 7);
+                        const uint32_t dst = smb + L::P + sw128_off(head, 2 * warp + (lane >> 3 & 1));
+                        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
+                                     :: "r"(dst), "r"(pack_bf(x[4 * e], x[4 * e + 1])),
+                                        "r"(pack_bf(x[4 * e + 2], x[4 * e + 3])),
+                                        "r"(pack_bf(x[4 * e + 4], x[4 * e + 5])),
+                                        "r"(pack_bf(x[4 * e + 6], x[4 * e + 7])) : "memory");
+                    }
+                    fence_async_smem();
+                    fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_full);
+                }
+                if (stop) break;
+                // the segment's end: sums over the tokens, outputs out of tensor memory
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) l[v] += __shfl_xor_sync(0xffffffffu, l[v], o);
+                }
+                float *rd = red + (k & 1) * 4 * N;
+                if (lane < 4) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        const int at = (v >> 1) * 8 + 2 * lane + (v & 1);
+                        rd[warp * N + at] = l[v];
+                        if (warp == 0) col_b[at] = m[v];
+                    }
+                }
+                const int64_t all = tiles_of(w.len);
+                const bool whole = w.lo == 0 && w.hi == all;
+                const int64_t slot = 2 * (int64_t)blockIdx.x + (w.lo == 0 ? 1 : 0);
+                bar_sync(1, 128);
+                if (tid < N) {
+                    const float sum = rd[tid] + rd[N + tid] + rd[2 * N + tid] + rd[3 * N + tid];
+                    const float top = col_b[tid];
+                    col_a[tid] = whole ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
+                    if (whole) {
+                        if (p.lse && tid < nh)
+                            p.lse[(int64_t)w.b * p.H + h0 + tid] =
+                                sum > 0.f ? (top + log2f(sum)) * CUDART_LN2_F : -CUDART_INF_F;
+                    } else {
+                        float2 *to = reinterpret_cast<float2 *>(p.stat + slot * N * 2) + tid;
+                        *to = make_float2(top, sum);
+                    }
+                }
+                ok = ok && wait_or_fail(o_full, (k - 1) & 1, fail);
+                stop = bar_or(1, 128, !ok);
+                if (stop) break;
+                fence_after_sync();
+                for (int cb = 0; cb < 4 * N; cb += 16) {
+                    const int ch = (cb / N) * 128 + tid, n0 = cb % N;      // this thread's channel
+                    if (n0 >= nh) continue;
+                    float y[16];
+                    tmem_ld16(tmem_at(tmem, warp, O_COL + cb), y);
+                    tmem_wait_ld();
+                    reg_fence(y);
+                    if (whole) {
+                        __nv_bfloat16 *to = p.o + ((int64_t)w.b * p.H + h0 + n0) * LATENT + ch;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (n0 + e < nh) to[e * LATENT] = __float2bfloat16_rn(y[e] * col_a[n0 + e]);
+                    } else {
+                        float *to = p.part + (slot * N + n0) * LATENT + ch;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (n0 + e < nh) to[e * LATENT] = y[e];
+                    }
+                }
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(o_empty);
+                bar_sync(1, 128);                           // col_a, col_b are free again
+            } while (next(w));
+        }
+    }
+    fence_before_sync();
+    __syncthreads();
+    if (tid == 0) p.status[blockIdx.x] = *fail;
+    if (warp == W_MMA) tmem_dealloc<TCOLS>(tmem);
+}
+
+// Adds up the partial results of the sequences that a share boundary cuts.
+// Block (boundary, r) works for the sequence its boundary lies in, together
+// with the blocks of that sequence's other boundaries; an item is 128
+// channels of a head, taken by one to eight warps, the more the more pieces
+// there are.  Pieces are added in order of the shares: a fixed order.
+template <int N>
+__global__ void __launch_bounds__(256) join_kernel(const DecParams p, int ctas, int32_t *header) {
+    __shared__ float4 buf[8][32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (blockIdx.x == 0 && blockIdx.y == 0) {              // the call's status, from the CTAs'
+        int st = 0;
+        for (int i = tid; i < ctas; i += 256) st |= p.status[i];
+        st = __syncthreads_or(st);
+        if (tid == 0) *header = st ? FAIL_TIMEOUT : 0;
+    }
+    const int cta = blockIdx.x + p.groups;                  // shares 1 .. of every group
+    if (cta >= ctas) return;
+    const int group = cta % p.groups, c = cta / p.groups;
+    const Meta m = p.meta[cta];
+    if (m.b < 0 || share_start(m.T, c, m.C) <= m.t0) return;
+    const int first = (int)(((m.t0 + 1) * m.C + m.T - 1) / m.T);   // boundaries inside the sequence
+    const int last = (int)((m.t1 * m.C + m.T - 1) / m.T) - 1;
+    const int pieces = last - first + 2;
+    const int team = pieces <= 4 ? 1 : (pieces <= 16 ? 2 : 8);     // warps an item
+    const int h0 = group * N, nh = min(N, p.H - h0), items = nh * 4;
+    const int teams = 8 / team, blocks = (last - first + 1) * gridDim.y;
+    const int block = (c - first) * gridDim.y + blockIdx.y;
+    auto slot_of = [&](int i) -> int64_t {                  // piece i, of share first - 1 + i
+        const int64_t cta_i = (int64_t)(first - 1 + i) * p.groups + group;
+        return 2 * cta_i + (i == 0 ? 1 : 0);
+    };
+    for (int base = block * teams; base < items; base += blocks * teams) {
+        const int item = base + warp / team, j = warp % team;
+        bool on = item < items;
+        const int h = item >> 2, q = item & 3;
+        float top = -CUDART_INF_F, sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (on) {
+            int bad = 0;                    // a share that gave up: o stays as it is
+            for (int i = lane; i < pieces; i += 32) {
+                top = fmaxf(top, p.stat[(slot_of(i) * N + h) * 2]);
+                bad |= p.status[slot_of(i) >> 1];
+            }
+            on = !__any_sync(0xffffffffu, bad);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float ref = top == -CUDART_INF_F ? 0.f : top;
+            for (int i = lane; i < pieces; i += 32) {
+                const float2 s = *reinterpret_cast<const float2 *>(p.stat + (slot_of(i) * N + h) * 2);
+                sum += ex2(s.x - ref) * s.y;
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+#pragma unroll 4
+            for (int i = j; i < pieces; i += team) {
+                const int64_t s = slot_of(i) * N + h;
+                const float f = ex2(p.stat[s * 2] - ref);
+                const float4 y = load4(p.part + s * LATENT + q * 128 + 4 * lane);
+                acc.x += f * y.x; acc.y += f * y.y; acc.z += f * y.z; acc.w += f * y.w;
+            }
+        }
+        if (team > 1) {
+            __syncthreads();
+            buf[warp][lane] = acc;
+            __syncthreads();
+            if (j == 0)
+                for (int i = 1; i < team; ++i) {
+                    const float4 y = buf[warp + i][lane];
+                    acc.x += y.x; acc.y += y.y; acc.z += y.z; acc.w += y.w;
+                }
+        }
+        if (on && j == 0) {
+            const float r = sum > 0.f ? 1.f / sum : 0.f;
+            const int64_t at = (int64_t)m.b * p.H + h0 + h;
+            store4(p.o + at * LATENT + q * 128 + 4 * lane,
+                   make_float4(acc.x * r, acc.y * r, acc.z * r, acc.w * r));
+            if (p.lse && q == 0 && lane == 0)
+                p.lse[at] = sum > 0.f ? (top + log2f(sum)) * CUDART_LN2_F : -CUDART_INF_F;
+        }
+    }
+}
+
+constexpr int JOIN_BLOCKS = 8;        // per boundary
+
+// Heads a CTA: the fewest that hold all H, else 64 a group.
+int heads_per_cta(int32_t H) { return H <= 16 ? 16 : (H <= 32 ? 32 : 64); }
+struct Plan { int N, groups, ctas; };
+Plan plan_of(int32_t H, int nsm) {
+    Plan pl;
+    pl.N = heads_per_cta(H);
+    pl.groups = (H + pl.N - 1) / pl.N;
+    const int shares = nsm / pl.groups;
+    pl.ctas = pl.groups * (shares > 0 ? shares : 1);
+    return pl;
+}
+
+cudaError_t sm_count(int *nsm) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(nsm, cudaDevAttrMultiProcessorCount, dev);
+    if (*nsm > MAX_CTAS) *nsm = MAX_CTAS;
+    return e;
+}
+
+uint64_t ws_meta(int ctas) { return WS_STATUS + ((uint64_t)ctas * 4 + 255) / 256 * 256; }
+uint64_t ws_stat(int ctas) { return ws_meta(ctas) + ((uint64_t)ctas * sizeof(Meta) + 255) / 256 * 256; }
+uint64_t ws_part(int ctas, int N) { return ws_stat(ctas) + (uint64_t)ctas * 2 * N * 8; }
+
+template <int N>
+cudaError_t run(const DecodeArgs &a, const Plan &pl, cudaStream_t st) {
+    static std::mutex mu;
+    static bool ready[64] = {false};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!ready[dev]) {
+            e = cudaFuncSetAttribute(decode_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)Smem<N>::BYTES);
+            if (e != cudaSuccess) return e;
+            ready[dev] = true;
+        }
+    }
+    uint8_t *ws = static_cast<uint8_t *>(a.ws);
+    DecParams p;
+    const uint64_t rows = (uint64_t)a.n_pages * a.page;
+    const uint64_t cd[4] = {64, 8, CHUNKS, rows / 8}, cs[3] = {ROW * 2, 128, GROUP};
+    const uint32_t cb[4] = {64, 8, CHUNKS, (uint32_t)(a.page < TOK ? a.page : TOK) / 8};
+    const uint64_t qd[4] = {64, (uint64_t)a.H, CHUNKS, (uint64_t)a.B};
+    const uint64_t qs[3] = {ROW * 2, 128, (uint64_t)a.H * ROW * 2};
+    const uint32_t qb[4] = {64, N, CHUNKS, 1};
+    if (!map4(&p.tm_c, a.cache, cd, cs, cb) || !map4(&p.tm_q, a.q, qd, qs, qb))
+        return cudaErrorInvalidValue;
+    p.table = a.table; p.seq_lens = a.seq_lens;
+    p.o = (__nv_bfloat16 *)a.o; p.lse = a.lse;
+    p.status = reinterpret_cast<int32_t *>(ws + WS_STATUS);
+    p.meta = reinterpret_cast<Meta *>(ws + ws_meta(pl.ctas));
+    p.stat = reinterpret_cast<float *>(ws + ws_stat(pl.ctas));
+    p.part = reinterpret_cast<float *>(ws + ws_part(pl.ctas, N));
+    p.B = a.B; p.H = a.H; p.n_pages = a.n_pages; p.page = a.page; p.max_pages = a.max_pages;
+    p.groups = pl.groups;
+    p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.force_timeout = fault_force_timeout();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)pl.ctas);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = Smem<N>::BYTES;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, decode_kernel<N>, p);
+    if (e != cudaSuccess) return e;
+    const int joins = pl.ctas - pl.groups;
+    cfg.gridDim = dim3((unsigned)(joins > 0 ? joins : 1), JOIN_BLOCKS);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, join_kernel<N>, p, pl.ctas, reinterpret_cast<int32_t *>(ws));
+}
+
+}  // namespace
+
+uint64_t decode_tc_workspace_bytes(int32_t H) {
+    const Plan pl = plan_of(H, MAX_CTAS);      // the most any device takes
+    return ws_part(pl.ctas, pl.N) + (uint64_t)pl.ctas * 2 * pl.N * LATENT * 4;
+}
+
+cudaError_t launch_decode_tc(const DecodeArgs &a, cudaStream_t st) {
+    int nsm = 1;
+    const cudaError_t e = sm_count(&nsm);
+    if (e != cudaSuccess) return e;
+    const Plan pl = plan_of(a.H, nsm);
+    switch (pl.N) {
+    case 16: return run<16>(a, pl, st);
+    case 32: return run<32>(a, pl, st);
+    default: return run<64>(a, pl, st);
+    }
+}
+
+}  // namespace mla
+}  // namespace kda

@@ -324,7 +324,7 @@ cudaError_t launch_prefill_simt(const PrefillArgs &a, cudaStream_t st) {
 cudaError_t launch_decode_simt(const DecodeArgs &a, cudaStream_t st) {
     cudaError_t e = cudaMemsetAsync(a.ws, 0, 256, st);
     if (e != cudaSuccess) return e;
-    return a.dtype == 0 ? run_decode<__nv_bfloat16>(a, st) : run_decode<float>(a, st);
+    return run_decode<float>(a, st);
 }
 
 }  // namespace mla
