@@ -323,8 +323,8 @@ kda_status kda_mla_append(const void *c, int64_t c_stride, const void *k_r, int6
 }
 
 uint64_t kda_mla_prefill_workspace_size(int32_t N, int64_t Tq, int32_t H, int32_t dtype) {
-    (void)N; (void)Tq; (void)H; (void)dtype;
-    return 0;
+    if (N <= 0 || Tq <= 0 || H <= 0 || dtype != KDA_BF16) return 0;
+    return kda::mla::prefill_tc_workspace_bytes(N, Tq);
 }
 
 kda_status kda_mla_prefill(const void *q, const void *kv, const void *k_r, const int32_t *cu_q,
@@ -356,7 +356,8 @@ kda_status kda_mla_prefill(const void *q, const void *kv, const void *k_r, const
     a.q = q; a.kv = kv; a.k_r = k_r; a.cu_q = cu_q; a.cu_k = cu_k; a.o = o; a.lse = lse;
     a.ws = workspace; a.Tq = Tq; a.Tk = Tk; a.N = N; a.H = H; a.dtype = dtype;
     a.causal = causal; a.scale = scale;
-    return cuda_status(kda::mla::launch_prefill_simt(a, (cudaStream_t)stream));
+    return cuda_status(dtype == KDA_BF16 ? kda::mla::launch_prefill_tc(a, (cudaStream_t)stream)
+                                         : kda::mla::launch_prefill_simt(a, (cudaStream_t)stream));
 }
 
 uint64_t kda_mla_decode_workspace_size(int32_t B, int32_t H, int32_t dtype) {

@@ -48,6 +48,8 @@ cudaError_t launch_decode_simt(const DecodeArgs &a, cudaStream_t st);
 uint64_t decode_simt_workspace_bytes(int32_t B, int32_t H);
 cudaError_t launch_decode_tc(const DecodeArgs &a, cudaStream_t st);
 uint64_t decode_tc_workspace_bytes(int32_t H);
+cudaError_t launch_prefill_tc(const PrefillArgs &a, cudaStream_t st);
+uint64_t prefill_tc_workspace_bytes(int32_t N, int64_t Tq);
 
 // Queries [bos, eos) of sequence n and its keys, from clamped offsets.
 struct SeqSpan { int64_t q0, k0; int nq, nk; };

@@ -100,18 +100,6 @@ template <> __device__ __forceinline__ void ld_scores<64>(uint32_t a, float (&v)
                    "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]),
                    "=f"(v[30]), "=f"(v[31]) : "r"(a) : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t a, const float (&v)[16]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-                 "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-                 :: "r"(a), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]),
-                    "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]),
-                    "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]) : "memory");
-}
-__device__ __forceinline__ uint32_t pack_bf(float a, float b) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
 template <int N>
 __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constant__ DecParams p) {
     using L = Smem<N>;

@@ -1,0 +1,528 @@
+// kda_mla_prefill.cu -- expanded latent attention of packed prompts on the
+// tensor cores, bf16 (kda_mla_prefill in kda.h).
+//
+// Per head, with queries q_i and keys k_j (192 values) and values v_j (128):
+//   s_ij = scale q_i . k_j,  o_i = sum_j exp(s_ij - m_i) v_j / sum_j exp(s_ij - m_i)
+// in one pass over the keys with the running maximum m_i and sum.
+//
+// What bounds it: 640 operations per (query, key, head) against 256 query
+// rows of reuse for every key read from L2: the tensor cores.  A CTA takes 256
+// queries of one head as two tiles (A, B) of 128 rows, so that one tile's
+// products run while the other tile's softmax does, and each key tile of 128
+// tokens is read once for both.
+//
+// Tensor memory (all 512 columns): scores of A and B (128 columns each), their
+// outputs (128 each).  The weights P replace the scores they come from, as
+// bf16 pairs, and are the A operand of the output product straight from
+// tensor memory.  Shared memory: both query tiles (96 KB) and a ring of eight
+// 16 KB blocks: a key tile is three blocks of 64 channels (two of the head's
+// own, one of the shared position key, which is never copied out per head), a
+// value tile two blocks of 64 tokens.
+//
+// Warps 0-3: softmax of tile A, warps 4-7: of tile B, one thread a row;
+// warp 8: MMA issue; warp 9: loads.  MMAs of a tile run in issue order:
+//   S_A(j)  O_B(j-1)  S_B(j)  O_A(j)  S_A(j+1)  ...
+// so the scores of step j are complete only after the tile's output product of
+// step j - 1, and then its output may be rescaled and its P overwritten.
+#include "kda_mla_tc.cuh"
+
+#include <float.h>
+#include <math_constants.h>
+#include <mutex>
+
+namespace kda {
+namespace mla {
+namespace {
+
+constexpr int BQ = 128, BK = 128, ROWS = 2 * BQ;            // rows a tile, keys a tile, rows a CTA
+constexpr int THREADS = 320, W_MMA = 8, W_LOAD = 9;
+constexpr uint32_t BLOCK = 16384;
+constexpr int RING = 8, PER = 5;                            // blocks in the ring, blocks a key tile
+constexpr uint32_t SM_Q = 0, SM_RING = 6 * BLOCK, SM_MISC = SM_RING + RING * BLOCK, SM_BYTES = SM_MISC + 256;
+static_assert(SM_BYTES <= 232448, "shared memory");
+constexpr uint32_t S_COL = 0, O_COL = 256;                  // + 128 for tile B
+constexpr float RESCALE = 8.f;
+
+// workspace: [0] status, [1] entries; then the offsets of the sequences' first
+// entries, then the entries (sequence, block of 256 queries), most keys first
+constexpr uint32_t WS_BASE = 256;
+__host__ __device__ inline uint64_t ws_list(int N) {
+    return (WS_BASE + 4ull * ((uint64_t)N + 1) + 15) / 16 * 16;
+}
+
+struct PreParams {
+    CUtensorMap tm_q, tm_k, tm_v, tm_r;
+    const int32_t *cu_q, *cu_k;
+    __nv_bfloat16 *o;
+    float *lse;
+    int32_t *ws;
+    int64_t Tq, Tk;
+    int32_t N, H, causal, negative;   // negative: the scale is; scale_log2 is its magnitude
+    float scale_log2;
+    int32_t force_timeout;
+};
+
+__device__ __forceinline__ int2 *list_of(const PreParams &p) {
+    return reinterpret_cast<int2 *>(reinterpret_cast<uint8_t *>(p.ws) + ws_list(p.N));
+}
+// Keys that row i (of nq) sees, and key tiles that the rows up to `last` need.
+__device__ __forceinline__ int keys_seen(const SeqSpan &s, int i, int causal) {
+    if (!causal) return s.nk;
+    const int64_t e = (int64_t)i + s.nk - s.nq + 1;
+    return e < 0 ? 0 : (e > s.nk ? s.nk : (int)e);
+}
+__device__ __forceinline__ int key_tiles(const SeqSpan &s, int row0, int rows, int causal) {
+    if (row0 >= s.nq) return 0;
+    const int last = min(row0 + rows, s.nq) - 1;
+    return (keys_seen(s, last, causal) + BK - 1) / BK;
+}
+
+// Lists the blocks of queries, those with the most keys first (CTAs start in
+// list order, so the longest do not end last), and clears the status.  At most
+// `cap` of them: offsets that overlap or run backwards lose the rest.
+__global__ void __launch_bounds__(1024) plan_kernel(const PreParams p, int cap) {
+    constexpr int NB = 1024;
+    __shared__ int start[NB + 1];
+    __shared__ int64_t warp_tot[32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int32_t *base = p.ws + WS_BASE / 4;
+    auto block_scan = [&](int64_t x) -> int64_t {           // inclusive
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) warp_tot[warp] = x;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) x += warp_tot[w];
+        return x;
+    };
+    const int per = (p.N + 1023) / 1024;
+    const int n0 = min(p.N, tid * per), n1 = min(p.N, n0 + per);
+    int64_t mine = 0;
+    for (int n = n0; n < n1; ++n) mine += (seq_span(p.cu_q, p.cu_k, n, p.Tq, p.Tk).nq + ROWS - 1) / ROWS;
+    int64_t at = block_scan(mine) - mine;
+    for (int n = n0; n < n1; ++n) {
+        base[n] = (int)(at < cap ? at : cap);
+        at += (seq_span(p.cu_q, p.cu_k, n, p.Tq, p.Tk).nq + ROWS - 1) / ROWS;
+    }
+    start[tid] = 0;
+    if (tid == 1023) {
+        const int all = (int)(at < cap ? at : cap);
+        base[p.N] = all;
+        p.ws[0] = 0;
+        p.ws[1] = all;
+        start[NB] = all;
+    }
+    __syncthreads();
+    const int E = start[NB];
+    auto entry = [&](int e, int &bin) -> int2 {
+        int lo = 0, hi = p.N - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (base[mid] <= e) lo = mid; else hi = mid - 1;
+        }
+        const int qb = e - base[lo];
+        const SeqSpan s = seq_span(p.cu_q, p.cu_k, lo, p.Tq, p.Tk);
+        bin = NB - 1 - min(key_tiles(s, qb * ROWS, ROWS, p.causal), NB - 1);
+        return make_int2(lo, qb);
+    };
+    int bin;
+    for (int e = tid; e < E; e += 1024) { entry(e, bin); atomicAdd(&start[bin], 1); }
+    __syncthreads();
+    const int count = start[tid];
+    const int incl = (int)block_scan(count);
+    start[tid] = incl - count;
+    __syncthreads();
+    int2 *list = list_of(p);
+    for (int e = tid; e < E; e += 1024) {
+        const int2 x = entry(e, bin);
+        list[atomicAdd(&start[bin], 1)] = x;
+    }
+}
+
+__device__ __forceinline__ void mma_f16_tmem_a(uint32_t d, uint32_t a, uint64_t b, uint32_t id,
+                                               uint32_t accumulate) {
+    asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+                 :: "r"(d), "r"(a), "l"(b), "r"(id), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t a, float *v) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+                   "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]),
+                   "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]),
+                   "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+                   "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]),
+                   "=f"(v[30]), "=f"(v[31]) : "r"(a) : "memory");
+}
+// Two float32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)),
+          "l"(reinterpret_cast<uint64_t &>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+__global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_constant__ PreParams p) {
+    extern __shared__ __align__(1024) uint8_t sm[];
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm + SM_MISC);    // [8] ring block loaded
+    uint64_t *empty = full + RING;                          // [8] ring block read
+    uint64_t *q_full = full + 16;                           // [2] query tiles
+    uint64_t *s_full = full + 18, *p_full = full + 20, *o_full = full + 22, *drain = full + 24;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(full + 25);
+    volatile int *fail = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    if (tid == 0) {
+        for (int i = 0; i < 25; ++i) mbar_init(&full[i], i == 20 || i == 21 ? 4 : 1);
+        mbar_fence_init();
+        *fail = 0;
+    }
+    if (warp == W_MMA) tmem_alloc<512>(tmem_slot);
+    if (warp == W_LOAD && lane == 0) {
+        prefetch_map(&p.tm_q); prefetch_map(&p.tm_k); prefetch_map(&p.tm_v); prefetch_map(&p.tm_r);
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tmem = warp_uniform(*tmem_slot);
+    const uint32_t smb = warp_uniform(smem_addr(sm));
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    const int e = blockIdx.x / p.H, h = blockIdx.x % p.H;
+    const bool forced = p.force_timeout;
+    if (forced) {          // test build only: a wait that nothing ends, before any copy or MMA
+        if (tid == 0 && !mbar_wait(drain, 0, 64)) *fail = FAIL_TIMEOUT;
+        __syncthreads();
+    }
+    if (e < p.ws[1] && !forced) {
+        const int2 ent = list_of(p)[e];
+        const SeqSpan s = seq_span(p.cu_q, p.cu_k, ent.x, p.Tq, p.Tk);
+        const int i0 = ent.y * ROWS;
+        const int nA = key_tiles(s, i0, BQ, p.causal), nB = key_tiles(s, i0 + BQ, BQ, p.causal);
+        const int n = max(nA, nB);
+        if (warp == W_LOAD) {
+            bool ok = true;
+            int q = 0;                                      // blocks asked for
+            if (n > 0) {
+                if (elect_one()) {
+                    if (nA > 0) {
+                        mbar_arrive_expect_tx(&q_full[0], 3 * BLOCK);
+                        tma4(smb + SM_Q, &p.tm_q, 0, (int)s.q0 + i0, 0, h, &q_full[0]);
+                    }
+                    if (nB > 0) {
+                        mbar_arrive_expect_tx(&q_full[1], 3 * BLOCK);
+                        tma4(smb + SM_Q + 3 * BLOCK, &p.tm_q, 0, (int)s.q0 + i0 + BQ, 0, h, &q_full[1]);
+                    }
+                }
+                __syncwarp();
+                for (int j = 0; ok && j < n; ++j) {
+                    const int t = (int)s.k0 + j * BK;
+#pragma unroll
+                    for (int b = 0; b < PER; ++b) {
+                        const int slot = q % RING;
+                        if (q >= RING) ok = wait_or_fail(&empty[slot], ((q / RING) & 1) ^ 1, fail);
+                        if (!ok) break;
+                        if (elect_one()) {
+                            const uint32_t dst = smb + SM_RING + slot * BLOCK;
+                            mbar_arrive_expect_tx(&full[slot], BLOCK);
+                            if (b < 2) tma4(dst, &p.tm_k, 0, t, b, h, &full[slot]);
+                            else if (b == 2) tma4(dst, &p.tm_r, 0, t, 0, 0, &full[slot]);
+                            else tma4(dst, &p.tm_v, 0, t + (b - 3) * 64, 2, h, &full[slot]);
+                        }
+                        __syncwarp();
+                        ++q;
+                    }
+                }
+            }
+            if (!ok) {         // let what is in flight land before the CTA ends
+                for (int b = max(0, q - RING); b < q; ++b) mbar_wait(&full[b % RING], (b / RING) & 1);
+                if (nA > 0) mbar_wait(&q_full[0], 0);
+                if (nB > 0) mbar_wait(&q_full[1], 0);
+            }
+        } else if (warp == W_MMA) {
+            constexpr uint32_t id_s = idesc(128, 128, FMT_BF16, FMT_BF16, 0, 0);
+            constexpr uint32_t id_o = idesc(128, 128, FMT_BF16, FMT_BF16, 0, 1);
+            bool ok = true;
+            // S of tile x, step j; `last` user of the key blocks frees them
+            auto scores = [&](int x, int j, bool first, bool last) {
+                if (j == 0) ok = ok && wait_or_fail(&q_full[x], 0, fail);
+                const uint32_t d = warp_uniform(tmem + S_COL + 128 * x);
+                const uint64_t dq = sdesc_k_sw128(warp_uniform(smb + SM_Q + x * 3 * BLOCK));
+#pragma unroll
+                for (int b = 0; b < 3; ++b) {
+                    const int q = PER * j + b, slot = q % RING;
+                    if (first) ok = ok && wait_or_fail(&full[slot], (q / RING) & 1, fail);
+                    if (!ok) return;
+                    const uint64_t dk = sdesc_k_sw128(warp_uniform(smb + SM_RING + slot * BLOCK));
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_f16(d, sdesc_add(dq, b * BLOCK + k * 32), sdesc_add(dk, k * 32), id_s,
+                                    b > 0 || k > 0);
+                        if (last) mma_commit(&empty[slot]);
+                        if (b == 2) mma_commit(&s_full[x]);
+                    }
+                    __syncwarp();
+                }
+            };
+            auto outputs = [&](int x, int j, bool first, bool last, bool end) {
+                ok = ok && wait_or_fail(&p_full[x], j & 1, fail);
+                if (!ok) return;
+                fence_after_sync();
+                const uint32_t d = warp_uniform(tmem + O_COL + 128 * x);
+                const uint32_t a = warp_uniform(tmem + S_COL + 128 * x);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const int q = PER * j + 3 + b, slot = q % RING;
+                    if (first) ok = ok && wait_or_fail(&full[slot], (q / RING) & 1, fail);
+                    if (!ok) return;
+                    // values [2 chunks of 64 channels][64 tokens][128 bytes]: MN-major B
+                    const uint64_t dv = sdesc(warp_uniform(smb + SM_RING + slot * BLOCK), 8192, 1024, LAYOUT_SW128);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_f16_tmem_a(d, a + (b * 4 + k) * 8, sdesc_add(dv, k * 2048), id_o,
+                                           j > 0 || b > 0 || k > 0);
+                        if (last) mma_commit(&empty[slot]);
+                        if (b == 1 && end) mma_commit(&o_full[x]);
+                    }
+                    __syncwarp();
+                }
+            };
+            for (int j = 0; ok && j <= n; ++j) {
+                if (j < nA) scores(0, j, true, j >= nB);
+                if (j > 0 && j - 1 < nB) outputs(1, j - 1, j - 1 >= nA, true, j == nB);
+                if (j < nB) scores(1, j, j >= nA, true);
+                if (j < nA) outputs(0, j, true, j >= nB, j == nA - 1);
+            }
+            if (!ok) {         // MMAs in flight end before tensor memory is freed
+                if (elect_one()) mma_commit(drain);
+                __syncwarp();
+                mbar_wait(drain, 0);
+            }
+        } else {
+            const int x = warp >> 2, row = tid & 127;       // tile, row in it
+            const int i = i0 + x * BQ + row;                // query of the sequence
+            const int nX = x ? nB : nA;
+            const int end = i < s.nq ? keys_seen(s, i, p.causal) : s.nk;
+            // keys that every row of this warp sees
+            const int warp_end = __reduce_min_sync(0xffffffffu, end);
+            const uint32_t t_s = tmem_at(tmem, warp, S_COL + 128 * x);
+            const uint32_t t_o = tmem_at(tmem, warp, O_COL + 128 * x);
+            const float sc = p.scale_log2;
+            float m = -CUDART_INF_F;                        // unscaled
+            float2 l2 = make_float2(0.f, 0.f);
+            bool ok = true;
+            for (int j = 0; j < nX; ++j) {
+                ok = wait_or_fail(&s_full[x], j & 1, fail);
+                if (!ok) break;
+                fence_after_sync();
+                float v[128];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, v + 32 * c);
+                tmem_wait_ld();
+                reg_fence(v);
+                if (p.negative) {
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) v[c] = -v[c];
+                }
+                if ((j + 1) * BK > warp_end) {
+                    const int lim = end - j * BK;
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) v[c] = c < lim ? v[c] : -CUDART_INF_F;
+                }
+                const int valid = s.nk - j * BK;            // keys of the sequence in this tile
+                if (valid < BK && (x == 0 || j >= nA)) {
+                    // values behind the sequence's end hold anything: zero them
+                    // (whichever tile's product comes first)
+                    const int q = PER * j + 3 + (row >> 6), slot = q % RING;
+                    ok = wait_or_fail(&full[slot], (q / RING) & 1, fail);
+                    if (!ok) break;
+                    if (row >= valid) {
+                        uint8_t *r = sm + SM_RING + slot * BLOCK + (row & 63) * 128;
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            *reinterpret_cast<uint4 *>(r + (c >> 3) * 8192 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async_smem();
+                }
+                float t0 = v[0], t1 = v[1], t2 = v[2], t3 = v[3];
+#pragma unroll
+                for (int c = 4; c < 124; c += 8) {
+                    t0 = max3(t0, v[c], v[c + 1]);
+                    t1 = max3(t1, v[c + 2], v[c + 3]);
+                    t2 = max3(t2, v[c + 4], v[c + 5]);
+                    t3 = max3(t3, v[c + 6], v[c + 7]);
+                }
+                t0 = max3(t0, v[124], v[125]);
+                t1 = max3(t1, v[126], v[127]);
+                const float top = max3(t0, t1, fmaxf(t2, t3));
+                // The reference is raised only when a score exceeds it by more
+                // than 2^8 (weights stay below 2^8, which float32 sums and bf16
+                // weights hold as well as ones below 1): the output in tensor
+                // memory is then rarely rescaled.
+                if (__any_sync(0xffffffffu, (top - m) * sc > RESCALE || (m == -CUDART_INF_F && top > m))) {
+                    const float to = fmaxf(m, top);
+                    const float f = to == -CUDART_INF_F ? 1.f : ex2((m - to) * sc);
+                    m = to;
+                    l2.x *= f; l2.y *= f;
+                    if (j > 0) {
+                        for (int c = 0; c < 128; c += 16) {
+                            float y[16];
+                            tmem_ld16(t_o + c, y);
+                            tmem_wait_ld();
+                            reg_fence(y);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) y[k] *= f;
+                            tmem_st16(t_o + c, y);
+                        }
+                    }
+                }
+                const float off = m == -CUDART_INF_F ? 0.f : -m * sc;
+                const float2 sc2 = make_float2(sc, sc), off2 = make_float2(off, off);
+                float2 a0 = make_float2(0.f, 0.f), a1 = a0;
+#pragma unroll
+                for (int c = 0; c < 128; c += 32) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4) {
+                        float2 y0 = fma2(make_float2(v[c + k], v[c + k + 1]), sc2, off2);
+                        float2 y1 = fma2(make_float2(v[c + k + 2], v[c + k + 3]), sc2, off2);
+                        y0.x = ex2(y0.x); y0.y = ex2(y0.y);
+                        y1.x = ex2(y1.x); y1.y = ex2(y1.y);
+                        a0 = add2(a0, y0);
+                        a1 = add2(a1, y1);
+                        w[k / 2] = pack_bf(y0.x, y0.y);
+                        w[k / 2 + 1] = pack_bf(y1.x, y1.y);
+                    }
+                    tmem_st16(t_s + c / 2, w);
+                }
+                l2 = add2(l2, add2(a0, a1));
+                tmem_wait_st();
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[x]);
+            }
+            if (ok && nX > 0) ok = wait_or_fail(&o_full[x], 0, fail);
+            if (ok && i0 + x * BQ < s.nq) {
+                const float l = l2.x + l2.y;
+                const float r = l > 0.f ? 1.f / l : 0.f;
+                const int64_t at = (s.q0 + i) * p.H + h;
+                fence_after_sync();
+#pragma unroll
+                for (int c = 0; c < 128; c += 16) {
+                    float y[16];
+                    if (nX > 0) {
+                        tmem_ld16(t_o + c, y);
+                        tmem_wait_ld();
+                        reg_fence(y);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) y[k] = 0.f;
+                    }
+                    if (i < s.nq) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) w[k] = pack_bf(y[2 * k] * r, y[2 * k + 1] * r);
+                        uint4 *to = reinterpret_cast<uint4 *>(p.o + at * DV + c);
+                        to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                        to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                    }
+                }
+                if (p.lse && i < s.nq)
+                    p.lse[at] = l > 0.f ? (m * sc + log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
+            }
+        }
+    }
+    fence_before_sync();
+    __syncthreads();
+    if (tid == 0 && *fail) atomicExch(p.ws, *fail);
+    if (warp == W_MMA) tmem_dealloc<512>(tmem);
+}
+
+}  // namespace
+
+uint64_t prefill_tc_workspace_bytes(int32_t N, int64_t Tq) {
+    return ws_list(N) + 8ull * ((uint64_t)Tq / ROWS + N);
+}
+
+cudaError_t launch_prefill_tc(const PrefillArgs &a, cudaStream_t st) {
+    static std::mutex mu;
+    static bool ready[64] = {false};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!ready[dev]) {
+            e = cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)SM_BYTES);
+            if (e != cudaSuccess) return e;
+            ready[dev] = true;
+        }
+    }
+    PreParams p;
+    const uint64_t H = (uint64_t)a.H, Tq = (uint64_t)a.Tq, Tk = (uint64_t)a.Tk;
+    const uint64_t qd[4] = {64, Tq, 3, H}, qs[3] = {H * DQK * 2, 128, DQK * 2};
+    const uint32_t qb[4] = {64, BQ, 3, 1};
+    if (!map4(&p.tm_q, a.q, qd, qs, qb)) return cudaErrorInvalidValue;
+    if (Tk > 0) {      // without keys no tile is loaded
+        const uint64_t kd[4] = {64, Tk, 4, H}, ks[3] = {H * (NOPE + DV) * 2, 128, (NOPE + DV) * 2};
+        const uint32_t kb[4] = {64, BK, 1, 1}, vb[4] = {64, 64, 2, 1};
+        const uint64_t rd[4] = {64, Tk, 1, 1}, rs[3] = {ROPE * 2, ROPE * 2, ROPE * 2};
+        if (!map4(&p.tm_k, a.kv, kd, ks, kb) || !map4(&p.tm_v, a.kv, kd, ks, vb) ||
+            !map4(&p.tm_r, a.k_r, rd, rs, kb))
+            return cudaErrorInvalidValue;
+    }
+    p.cu_q = a.cu_q; p.cu_k = a.cu_k; p.o = (__nv_bfloat16 *)a.o; p.lse = a.lse;
+    p.ws = static_cast<int32_t *>(a.ws);
+    p.Tq = a.Tq; p.Tk = a.Tk; p.N = a.N; p.H = a.H; p.causal = a.causal;
+    // a negative scale flips the scores' sign; a zero one makes them (almost) equal
+    const float s2 = a.scale * 1.4426950408889634f;
+    p.negative = s2 < 0.f;
+    p.scale_log2 = fmaxf(fabsf(s2), FLT_MIN);
+    p.force_timeout = fault_force_timeout();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const int cap = (int)(a.Tq / ROWS + a.N);
+    e = cudaLaunchKernelEx(&cfg, plan_kernel, p, cap);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3((unsigned)cap * (unsigned)a.H);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = SM_BYTES;
+    return cudaLaunchKernelEx(&cfg, prefill_kernel, p);
+}
+
+}  // namespace mla
+}  // namespace kda

@@ -318,7 +318,7 @@ uint64_t decode_simt_workspace_bytes(int32_t B, int32_t H) {
 }
 
 cudaError_t launch_prefill_simt(const PrefillArgs &a, cudaStream_t st) {
-    return a.dtype == 0 ? run_prefill<__nv_bfloat16>(a, st) : run_prefill<float>(a, st);
+    return run_prefill<float>(a, st);
 }
 
 cudaError_t launch_decode_simt(const DecodeArgs &a, cudaStream_t st) {

@@ -196,6 +196,18 @@ def test_prefill_offsets_are_clamped_and_leave_the_rest_alone(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_prefill_backward_offsets_stay_in_bounds(dtype):
+    """Offsets that run backwards describe overlapping sequences: more tiles
+    than the tensors hold.  Nothing outside is touched, what is written is finite."""
+    T, N = 700, 40
+    q, kv, kr, _, _ = _prefill_inputs([(T, T)], 1, dtype, seed=9)
+    cu = torch.tensor([0, T] * N, dtype=torch.int32, device=DEV)
+    o, lse = _call_prefill(q, kv, kr, cu, cu, True)
+    done = ~torch.isnan(lse)
+    assert bool(done.any()) and bool(torch.isfinite(o[done]).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_prefill_without_lse_repeats_and_streams(dtype):
     lens = [(300, 300), (70, 500)]
     q, kv, kr, cu_q, cu_k = _prefill_inputs(lens, 4, dtype, seed=8)
