@@ -281,7 +281,10 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                 if (seg > 0) mbar_wait(q_full, (seg - 1) & 1);
             }
         } else if (warp == W_MMA) {
-            // ---- MMA issue: S^T of tile i, then O^T of tile i - 1 ----
+            // ---- MMA issue ----
+            // O^T of tile i - 1 goes before S^T of tile i when its P is ready
+            // and tile i has not landed: waiting for tile i first would keep
+            // tile i - 1's stage, and with it the load of tile i + 1, waiting.
             constexpr uint32_t id_s = idesc(64, N, FMT_BF16, FMT_BF16, 0, 0);
             constexpr uint32_t id_o = idesc(128, N, FMT_BF16, FMT_BF16, 1, 0);
             const uint64_t dq = sdesc_k_sw128(smb + L::Q);
@@ -311,7 +314,21 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                 ok = wait_or_fail(q_full, seg & 1, fail);
                 for (int64_t i = w.lo; ok && i < w.hi; ++i, ++k) {
                     const int st = k & 1;
-                    ok = wait_or_fail(&full[st], (k >> 1) & 1, fail);
+                    bool owed = i > w.lo;                   // O^T of tile k - 1
+                    if (owed) {
+                        bool landed = false, ready = false;
+                        for (int n = 0; n < (1 << 20) && !landed && !ready; ++n) {
+                            landed = mbar_test(&full[st], (k >> 1) & 1);
+                            ready = mbar_test(p_full, (k - 1) & 1);
+                            landed = __any_sync(0xffffffffu, landed);
+                            ready = __any_sync(0xffffffffu, ready);
+                        }
+                        if (!landed) {
+                            out(k - 1, i - 1 == w.lo);
+                            owed = false;
+                        }
+                    }
+                    ok = ok && wait_or_fail(&full[st], (k >> 1) & 1, fail);
                     if (!ok) break;
                     fence_after_sync();
                     const uint64_t dc = sdesc(warp_uniform(smb + st * STAGE), 16, GROUP, LAYOUT_SW128);
@@ -325,7 +342,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                         if (i == w.hi - 1) mma_commit(q_empty);
                     }
                     __syncwarp();
-                    if (i > w.lo) out(k - 1, i - 1 == w.lo);
+                    if (owed) out(k - 1, i - 1 == w.lo);
                 }
                 if (ok) out(k - 1, w.hi - 1 == w.lo);
                 ++seg;

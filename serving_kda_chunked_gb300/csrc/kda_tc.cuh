@@ -196,6 +196,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *mbar, uint32_t parity,
     return false;
 }
 
+// Whether that phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t *mbar, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+                 "selp.b32 %0, 1, 0, p;\n}" : "=r"(done) : "r"(smem_addr(mbar)), "r"(parity) : "memory");
+    return done != 0;
+}
+
 // ---- bulk async copy (global -> shared), completion counted on an mbarrier ----
 __device__ __forceinline__ void bulk_g2s(void *smem_dst, const void *gmem_src, uint32_t bytes,
                                          uint64_t *mbar) {
