@@ -287,18 +287,18 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
             // tile i - 1's stage, and with it the load of tile i + 1, waiting.
             constexpr uint32_t id_s = idesc(64, N, FMT_BF16, FMT_BF16, 0, 0);
             constexpr uint32_t id_o = idesc(128, N, FMT_BF16, FMT_BF16, 1, 0);
-            const uint64_t dq = sdesc_k_sw128(smb + L::Q);
-            const uint64_t dp = sdesc_k_sw128(smb + L::P);
-            uint32_t k = 0;                                 // tiles whose S^T has been issued
-            int seg = 0;
-            bool ok = true;
-            auto out = [&](uint32_t j, bool first) {        // O^T of tile j
-                ok = ok && wait_or_fail(p_full, j & 1, fail);
-                if (first && seg > 0) ok = ok && wait_or_fail(o_empty, (seg - 1) & 1, fail);
-                if (!ok) return;
-                fence_after_sync();
-                const uint64_t dv = sdesc(warp_uniform(smb + (j & 1) * STAGE), 1024, GROUP, LAYOUT_SW128);
-                if (elect_one()) {
+            if (elect_one()) {
+                const uint64_t dq = sdesc_k_sw128(smb + L::Q);
+                const uint64_t dp = sdesc_k_sw128(smb + L::P);
+                uint32_t k = 0;                             // tiles whose S^T has been issued
+                int seg = 0;
+                bool ok = true;
+                auto out = [&](uint32_t j, bool first) {    // O^T of tile j
+                    ok = ok && wait_one(p_full, j & 1, fail);
+                    if (first && seg > 0) ok = ok && wait_one(o_empty, (seg - 1) & 1, fail);
+                    if (!ok) return;
+                    fence_after_sync();
+                    const uint64_t dv = sdesc(smb + (j & 1) * STAGE, 1024, GROUP, LAYOUT_SW128);
 #pragma unroll
                     for (int mb = 0; mb < 4; ++mb)
 #pragma unroll
@@ -307,51 +307,44 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                                     sdesc_add(dp, s * 32), id_o, !(first && s == 0));
                     mma_commit(&empty[j & 1]);
                     mma_commit(o_full);
-                }
-                __syncwarp();
-            };
-            do {
-                ok = wait_or_fail(q_full, seg & 1, fail);
-                for (int64_t i = w.lo; ok && i < w.hi; ++i, ++k) {
-                    const int st = k & 1;
-                    bool owed = i > w.lo;                   // O^T of tile k - 1
-                    if (owed) {
-                        bool landed = false, ready = false;
-                        for (int n = 0; n < (1 << 20) && !landed && !ready; ++n) {
-                            landed = mbar_test(&full[st], (k >> 1) & 1);
-                            ready = mbar_test(p_full, (k - 1) & 1);
-                            landed = __any_sync(0xffffffffu, landed);
-                            ready = __any_sync(0xffffffffu, ready);
+                };
+                do {
+                    ok = wait_one(q_full, seg & 1, fail);
+                    for (int64_t i = w.lo; ok && i < w.hi; ++i, ++k) {
+                        const int st = k & 1;
+                        bool owed = i > w.lo;               // O^T of tile k - 1
+                        if (owed) {
+                            bool landed = false, ready = false;
+                            for (int n = 0; n < (1 << 20) && !landed && !ready; ++n) {
+                                landed = mbar_test(&full[st], (k >> 1) & 1);
+                                ready = mbar_test(p_full, (k - 1) & 1);
+                            }
+                            if (!landed) {
+                                out(k - 1, i - 1 == w.lo);
+                                owed = false;
+                            }
                         }
-                        if (!landed) {
-                            out(k - 1, i - 1 == w.lo);
-                            owed = false;
-                        }
-                    }
-                    ok = ok && wait_or_fail(&full[st], (k >> 1) & 1, fail);
-                    if (!ok) break;
-                    fence_after_sync();
-                    const uint64_t dc = sdesc(warp_uniform(smb + st * STAGE), 16, GROUP, LAYOUT_SW128);
-                    const uint32_t d_s = warp_uniform(tmem + S_COL + st * N);
-                    if (elect_one()) {
+                        ok = ok && wait_one(&full[st], (k >> 1) & 1, fail);
+                        if (!ok) break;
+                        fence_after_sync();
+                        const uint64_t dc = sdesc(smb + st * STAGE, 16, GROUP, LAYOUT_SW128);
 #pragma unroll
                         for (int s = 0; s < ROW / 16; ++s)
-                            mma_f16(d_s, sdesc_add(dc, (s >> 2) * 1024 + (s & 3) * 32),
+                            mma_f16(tmem + S_COL + st * N, sdesc_add(dc, (s >> 2) * 1024 + (s & 3) * 32),
                                     sdesc_add(dq, (s >> 2) * (N * 128) + (s & 3) * 32), id_s, s > 0);
                         mma_commit(&s_full[st]);
                         if (i == w.hi - 1) mma_commit(q_empty);
+                        if (owed) out(k - 1, i - 1 == w.lo);
                     }
-                    __syncwarp();
-                    if (owed) out(k - 1, i - 1 == w.lo);
+                    if (ok) out(k - 1, w.hi - 1 == w.lo);
+                    ++seg;
+                } while (ok && next(w));
+                if (!ok) {       // MMAs in flight end before tensor memory is freed
+                    mma_commit(drain);
+                    mbar_wait(drain, 0);
                 }
-                if (ok) out(k - 1, w.hi - 1 == w.lo);
-                ++seg;
-            } while (ok && next(w));
-            if (!ok) {           // MMAs in flight end before tensor memory is freed
-                if (elect_one()) mma_commit(drain);
-                __syncwarp();
-                mbar_wait(drain, 0);
             }
+            __syncwarp();
         } else {
             // ---- softmax and epilogue ----
             // A warp whose wait failed stays in step with the others (their barriers

@@ -263,66 +263,58 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
                 if (nB > 0) mbar_wait(&q_full[1], 0);
             }
         } else if (warp == W_MMA) {
-            constexpr uint32_t id_s = idesc(128, 128, FMT_BF16, FMT_BF16, 0, 0);
-            constexpr uint32_t id_o = idesc(128, 128, FMT_BF16, FMT_BF16, 0, 1);
-            bool ok = true;
-            // S of tile x, step j; `last` user of the key blocks frees them
-            auto scores = [&](int x, int j, bool first, bool last) {
-                if (j == 0) ok = ok && wait_or_fail(&q_full[x], 0, fail);
-                const uint32_t d = warp_uniform(tmem + S_COL + 128 * x);
-                const uint64_t dq = sdesc_k_sw128(warp_uniform(smb + SM_Q + x * 3 * BLOCK));
+            if (elect_one()) {
+                constexpr uint32_t id_s = idesc(128, 128, FMT_BF16, FMT_BF16, 0, 0);
+                constexpr uint32_t id_o = idesc(128, 128, FMT_BF16, FMT_BF16, 0, 1);
+                bool ok = true;
+                // S of tile x, step j; the `last` user of the key blocks frees them
+                auto scores = [&](int x, int j, bool first, bool last) {
+                    if (j == 0) ok = ok && wait_one(&q_full[x], 0, fail);
+                    const uint64_t dq = sdesc_k_sw128(smb + SM_Q + x * 3 * BLOCK);
 #pragma unroll
-                for (int b = 0; b < 3; ++b) {
-                    const int q = PER * j + b, slot = q % RING;
-                    if (first) ok = ok && wait_or_fail(&full[slot], (q / RING) & 1, fail);
-                    if (!ok) return;
-                    const uint64_t dk = sdesc_k_sw128(warp_uniform(smb + SM_RING + slot * BLOCK));
-                    if (elect_one()) {
+                    for (int b = 0; b < 3; ++b) {
+                        const int q = PER * j + b, slot = q % RING;
+                        if (first) ok = ok && wait_one(&full[slot], (q / RING) & 1, fail);
+                        if (!ok) return;
+                        const uint64_t dk = sdesc_k_sw128(smb + SM_RING + slot * BLOCK);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma_f16(d, sdesc_add(dq, b * BLOCK + k * 32), sdesc_add(dk, k * 32), id_s,
-                                    b > 0 || k > 0);
+                            mma_f16(tmem + S_COL + 128 * x, sdesc_add(dq, b * BLOCK + k * 32),
+                                    sdesc_add(dk, k * 32), id_s, b > 0 || k > 0);
                         if (last) mma_commit(&empty[slot]);
                         if (b == 2) mma_commit(&s_full[x]);
                     }
-                    __syncwarp();
-                }
-            };
-            auto outputs = [&](int x, int j, bool first, bool last, bool end) {
-                ok = ok && wait_or_fail(&p_full[x], j & 1, fail);
-                if (!ok) return;
-                fence_after_sync();
-                const uint32_t d = warp_uniform(tmem + O_COL + 128 * x);
-                const uint32_t a = warp_uniform(tmem + S_COL + 128 * x);
+                };
+                auto outputs = [&](int x, int j, bool first, bool last, bool end) {
+                    ok = ok && wait_one(&p_full[x], j & 1, fail);
+                    fence_after_sync();
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const int q = PER * j + 3 + b, slot = q % RING;
-                    if (first) ok = ok && wait_or_fail(&full[slot], (q / RING) & 1, fail);
-                    if (!ok) return;
-                    // values [2 chunks of 64 channels][64 tokens][128 bytes]: MN-major B
-                    const uint64_t dv = sdesc(warp_uniform(smb + SM_RING + slot * BLOCK), 8192, 1024, LAYOUT_SW128);
-                    if (elect_one()) {
+                    for (int b = 0; b < 2; ++b) {
+                        const int q = PER * j + 3 + b, slot = q % RING;
+                        if (first) ok = ok && wait_one(&full[slot], (q / RING) & 1, fail);
+                        if (!ok) return;
+                        // values [2 chunks of 64 channels][64 tokens][128 bytes]: MN-major B
+                        const uint64_t dv = sdesc(smb + SM_RING + slot * BLOCK, 8192, 1024, LAYOUT_SW128);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma_f16_tmem_a(d, a + (b * 4 + k) * 8, sdesc_add(dv, k * 2048), id_o,
-                                           j > 0 || b > 0 || k > 0);
+                            mma_f16_tmem_a(tmem + O_COL + 128 * x, tmem + S_COL + 128 * x + (b * 4 + k) * 8,
+                                           sdesc_add(dv, k * 2048), id_o, j > 0 || b > 0 || k > 0);
                         if (last) mma_commit(&empty[slot]);
                         if (b == 1 && end) mma_commit(&o_full[x]);
                     }
-                    __syncwarp();
+                };
+                for (int j = 0; ok && j <= n; ++j) {
+                    if (j < nA) scores(0, j, true, j >= nB);
+                    if (j > 0 && j - 1 < nB) outputs(1, j - 1, j - 1 >= nA, true, j == nB);
+                    if (j < nB) scores(1, j, j >= nA, true);
+                    if (j < nA) outputs(0, j, true, j >= nB, j == nA - 1);
                 }
-            };
-            for (int j = 0; ok && j <= n; ++j) {
-                if (j < nA) scores(0, j, true, j >= nB);
-                if (j > 0 && j - 1 < nB) outputs(1, j - 1, j - 1 >= nA, true, j == nB);
-                if (j < nB) scores(1, j, j >= nA, true);
-                if (j < nA) outputs(0, j, true, j >= nB, j == nA - 1);
+                if (!ok) {     // MMAs in flight end before tensor memory is freed
+                    mma_commit(drain);
+                    mbar_wait(drain, 0);
+                }
             }
-            if (!ok) {         // MMAs in flight end before tensor memory is freed
-                if (elect_one()) mma_commit(drain);
-                __syncwarp();
-                mbar_wait(drain, 0);
-            }
+            __syncwarp();
         } else {
             const int x = warp >> 2, row = tid & 127;       // tile, row in it
             const int i = i0 + x * BQ + row;                // query of the sequence

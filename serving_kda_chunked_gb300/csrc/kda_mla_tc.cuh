@@ -58,6 +58,20 @@ __device__ __forceinline__ bool wait_or_fail(uint64_t *mbar, uint32_t parity, vo
     if (!ok) *fail = FAIL_TIMEOUT;
     return ok;
 }
+// The same for one thread.  The thread that issues MMAs waits by itself: at
+// most two or three MMAs are queued ahead of it, so what it does between two
+// groups of them has to fit into about 150 cycles, and a vote of the warp, an
+// election and a reconvergence around each wait do not (the prefill's step of
+// 40 MMAs took 4600 cycles with them, 2570 of those in the MMAs).
+__device__ __forceinline__ bool wait_one(uint64_t *mbar, uint32_t parity, volatile int *fail) {
+    if (mbar_wait(mbar, parity, 1u << 16)) return true;
+    for (int i = 1; i < 64; ++i) {
+        if (*fail) return false;
+        if (mbar_wait(mbar, parity, 1u << 16)) return true;
+    }
+    *fail = FAIL_TIMEOUT;
+    return false;
+}
 // Barrier of `nthreads` threads that tells all of them whether any passed true.
 __device__ __forceinline__ bool bar_or(uint32_t id, uint32_t nthreads, bool x) {
     uint32_t y;
