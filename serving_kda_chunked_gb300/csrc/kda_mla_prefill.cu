@@ -20,7 +20,7 @@
 // value tile two blocks of 64 tokens.
 //
 // Warps 0-3: softmax of tile A, warps 4-7: of tile B, one thread a row;
-// warp 8: MMA issue; warp 9: loads.  MMAs of a tile run in issue order:
+// warp 8: MMA issue; warp 9: loads.  MMAs run in issue order:
 //   S_A(j)  O_B(j-1)  S_B(j)  O_A(j)  S_A(j+1)  ...
 // so the scores of step j are complete only after the tile's output product of
 // step j - 1, and then its output may be rescaled and its P overwritten.
@@ -188,14 +188,16 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + SM_MISC);    // [8] ring block loaded
     uint64_t *empty = full + RING;                          // [8] ring block read
     uint64_t *q_full = full + 16;                           // [2] query tiles
-    uint64_t *s_full = full + 18, *p_full = full + 20, *o_full = full + 22, *drain = full + 24;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(full + 25);
+    uint64_t *s_full = full + 18;                           // [2] scores
+    uint64_t *p_full = full + 20;                           // [2][2] halves of P
+    uint64_t *o_full = full + 24, *drain = full + 25;       // all outputs
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(full + 26);
     volatile int *fail = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     if (tid == 0) {
-        for (int i = 0; i < 25; ++i) mbar_init(&full[i], i == 20 || i == 21 ? 4 : 1);
+        for (int i = 0; i < 26; ++i) mbar_init(&full[i], i >= 20 && i < 24 ? 4 : 1);
         mbar_fence_init();
         *fail = 0;
     }
@@ -267,48 +269,72 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
                 constexpr uint32_t id_s = idesc(128, 128, FMT_BF16, FMT_BF16, 0, 0);
                 constexpr uint32_t id_o = idesc(128, 128, FMT_BF16, FMT_BF16, 0, 1);
                 bool ok = true;
-                // S of tile x, step j; the `last` user of the key blocks frees them
-                auto scores = [&](int x, int j, bool first, bool last) {
-                    if (j == 0) ok = ok && wait_one(&q_full[x], 0, fail);
-                    const uint64_t dq = sdesc_k_sw128(smb + SM_Q + x * 3 * BLOCK);
-#pragma unroll
-                    for (int b = 0; b < 3; ++b) {
-                        const int q = PER * j + b, slot = q % RING;
-                        if (first) ok = ok && wait_one(&full[slot], (q / RING) & 1, fail);
-                        if (!ok) return;
-                        const uint64_t dk = sdesc_k_sw128(smb + SM_RING + slot * BLOCK);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_f16(tmem + S_COL + 128 * x, sdesc_add(dq, b * BLOCK + k * 32),
-                                    sdesc_add(dk, k * 32), id_s, b > 0 || k > 0);
-                        if (last) mma_commit(&empty[slot]);
-                        if (b == 2) mma_commit(&s_full[x]);
-                    }
+                auto landed = [&](uint32_t q) {             // ring block q
+                    ok = ok && wait_one(&full[q % RING], (q / RING) & 1, fail);
                 };
-                auto outputs = [&](int x, int j, bool first, bool last, bool end) {
-                    ok = ok && wait_one(&p_full[x], j & 1, fail);
+                auto key_block = [&](uint32_t x, uint32_t q, uint32_t b, bool last) {
+                    const uint64_t dq = sdesc_k_sw128(smb + SM_Q + x * 3 * BLOCK + b * BLOCK);
+                    const uint64_t dk = sdesc_k_sw128(smb + SM_RING + q % RING * BLOCK);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_f16(tmem + S_COL + 128 * x, sdesc_add(dq, k * 32), sdesc_add(dk, k * 32), id_s,
+                                b > 0 || k > 0);
+                    if (last) mma_commit(&empty[q % RING]);
+                };
+                // values [2 chunks of 64 channels][64 tokens][128 bytes]: MN-major B
+                auto value_block = [&](uint32_t x, uint32_t q, uint32_t b, bool begin, bool last) {
+                    const uint64_t dv = sdesc(smb + SM_RING + q % RING * BLOCK, 8192, 1024, LAYOUT_SW128);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_f16_tmem_a(tmem + O_COL + 128 * x, tmem + S_COL + 128 * x + (b * 4 + k) * 8,
+                                       sdesc_add(dv, k * 2048), id_o, !begin || b > 0 || k > 0);
+                    if (last) mma_commit(&empty[q % RING]);
+                };
+                // S of tile x, step j.  A tile's query and key blocks are waited
+                // for one ahead, behind the MMAs before them.
+                auto scores = [&](uint32_t x, uint32_t j, bool first, bool last) {
+                    const uint32_t q = PER * j;
+                    if (first) landed(q);
+                    if (!ok) return;
+                    key_block(x, q, 0, last);
+                    if (first) landed(q + 1);
+                    if (!ok) return;
+                    key_block(x, q + 1, 1, last);
+                    if (first) landed(q + 2);
+                    if (!ok) return;
+                    key_block(x, q + 2, 2, last);
+                    mma_commit(&s_full[x]);
+                };
+                // O of tile x, step j, as the halves of P arrive
+                auto outputs = [&](uint32_t x, uint32_t j, bool first, bool last) {
+                    const uint32_t q = PER * j + 3;
+                    if (first) landed(q);
+                    ok = ok && wait_one(&p_full[2 * x], j & 1, fail);
+                    if (!ok) return;
                     fence_after_sync();
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const int q = PER * j + 3 + b, slot = q % RING;
-                        if (first) ok = ok && wait_one(&full[slot], (q / RING) & 1, fail);
-                        if (!ok) return;
-                        // values [2 chunks of 64 channels][64 tokens][128 bytes]: MN-major B
-                        const uint64_t dv = sdesc(smb + SM_RING + slot * BLOCK, 8192, 1024, LAYOUT_SW128);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_f16_tmem_a(tmem + O_COL + 128 * x, tmem + S_COL + 128 * x + (b * 4 + k) * 8,
-                                           sdesc_add(dv, k * 2048), id_o, j > 0 || b > 0 || k > 0);
-                        if (last) mma_commit(&empty[slot]);
-                        if (b == 1 && end) mma_commit(&o_full[x]);
-                    }
+                    value_block(x, q, 0, j == 0, last);
+                    if (first) landed(q + 1);
+                    ok = ok && wait_one(&p_full[2 * x + 1], j & 1, fail);
+                    if (!ok) return;
+                    fence_after_sync();
+                    value_block(x, q + 1, 1, j == 0, last);
                 };
-                for (int j = 0; ok && j <= n; ++j) {
-                    if (j < nA) scores(0, j, true, j >= nB);
-                    if (j > 0 && j - 1 < nB) outputs(1, j - 1, j - 1 >= nA, true, j == nB);
-                    if (j < nB) scores(1, j, j >= nA, true);
-                    if (j < nA) outputs(0, j, true, j >= nB, j == nA - 1);
+                const uint32_t both = min(nA, nB);
+                if (nA > 0) ok = wait_one(&q_full[0], 0, fail);
+                if (nB > 0) ok = ok && wait_one(&q_full[1], 0, fail);
+                for (uint32_t j = 0; ok && j < both; ++j) { // S_A(j) O_B(j-1) S_B(j) O_A(j)
+                    scores(0, j, true, false);
+                    if (j > 0) outputs(1, j - 1, false, true);
+                    scores(1, j, false, true);
+                    outputs(0, j, true, false);
                 }
+                if (ok && both > 0) outputs(1, both - 1, false, true);
+                for (uint32_t j = both; ok && j < n; ++j) { // steps that only one tile has
+                    const uint32_t x = nB > nA;
+                    scores(x, j, true, true);
+                    if (ok) outputs(x, j, true, true);
+                }
+                mma_commit(o_full);
                 if (!ok) {     // MMAs in flight end before tensor memory is freed
                     mma_commit(drain);
                     mbar_wait(drain, 0);
@@ -411,14 +437,16 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
                         w[k / 2 + 1] = pack_bf(y1.x, y1.y);
                     }
                     tmem_st16(t_s + c / 2, w);
+                    if (c & 32) {                           // a half: its product may begin
+                        tmem_wait_st();
+                        fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&p_full[2 * x + (c >> 6)]);
+                    }
                 }
                 l2 = add2(l2, add2(a0, a1));
-                tmem_wait_st();
-                fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[x]);
             }
-            if (ok && nX > 0) ok = wait_or_fail(&o_full[x], 0, fail);
+            if (ok && nX > 0) ok = wait_or_fail(o_full, 0, fail);
             if (ok && i0 + x * BQ < s.nq) {
                 const float l = l2.x + l2.y;
                 const float r = l > 0.f ? 1.f / l : 0.f;

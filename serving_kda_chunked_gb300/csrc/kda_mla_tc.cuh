@@ -58,16 +58,18 @@ __device__ __forceinline__ bool wait_or_fail(uint64_t *mbar, uint32_t parity, vo
     if (!ok) *fail = FAIL_TIMEOUT;
     return ok;
 }
-// The same for one thread.  The thread that issues MMAs waits by itself: at
-// most two or three MMAs are queued ahead of it, so what it does between two
-// groups of them has to fit into about 150 cycles, and a vote of the warp, an
-// election and a reconvergence around each wait do not (the prefill's step of
-// 40 MMAs took 4600 cycles with them, 2570 of those in the MMAs).
+// The same for one thread.  The thread that issues MMAs waits by itself, and
+// tests before it waits: two or three MMAs at most are queued ahead of it, so
+// what it does between two groups of them has to fit into about 150 cycles; a
+// vote of the warp, an election and a reconvergence around each wait, or a
+// try_wait where the phase has long completed, take more than that (a step of
+// the prefill, 2570 cycles of MMAs: 4600 cycles with the first, 4340 with the
+// second).
 __device__ __forceinline__ bool wait_one(uint64_t *mbar, uint32_t parity, volatile int *fail) {
-    if (mbar_wait(mbar, parity, 1u << 16)) return true;
-    for (int i = 1; i < 64; ++i) {
-        if (*fail) return false;
+    if (mbar_test(mbar, parity)) return true;
+    for (int i = 0; i < 64; ++i) {
         if (mbar_wait(mbar, parity, 1u << 16)) return true;
+        if (*fail) return false;
     }
     *fail = FAIL_TIMEOUT;
     return false;
