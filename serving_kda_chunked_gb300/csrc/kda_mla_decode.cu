@@ -294,9 +294,8 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                 int seg = 0;
                 bool ok = true;
                 auto out = [&](uint32_t j, bool first) {    // O^T of tile j
-                    ok = ok && wait_one(p_full, j & 1, fail);
-                    if (first && seg > 0) ok = ok && wait_one(o_empty, (seg - 1) & 1, fail);
-                    if (!ok) return;
+                    ok &= wait_one(p_full, j & 1);
+                    if (first && seg > 0) ok &= wait_one(o_empty, (seg - 1) & 1);
                     fence_after_sync();
                     const uint64_t dv = sdesc(smb + (j & 1) * STAGE, 1024, GROUP, LAYOUT_SW128);
 #pragma unroll
@@ -309,7 +308,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                     mma_commit(o_full);
                 };
                 do {
-                    ok = wait_one(q_full, seg & 1, fail);
+                    ok &= wait_one(q_full, seg & 1);
                     for (int64_t i = w.lo; ok && i < w.hi; ++i, ++k) {
                         const int st = k & 1;
                         bool owed = i > w.lo;               // O^T of tile k - 1
@@ -324,8 +323,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                                 owed = false;
                             }
                         }
-                        ok = ok && wait_one(&full[st], (k >> 1) & 1, fail);
-                        if (!ok) break;
+                        ok &= wait_one(&full[st], (k >> 1) & 1);
                         fence_after_sync();
                         const uint64_t dc = sdesc(smb + st * STAGE, 16, GROUP, LAYOUT_SW128);
 #pragma unroll
@@ -336,10 +334,11 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                         if (i == w.hi - 1) mma_commit(q_empty);
                         if (owed) out(k - 1, i - 1 == w.lo);
                     }
-                    if (ok) out(k - 1, w.hi - 1 == w.lo);
+                    out(k - 1, w.hi - 1 == w.lo);
                     ++seg;
                 } while (ok && next(w));
                 if (!ok) {       // MMAs in flight end before tensor memory is freed
+                    *fail = FAIL_TIMEOUT;
                     mma_commit(drain);
                     mbar_wait(drain, 0);
                 }

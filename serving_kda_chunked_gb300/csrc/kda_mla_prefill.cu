@@ -19,8 +19,9 @@
 // own, one of the shared position key, which is never copied out per head), a
 // value tile two blocks of 64 tokens.
 //
-// Warps 0-3: softmax of tile A, warps 4-7: of tile B, one thread a row;
-// warp 8: MMA issue; warp 9: loads.  MMAs run in issue order:
+// Warps 0-7: softmax of tile A, warps 8-15: of tile B, two threads a row (with
+// one, a tile's softmax took longer than the other tile's products);
+// warp 16: MMA issue; warp 17: loads.  MMAs run in issue order:
 //   S_A(j)  O_B(j-1)  S_B(j)  O_A(j)  S_A(j+1)  ...
 // so the scores of step j are complete only after the tile's output product of
 // step j - 1, and then its output may be rescaled and its P overwritten.
@@ -35,10 +36,11 @@ namespace mla {
 namespace {
 
 constexpr int BQ = 128, BK = 128, ROWS = 2 * BQ;            // rows a tile, keys a tile, rows a CTA
-constexpr int THREADS = 320, W_MMA = 8, W_LOAD = 9;
+constexpr int THREADS = 576, W_MMA = 16, W_LOAD = 17;
 constexpr uint32_t BLOCK = 16384;
 constexpr int RING = 8, PER = 5;                            // blocks in the ring, blocks a key tile
-constexpr uint32_t SM_Q = 0, SM_RING = 6 * BLOCK, SM_MISC = SM_RING + RING * BLOCK, SM_BYTES = SM_MISC + 256;
+constexpr uint32_t SM_Q = 0, SM_RING = 6 * BLOCK, SM_MISC = SM_RING + RING * BLOCK,
+                   SM_SWAP = SM_MISC + 256, SM_BYTES = SM_SWAP + 4 * 128 * 4;
 static_assert(SM_BYTES <= 232448, "shared memory");
 constexpr uint32_t S_COL = 0, O_COL = 256;                  // + 128 for tile B
 constexpr float RESCALE = 8.f;
@@ -194,6 +196,8 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(full + 26);
     volatile int *fail = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
+    float *swap = reinterpret_cast<float *>(sm + SM_SWAP);  // [2 tiles][2 halves][128 rows]
+
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     if (tid == 0) {
@@ -269,59 +273,43 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
                 constexpr uint32_t id_s = idesc(128, 128, FMT_BF16, FMT_BF16, 0, 0);
                 constexpr uint32_t id_o = idesc(128, 128, FMT_BF16, FMT_BF16, 0, 1);
                 bool ok = true;
-                auto landed = [&](uint32_t q) {             // ring block q
-                    ok = ok && wait_one(&full[q % RING], (q / RING) & 1, fail);
-                };
-                auto key_block = [&](uint32_t x, uint32_t q, uint32_t b, bool last) {
-                    const uint64_t dq = sdesc_k_sw128(smb + SM_Q + x * 3 * BLOCK + b * BLOCK);
-                    const uint64_t dk = sdesc_k_sw128(smb + SM_RING + q % RING * BLOCK);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_f16(tmem + S_COL + 128 * x, sdesc_add(dq, k * 32), sdesc_add(dk, k * 32), id_s,
-                                b > 0 || k > 0);
-                    if (last) mma_commit(&empty[q % RING]);
-                };
-                // values [2 chunks of 64 channels][64 tokens][128 bytes]: MN-major B
-                auto value_block = [&](uint32_t x, uint32_t q, uint32_t b, bool begin, bool last) {
-                    const uint64_t dv = sdesc(smb + SM_RING + q % RING * BLOCK, 8192, 1024, LAYOUT_SW128);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_f16_tmem_a(tmem + O_COL + 128 * x, tmem + S_COL + 128 * x + (b * 4 + k) * 8,
-                                       sdesc_add(dv, k * 2048), id_o, !begin || b > 0 || k > 0);
-                    if (last) mma_commit(&empty[q % RING]);
-                };
-                // S of tile x, step j.  A tile's query and key blocks are waited
-                // for one ahead, behind the MMAs before them.
+                auto landed = [&](uint32_t q) { ok &= wait_one(&full[q % RING], (q / RING) & 1); };  // ring block q
+                // S of tile x, step j
                 auto scores = [&](uint32_t x, uint32_t j, bool first, bool last) {
-                    const uint32_t q = PER * j;
-                    if (first) landed(q);
-                    if (!ok) return;
-                    key_block(x, q, 0, last);
-                    if (first) landed(q + 1);
-                    if (!ok) return;
-                    key_block(x, q + 1, 1, last);
-                    if (first) landed(q + 2);
-                    if (!ok) return;
-                    key_block(x, q + 2, 2, last);
+                    const uint64_t dq = sdesc_k_sw128(smb + SM_Q + x * 3 * BLOCK);
+#pragma unroll
+                    for (uint32_t b = 0; b < 3; ++b) {
+                        const uint32_t q = PER * j + b;
+                        if (first) landed(q);
+                        const uint64_t dk = sdesc_k_sw128(smb + SM_RING + q % RING * BLOCK);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_f16(tmem + S_COL + 128 * x, sdesc_add(dq, b * BLOCK + k * 32),
+                                    sdesc_add(dk, k * 32), id_s, b > 0 || k > 0);
+                        if (last) mma_commit(&empty[q % RING]);
+                    }
                     mma_commit(&s_full[x]);
                 };
                 // O of tile x, step j, as the halves of P arrive
                 auto outputs = [&](uint32_t x, uint32_t j, bool first, bool last) {
-                    const uint32_t q = PER * j + 3;
-                    if (first) landed(q);
-                    ok = ok && wait_one(&p_full[2 * x], j & 1, fail);
-                    if (!ok) return;
-                    fence_after_sync();
-                    value_block(x, q, 0, j == 0, last);
-                    if (first) landed(q + 1);
-                    ok = ok && wait_one(&p_full[2 * x + 1], j & 1, fail);
-                    if (!ok) return;
-                    fence_after_sync();
-                    value_block(x, q + 1, 1, j == 0, last);
+#pragma unroll
+                    for (uint32_t b = 0; b < 2; ++b) {
+                        const uint32_t q = PER * j + 3 + b;
+                        if (first) landed(q);
+                        ok &= wait_one(&p_full[2 * x + b], j & 1);
+                        fence_after_sync();
+                        // values [2 chunks of 64 channels][64 tokens][128 bytes]: MN-major B
+                        const uint64_t dv = sdesc(smb + SM_RING + q % RING * BLOCK, 8192, 1024, LAYOUT_SW128);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_f16_tmem_a(tmem + O_COL + 128 * x, tmem + S_COL + 128 * x + (b * 4 + k) * 8,
+                                           sdesc_add(dv, k * 2048), id_o, j > 0 || b > 0 || k > 0);
+                        if (last) mma_commit(&empty[q % RING]);
+                    }
                 };
                 const uint32_t both = min(nA, nB);
-                if (nA > 0) ok = wait_one(&q_full[0], 0, fail);
-                if (nB > 0) ok = ok && wait_one(&q_full[1], 0, fail);
+                if (nA > 0) ok &= wait_one(&q_full[0], 0);
+                if (nB > 0) ok &= wait_one(&q_full[1], 0);
                 for (uint32_t j = 0; ok && j < both; ++j) { // S_A(j) O_B(j-1) S_B(j) O_A(j)
                     scores(0, j, true, false);
                     if (j > 0) outputs(1, j - 1, false, true);
@@ -330,85 +318,97 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
                 }
                 if (ok && both > 0) outputs(1, both - 1, false, true);
                 for (uint32_t j = both; ok && j < n; ++j) { // steps that only one tile has
-                    const uint32_t x = nB > nA;
-                    scores(x, j, true, true);
-                    if (ok) outputs(x, j, true, true);
+                    if (nB > nA) {
+                        scores(1, j, true, true);
+                        outputs(1, j, true, true);
+                    } else {
+                        scores(0, j, true, true);
+                        outputs(0, j, true, true);
+                    }
                 }
                 mma_commit(o_full);
                 if (!ok) {     // MMAs in flight end before tensor memory is freed
+                    *fail = FAIL_TIMEOUT;
                     mma_commit(drain);
                     mbar_wait(drain, 0);
                 }
             }
             __syncwarp();
         } else {
-            const int x = warp >> 2, row = tid & 127;       // tile, row in it
+            // ---- softmax: two threads a row, each half of a key tile's columns ----
+            const int x = warp >> 3, half = warp >> 2 & 1;  // tile, columns 64 half ..
+            const int row = tid & 127;                      // row of the tile
             const int i = i0 + x * BQ + row;                // query of the sequence
             const int nX = x ? nB : nA;
             const int end = i < s.nq ? keys_seen(s, i, p.causal) : s.nk;
             // keys that every row of this warp sees
             const int warp_end = __reduce_min_sync(0xffffffffu, end);
             const uint32_t t_s = tmem_at(tmem, warp, S_COL + 128 * x);
-            const uint32_t t_o = tmem_at(tmem, warp, O_COL + 128 * x);
+            const uint32_t t_o = tmem_at(tmem, warp, O_COL + 128 * x + 64 * half);
+            const uint32_t pair = 1 + 4 * x + (warp & 3);   // named barrier of the rows' two warps
+            float *mine = swap + (2 * x + half) * 128 + row, *theirs = swap + (2 * x + 1 - half) * 128 + row;
             const float sc = p.scale_log2;
             float m = -CUDART_INF_F;                        // unscaled
             float2 l2 = make_float2(0.f, 0.f);
             bool ok = true;
             for (int j = 0; j < nX; ++j) {
                 ok = wait_or_fail(&s_full[x], j & 1, fail);
-                if (!ok) break;
                 fence_after_sync();
-                float v[128];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, v + 32 * c);
+                float v[64];
+                tmem_ld32(t_s + 64 * half, v);
+                tmem_ld32(t_s + 64 * half + 32, v + 32);
                 tmem_wait_ld();
                 reg_fence(v);
                 if (p.negative) {
 #pragma unroll
-                    for (int c = 0; c < 128; ++c) v[c] = -v[c];
+                    for (int c = 0; c < 64; ++c) v[c] = -v[c];
                 }
                 if ((j + 1) * BK > warp_end) {
-                    const int lim = end - j * BK;
+                    const int lim = end - j * BK - 64 * half;
 #pragma unroll
-                    for (int c = 0; c < 128; ++c) v[c] = c < lim ? v[c] : -CUDART_INF_F;
-                }
-                const int valid = s.nk - j * BK;            // keys of the sequence in this tile
-                if (valid < BK && (x == 0 || j >= nA)) {
-                    // values behind the sequence's end hold anything: zero them
-                    // (whichever tile's product comes first)
-                    const int q = PER * j + 3 + (row >> 6), slot = q % RING;
-                    ok = wait_or_fail(&full[slot], (q / RING) & 1, fail);
-                    if (!ok) break;
-                    if (row >= valid) {
-                        uint8_t *r = sm + SM_RING + slot * BLOCK + (row & 63) * 128;
-#pragma unroll
-                        for (int c = 0; c < 16; ++c)
-                            *reinterpret_cast<uint4 *>(r + (c >> 3) * 8192 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-                    }
-                    fence_async_smem();
+                    for (int c = 0; c < 64; ++c) v[c] = c < lim ? v[c] : -CUDART_INF_F;
                 }
                 float t0 = v[0], t1 = v[1], t2 = v[2], t3 = v[3];
 #pragma unroll
-                for (int c = 4; c < 124; c += 8) {
+                for (int c = 4; c < 60; c += 8) {
                     t0 = max3(t0, v[c], v[c + 1]);
                     t1 = max3(t1, v[c + 2], v[c + 3]);
                     t2 = max3(t2, v[c + 4], v[c + 5]);
                     t3 = max3(t3, v[c + 6], v[c + 7]);
                 }
-                t0 = max3(t0, v[124], v[125]);
-                t1 = max3(t1, v[126], v[127]);
-                const float top = max3(t0, t1, fmaxf(t2, t3));
+                t0 = max3(t0, v[60], v[61]);
+                t1 = max3(t1, v[62], v[63]);
+                const float part = max3(t0, t1, fmaxf(t2, t3));
+                // The other half's maximum.  It is read before the other thread's
+                // next write: that follows the next scores, which follow this P.
+                *mine = part;
+                const bool stop = bar_or(pair, 64, !ok);
+                const float top = fmaxf(part, *theirs);
+                if (stop) { ok = false; break; }
+                const int valid = s.nk - j * BK;            // keys of the sequence in this tile
+                if (valid < BK) {
+                    // values behind the sequence's end hold anything: zero them
+                    // (each tile for its own product)
+                    const int q = PER * j + 3 + (row >> 6), slot = q % RING;
+                    ok = wait_or_fail(&full[slot], (q / RING) & 1, fail);
+                    if (row >= valid) {
+                        uint8_t *r = sm + SM_RING + slot * BLOCK + half * 8192 + (row & 63) * 128;
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(r + c * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async_smem();
+                }
                 // The reference is raised only when a score exceeds it by more
                 // than 2^8 (weights stay below 2^8, which float32 sums and bf16
                 // weights hold as well as ones below 1): the output in tensor
-                // memory is then rarely rescaled.
+                // memory is then rarely rescaled.  Both halves decide alike.
                 if (__any_sync(0xffffffffu, (top - m) * sc > RESCALE || (m == -CUDART_INF_F && top > m))) {
                     const float to = fmaxf(m, top);
                     const float f = to == -CUDART_INF_F ? 1.f : ex2((m - to) * sc);
                     m = to;
                     l2.x *= f; l2.y *= f;
                     if (j > 0) {
-                        for (int c = 0; c < 128; c += 16) {
+                        for (int c = 0; c < 64; c += 16) {
                             float y[16];
                             tmem_ld16(t_o + c, y);
                             tmem_wait_ld();
@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
                 const float2 sc2 = make_float2(sc, sc), off2 = make_float2(off, off);
                 float2 a0 = make_float2(0.f, 0.f), a1 = a0;
 #pragma unroll
-                for (int c = 0; c < 128; c += 32) {
+                for (int c = 0; c < 64; c += 32) {
                     uint32_t w[16];
 #pragma unroll
                     for (int k = 0; k < 32; k += 4) {
@@ -436,24 +436,25 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
                         w[k / 2] = pack_bf(y0.x, y0.y);
                         w[k / 2 + 1] = pack_bf(y1.x, y1.y);
                     }
-                    tmem_st16(t_s + c / 2, w);
-                    if (c & 32) {                           // a half: its product may begin
-                        tmem_wait_st();
-                        fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&p_full[2 * x + (c >> 6)]);
-                    }
+                    tmem_st16(t_s + 32 * half + c / 2, w);
                 }
+                tmem_wait_st();
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[2 * x + half]);
                 l2 = add2(l2, add2(a0, a1));
             }
             if (ok && nX > 0) ok = wait_or_fail(o_full, 0, fail);
+            const float part = l2.x + l2.y;
+            *mine = part;
+            ok = !bar_or(pair, 64, !ok);
             if (ok && i0 + x * BQ < s.nq) {
-                const float l = l2.x + l2.y;
+                const float l = part + *theirs;
                 const float r = l > 0.f ? 1.f / l : 0.f;
                 const int64_t at = (s.q0 + i) * p.H + h;
                 fence_after_sync();
 #pragma unroll
-                for (int c = 0; c < 128; c += 16) {
+                for (int c = 0; c < 64; c += 16) {
                     float y[16];
                     if (nX > 0) {
                         tmem_ld16(t_o + c, y);
@@ -467,12 +468,12 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
                         uint32_t w[8];
 #pragma unroll
                         for (int k = 0; k < 8; ++k) w[k] = pack_bf(y[2 * k] * r, y[2 * k + 1] * r);
-                        uint4 *to = reinterpret_cast<uint4 *>(p.o + at * DV + c);
+                        uint4 *to = reinterpret_cast<uint4 *>(p.o + at * DV + 64 * half + c);
                         to[0] = make_uint4(w[0], w[1], w[2], w[3]);
                         to[1] = make_uint4(w[4], w[5], w[6], w[7]);
                     }
                 }
-                if (p.lse && i < s.nq)
+                if (p.lse && half == 0 && i < s.nq)
                     p.lse[at] = l > 0.f ? (m * sc + log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
             }
         }

@@ -58,21 +58,15 @@ __device__ __forceinline__ bool wait_or_fail(uint64_t *mbar, uint32_t parity, vo
     if (!ok) *fail = FAIL_TIMEOUT;
     return ok;
 }
-// The same for one thread.  The thread that issues MMAs waits by itself, and
-// tests before it waits: two or three MMAs at most are queued ahead of it, so
-// what it does between two groups of them has to fit into about 150 cycles; a
-// vote of the warp, an election and a reconvergence around each wait, or a
-// try_wait where the phase has long completed, take more than that (a step of
-// the prefill, 2570 cycles of MMAs: 4600 cycles with the first, 4340 with the
-// second).
-__device__ __forceinline__ bool wait_one(uint64_t *mbar, uint32_t parity, volatile int *fail) {
-    if (mbar_test(mbar, parity)) return true;
-    for (int i = 0; i < 64; ++i) {
-        if (mbar_wait(mbar, parity, 1u << 16)) return true;
-        if (*fail) return false;
-    }
-    *fail = FAIL_TIMEOUT;
-    return false;
+// The wait of the thread that issues MMAs.  Two or three MMAs at most are
+// queued ahead of it, so what it does between two groups of them has to fit
+// into about 150 cycles.  Hence one thread, a test before the wait, and an
+// answer that is collected rather than branched on: with a vote, an election
+// or an early exit around each of seven waits a step of 2570 cycles of MMAs
+// took 3100 to 4600, in this form 2580.  After a wait that gave up, the MMAs
+// of the step still run, on whatever shared and tensor memory hold.
+__device__ __forceinline__ bool wait_one(uint64_t *mbar, uint32_t parity) {
+    return mbar_test(mbar, parity) || mbar_wait(mbar, parity);
 }
 // Barrier of `nthreads` threads that tells all of them whether any passed true.
 __device__ __forceinline__ bool bar_or(uint32_t id, uint32_t nthreads, bool x) {
