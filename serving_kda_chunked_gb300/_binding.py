@@ -430,21 +430,97 @@ def kda_gdn_decode_step_pooled(q, k, v, g, beta, S_pool, slots, *, o=None, strea
 
 
 MLA_LATENT, MLA_ROPE, MLA_NOPE, MLA_DV = 512, 64, 128, 128
+_MLA_ROW, _MLA_QK = MLA_LATENT + MLA_ROPE, MLA_NOPE + MLA_ROPE
+_MLA_SCALE = _MLA_QK ** -0.5
+_mla = None
 
 
-def _check_rows(name, t, dtype, shape):
-    """A CUDA tensor whose last dimension is contiguous (the others may be
-    strided: views of a projection's output)."""
+def _mla_lib():
+    """The latent-attention entry points, bound once: a decode step launches
+    them every few tens of microseconds, so the checks and the marshalling in
+    front of them are kept short (raw addresses, one comparison per property,
+    no device or stream objects where the current ones are meant)."""
+    global _mla
+    if _mla is None:
+        _mla = load()
+    return _mla
+
+
+def _first(name, t, ndim):
+    """Type, device and number of dimensions of a call's first tensor, which
+    the others have to match."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if not t.is_cuda:
+    if t.dtype not in _DTYPE_CODE:
+        raise ValueError("%s must be bfloat16 or float32" % name)
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("%s must be a CUDA tensor (the KDA kernels run on the GPU only)" % name)
-    if t.dtype != dtype:
+    if t.dim() != ndim:
+        raise ValueError("%s must have %d dimensions, got shape %s" % (name, ndim, tuple(t.shape)))
+    return t.dtype, dev
+
+
+def _need(name, t, dtype, shape, dev, rows=False):
+    """A tensor of this type, shape and device, contiguous (``rows``: along its
+    last dimension, so that views of a projection's output can be passed)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype is not dtype:
         raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if t.numel() and t.stride(-1) != 1:
-        raise ValueError("%s must be contiguous along its last dimension" % name)
+    if not (t.is_contiguous() or (rows and t.stride(-1) == 1)):
+        raise ValueError("%s must be contiguous%s" % (name, " along its last dimension" if rows else ""))
+    if t.get_device() != dev:
+        if not t.is_cuda:
+            raise ValueError("%s must be a CUDA tensor (the KDA kernels run on the GPU only)" % name)
+        raise ValueError("%s is on %s, but the call is on cuda:%d: all tensors of a call must be "
+                         "on one device" % (name, t.device, dev))
+    return t.data_ptr()
+
+
+def _call(fn, dev, stream, *args):
+    """Call on device ``dev`` and ``stream`` (default: its current stream)."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device.index != dev:
+        raise ValueError("stream is on %s, the tensors on cuda:%d" % (stream.device, dev))
+    else:
+        raw = int(stream.cuda_stream)
+    if torch.cuda.current_device() == dev:
+        st = getattr(_mla_lib(), fn)(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            st = getattr(_mla_lib(), fn)(*args, raw)
+    if st != KDA_OK:
+        raise KdaError(fn, st)
+
+
+def _given(name, t, dtype, shape, dev, device):
+    """(tensor, address) of an output or a workspace; allocated when omitted."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        return t, t.data_ptr()
+    return t, _need(name, t, dtype, shape, dev)
+
+
+def _scratch(workspace, need, dev, device):
+    """(tensor, address, bytes) of the workspace; allocated when omitted."""
+    if workspace is not None:
+        n = workspace.numel() if isinstance(workspace, torch.Tensor) else 0
+        return workspace, _need("workspace", workspace, torch.uint8, (n,), dev), n
+    if not need:
+        return None, None, 0
+    return _given("workspace", None, torch.uint8, (need,), dev, device) + (need,)
+
+
+def _cache_shape(cache):
+    if not isinstance(cache, torch.Tensor):
+        raise TypeError("cache must be a torch.Tensor")
+    if cache.dim() != 3 or cache.shape[2] != _MLA_ROW:
+        raise ValueError("cache must have shape [n_pages, page, %d]" % _MLA_ROW)
+    return cache.shape
 
 
 def kda_mla_append(c, k_r, slots, cache, *, positions=None, rope=None, interleaved=False,
@@ -458,64 +534,51 @@ def kda_mla_append(c, k_r, slots, cache, *, positions=None, rope=None, interleav
     them; ``q_r`` [T, H, 64] (strided) is rotated into ``q_out`` (allocated if
     omitted).  Returns q_out (None without q_r).
     """
-    if not isinstance(c, torch.Tensor):
-        raise TypeError("c must be a torch.Tensor")
-    if c.dtype not in _DTYPE_CODE:
-        raise ValueError("c must be bfloat16 or float32")
+    dt, dev = _first("c", c, 2)
     T = c.shape[0]
-    _check_rows("c", c, c.dtype, (T, MLA_LATENT))
-    _check_rows("k_r", k_r, c.dtype, (T, MLA_ROPE))
-    _check_cuda("slots", slots, torch.int32, (T,))
-    _check_cuda("cache", cache, c.dtype)
-    if cache.dim() != 3 or cache.shape[2] != MLA_LATENT + MLA_ROPE:
-        raise ValueError("cache must have shape [n_pages, page, %d]" % (MLA_LATENT + MLA_ROPE))
-    max_pos = 0
+    pc = _need("c", c, dt, (T, MLA_LATENT), dev, True)
+    pk = _need("k_r", k_r, dt, (T, MLA_ROPE), dev, True)
+    ps = _need("slots", slots, torch.int32, (T,), dev)
+    cs = _cache_shape(cache)
+    pcache = _need("cache", cache, dt, cs, dev)
+    pp = pr = pko = pq = pqo = None
+    max_pos = kos = H = qt = qh = ot = oh = 0
     if (rope is None) != (positions is None):
         raise ValueError("positions and rope go together")
     if rope is not None:
-        _check_cuda("positions", positions, torch.int32, (T,))
-        _check_cuda("rope", rope, torch.float32)
-        if rope.dim() != 2 or rope.shape[1] != MLA_ROPE:
-            raise ValueError("rope must have shape [max_pos, %d]" % MLA_ROPE)
+        pp = _need("positions", positions, torch.int32, (T,), dev)
         max_pos = rope.shape[0]
+        pr = _need("rope", rope, torch.float32, (max_pos, MLA_ROPE), dev)
     if k_out is not None:
-        _check_rows("k_out", k_out, c.dtype, (T, MLA_ROPE))
-    H, qs, os_ = 0, (0, 0), (0, 0)
+        pko = _need("k_out", k_out, dt, (T, MLA_ROPE), dev, True)
+        kos = k_out.stride(0)
     if q_r is not None:
-        if not isinstance(q_r, torch.Tensor) or q_r.dim() != 3:
-            raise ValueError("q_r must be a tensor of shape [T, H, %d]" % MLA_ROPE)
-        H = q_r.shape[1]
-        _check_rows("q_r", q_r, c.dtype, (T, H, MLA_ROPE))
+        H = q_r.shape[1] if isinstance(q_r, torch.Tensor) and q_r.dim() == 3 else -1
+        pq = _need("q_r", q_r, dt, (T, H, MLA_ROPE), dev, True)
         if q_out is None:
-            q_out = torch.empty((T, H, MLA_ROPE), dtype=c.dtype, device=c.device)
-        _check_rows("q_out", q_out, c.dtype, (T, H, MLA_ROPE))
-        qs, os_ = q_r.stride()[:2], q_out.stride()[:2]
+            q_out, pqo = _given("q_out", None, dt, (T, H, MLA_ROPE), dev, c.device)
+        else:
+            pqo = _need("q_out", q_out, dt, (T, H, MLA_ROPE), dev, True)
+        qt, qh, _ = q_r.stride()
+        ot, oh, _ = q_out.stride()
     elif q_out is not None:
         raise ValueError("q_out needs q_r")
-    _same_device(c.device, k_r=k_r, slots=slots, cache=cache, positions=positions, rope=rope,
-                 k_out=k_out, q_r=q_r, q_out=q_out)
-    with torch.cuda.device(c.device):
-        st = load().kda_mla_append(
-            _ptr(c), c.stride(0), _ptr(k_r), k_r.stride(0), _ptr(slots), _ptr(positions),
-            _ptr(rope), max_pos, int(bool(interleaved)), T, _ptr(cache), cache.shape[0],
-            cache.shape[1], MLA_LATENT, MLA_ROPE, _DTYPE_CODE[c.dtype], _ptr(k_out),
-            0 if k_out is None else k_out.stride(0), _ptr(q_r), qs[0], qs[1], H, _ptr(q_out),
-            os_[0], os_[1], _stream(stream, c.device))
-    if st != KDA_OK:
-        raise KdaError("kda_mla_append", st)
+    _call("kda_mla_append", dev, stream, pc, c.stride(0), pk, k_r.stride(0), ps, pp, pr, max_pos,
+          1 if interleaved else 0, T, pcache, cs[0], cs[1], MLA_LATENT, MLA_ROPE, _DTYPE_CODE[dt],
+          pko, kos, pq, qt, qh, H, pqo, ot, oh)
     return q_out
 
 
 def kda_mla_prefill_workspace_size(N, Tq, H, dtype) -> int:
     """Workspace bytes ``kda_mla_prefill`` needs (0: none)."""
     code = _DTYPE_CODE[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
-    return int(load().kda_mla_prefill_workspace_size(N, Tq, H, code))
+    return int(_mla_lib().kda_mla_prefill_workspace_size(N, Tq, H, code))
 
 
 def kda_mla_decode_workspace_size(B, H, dtype) -> int:
     """Workspace bytes ``kda_mla_decode`` needs."""
     code = _DTYPE_CODE[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
-    return int(load().kda_mla_decode_workspace_size(B, H, code))
+    return int(_mla_lib().kda_mla_decode_workspace_size(B, H, code))
 
 
 def kda_mla_check(workspace, stream=None) -> int:
@@ -524,17 +587,6 @@ def kda_mla_check(workspace, stream=None) -> int:
     dev = None if workspace is None else workspace.device
     with torch.cuda.device(dev):
         return int(load().kda_mla_check(_ptr(workspace), _stream(stream, dev)))
-
-
-def _scale(scale):
-    return (MLA_NOPE + MLA_ROPE) ** -0.5 if scale is None else float(scale)
-
-
-def _workspace(workspace, need, device):
-    if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    _check_cuda("workspace", workspace, torch.uint8)
-    return workspace
 
 
 def kda_mla_prefill(q, kv, k_r, cu_q, cu_k, *, scale=None, causal=True, o=None, lse=None,
@@ -547,39 +599,23 @@ def kda_mla_prefill(q, kv, k_r, cu_q, cu_k, *, scale=None, causal=True, o=None, 
     queries are the last tokens of their sequence's keys.  Returns
     (o [Tq, H, 128], lse [Tq, H] fp32).
     """
-    _check_cuda("q", q)
-    if q.dtype not in _DTYPE_CODE:
-        raise ValueError("q must be bfloat16 or float32")
-    if q.dim() != 3:
-        raise ValueError("q must have shape [Tq, H, %d]" % (MLA_NOPE + MLA_ROPE))
-    Tq, H = q.shape[:2]
-    _check_cuda("q", q, None, (Tq, H, MLA_NOPE + MLA_ROPE))
-    _check_cuda("kv", kv, q.dtype)
-    Tk = kv.shape[0]
-    _check_cuda("kv", kv, None, (Tk, H, MLA_NOPE + MLA_DV))
-    _check_cuda("k_r", k_r, q.dtype, (Tk, MLA_ROPE))
-    _check_cuda("cu_q", cu_q, torch.int32)
-    N = cu_q.shape[0] - 1
-    _check_cuda("cu_k", cu_k, torch.int32, (N + 1,))
-    if o is None:
-        o = torch.empty((Tq, H, MLA_DV), dtype=q.dtype, device=q.device)
-    else:
-        _check_cuda("o", o, q.dtype, (Tq, H, MLA_DV))
-    if lse is None:
-        lse = torch.empty((Tq, H), dtype=torch.float32, device=q.device)
-    else:
-        _check_cuda("lse", lse, torch.float32, (Tq, H))
-    workspace = _workspace(workspace, kda_mla_prefill_workspace_size(N, Tq, H, q.dtype), q.device)
-    _same_device(q.device, kv=kv, k_r=k_r, cu_q=cu_q, cu_k=cu_k, o=o, lse=lse,
-                 workspace=workspace)
-    with torch.cuda.device(q.device):
-        st = load().kda_mla_prefill(
-            _ptr(q), _ptr(kv), _ptr(k_r), _ptr(cu_q), _ptr(cu_k), N, Tq, Tk, H, MLA_NOPE,
-            MLA_ROPE, MLA_DV, _DTYPE_CODE[q.dtype], _scale(scale), int(bool(causal)), _ptr(o),
-            _ptr(lse), _ptr(workspace), 0 if workspace is None else workspace.numel(),
-            _stream(stream, q.device))
-    if st != KDA_OK:
-        raise KdaError("kda_mla_prefill", st)
+    dt, dev = _first("q", q, 3)
+    Tq, H, _ = q.shape
+    pq = _need("q", q, dt, (Tq, H, _MLA_QK), dev)
+    Tk = kv.shape[0] if isinstance(kv, torch.Tensor) and kv.dim() else -1
+    pkv = _need("kv", kv, dt, (Tk, H, MLA_NOPE + MLA_DV), dev)
+    pk = _need("k_r", k_r, dt, (Tk, MLA_ROPE), dev)
+    N = (cu_q.shape[0] if isinstance(cu_q, torch.Tensor) and cu_q.dim() else 0) - 1
+    pcq = _need("cu_q", cu_q, torch.int32, (N + 1,), dev)
+    pck = _need("cu_k", cu_k, torch.int32, (N + 1,), dev)
+    device = q.device
+    o, po = _given("o", o, dt, (Tq, H, MLA_DV), dev, device)
+    lse, pl = _given("lse", lse, torch.float32, (Tq, H), dev, device)
+    code = _DTYPE_CODE[dt]
+    need = _mla_lib().kda_mla_prefill_workspace_size(N, Tq, H, code)
+    workspace, pw, nw = _scratch(workspace, need, dev, device)
+    _call("kda_mla_prefill", dev, stream, pq, pkv, pk, pcq, pck, N, Tq, Tk, H, MLA_NOPE, MLA_ROPE,
+          MLA_DV, code, _MLA_SCALE if scale is None else scale, 1 if causal else 0, po, pl, pw, nw)
     return o, lse
 
 
@@ -593,37 +629,20 @@ def kda_mla_decode(q, cache, table, seq_lens, *, scale=None, o=None, lse=None, w
     ``scale`` defaults to 192 ** -0.5, that of the expanded heads.  Returns
     (o [B, H, 512], lse [B, H] fp32).
     """
-    _check_cuda("q", q)
-    if q.dtype not in _DTYPE_CODE:
-        raise ValueError("q must be bfloat16 or float32")
-    if q.dim() != 3:
-        raise ValueError("q must have shape [B, H, %d]" % (MLA_LATENT + MLA_ROPE))
-    B, H = q.shape[:2]
-    _check_cuda("q", q, None, (B, H, MLA_LATENT + MLA_ROPE))
-    _check_cuda("cache", cache, q.dtype)
-    if cache.dim() != 3 or cache.shape[2] != MLA_LATENT + MLA_ROPE:
-        raise ValueError("cache must have shape [n_pages, page, %d]" % (MLA_LATENT + MLA_ROPE))
-    _check_cuda("table", table, torch.int32)
-    if table.dim() != 2 or table.shape[0] != B:
-        raise ValueError("table must have shape [%d, max_pages]" % B)
-    _check_cuda("seq_lens", seq_lens, torch.int32, (B,))
-    if o is None:
-        o = torch.empty((B, H, MLA_LATENT), dtype=q.dtype, device=q.device)
-    else:
-        _check_cuda("o", o, q.dtype, (B, H, MLA_LATENT))
-    if lse is None:
-        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
-    else:
-        _check_cuda("lse", lse, torch.float32, (B, H))
-    workspace = _workspace(workspace, kda_mla_decode_workspace_size(B, H, q.dtype), q.device)
-    _same_device(q.device, cache=cache, table=table, seq_lens=seq_lens, o=o, lse=lse,
-                 workspace=workspace)
-    with torch.cuda.device(q.device):
-        st = load().kda_mla_decode(
-            _ptr(q), _ptr(cache), _ptr(table), _ptr(seq_lens), B, H, cache.shape[0],
-            cache.shape[1], table.shape[1], MLA_LATENT, MLA_ROPE, _DTYPE_CODE[q.dtype],
-            _scale(scale), _ptr(o), _ptr(lse), _ptr(workspace),
-            0 if workspace is None else workspace.numel(), _stream(stream, q.device))
-    if st != KDA_OK:
-        raise KdaError("kda_mla_decode", st)
+    dt, dev = _first("q", q, 3)
+    B, H, _ = q.shape
+    pq = _need("q", q, dt, (B, H, _MLA_ROW), dev)
+    cs = _cache_shape(cache)
+    pc = _need("cache", cache, dt, cs, dev)
+    width = table.shape[1] if isinstance(table, torch.Tensor) and table.dim() == 2 else -1
+    pt = _need("table", table, torch.int32, (B, width), dev)
+    pn = _need("seq_lens", seq_lens, torch.int32, (B,), dev)
+    device = q.device
+    o, po = _given("o", o, dt, (B, H, MLA_LATENT), dev, device)
+    lse, pl = _given("lse", lse, torch.float32, (B, H), dev, device)
+    code = _DTYPE_CODE[dt]
+    need = _mla_lib().kda_mla_decode_workspace_size(B, H, code)
+    workspace, pw, nw = _scratch(workspace, need, dev, device)
+    _call("kda_mla_decode", dev, stream, pq, pc, pt, pn, B, H, cs[0], cs[1], width, MLA_LATENT,
+          MLA_ROPE, code, _MLA_SCALE if scale is None else scale, po, pl, pw, nw)
     return o, lse
