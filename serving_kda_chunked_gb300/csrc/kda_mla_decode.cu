@@ -26,7 +26,8 @@
 // the lengths; a sequence cut by a boundary leaves unnormalised partial
 // results that join_kernel adds up in a fixed order.
 //
-// Warps 0-3: softmax and epilogue; warp 4: MMA issue; warp 5: loads.
+// Warps 0-3 and 4-7: softmax and epilogue of half the heads each; warp 8: MMA
+// issue; warp 9: loads.
 #include "kda_mla_tc.cuh"
 
 #include <math_constants.h>
@@ -39,7 +40,7 @@ namespace {
 constexpr int TOK = 64, CHUNKS = ROW / 64;                  // tokens a tile, 128-byte chunks a row
 constexpr uint32_t GROUP = CHUNKS * 1024;                   // 8 tokens
 constexpr uint32_t STAGE = 8 * GROUP;
-constexpr int THREADS = 192, W_MMA = 4, W_LOAD = 5;
+constexpr int THREADS = 320, W_MMA = 8, W_LOAD = 9;
 constexpr int MAX_CTAS = 160;                               // per launch, up to one wave
 constexpr float RESCALE = 8.f;                              // see the softmax below
 constexpr uint32_t WS_STATUS = 256;                         // workspace: header | status | meta | ...
@@ -74,9 +75,13 @@ __device__ __forceinline__ int64_t seq_len(const DecParams &p, int b) {
 __device__ __forceinline__ int64_t tiles_of(int64_t len) { return (len + TOK - 1) / TOK; }
 __device__ __forceinline__ int64_t share_start(int64_t T, int c, int C) { return T * c / C; }
 
-// S^T accumulator (M = 64) of this warp's 16 tokens: register 4 i + 2 r + j is
-// token lane / 4 + 8 r, head 8 i + 2 (lane % 4) + j.
-template <int N> __device__ __forceinline__ void ld_scores(uint32_t a, float (&v)[N / 2]);
+// NW columns of the S^T accumulator (M = 64) of this warp's 16 tokens: register
+// 4 i + 2 r + j is token lane / 4 + 8 r, head 8 i + 2 (lane % 4) + j.
+template <int NW> __device__ __forceinline__ void ld_scores(uint32_t a, float (&v)[NW / 2]);
+template <> __device__ __forceinline__ void ld_scores<8>(uint32_t a, float (&v)[4]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(a) : "memory");
+}
 template <> __device__ __forceinline__ void ld_scores<16>(uint32_t a, float (&v)[8]) {
     asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
@@ -89,21 +94,23 @@ template <> __device__ __forceinline__ void ld_scores<32>(uint32_t a, float (&v)
                    "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]),
                    "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]) : "r"(a) : "memory");
 }
-template <> __device__ __forceinline__ void ld_scores<64>(uint32_t a, float (&v)[32]) {
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+// 32 lanes x 8 consecutive columns.
+__device__ __forceinline__ void ld_cols(uint32_t a, float (&v)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
-                   "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]),
-                   "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]),
-                   "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
-                   "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]),
-                   "=f"(v[30]), "=f"(v[31]) : "r"(a) : "memory");
+                   "=f"(v[6]), "=f"(v[7]) : "r"(a) : "memory");
 }
+__device__ __forceinline__ void st_cols(uint32_t a, const float (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 :: "r"(a), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]),
+                    "f"(v[6]), "f"(v[7]) : "memory");
+}
+__device__ __forceinline__ void ld_cols(uint32_t a, float (&v)[16]) { tmem_ld16(a, v); }
+__device__ __forceinline__ void st_cols(uint32_t a, const float (&v)[16]) { tmem_st16(a, v); }
+
 template <int N>
 __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constant__ DecParams p) {
     using L = Smem<N>;
-    constexpr int V = N / 4;                                // heads a softmax thread looks at
     constexpr uint32_t TCOLS = N == 64 ? 512 : 256;
     constexpr uint32_t S_COL = 0, O_COL = 2 * N;            // S^T twice, O^T in 4 blocks of 128 channels
     extern __shared__ __align__(1024) uint8_t sm[];
@@ -117,7 +124,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(full + 16);
     volatile int *fail = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *s_b = reinterpret_cast<int *>(tmem_slot + 2);
-    int64_t *scan = reinterpret_cast<int64_t *>(full + 20);  // [6] warp sums
+    int64_t *scan = reinterpret_cast<int64_t *>(full + 20);  // [10] warp sums
     float *red = reinterpret_cast<float *>(sm + L::RED);    // [2][4 warps][N]
     float *col_a = reinterpret_cast<float *>(sm + L::COL);  // [N]
     float *col_b = col_a + N;                               // [N]
@@ -129,7 +136,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
     const int h0 = group * N, nh = min(N, p.H - h0);
 
     if (tid == 0) {
-        for (int i = 0; i < 12; ++i) mbar_init(&full[i], i == 6 || i == 10 ? 4 : 1);
+        for (int i = 0; i < 12; ++i) mbar_init(&full[i], i == 6 || i == 10 ? 8 : 1);
         mbar_fence_init();
         *fail = 0;
         *s_b = -1;
@@ -223,10 +230,13 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
         Walk w;
         open(w, b0, t00, g0);
         if (warp == W_LOAD) {
-            // ---- loads: the table is read 32 entries at a time ----
-            const int piece = min(p.page, TOK), per_tile = TOK / piece;    // tokens a box, boxes a tile
+            // ---- loads: the table is read 32 entries at a time; what a tile
+            // needs is ready before its stage is ----
+            const int sh = 31 - __clz(p.page);                             // page = 1 << sh
+            const int psh = sh < 6 ? sh : 6, piece = 1 << psh;             // tokens a box
+            const int per_tile = TOK >> psh, bsh = 5 - (6 - psh);          // boxes a tile; 1 << bsh tiles a table read
             const uint32_t box_bytes = (uint32_t)piece * ROW * 2;
-            const int64_t rows8 = (int64_t)p.n_pages * p.page / 8;         // out of range: zeros arrive
+            const int rows8 = (int)((int64_t)p.n_pages * p.page / 8);      // out of range: zeros arrive
             uint32_t k = 0;                                                // tiles asked for
             int seg = 0;                                                   // queries asked for
             bool ok = true;
@@ -240,38 +250,34 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                 __syncwarp();
                 ++seg;
                 const int32_t *tab = p.table + (int64_t)w.b * p.max_pages;
-                const int batch = 32 / per_tile;                           // tiles per table read
-                int mypage = -1;
+                int at8 = rows8;                                           // this lane's box: first row / 8
                 for (int64_t i = w.lo; i < w.hi; ++i, ++k) {
-                    const int r = (int)((i - w.lo) % batch);
+                    const int r = (int)(i - w.lo) & ((1 << bsh) - 1);
                     if (r == 0) {
-                        const int64_t t = i * TOK + (int64_t)lane * piece;
-                        mypage = t < w.len ? tab[t / p.page] : -1;
-                        if (mypage < 0 || mypage >= p.n_pages) mypage = -1;
+                        const int64_t t = i * TOK + ((int64_t)lane << psh);
+                        const int pg = t < w.len ? tab[t >> sh] : -1;
+                        at8 = pg < 0 || pg >= p.n_pages ? rows8 : ((pg << sh) + ((int)t & (p.page - 1))) >> 3;
                     }
                     const int st = k & 1;
-                    if (k >= 2) ok = wait_or_fail(&empty[st], ((k >> 1) & 1) ^ 1, fail);
-                    if (!ok) break;
                     uint64_t mask = 0;
-                    int pg[4];
+                    int g8[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        pg[j] = __shfl_sync(0xffffffffu, mypage, (r * per_tile + j) & 31);
-                        if (j < per_tile && pg[j] >= 0)
+                        g8[j] = __shfl_sync(0xffffffffu, at8, (r * per_tile + j) & 31);
+                        if (j < per_tile && g8[j] < rows8)
                             mask |= (piece == 64 ? ~0ull : (1ull << piece) - 1) << (j * piece);
                     }
                     const int64_t left = w.len - i * TOK;
                     if (left < TOK) mask &= (1ull << left) - 1;
+                    if (k >= 2) ok = wait_or_fail(&empty[st], ((k >> 1) & 1) ^ 1, fail);
+                    if (!ok) break;
                     if (elect_one()) {
                         vmask[st] = mask;
                         mbar_arrive_expect_tx(&full[st], STAGE);
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            if (j < per_tile) {
-                                const int64_t in_page = (i * TOK + j * piece) % p.page;
-                                const int64_t g8 = pg[j] < 0 ? rows8 : ((int64_t)pg[j] * p.page + in_page) / 8;
-                                tma4(smb + st * STAGE + j * box_bytes, &p.tm_c, 0, 0, 0, (int)g8, &full[st]);
-                            }
+                            if (j < per_tile)
+                                tma4(smb + st * STAGE + j * box_bytes, &p.tm_c, 0, 0, 0, g8[j], &full[st]);
                     }
                     __syncwarp();
                 }
@@ -314,9 +320,9 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                         bool owed = i > w.lo;               // O^T of tile k - 1
                         if (owed) {
                             bool landed = false, ready = false;
-                            for (int n = 0; n < (1 << 20) && !landed && !ready; ++n) {
-                                landed = mbar_test(&full[st], (k >> 1) & 1);
+                            for (int n = 0; n < (1 << 20) && !(landed || ready); ++n) {
                                 ready = mbar_test(p_full, (k - 1) & 1);
+                                landed = mbar_test(&full[st], (k >> 1) & 1);
                             }
                             if (!landed) {
                                 out(k - 1, i - 1 == w.lo);
@@ -345,37 +351,44 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
             }
             __syncwarp();
         } else {
-            // ---- softmax and epilogue ----
+            // ---- softmax and epilogue of half the heads a warpgroup ----
             // A warp whose wait failed stays in step with the others (their barriers
             // count all 128 threads) until the next bar_or tells all of them.
+            constexpr int NW = N / 2, V = NW / 4;           // heads a warpgroup, heads a thread looks at
+            constexpr int EC = NW < 16 ? NW : 16;           // columns moved at a time in the epilogue
+            const int wg = warp >> 2, wt = tid & 127, w4 = warp & 3;
+            const int n0 = wg * NW;                         // its first head of the CTA's
+            const uint32_t bar = 1 + wg;
+            float *red_w = red + wg * 8 * NW;               // [2][4 warps][NW]
+            float *ca = col_a + n0, *cb = col_b + n0;
             uint32_t k = 0;
             bool ok = true, stop = false;
-            const int row = 16 * warp + (lane >> 2);        // this thread's tokens: row, row + 8
+            const int row = 16 * w4 + (lane >> 2);          // this thread's tokens: row, row + 8
             do {
                 float m[V], l[V];                           // heads 8 (v / 2) + 2 (lane % 4) + v % 2
 #pragma unroll
                 for (int v = 0; v < V; ++v) { m[v] = -CUDART_INF_F; l[v] = 0.f; }
                 for (int64_t i = w.lo; i < w.hi; ++i, ++k) {
                     const int st = k & 1;
-                    ok = wait_or_fail(&full[st], (k >> 1) & 1, fail);        // for vmask
-                    ok = ok && wait_or_fail(&s_full[st], (k >> 1) & 1, fail);
+                    ok = wait_or_fail(&s_full[st], (k >> 1) & 1, fail);
+                    ok = ok && test_or_fail(&full[st], (k >> 1) & 1, fail);  // for vmask
                     fence_after_sync();
-                    float x[N / 2];
-                    ld_scores<N>(tmem_at(tmem, warp, S_COL + st * N), x);
+                    float x[NW / 2];
+                    ld_scores<NW>(tmem_at(tmem, warp, S_COL + st * N + n0), x);
                     const uint64_t vm = vmask[st];
                     tmem_wait_ld();
                     reg_fence(x);
                     const bool see0 = vm >> row & 1, see1 = vm >> (row + 8) & 1;
 #pragma unroll
-                    for (int e = 0; e < N / 2; ++e)
+                    for (int e = 0; e < NW / 2; ++e)
                         x[e] = (e & 2 ? see1 : see0) ? x[e] * p.scale_log2 : -CUDART_INF_F;
                     if (vm != ~0ull) {
                         // rows that are not seen hold anything: zero them as values
-                        const int t = tid >> 1;
+                        const int t = tid >> 2;
                         if (!(vm >> t & 1)) {
-                            uint8_t *r = sm + st * STAGE + (t >> 3) * GROUP + (t & 7) * 128 + (tid & 1) * 4096;
+                            uint8_t *r = sm + st * STAGE + (t >> 3) * GROUP + (t & 7) * 128 + (tid & 3) * 2048;
 #pragma unroll
-                            for (int ch = 0; ch < 4; ++ch)
+                            for (int ch = 0; ch < 2; ++ch)
 #pragma unroll
                                 for (int e = 0; e < 8; ++e)
                                     *reinterpret_cast<uint4 *>(r + ch * 1024 + e * 16) = make_uint4(0, 0, 0, 0);
@@ -387,7 +400,6 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
 #pragma unroll
                     for (int v = 0; v < V; ++v) t[v] = fmaxf(x[(v >> 1) * 4 + (v & 1)], x[(v >> 1) * 4 + 2 + (v & 1)]);
                     int keep = 0;
-                    constexpr int LAST = V >= 8 ? V / 8 : 1;
 #pragma unroll
                     for (int bit = 16, half = V / 2; bit >= 4; bit >>= 1, half >>= 1) {
                         if (half >= 1) {
@@ -403,13 +415,9 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                             t[0] = fmaxf(t[0], __shfl_xor_sync(0xffffffffu, t[0], bit));
                         }
                     }
-                    float *rd = red + (k & 1) * 4 * N;
-#pragma unroll
-                    for (int v = 0; v < LAST; ++v) {
-                        const int at = keep + v;
-                        rd[warp * N + (at >> 1) * 8 + 2 * (lane & 3) + (at & 1)] = t[v];
-                    }
-                    stop = bar_or(1, 128, !ok);
+                    float *rd = red_w + (k & 1) * 4 * NW;
+                    rd[w4 * NW + (keep >> 1) * 8 + 2 * (lane & 3) + (keep & 1)] = t[0];
+                    stop = bar_or(bar, 128, !ok);
                     if (stop) break;
                     bool grow = false;
                     float mx[V];
@@ -419,7 +427,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                         float2 y = *reinterpret_cast<const float2 *>(rd + at);
 #pragma unroll
                         for (int q = 1; q < 4; ++q) {
-                            const float2 z = *reinterpret_cast<const float2 *>(rd + q * N + at);
+                            const float2 z = *reinterpret_cast<const float2 *>(rd + q * NW + at);
                             y.x = fmaxf(y.x, z.x); y.y = fmaxf(y.y, z.y);
                         }
                         mx[v] = y.x; mx[v + 1] = y.y;
@@ -428,8 +436,8 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                     // The reference maximum is raised only when a score exceeds it by
                     // more than 2^8: until then weights stay below 2^8, which float32
                     // sums and bf16 weights hold as well as ones below 1, and the
-                    // output in tensor memory need not be rescaled.  All warps see
-                    // the same maxima and decide alike.
+                    // output in tensor memory need not be rescaled.  All warps of the
+                    // warpgroup see the same maxima and decide alike.
                     if (__any_sync(0xffffffffu, grow)) {
                         const bool scale_o = i > w.lo;
 #pragma unroll
@@ -438,21 +446,24 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                             const float f = to == -CUDART_INF_F ? 1.f : ex2(m[v] - to);
                             l[v] *= f;
                             m[v] = to;
-                            if (warp == 0 && lane < 4) col_a[(v >> 1) * 8 + 2 * lane + (v & 1)] = f;
+                            if (w4 == 0 && lane < 4) ca[(v >> 1) * 8 + 2 * lane + (v & 1)] = f;
                         }
                         if (scale_o) {
                             ok = wait_or_fail(o_full, (k - 1) & 1, fail);
-                            bar_sync(1, 128);               // col_a
+                            bar_sync(bar, 128);             // ca
                             fence_after_sync();
-                            for (int cb = 0; cb < 4 * N; cb += 16) {
-                                float y[16];
-                                tmem_ld16(tmem_at(tmem, warp, O_COL + cb), y);
-                                tmem_wait_ld();
-                                reg_fence(y);
+                            for (int mb = 0; mb < 4; ++mb)
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) y[e] *= col_a[(cb + e) % N];
-                                tmem_st16(tmem_at(tmem, warp, O_COL + cb), y);
-                            }
+                                for (int c = 0; c < NW; c += EC) {
+                                    float y[EC];
+                                    const uint32_t at = tmem_at(tmem, warp, O_COL + mb * N + n0 + c);
+                                    ld_cols(at, y);
+                                    tmem_wait_ld();
+                                    reg_fence(y);
+#pragma unroll
+                                    for (int e = 0; e < EC; ++e) y[e] *= ca[c + e];
+                                    st_cols(at, y);
+                                }
                             tmem_wait_st();
                         }
                     }
@@ -465,16 +476,22 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                         l[v] += a + d;
                     }
                     // P [head][token] bf16, K-major: the previous product must have read it
-                    if (k > 0) ok = ok && wait_or_fail(o_full, (k - 1) & 1, fail);
+                    if (k > 0) ok = ok && test_or_fail(o_full, (k - 1) & 1, fail);
+                    if (NW == 8) {
+                        const uint32_t dst = smb + L::P + sw128_off(n0 + (lane & 7), 2 * w4 + (lane >> 3 & 1));
+                        asm volatile("stmatrix.sync.aligned.m8n8.x2.trans.shared.b16 [%0], {%1, %2};"
+                                     :: "r"(dst), "r"(pack_bf(x[0], x[1])), "r"(pack_bf(x[2], x[3])) : "memory");
+                    } else {
 #pragma unroll
-                    for (int e = 0; e < N / 8; e += 2) {
-                        const uint32_t head = 8 * (e + (lane >> 4)) + (lane & 7);
-                        const uint32_t dst = smb + L::P + sw128_off(head, 2 * warp + (lane >> 3 & 1));
-                        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
-                                     :: "r"(dst), "r"(pack_bf(x[4 * e], x[4 * e + 1])),
-                                        "r"(pack_bf(x[4 * e + 2], x[4 * e + 3])),
-                                        "r"(pack_bf(x[4 * e + 4], x[4 * e + 5])),
-                                        "r"(pack_bf(x[4 * e + 6], x[4 * e + 7])) : "memory");
+                        for (int e = 0; e + 1 < NW / 8; e += 2) {
+                            const uint32_t head = n0 + 8 * (e + (lane >> 4)) + (lane & 7);
+                            const uint32_t dst = smb + L::P + sw128_off(head, 2 * w4 + (lane >> 3 & 1));
+                            asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
+                                         :: "r"(dst), "r"(pack_bf(x[4 * e], x[4 * e + 1])),
+                                            "r"(pack_bf(x[4 * e + 2], x[4 * e + 3])),
+                                            "r"(pack_bf(x[4 * e + 4], x[4 * e + 5])),
+                                            "r"(pack_bf(x[4 * e + 6], x[4 * e + 7])) : "memory");
+                        }
                     }
                     fence_async_smem();
                     fence_before_sync();
@@ -488,59 +505,61 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) l[v] += __shfl_xor_sync(0xffffffffu, l[v], o);
                 }
-                float *rd = red + (k & 1) * 4 * N;
+                float *rd = red_w + (k & 1) * 4 * NW;
                 if (lane < 4) {
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
                         const int at = (v >> 1) * 8 + 2 * lane + (v & 1);
-                        rd[warp * N + at] = l[v];
-                        if (warp == 0) col_b[at] = m[v];
+                        rd[w4 * NW + at] = l[v];
+                        if (w4 == 0) cb[at] = m[v];
                     }
                 }
                 const int64_t all = tiles_of(w.len);
                 const bool whole = w.lo == 0 && w.hi == all;
                 const int64_t slot = 2 * (int64_t)blockIdx.x + (w.lo == 0 ? 1 : 0);
-                bar_sync(1, 128);
-                if (tid < N) {
-                    const float sum = rd[tid] + rd[N + tid] + rd[2 * N + tid] + rd[3 * N + tid];
-                    const float top = col_b[tid];
-                    col_a[tid] = whole ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
+                bar_sync(bar, 128);
+                if (wt < NW) {
+                    const float sum = rd[wt] + rd[NW + wt] + rd[2 * NW + wt] + rd[3 * NW + wt];
+                    const float top = cb[wt];
+                    ca[wt] = whole ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
                     if (whole) {
-                        if (p.lse && tid < nh)
-                            p.lse[(int64_t)w.b * p.H + h0 + tid] =
+                        if (p.lse && n0 + wt < nh)
+                            p.lse[(int64_t)w.b * p.H + h0 + n0 + wt] =
                                 sum > 0.f ? (top + log2f(sum)) * CUDART_LN2_F : -CUDART_INF_F;
                     } else {
-                        float2 *to = reinterpret_cast<float2 *>(p.stat + slot * N * 2) + tid;
+                        float2 *to = reinterpret_cast<float2 *>(p.stat + slot * N * 2) + n0 + wt;
                         *to = make_float2(top, sum);
                     }
                 }
                 ok = ok && wait_or_fail(o_full, (k - 1) & 1, fail);
-                stop = bar_or(1, 128, !ok);
+                stop = bar_or(bar, 128, !ok);
                 if (stop) break;
                 fence_after_sync();
-                for (int cb = 0; cb < 4 * N; cb += 16) {
-                    const int ch = (cb / N) * 128 + tid, n0 = cb % N;      // this thread's channel
-                    if (n0 >= nh) continue;
-                    float y[16];
-                    tmem_ld16(tmem_at(tmem, warp, O_COL + cb), y);
-                    tmem_wait_ld();
-                    reg_fence(y);
-                    if (whole) {
-                        __nv_bfloat16 *to = p.o + ((int64_t)w.b * p.H + h0 + n0) * LATENT + ch;
+                for (int mb = 0; mb < 4; ++mb)
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (n0 + e < nh) to[e * LATENT] = __float2bfloat16_rn(y[e] * col_a[n0 + e]);
-                    } else {
-                        float *to = p.part + (slot * N + n0) * LATENT + ch;
+                    for (int c = 0; c < NW; c += EC) {
+                        const int ch = mb * 128 + wt, n = n0 + c;          // this thread's channel
+                        if (n >= nh) continue;
+                        float y[EC];
+                        ld_cols(tmem_at(tmem, warp, O_COL + mb * N + n), y);
+                        tmem_wait_ld();
+                        reg_fence(y);
+                        if (whole) {
+                            __nv_bfloat16 *to = p.o + ((int64_t)w.b * p.H + h0 + n) * LATENT + ch;
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (n0 + e < nh) to[e * LATENT] = y[e];
+                            for (int e = 0; e < EC; ++e)
+                                if (n + e < nh) to[e * LATENT] = __float2bfloat16_rn(y[e] * ca[c + e]);
+                        } else {
+                            float *to = p.part + (slot * N + n) * LATENT + ch;
+#pragma unroll
+                            for (int e = 0; e < EC; ++e)
+                                if (n + e < nh) to[e * LATENT] = y[e];
+                        }
                     }
-                }
                 fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(o_empty);
-                bar_sync(1, 128);                           // col_a, col_b are free again
+                bar_sync(bar, 128);                         // ca, cb are free again
             } while (next(w));
         }
     }

@@ -58,6 +58,14 @@ __device__ __forceinline__ bool wait_or_fail(uint64_t *mbar, uint32_t parity, vo
     if (!ok) *fail = FAIL_TIMEOUT;
     return ok;
 }
+// The same where the phase has most often completed: test_wait says so in a few
+// tens of cycles, the loop above in about 300 (and where it has not, the test
+// delays the loop: the prefill's softmax, whose scores are never there yet, is
+// 5% slower with it).
+__device__ __forceinline__ bool test_or_fail(uint64_t *mbar, uint32_t parity, volatile int *fail) {
+    const bool ok = mbar_test(mbar, parity);
+    return __all_sync(0xffffffffu, ok) || wait_or_fail(mbar, parity, fail);
+}
 // The wait of the thread that issues MMAs.  Two or three MMAs at most are
 // queued ahead of it, so what it does between two groups of them has to fit
 // into about 150 cycles.  Hence one thread, a test before the wait, and an
