@@ -295,7 +295,7 @@ kda_status kda_mla_append(const void *c, int64_t c_stride, const void *k_r, int6
         return KDA_ERR_INVALID_ARG;
     if (dtype != KDA_BF16 && dtype != KDA_FP32) return KDA_ERR_INVALID_ARG;
     if (latent != kda::mla::LATENT || rope_dim != kda::mla::ROPE || !page_ok(page) ||
-        T > 0x7fffffffLL || (int64_t)n_pages * page > 0x7fffffffLL)
+        T > 0x7fffffffLL || (int64_t)n_pages * page > 0x7fffffffLL || H > 65535)
         return KDA_ERR_UNSUPPORTED;
     if (T == 0) return KDA_OK;
     if (!c || !k_r || !slots || !cache || (q_r == nullptr) != (q_out == nullptr) || (q_r && H == 0))

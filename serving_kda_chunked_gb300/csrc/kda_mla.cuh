@@ -51,6 +51,13 @@ uint64_t decode_tc_workspace_bytes(int32_t H);
 cudaError_t launch_prefill_tc(const PrefillArgs &a, cudaStream_t st);
 uint64_t prefill_tc_workspace_bytes(int32_t N, int64_t Tq);
 
+// SMs of the current device.
+inline cudaError_t sm_count(int *nsm) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    return e != cudaSuccess ? e : cudaDeviceGetAttribute(nsm, cudaDevAttrMultiProcessorCount, dev);
+}
+
 // Queries [bos, eos) of sequence n and its keys, from clamped offsets.
 struct SeqSpan { int64_t q0, k0; int nq, nk; };
 __device__ __forceinline__ SeqSpan seq_span(const int32_t *cu_q, const int32_t *cu_k, int n,

@@ -666,14 +666,6 @@ Plan plan_of(int32_t H, int nsm) {
     return pl;
 }
 
-cudaError_t sm_count(int *nsm) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(nsm, cudaDevAttrMultiProcessorCount, dev);
-    if (*nsm > MAX_CTAS) *nsm = MAX_CTAS;
-    return e;
-}
-
 uint64_t ws_meta(int ctas) { return WS_STATUS + ((uint64_t)ctas * 4 + 255) / 256 * 256; }
 uint64_t ws_stat(int ctas) { return ws_meta(ctas) + ((uint64_t)ctas * sizeof(Meta) + 255) / 256 * 256; }
 uint64_t ws_part(int ctas, int N) { return ws_stat(ctas) + (uint64_t)ctas * 2 * N * 8; }
@@ -745,6 +737,7 @@ cudaError_t launch_decode_tc(const DecodeArgs &a, cudaStream_t st) {
     int nsm = 1;
     const cudaError_t e = sm_count(&nsm);
     if (e != cudaSuccess) return e;
+    if (nsm > MAX_CTAS) nsm = MAX_CTAS;
     const Plan pl = plan_of(a.H, nsm);
     switch (pl.N) {
     case 16: return run<16>(a, pl, st);
