@@ -363,7 +363,7 @@ kda_status kda_mla_prefill(const void *q, const void *kv, const void *k_r, const
 uint64_t kda_mla_decode_workspace_size(int32_t B, int32_t H, int32_t dtype) {
     if (B <= 0 || H <= 0 || (dtype != KDA_BF16 && dtype != KDA_FP32)) return 0;
     return dtype == KDA_BF16 ? kda::mla::decode_tc_workspace_bytes(H)
-                             : kda::mla::decode_simt_workspace_bytes(B, H);
+                             : kda::mla::decode_simt_workspace_bytes(H);
 }
 
 kda_status kda_mla_decode(const void *q, const void *cache, const int32_t *table,

@@ -21,16 +21,13 @@
 // whole page piece, and both the K-major (scores) and the MN-major (output)
 // descriptors see uniform strides.
 //
-// Work split: the tiles of all sequences, laid end to end, are cut into equal
-// contiguous shares, one per CTA, by arithmetic that every CTA repeats from
-// the lengths; a sequence cut by a boundary leaves unnormalised partial
-// results that join_kernel adds up in a fixed order.
+// Work split and join: kda_mla_split.cuh, one share per SM.
 //
 // Warps 0-3 and 4-7: softmax and epilogue of half the heads each; warp 8: MMA
 // issue; warp 9: loads.
+#include "kda_mla_split.cuh"
 #include "kda_mla_tc.cuh"
 
-#include <math_constants.h>
 #include <mutex>
 
 namespace kda {
@@ -43,7 +40,6 @@ constexpr uint32_t STAGE = 8 * GROUP;
 constexpr int THREADS = 320, W_MMA = 8, W_LOAD = 9;
 constexpr int MAX_CTAS = 160;                               // per launch, up to one wave
 constexpr float RESCALE = 8.f;                              // see the softmax below
-constexpr uint32_t WS_STATUS = 256;                         // workspace: header | status | meta | ...
 
 template <int N> struct Smem {
     static constexpr uint32_t Q = 2 * STAGE, P = Q + CHUNKS * N * 128, RED = P + N * 128,
@@ -51,29 +47,10 @@ template <int N> struct Smem {
 };
 static_assert(Smem<64>::BYTES <= 232448, "shared memory");
 
-// What the CTA with share c of C starts in: sequence b, whose tiles are
-// [t0, t1) of all T; b < 0 marks an idle CTA.
-struct Meta { int64_t t0, t1, T; int32_t b, C; };
-
-struct DecParams {
+struct DecParams : SplitParams {
     CUtensorMap tm_c, tm_q;
-    const int32_t *table, *seq_lens;
-    __nv_bfloat16 *o;
-    float *lse;
-    int32_t *status;           // one word per CTA
-    Meta *meta;                // per CTA
-    float *part, *stat;        // two slots per CTA: [N][512], and [N][2] (maximum, sum)
-    int32_t B, H, n_pages, page, max_pages, groups;
-    float scale_log2;
     int32_t force_timeout;
 };
-
-__device__ __forceinline__ int64_t seq_len(const DecParams &p, int b) {
-    const int64_t cap = (int64_t)p.max_pages * p.page, n = p.seq_lens[b];
-    return n < 0 ? 0 : (n > cap ? cap : n);
-}
-__device__ __forceinline__ int64_t tiles_of(int64_t len) { return (len + TOK - 1) / TOK; }
-__device__ __forceinline__ int64_t share_start(int64_t T, int c, int C) { return T * c / C; }
 
 // NW columns of the S^T accumulator (M = 64) of this warp's 16 tokens: register
 // 4 i + 2 r + j is token lane / 4 + 8 r, head 8 i + 2 (lane % 4) + j.
@@ -120,115 +97,41 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
     uint64_t *p_full = full + 6, *o_full = full + 7;        // P written; its O^T product done
     uint64_t *q_full = full + 8, *q_empty = full + 9, *o_empty = full + 10, *drain = full + 11;
     uint64_t *vmask = full + 12;                            // [2] tokens of the stage that are seen
-    int64_t *s_t0 = reinterpret_cast<int64_t *>(full + 14);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(full + 16);
     volatile int *fail = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    int *s_b = reinterpret_cast<int *>(tmem_slot + 2);
-    int64_t *scan = reinterpret_cast<int64_t *>(full + 20);  // [10] warp sums
+    auto *scratch = reinterpret_cast<ShareScratch<THREADS> *>(full + 18);
     float *red = reinterpret_cast<float *>(sm + L::RED);    // [2][4 warps][N]
     float *col_a = reinterpret_cast<float *>(sm + L::COL);  // [N]
     float *col_b = col_a + N;                               // [N]
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-    const int group = blockIdx.x % p.groups, c = blockIdx.x / p.groups;
-    const int C0 = gridDim.x / p.groups;
-    const int h0 = group * N, nh = min(N, p.H - h0);
+    const int h0 = blockIdx.x % p.groups * N, nh = min(N, p.H - h0);
 
     if (tid == 0) {
         for (int i = 0; i < 12; ++i) mbar_init(&full[i], i == 6 || i == 10 ? 8 : 1);
         mbar_fence_init();
         *fail = 0;
-        *s_b = -1;
     }
     if (warp == W_MMA) tmem_alloc<TCOLS>(tmem_slot);
     if (warp == W_LOAD && lane == 0) { prefetch_map(&p.tm_c); prefetch_map(&p.tm_q); }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    // tiles of all sequences, and where this CTA's share starts
-    const int per = (p.B + THREADS - 1) / THREADS;
-    const int b_lo = min(p.B, tid * per), b_hi = min(p.B, b_lo + per);
-    int64_t mine = 0;
-    for (int b = b_lo; b < b_hi; ++b) mine += tiles_of(seq_len(p, b));
-    int64_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-    }
-    if (lane == 31) scan[warp] = incl;
     fence_before_sync();
-    __syncthreads();
+    const Share share = find_share<TOK, THREADS, N, __nv_bfloat16>(p, *scratch);
     fence_after_sync();
-    int64_t T = 0, excl = incl - mine;
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp) excl += scan[w];
-        T += scan[w];
-    }
-    const int C = (int)(T < C0 ? T : C0);
-    const bool busy = c < C;
-    const int64_t g0 = busy ? share_start(T, c, C) : 0, g1 = busy ? share_start(T, c + 1, C) : 0;
-    if (busy && excl <= g0 && g0 < excl + mine) {
-        int64_t at = excl;
-        int b = b_lo;
-        for (;; ++b) {
-            const int64_t n = tiles_of(seq_len(p, b));
-            if (g0 < at + n) {
-                Meta m;
-                m.t0 = at; m.t1 = at + n; m.T = T; m.b = b; m.C = C;
-                p.meta[blockIdx.x] = m;
-                break;
-            }
-            at += n;
-        }
-        *s_t0 = at;
-        *s_b = b;
-    }
-    if (!busy && tid == 0) p.meta[blockIdx.x].b = -1;
-    // sequences with nothing cached
-    for (int b = c; b < p.B; b += C0) {
-        if (seq_len(p, b) > 0) continue;
-        const int64_t at = (int64_t)b * p.H + h0;
-        for (int e = tid; e < nh * (LATENT / 8); e += THREADS)
-            *reinterpret_cast<uint4 *>(p.o + at * LATENT + 8 * e) = make_uint4(0, 0, 0, 0);
-        if (p.lse && tid < nh) p.lse[at + tid] = -CUDART_INF_F;
-    }
-    __syncthreads();
     const uint32_t tmem = warp_uniform(*tmem_slot);
     const uint32_t smb = warp_uniform(smem_addr(sm));
-    const int b0 = *s_b;
-    const int64_t t00 = *s_t0;
-    const bool forced = p.force_timeout && busy;
+    const bool forced = p.force_timeout && share.busy;
     if (forced) {      // test build only: a wait that nothing ends, before any copy or MMA
         if (tid == 0 && !mbar_wait(drain, 0, 64)) *fail = FAIL_TIMEOUT;
         __syncthreads();
     }
 
-    // The share as segments: (sequence, its first tile here, one past its last
-    // tile here).  Every role walks them with the same arithmetic.
-    struct Walk { int b; int64_t at, len, lo, hi; };       // `at`: the sequence's first tile of all
-    auto open = [&](Walk &w, int b, int64_t at, int64_t g) {
-        w.len = seq_len(p, b);
-        w.b = b; w.at = at;
-        w.lo = g - at;
-        const int64_t n = tiles_of(w.len);
-        w.hi = g1 - at < n ? g1 - at : n;
-    };
-    auto next = [&](Walk &w) -> bool {                      // the next sequence with tiles in the share
-        int64_t at = w.at + tiles_of(w.len);
-        if (at >= g1) return false;
-        int b = w.b + 1;
-        while (b < p.B && seq_len(p, b) == 0) ++b;
-        if (b >= p.B) return false;                         // lengths changed under the kernel
-        open(w, b, at, at);
-        return true;
-    };
-
-    if (busy && !forced) {
-        Walk w;
-        open(w, b0, t00, g0);
+    if (share.busy && !forced) {
+        Walk<TOK> w;
+        w.start(p, share);
         if (warp == W_LOAD) {
             // ---- loads: the table is read 32 entries at a time; what a tile
             // needs is ready before its stage is ----
@@ -281,7 +184,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                     }
                     __syncwarp();
                 }
-            } while (ok && next(w));
+            } while (ok && w.next(p, share));
             if (!ok) {           // let what is in flight land before the CTA ends
                 for (uint32_t j = k >= 2 ? k - 2 : 0; j < k; ++j) mbar_wait(&full[j & 1], (j >> 1) & 1);
                 if (seg > 0) mbar_wait(q_full, (seg - 1) & 1);
@@ -342,7 +245,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                     }
                     out(k - 1, w.hi - 1 == w.lo);
                     ++seg;
-                } while (ok && next(w));
+                } while (ok && w.next(p, share));
                 if (!ok) {       // MMAs in flight end before tensor memory is freed
                     *fail = FAIL_TIMEOUT;
                     mma_commit(drain);
@@ -514,9 +417,8 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                         if (w4 == 0) cb[at] = m[v];
                     }
                 }
-                const int64_t all = tiles_of(w.len);
-                const bool whole = w.lo == 0 && w.hi == all;
-                const int64_t slot = 2 * (int64_t)blockIdx.x + (w.lo == 0 ? 1 : 0);
+                const bool whole = w.whole();
+                const int64_t slot = w.slot();
                 bar_sync(bar, 128);
                 if (wt < NW) {
                     const float sum = rd[wt] + rd[NW + wt] + rd[2 * NW + wt] + rd[3 * NW + wt];
@@ -545,7 +447,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                         tmem_wait_ld();
                         reg_fence(y);
                         if (whole) {
-                            __nv_bfloat16 *to = p.o + ((int64_t)w.b * p.H + h0 + n) * LATENT + ch;
+                            __nv_bfloat16 *to = (__nv_bfloat16 *)p.o + ((int64_t)w.b * p.H + h0 + n) * LATENT + ch;
 #pragma unroll
                             for (int e = 0; e < EC; ++e)
                                 if (n + e < nh) to[e * LATENT] = __float2bfloat16_rn(y[e] * ca[c + e]);
@@ -560,7 +462,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                 __syncwarp();
                 if (lane == 0) mbar_arrive(o_empty);
                 bar_sync(bar, 128);                         // ca, cb are free again
-            } while (next(w));
+            } while (w.next(p, share));
         }
     }
     fence_before_sync();
@@ -569,109 +471,11 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
     if (warp == W_MMA) tmem_dealloc<TCOLS>(tmem);
 }
 
-// Adds up the partial results of the sequences that a share boundary cuts.
-// Block (boundary, r) works for the sequence its boundary lies in, together
-// with the blocks of that sequence's other boundaries; an item is 128
-// channels of a head, taken by one to eight warps, the more the more pieces
-// there are.  Pieces are added in order of the shares: a fixed order.
-template <int N>
-__global__ void __launch_bounds__(256) join_kernel(const DecParams p, int ctas, int32_t *header) {
-    __shared__ float4 buf[8][32];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (blockIdx.x == 0 && blockIdx.y == 0) {              // the call's status, from the CTAs'
-        int st = 0;
-        for (int i = tid; i < ctas; i += 256) st |= p.status[i];
-        st = __syncthreads_or(st);
-        if (tid == 0) *header = st ? FAIL_TIMEOUT : 0;
-    }
-    const int cta = blockIdx.x + p.groups;                  // shares 1 .. of every group
-    if (cta >= ctas) return;
-    const int group = cta % p.groups, c = cta / p.groups;
-    const Meta m = p.meta[cta];
-    if (m.b < 0 || share_start(m.T, c, m.C) <= m.t0) return;
-    const int first = (int)(((m.t0 + 1) * m.C + m.T - 1) / m.T);   // boundaries inside the sequence
-    const int last = (int)((m.t1 * m.C + m.T - 1) / m.T) - 1;
-    const int pieces = last - first + 2;
-    const int team = pieces <= 4 ? 1 : (pieces <= 16 ? 2 : 8);     // warps an item
-    const int h0 = group * N, nh = min(N, p.H - h0), items = nh * 4;
-    const int teams = 8 / team, blocks = (last - first + 1) * gridDim.y;
-    const int block = (c - first) * gridDim.y + blockIdx.y;
-    auto slot_of = [&](int i) -> int64_t {                  // piece i, of share first - 1 + i
-        const int64_t cta_i = (int64_t)(first - 1 + i) * p.groups + group;
-        return 2 * cta_i + (i == 0 ? 1 : 0);
-    };
-    for (int base = block * teams; base < items; base += blocks * teams) {
-        const int item = base + warp / team, j = warp % team;
-        bool on = item < items;
-        const int h = item >> 2, q = item & 3;
-        float top = -CUDART_INF_F, sum = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (on) {
-            int bad = 0;                    // a share that gave up: o stays as it is
-            for (int i = lane; i < pieces; i += 32) {
-                top = fmaxf(top, p.stat[(slot_of(i) * N + h) * 2]);
-                bad |= p.status[slot_of(i) >> 1];
-            }
-            on = !__any_sync(0xffffffffu, bad);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float ref = top == -CUDART_INF_F ? 0.f : top;
-            for (int i = lane; i < pieces; i += 32) {
-                const float2 s = *reinterpret_cast<const float2 *>(p.stat + (slot_of(i) * N + h) * 2);
-                sum += ex2(s.x - ref) * s.y;
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-#pragma unroll 4
-            for (int i = j; i < pieces; i += team) {
-                const int64_t s = slot_of(i) * N + h;
-                const float f = ex2(p.stat[s * 2] - ref);
-                const float4 y = load4(p.part + s * LATENT + q * 128 + 4 * lane);
-                acc.x += f * y.x; acc.y += f * y.y; acc.z += f * y.z; acc.w += f * y.w;
-            }
-        }
-        if (team > 1) {
-            __syncthreads();
-            buf[warp][lane] = acc;
-            __syncthreads();
-            if (j == 0)
-                for (int i = 1; i < team; ++i) {
-                    const float4 y = buf[warp + i][lane];
-                    acc.x += y.x; acc.y += y.y; acc.z += y.z; acc.w += y.w;
-                }
-        }
-        if (on && j == 0) {
-            const float r = sum > 0.f ? 1.f / sum : 0.f;
-            const int64_t at = (int64_t)m.b * p.H + h0 + h;
-            store4(p.o + at * LATENT + q * 128 + 4 * lane,
-                   make_float4(acc.x * r, acc.y * r, acc.z * r, acc.w * r));
-            if (p.lse && q == 0 && lane == 0)
-                p.lse[at] = sum > 0.f ? (top + log2f(sum)) * CUDART_LN2_F : -CUDART_INF_F;
-        }
-    }
-}
-
-constexpr int JOIN_BLOCKS = 8;        // per boundary
-
 // Heads a CTA: the fewest that hold all H, else 64 a group.
-int heads_per_cta(int32_t H) { return H <= 16 ? 16 : (H <= 32 ? 32 : 64); }
-struct Plan { int N, groups, ctas; };
-Plan plan_of(int32_t H, int nsm) {
-    Plan pl;
-    pl.N = heads_per_cta(H);
-    pl.groups = (H + pl.N - 1) / pl.N;
-    const int shares = nsm / pl.groups;
-    pl.ctas = pl.groups * (shares > 0 ? shares : 1);
-    return pl;
-}
-
-uint64_t ws_meta(int ctas) { return WS_STATUS + ((uint64_t)ctas * 4 + 255) / 256 * 256; }
-uint64_t ws_stat(int ctas) { return ws_meta(ctas) + ((uint64_t)ctas * sizeof(Meta) + 255) / 256 * 256; }
-uint64_t ws_part(int ctas, int N) { return ws_stat(ctas) + (uint64_t)ctas * 2 * N * 8; }
+SplitPlan plan_of(int32_t H, int nsm) { return split_plan(H, H <= 16 ? 16 : (H <= 32 ? 32 : 64), nsm); }
 
 template <int N>
-cudaError_t run(const DecodeArgs &a, const Plan &pl, cudaStream_t st) {
+cudaError_t run(const DecodeArgs &a, const SplitPlan &pl, cudaStream_t st) {
     static std::mutex mu;
     static bool ready[64] = {false};
     int dev = 0;
@@ -687,8 +491,8 @@ cudaError_t run(const DecodeArgs &a, const Plan &pl, cudaStream_t st) {
             ready[dev] = true;
         }
     }
-    uint8_t *ws = static_cast<uint8_t *>(a.ws);
     DecParams p;
+    split_params(p, a, pl);
     const uint64_t rows = (uint64_t)a.n_pages * a.page;
     const uint64_t cd[4] = {64, 8, CHUNKS, rows / 8}, cs[3] = {ROW * 2, 128, GROUP};
     const uint32_t cb[4] = {64, 8, CHUNKS, (uint32_t)(a.page < TOK ? a.page : TOK) / 8};
@@ -697,40 +501,14 @@ cudaError_t run(const DecodeArgs &a, const Plan &pl, cudaStream_t st) {
     const uint32_t qb[4] = {64, N, CHUNKS, 1};
     if (!map4(&p.tm_c, a.cache, cd, cs, cb) || !map4(&p.tm_q, a.q, qd, qs, qb))
         return cudaErrorInvalidValue;
-    p.table = a.table; p.seq_lens = a.seq_lens;
-    p.o = (__nv_bfloat16 *)a.o; p.lse = a.lse;
-    p.status = reinterpret_cast<int32_t *>(ws + WS_STATUS);
-    p.meta = reinterpret_cast<Meta *>(ws + ws_meta(pl.ctas));
-    p.stat = reinterpret_cast<float *>(ws + ws_stat(pl.ctas));
-    p.part = reinterpret_cast<float *>(ws + ws_part(pl.ctas, N));
-    p.B = a.B; p.H = a.H; p.n_pages = a.n_pages; p.page = a.page; p.max_pages = a.max_pages;
-    p.groups = pl.groups;
-    p.scale_log2 = a.scale * 1.4426950408889634f;
     p.force_timeout = fault_force_timeout();
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)pl.ctas);
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = Smem<N>::BYTES;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, decode_kernel<N>, p);
-    if (e != cudaSuccess) return e;
-    const int joins = pl.ctas - pl.groups;
-    cfg.gridDim = dim3((unsigned)(joins > 0 ? joins : 1), JOIN_BLOCKS);
-    cfg.blockDim = dim3(256);
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, join_kernel<N>, p, pl.ctas, reinterpret_cast<int32_t *>(ws));
+    return launch_split<N, __nv_bfloat16>(decode_kernel<N>, p, pl, THREADS, Smem<N>::BYTES, a.ws, st);
 }
 
 }  // namespace
 
 uint64_t decode_tc_workspace_bytes(int32_t H) {
-    const Plan pl = plan_of(H, MAX_CTAS);      // the most any device takes
-    return ws_part(pl.ctas, pl.N) + (uint64_t)pl.ctas * 2 * pl.N * LATENT * 4;
+    return ws_bytes(plan_of(H, MAX_CTAS));     // the most any device takes
 }
 
 cudaError_t launch_decode_tc(const DecodeArgs &a, cudaStream_t st) {
@@ -738,7 +516,7 @@ cudaError_t launch_decode_tc(const DecodeArgs &a, cudaStream_t st) {
     const cudaError_t e = sm_count(&nsm);
     if (e != cudaSuccess) return e;
     if (nsm > MAX_CTAS) nsm = MAX_CTAS;
-    const Plan pl = plan_of(a.H, nsm);
+    const SplitPlan pl = plan_of(a.H, nsm);
     switch (pl.N) {
     case 16: return run<16>(a, pl, st);
     case 32: return run<32>(a, pl, st);

@@ -1,9 +1,7 @@
-// kda_mla_simt.cu -- latent attention on the CUDA cores in fp32 arithmetic:
-// the expanded form (flash-style tiles) and the absorbed form (tokens split
-// over blocks, joined by a second kernel).
-#include "kda_mla.cuh"
-
-#include <math_constants.h>
+// kda_mla_simt.cu -- latent attention of fp32 tensors on the CUDA cores: the
+// expanded form in tiles with a running maximum and sum, and the absorbed form.
+// (tf32 tensor-core products keep 11 of the 24 bits.)
+#include "kda_mla_split.cuh"
 
 namespace kda {
 namespace mla {
@@ -151,138 +149,130 @@ __global__ void __launch_bounds__(256) prefill_simt_kernel(const PrefillArgs p) 
 }
 
 // ---- absorbed form --------------------------------------------------------------
-// One block per (split of a sequence's tokens, group of 8 heads, sequence):
-// tiles of 32 tokens in shared memory; a warp computes the scores of its 72 of
-// the 576 channels (lane = token), one warp per head takes the softmax, and a
-// thread owns 2 of the 512 output channels of all 8 heads.
-constexpr int HG = 8, TT = 32, LDR = ROW + 4;
-constexpr int DEC_FLOATS = HG * ROW + TT * LDR + 8 * TT * HG + TT * HG + 2 * HG;
-constexpr int MAX_SPLITS = 64;
+// Shares and joins as in kda_mla_split.cuh, two CTAs per SM, groups of 8 heads,
+// tiles of 32 tokens.  A tile's rows go to shared memory (padded, so that 32
+// lanes read 32 rows without conflicts); a warp computes the scores of its 72
+// of the 576 channels (lane = token) for all heads, one warp per head takes the
+// softmax, and a thread owns 2 of the 512 output channels of all 8 heads.
+// Shared-memory reads bound it: 12 wavefronts for 32 FMAs in the scores.
+constexpr int HG = 8, TT = 32, LDR = ROW + 4, DTHREADS = 256;
+constexpr int DEC_FLOATS = HG * ROW + TT * LDR + 8 * TT * HG + TT * HG + HG;
+constexpr int DEC_CTAS = 320;                   // per launch, up to two per SM
 
-// [split][B][H]: unnormalised output (512), then maximum and sum
-__host__ __device__ inline int64_t part_index(int split, int b, int h, int B, int H) {
-    return ((int64_t)split * B + b) * H + h;
+__device__ __forceinline__ void copy16_or_zero(float *dst, const float *src, bool copy) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 :: "r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src), "r"(copy ? 16 : 0) : "memory");
 }
 
-int decode_splits(int32_t B, int32_t H) {
-    const int64_t units = (int64_t)B * ((H + HG - 1) / HG);
-    const int64_t want = (4 * 152 + units - 1) / units;
-    return (int)(want < 1 ? 1 : (want > MAX_SPLITS ? MAX_SPLITS : want));
-}
-
-template <typename T>
-__global__ void __launch_bounds__(256) decode_simt_kernel(const DecodeArgs p, int splits,
-                                                          float *part, float *stat) {
-    extern __shared__ float smf[];
+__global__ void __launch_bounds__(DTHREADS, 2) decode_simt_kernel(const SplitParams p, const float *q,
+                                                                  const float *cache) {
+    extern __shared__ __align__(16) float smf[];
     float *qs = smf;                        // [8][576]
     float *rows = qs + HG * ROW;            // [32][LDR]
     float *red = rows + TT * LDR;           // [8 warps][8 heads][32 tokens]
     float *ps = red + 8 * TT * HG;          // [32 tokens][8 heads]
-    float *fs = ps + TT * HG;               // rescale factor per head, then sums
+    float *fs = ps + TT * HG;               // rescale factor per head
+    __shared__ ShareScratch<DTHREADS> scratch;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int split = blockIdx.x, h0 = blockIdx.y * HG, b = blockIdx.z, H = p.H;
-    const int nh = min(HG, H - h0);
-    int64_t len = p.seq_lens[b];
-    const int64_t cap = (int64_t)p.max_pages * p.page;
-    len = len < 0 ? 0 : (len > cap ? cap : len);
-    const int64_t tiles = (len + TT - 1) / TT;
-    const int64_t t0 = tiles * split / splits * TT;
-    const int64_t t1 = min(len, tiles * (split + 1) / splits * TT);
-    const T *q = (const T *)p.q, *cache = (const T *)p.cache;
-    for (int e = tid; e < HG * ROW / 4; e += 256) {
-        const int r = e / (ROW / 4), c = e % (ROW / 4) * 4;
-        store4(qs + r * ROW + c, r < nh ? load4(q + ((int64_t)b * H + h0 + r) * ROW + c)
-                                        : make_float4(0.f, 0.f, 0.f, 0.f));
-    }
-    float m = -CUDART_INF_F, l = 0.f;       // of head `warp`
-    float acc[HG][2] = {};
-    for (int64_t t = t0; t < t1; t += TT) {
+    const int h0 = blockIdx.x % p.groups * HG, nh = min(HG, p.H - h0);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const Share share = find_share<TT, DTHREADS, HG, float>(p, scratch);
+    if (tid == 0) p.status[blockIdx.x] = 0;
+    if (!share.busy) return;
+    Walk<TT> w;
+    w.start(p, share);
+    const int shift = 31 - __clz(p.page);
+    do {
+        const int32_t *tab = p.table + (int64_t)w.b * p.max_pages;
         __syncthreads();
-        for (int e = tid; e < TT * (ROW / 4); e += 256) {
+        for (int e = tid; e < HG * ROW / 4; e += DTHREADS) {
             const int r = e / (ROW / 4), c = e % (ROW / 4) * 4;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (t + r < t1) {
-                const int pg = p.table[(int64_t)b * p.max_pages + (t + r) / p.page];
-                if (pg >= 0 && pg < p.n_pages)
-                    x = load4(cache + ((int64_t)pg * p.page + (t + r) % p.page) * ROW + c);
+            store4(qs + r * ROW + c, r < nh ? load4(q + ((int64_t)w.b * p.H + h0 + r) * ROW + c)
+                                            : make_float4(0.f, 0.f, 0.f, 0.f));
+        }
+        float m = -CUDART_INF_F, l = 0.f;   // of head `warp`, this lane's tokens
+        float acc[HG][2] = {};
+        for (int64_t i = w.lo; i < w.hi; ++i) {
+            const int64_t t = i * TT;
+            // lane = token: its row of the cache, or none
+            int at = -1;
+            if (t + lane < w.len) {
+                const int pg = tab[(t + lane) >> shift];
+                if (pg >= 0 && pg < p.n_pages) at = (pg << shift) + ((int)(t + lane) & (p.page - 1));
             }
-            store4(rows + r * LDR + c, x);
-        }
-        __syncthreads();
-        float sc[HG] = {};
-        for (int c = warp * (ROW / 8); c < (warp + 1) * (ROW / 8); c += 4) {
-            const float4 x = load4(rows + lane * LDR + c);
+            __syncthreads();                // the previous tile has been read
 #pragma unroll
-            for (int h = 0; h < HG; ++h) {
-                const float4 y = load4(qs + h * ROW + c);
-                sc[h] += x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
+            for (int r = 0; r < TT / 8; ++r) {              // a warp copies rows warp, warp + 8, ...
+                const int row = warp + 8 * r;
+                const int src = __shfl_sync(0xffffffffu, at, row);
+                for (int c = 4 * lane; c < ROW; c += 128)
+                    copy16_or_zero(rows + row * LDR + c, cache + (src < 0 ? 0 : (int64_t)src * ROW + c), src >= 0);
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncthreads();
+            float sc[HG] = {};
+#pragma unroll 6
+            for (int c = warp * (ROW / 8); c < (warp + 1) * (ROW / 8); c += 4) {
+                const float4 x = load4(rows + lane * LDR + c);
+#pragma unroll
+                for (int h = 0; h < HG; ++h) {
+                    const float4 y = load4(qs + h * ROW + c);
+                    sc[h] += x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < HG; ++h) red[(warp * HG + h) * TT + lane] = sc[h];
+            __syncthreads();
+            {                               // head `warp`, token `lane`
+                float x = 0.f;
+#pragma unroll
+                for (int v = 0; v < 8; ++v) x += red[(v * HG + warp) * TT + lane];
+                x = at >= 0 ? x * p.scale_log2 : -CUDART_INF_F;
+                const float top = fmaxf(m, warp_max(x));
+                const float ref = top == -CUDART_INF_F ? 0.f : top;
+                const float f = exp2f(m - ref), e = exp2f(x - ref);
+                l = l * f + e;
+                m = top;
+                ps[lane * HG + warp] = e;
+                if (lane == 0) fs[warp] = f;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int h = 0; h < HG; ++h) { acc[h][0] *= fs[h]; acc[h][1] *= fs[h]; }
+#pragma unroll 8
+            for (int r = 0; r < TT; ++r) {
+                const float2 v = *reinterpret_cast<const float2 *>(rows + r * LDR + 2 * tid);
+                const float4 a = load4(ps + r * HG), c = load4(ps + r * HG + 4);
+                const float e[HG] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+#pragma unroll
+                for (int h = 0; h < HG; ++h) { acc[h][0] += e[h] * v.x; acc[h][1] += e[h] * v.y; }
             }
         }
-#pragma unroll
-        for (int h = 0; h < HG; ++h) red[(warp * HG + h) * TT + lane] = sc[h];
-        __syncthreads();
-        {                                   // head `warp`, token `lane`
-            float x = 0.f;
-#pragma unroll
-            for (int w = 0; w < 8; ++w) x += red[(w * HG + warp) * TT + lane];
-            bool seen = t + lane < t1;
-            if (seen) {
-                const int pg = p.table[(int64_t)b * p.max_pages + (t + lane) / p.page];
-                seen = pg >= 0 && pg < p.n_pages;
+        // the segment's end
+        l = warp_sum(l);
+        const bool whole = w.whole();
+        const int64_t slot = w.slot();
+        if (lane == 0 && warp < nh) {
+            if (whole) {
+                if (p.lse)
+                    p.lse[(int64_t)w.b * p.H + h0 + warp] =
+                        l > 0.f ? (m + log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
+            } else {
+                *reinterpret_cast<float2 *>(p.stat + (slot * HG + warp) * 2) = make_float2(m, l);
             }
-            x = seen ? x * p.scale : -CUDART_INF_F;
-            const float top = fmaxf(m, warp_max(x));
-            const float ref = top == -CUDART_INF_F ? 0.f : top;
-            const float f = expf(m - ref), e = expf(x - ref);
-            l = l * f + e;                  // this lane's tokens
-            m = top;
-            ps[lane * HG + warp] = e;
-            if (lane == 0) fs[warp] = f;
         }
+        __syncthreads();                    // fs has been read
+        if (lane == 0) fs[warp] = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
         __syncthreads();
 #pragma unroll
-        for (int h = 0; h < HG; ++h) { acc[h][0] *= fs[h]; acc[h][1] *= fs[h]; }
-#pragma unroll 4
-        for (int r = 0; r < TT; ++r) {
-            const float2 v = *reinterpret_cast<const float2 *>(rows + r * LDR + 2 * tid);
-            const float4 a = load4(ps + r * HG), c = load4(ps + r * HG + 4);
-            const float w[HG] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
-#pragma unroll
-            for (int h = 0; h < HG; ++h) { acc[h][0] += w[h] * v.x; acc[h][1] += w[h] * v.y; }
-        }
-    }
-    l = warp_sum(l);
-    if (lane == 0 && warp < nh) {
-        const int64_t at = part_index(split, b, h0 + warp, p.B, H);
-        stat[2 * at] = m;
-        stat[2 * at + 1] = l;
-    }
-    for (int h = 0; h < nh; ++h)
-        *reinterpret_cast<float2 *>(part + part_index(split, b, h0 + h, p.B, H) * LATENT + 2 * tid) =
-            make_float2(acc[h][0], acc[h][1]);
-}
-
-// joins the splits of one (sequence, head); 128 threads, 4 channels each
-template <typename T>
-__global__ void __launch_bounds__(128) decode_join_kernel(const DecodeArgs p, int splits,
-                                                          const float *part, const float *stat) {
-    const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
-    float m = -CUDART_INF_F;
-    for (int s = 0; s < splits; ++s) m = fmaxf(m, stat[2 * part_index(s, b, h, p.B, p.H)]);
-    const float ref = m == -CUDART_INF_F ? 0.f : m;
-    float l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < splits; ++s) {
-        const int64_t at = part_index(s, b, h, p.B, p.H);
-        const float f = expf(stat[2 * at] - ref);
-        const float4 x = load4(part + at * LATENT + 4 * tid);
-        l += f * stat[2 * at + 1];
-        acc.x += f * x.x; acc.y += f * x.y; acc.z += f * x.z; acc.w += f * x.w;
-    }
-    const float r = l > 0.f ? 1.f / l : 0.f;
-    const int64_t at = (int64_t)b * p.H + h;
-    store4((T *)p.o + at * LATENT + 4 * tid, make_float4(acc.x * r, acc.y * r, acc.z * r, acc.w * r));
-    if (p.lse && tid == 0) p.lse[at] = l > 0.f ? m + logf(l) : -CUDART_INF_F;
+        for (int h = 0; h < HG; ++h)
+            if (h < nh) {
+                float *to = whole ? (float *)p.o + ((int64_t)w.b * p.H + h0 + h) * LATENT
+                                  : p.part + (slot * HG + h) * LATENT;
+                *reinterpret_cast<float2 *>(to + 2 * tid) = make_float2(acc[h][0] * fs[h], acc[h][1] * fs[h]);
+            }
+    } while (w.next(p, share));
 }
 
 template <typename T>
@@ -296,35 +286,26 @@ cudaError_t run_prefill(const PrefillArgs &a, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t run_decode(const DecodeArgs &a, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(decode_simt_kernel<T>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         DEC_FLOATS * (int)sizeof(float));
-    if (e != cudaSuccess) return e;
-    const int splits = decode_splits(a.B, a.H);
-    float *part = reinterpret_cast<float *>((uint8_t *)a.ws + 256);
-    float *stat = part + (int64_t)splits * a.B * a.H * LATENT;
-    decode_simt_kernel<T><<<dim3(splits, (a.H + HG - 1) / HG, a.B), 256, DEC_FLOATS * sizeof(float), st>>>(
-        a, splits, part, stat);
-    decode_join_kernel<T><<<dim3(a.H, a.B), 128, 0, st>>>(a, splits, part, stat);
-    return cudaGetLastError();
-}
-
 }  // namespace
 
-uint64_t decode_simt_workspace_bytes(int32_t B, int32_t H) {
-    return 256 + (uint64_t)decode_splits(B, H) * B * H * (LATENT + 2) * sizeof(float);
-}
+uint64_t decode_simt_workspace_bytes(int32_t H) { return ws_bytes(split_plan(H, HG, DEC_CTAS)); }
 
 cudaError_t launch_prefill_simt(const PrefillArgs &a, cudaStream_t st) {
     return run_prefill<float>(a, st);
 }
 
 cudaError_t launch_decode_simt(const DecodeArgs &a, cudaStream_t st) {
-    cudaError_t e = cudaMemsetAsync(a.ws, 0, 256, st);
+    int nsm = 1;
+    cudaError_t e = sm_count(&nsm);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(decode_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 DEC_FLOATS * (int)sizeof(float));
     if (e != cudaSuccess) return e;
-    return run_decode<float>(a, st);
+    const SplitPlan pl = split_plan(a.H, HG, 2 * nsm < DEC_CTAS ? 2 * nsm : DEC_CTAS);
+    SplitParams p;
+    split_params(p, a, pl);
+    return launch_split<HG, float>(decode_simt_kernel, p, pl, DTHREADS, DEC_FLOATS * sizeof(float), a.ws, st,
+                                   (const float *)a.q, (const float *)a.cache);
 }
 
 }  // namespace mla

@@ -2,7 +2,7 @@
 // tensor maps, TMA loads, waits that end early once a CTA has failed.
 #pragma once
 
-#include "kda_mla.cuh"
+#include "kda_mla_split.cuh"
 #include "kda_tc.cuh"
 
 #include <cuda.h>
@@ -15,8 +15,6 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();   // kda_prefill_tc.cu
 namespace mla {
 
 using namespace tc;
-
-constexpr int FAIL_TIMEOUT = 4;      // status word of a wait that gave up
 
 // 4D bf16 map with 128-byte swizzle (boxes of 64 values along the first axis).
 inline bool map4(CUtensorMap *m, const void *base, const uint64_t (&dims)[4],
@@ -83,12 +81,6 @@ __device__ __forceinline__ bool bar_or(uint32_t id, uint32_t nthreads, bool x) {
                  "barrier.cta.red.or.pred q, %1, %2, p;\nselp.b32 %0, 1, 0, q;\n}"
                  : "=r"(y) : "r"(id), "r"(nthreads), "r"((uint32_t)x) : "memory");
     return y != 0;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 __device__ __forceinline__ uint32_t pack_bf(float a, float b) {
