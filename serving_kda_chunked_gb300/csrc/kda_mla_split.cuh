@@ -143,89 +143,103 @@ template <int TOK> struct Walk {
 };
 
 // Adds up the partial results of the sequences that a share boundary cuts.
-// Block (boundary, r) works for the sequence its boundary lies in, together
-// with the blocks of that sequence's other boundaries; an item is 128
-// channels of a head, taken by one to eight warps, the more the more pieces
-// there are.  Pieces are added in order of the shares: a fixed order.
+// Blocks (boundary, 0 .. N / 2 - 1) work for the sequence their boundary lies
+// in; an item is 128 channels of a head.  Up to eight pieces: one warp an item,
+// all pieces' rows loaded before the weights are known.  More (the sequence then
+// has eight boundaries' blocks or more): one block an item, every eighth piece
+// a warp.  Pieces are added in a fixed order.
 template <int N, typename To>
 __global__ void __launch_bounds__(256) join_kernel(const SplitParams p, int ctas, int32_t *header) {
     __shared__ float4 buf[8][32];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (blockIdx.x == 0 && blockIdx.y == 0) {              // the call's status, from the CTAs'
         int st = 0;
         for (int i = tid; i < ctas; i += 256) st |= p.status[i];
         st = __syncthreads_or(st);
         if (tid == 0) *header = st ? FAIL_TIMEOUT : 0;
     }
-    const int cta = blockIdx.x + p.groups;                  // shares 1 .. of every group
+    const int cta = blockIdx.y + p.groups;                  // shares 1 .. of every group
     if (cta >= ctas) return;
     const int group = cta % p.groups, c = cta / p.groups;
     const Meta m = p.meta[cta];
     if (m.b < 0 || share_start(m.T, c, m.C) <= m.t0) return;
     const int first = (int)(((m.t0 + 1) * m.C + m.T - 1) / m.T);   // boundaries inside the sequence
     const int last = (int)((m.t1 * m.C + m.T - 1) / m.T) - 1;
-    const int pieces = last - first + 2;
-    const int team = pieces <= 4 ? 1 : (pieces <= 16 ? 2 : 8);     // warps an item
-    const int h0 = group * N, nh = min(N, p.H - h0), items = nh * 4;
-    const int teams = 8 / team, blocks = (last - first + 1) * gridDim.y;
-    const int block = (c - first) * gridDim.y + blockIdx.y;
-    auto slot_of = [&](int i) -> int64_t {                  // piece i, of share first - 1 + i
-        const int64_t cta_i = (int64_t)(first - 1 + i) * p.groups + group;
-        return 2 * cta_i + (i == 0 ? 1 : 0);
-    };
-    for (int base = block * teams; base < items; base += blocks * teams) {
-        const int item = base + warp / team, j = warp % team;
-        bool on = item < items;
-        const int h = item >> 2, q = item & 3;
-        float top = -CUDART_INF_F, sum = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (on) {
-            int bad = 0;                    // a share that gave up: o stays as it is
-            for (int i = lane; i < pieces; i += 32) {
-                top = fmaxf(top, p.stat[(slot_of(i) * N + h) * 2]);
-                bad |= p.status[slot_of(i) >> 1];
-            }
-            on = !__any_sync(0xffffffffu, bad);
+    const int pieces = last - first + 2;                    // of shares first - 1 .. last
+    const int nh = min(N, p.H - group * N);
+    const int slot0 = 2 * ((first - 1) * p.groups + group); // of piece i: slot0 + 2 groups i, + 1 for the first
+    auto slot_of = [&](int i) { return slot0 + 2 * p.groups * i + (i == 0); };
+    const bool wide = pieces > 8;
+    const int block = (c - first) * gridDim.x + blockIdx.x;
+    const int item = wide ? block : (block * 8 + warp);
+    const int h = item >> 2, ch = (item & 3) * 128 + 4 * lane;
+    if (h >= nh) return;                                    // of a wide item: the whole block
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float top = -CUDART_INF_F, sum = 0.f, ref;
+    int bad = 0;                                            // a share that gave up: o stays as it is
+    if (!wide) {
+        float4 y[8];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float ref = top == -CUDART_INF_F ? 0.f : top;
-            for (int i = lane; i < pieces; i += 32) {
-                const float2 s = *reinterpret_cast<const float2 *>(p.stat + (slot_of(i) * N + h) * 2);
-                sum += ex2(s.x - ref) * s.y;
-            }
+        for (int i = 0; i < 8; ++i)
+            if (i < pieces) y[i] = load4(p.part + ((int64_t)slot_of(i) * N + h) * LATENT + ch);
+        float2 s = make_float2(-CUDART_INF_F, 0.f);
+        if (lane < pieces) {
+            s = *reinterpret_cast<const float2 *>(p.stat + ((int64_t)slot_of(lane) * N + h) * 2);
+            bad = p.status[slot_of(lane) >> 1];
+        }
+        top = s.x;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-#pragma unroll 4
-            for (int i = j; i < pieces; i += team) {
-                const int64_t s = slot_of(i) * N + h;
-                const float f = ex2(p.stat[s * 2] - ref);
-                const float4 y = load4(p.part + s * LATENT + q * 128 + 4 * lane);
-                acc.x += f * y.x; acc.y += f * y.y; acc.z += f * y.z; acc.w += f * y.w;
+        for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        top = __shfl_sync(0xffffffffu, top, 0);
+        ref = top == -CUDART_INF_F ? 0.f : top;
+        const float f = ex2(s.x - ref);
+        sum = f * s.y;
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        sum = __shfl_sync(0xffffffffu, sum, 0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < pieces) {
+                const float g = __shfl_sync(0xffffffffu, f, i);
+                acc.x += g * y[i].x; acc.y += g * y[i].y; acc.z += g * y[i].z; acc.w += g * y[i].w;
             }
+    } else {
+        for (int i = lane; i < pieces; i += 32) {
+            top = fmaxf(top, p.stat[((int64_t)slot_of(i) * N + h) * 2]);
+            bad |= p.status[slot_of(i) >> 1];
         }
-        if (team > 1) {
-            __syncthreads();
-            buf[warp][lane] = acc;
-            __syncthreads();
-            if (j == 0)
-                for (int i = 1; i < team; ++i) {
-                    const float4 y = buf[warp + i][lane];
-                    acc.x += y.x; acc.y += y.y; acc.z += y.z; acc.w += y.w;
-                }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        ref = top == -CUDART_INF_F ? 0.f : top;
+        for (int i = lane; i < pieces; i += 32) {
+            const float2 s = *reinterpret_cast<const float2 *>(p.stat + ((int64_t)slot_of(i) * N + h) * 2);
+            sum += ex2(s.x - ref) * s.y;
         }
-        if (on && j == 0) {
-            const float r = sum > 0.f ? 1.f / sum : 0.f;
-            const int64_t at = (int64_t)m.b * p.H + h0 + h;
-            store4((To *)p.o + at * LATENT + q * 128 + 4 * lane,
-                   make_float4(acc.x * r, acc.y * r, acc.z * r, acc.w * r));
-            if (p.lse && q == 0 && lane == 0)
-                p.lse[at] = sum > 0.f ? (top + log2f(sum)) * CUDART_LN2_F : -CUDART_INF_F;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+#pragma unroll 8
+        for (int i = warp; i < pieces; i += 8) {
+            const int64_t at = (int64_t)slot_of(i) * N + h;
+            const float f = ex2(p.stat[at * 2] - ref);
+            const float4 y = load4(p.part + at * LATENT + ch);
+            acc.x += f * y.x; acc.y += f * y.y; acc.z += f * y.z; acc.w += f * y.w;
+        }
+        buf[warp][lane] = acc;
+        __syncthreads();
+        if (warp != 0) return;
+        for (int i = 1; i < 8; ++i) {
+            const float4 y = buf[i][lane];
+            acc.x += y.x; acc.y += y.y; acc.z += y.z; acc.w += y.w;
         }
     }
+    if (__any_sync(0xffffffffu, bad)) return;
+    const float r = sum > 0.f ? 1.f / sum : 0.f;
+    const int64_t at = (int64_t)m.b * p.H + group * N + h;
+    store4((To *)p.o + at * LATENT + ch, make_float4(acc.x * r, acc.y * r, acc.z * r, acc.w * r));
+    if (p.lse && (item & 3) == 0 && lane == 0)
+        p.lse[at] = sum > 0.f ? (top + log2f(sum)) * CUDART_LN2_F : -CUDART_INF_F;
 }
-
-constexpr int JOIN_BLOCKS = 8;        // per boundary
 
 // workspace: header | status | meta | stat | part
 struct SplitPlan { int N, groups, ctas; };
@@ -274,7 +288,7 @@ cudaError_t launch_split(void (*kernel)(Params, More...), const Params &p, const
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p, more...);
     if (e != cudaSuccess) return e;
     const int joins = s.ctas - s.groups;
-    cfg.gridDim = dim3((unsigned)(joins > 0 ? joins : 1), JOIN_BLOCKS);
+    cfg.gridDim = dim3(N / 2, (unsigned)(joins > 0 ? joins : 1));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, join_kernel<N, To>, (const SplitParams &)p, s.ctas,
