@@ -323,8 +323,9 @@ kda_status kda_mla_append(const void *c, int64_t c_stride, const void *k_r, int6
 }
 
 uint64_t kda_mla_prefill_workspace_size(int32_t N, int64_t Tq, int32_t H, int32_t dtype) {
-    if (N <= 0 || Tq <= 0 || H <= 0 || dtype != KDA_BF16) return 0;
-    return kda::mla::prefill_tc_workspace_bytes(N, Tq);
+    if (N <= 0 || Tq <= 0 || H <= 0 || (dtype != KDA_BF16 && dtype != KDA_FP32)) return 0;
+    return dtype == KDA_BF16 ? kda::mla::prefill_tc_workspace_bytes(N, Tq)
+                             : kda::mla::prefill_simt_workspace_bytes(N, Tq, H);
 }
 
 kda_status kda_mla_prefill(const void *q, const void *kv, const void *k_r, const int32_t *cu_q,

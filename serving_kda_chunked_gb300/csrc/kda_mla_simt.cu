@@ -19,39 +19,90 @@ __device__ __forceinline__ float warp_sum(float x) {
 }
 
 // ---- expanded form -------------------------------------------------------------
-// One block per (64 queries of a sequence, head); 256 threads, each a 4 x 4
-// piece of the 64 x 64 scores and a 4 x 8 piece of the 64 x 128 output.
-constexpr int BQ = 64, BK = 64, LDT = BQ + 4;
-constexpr int PRE_FLOATS = 2 * DQK * LDT + BK * DV + BK * LDT;
+// One block per (64 queries of a sequence, head, part of their keys); 256
+// threads, each a 4 x 4 piece of the 64 x 64 scores and a 4 x 8 piece of the
+// 64 x 128 output: 64 FMAs for 12 shared-memory wavefronts, so the FMA pipes
+// bound it.  Keys arrive with asynchronous copies one tile ahead, values while
+// the scores are computed.  With few (queries, head) blocks the keys are cut
+// into up to SPLITS parts, whose unnormalised results a second kernel joins.
+constexpr int BQ = 64, BK = 64, LDQ = DQK + 4, LDP = BK + 4, SPLITS = 8, PTHREADS = 256;
+constexpr int PRE_FLOATS = (BQ + 2 * BK) * LDQ + BK * DV + BQ * LDP;
 
-template <typename T>
-__global__ void __launch_bounds__(256) prefill_simt_kernel(const PrefillArgs p) {
-    extern __shared__ float smf[];
-    float *Qt = smf;                       // [192][LDT], query fastest
-    float *Kt = Qt + DQK * LDT;            // [192][LDT], key fastest
-    float *Vs = Kt + DQK * LDT;            // [64][128]
-    float *Pt = Vs + BK * DV;              // [64 keys][LDT], query fastest
-    const int tid = threadIdx.x, h = blockIdx.y, H = p.H;
-    // tile -> (sequence, first query): every sequence has ceil(nq / 64) tiles
-    int tile = blockIdx.x, n = 0;
-    SeqSpan s{0, 0, 0, 0};
-    for (; n < p.N; ++n) {
-        s = seq_span(p.cu_q, p.cu_k, n, p.Tq, p.Tk);
-        const int tiles = (s.nq + BQ - 1) / BQ;
+__device__ __forceinline__ void copy16_or_zero(float *dst, const float *src, bool copy) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 :: "r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src), "r"(copy ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
+}
+
+struct PreSplit { float *part, *stat; int parts; };     // [parts][Tq][H]: output (128), then maximum and sum
+
+// What a block works on: sequence span, first query, keys of its part.
+struct PreUnit { SeqSpan s; int i0, j0, j1, parts; };
+__device__ __forceinline__ bool pre_unit(const PrefillArgs &p, int tile, int part, int parts, PreUnit &u) {
+    int n = 0;
+    for (; n < p.N; ++n) {               // every sequence has ceil(nq / 64) tiles
+        u.s = seq_span(p.cu_q, p.cu_k, n, p.Tq, p.Tk);
+        const int tiles = (u.s.nq + BQ - 1) / BQ;
         if (tile < tiles) break;
         tile -= tiles;
     }
-    if (n == p.N) return;
-    const int i0 = tile * BQ;
-    const T *q = (const T *)p.q, *kv = (const T *)p.kv, *kr = (const T *)p.k_r;
-    for (int e = tid; e < BQ * (DQK / 4); e += 256) {
-        const int r = e / (DQK / 4), c = e % (DQK / 4) * 4;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i0 + r < s.nq) x = load4(q + ((s.q0 + i0 + r) * H + h) * DQK + c);
-        Qt[(c + 0) * LDT + r] = x.x; Qt[(c + 1) * LDT + r] = x.y;
-        Qt[(c + 2) * LDT + r] = x.z; Qt[(c + 3) * LDT + r] = x.w;
+    if (n == p.N) return false;
+    u.i0 = tile * BQ;
+    const int last = min(u.i0 + BQ, u.s.nq) - 1;         // keys seen by the tile's last query
+    const int64_t seen = p.causal ? (int64_t)last + u.s.nk - u.s.nq + 1 : u.s.nk;
+    const int hi = seen < 0 ? 0 : (seen > u.s.nk ? u.s.nk : (int)seen);
+    int len = ((hi + parts - 1) / parts + BK - 1) / BK * BK;
+    len = max(len, 2 * BK);              // a part is worth two tiles at least
+    u.parts = max(1, (hi + len - 1) / len);
+    u.j0 = part * len;
+    u.j1 = min(hi, u.j0 + len);
+    return part < u.parts;
+}
+
+__global__ void __launch_bounds__(PTHREADS) prefill_simt_kernel(const PrefillArgs p, const PreSplit sp) {
+    extern __shared__ __align__(16) float smf[];
+    float *Qs = smf;                       // [64][LDQ]
+    float *Ks = Qs + BQ * LDQ;             // [2][64][LDQ]
+    float *Vs = Ks + 2 * BK * LDQ;         // [64][128]
+    float *Ps = Vs + BK * DV;              // [64 queries][LDP]
+    const int tid = threadIdx.x, h = blockIdx.y, H = p.H;
+    PreUnit u;                             // long blocks first: the last queries see the most keys
+    if (!pre_unit(p, gridDim.x - 1 - blockIdx.x, blockIdx.z, sp.parts, u)) return;
+    const SeqSpan s = u.s;
+    const float *q = (const float *)p.q, *kv = (const float *)p.kv, *kr = (const float *)p.k_r;
+    auto load_keys = [&](int j, int buf) {
+        float *K = Ks + buf * BK * LDQ;
+        for (int e = tid; e < BK * (DQK / 4); e += PTHREADS) {
+            const int r = e / (DQK / 4), c = e % (DQK / 4) * 4;
+            const bool in = j + r < u.j1;
+            const int64_t t = s.k0 + (in ? j + r : u.j0);
+            copy16_or_zero(K + r * LDQ + c, c < NOPE ? kv + (t * H + h) * (NOPE + DV) + c : kr + t * ROPE + c - NOPE, in);
+        }
+        copy_commit();
+    };
+    auto load_values = [&](int j) {
+        for (int e = tid; e < BK * (DV / 4); e += PTHREADS) {
+            const int r = e / (DV / 4), c = e % (DV / 4) * 4;
+            const bool in = j + r < u.j1;
+            const int64_t t = s.k0 + (in ? j + r : u.j0);
+            copy16_or_zero(Vs + r * DV + c, kv + (t * H + h) * (NOPE + DV) + NOPE + c, in);
+        }
+        copy_commit();
+    };
+    if (u.j0 < u.j1) {
+        for (int e = tid; e < BQ * (DQK / 4); e += PTHREADS) {
+            const int r = e / (DQK / 4), c = e % (DQK / 4) * 4;
+            const bool in = u.i0 + r < s.nq;
+            copy16_or_zero(Qs + r * LDQ + c, q + ((s.q0 + (in ? u.i0 + r : 0)) * H + h) * DQK + c, in);
+        }
+        load_keys(u.j0, 0);
+        load_values(u.j0);
     }
-    const int tr = tid / 16, tc = tid % 16;          // rows 4 tr .., score columns 4 tc ..
+    const int tr = tid / 16, tc = tid % 16;          // rows 4 tr .., keys tc + 16 k
+    const float sl = p.scale * 1.4426950408889634f;
     float m[4], l[4], acc[4][8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -59,93 +110,133 @@ __global__ void __launch_bounds__(256) prefill_simt_kernel(const PrefillArgs p) 
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
     }
-    const int last = min(i0 + BQ, s.nq) - 1;         // keys seen by the tile's last query
-    int64_t hi = p.causal ? (int64_t)last + s.nk - s.nq + 1 : s.nk;
-    hi = hi < 0 ? 0 : (hi > s.nk ? s.nk : hi);
-    for (int64_t j0 = 0; j0 < hi; j0 += BK) {
+    int buf = 0;
+    for (int j0 = u.j0; j0 < u.j1; j0 += BK, buf ^= 1) {
+        if (j0 + BK < u.j1) load_keys(j0 + BK, buf ^ 1); else copy_commit();
+        copy_wait<2>();                              // these keys (and the queries)
         __syncthreads();
-        for (int e = tid; e < BK * (DQK / 4); e += 256) {
-            const int r = e / (DQK / 4), c = e % (DQK / 4) * 4;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (j0 + r < hi) {
-                const int64_t t = s.k0 + j0 + r;
-                x = c < NOPE ? load4(kv + (t * H + h) * (NOPE + DV) + c)
-                             : load4(kr + t * ROPE + c - NOPE);
-            }
-            Kt[(c + 0) * LDT + r] = x.x; Kt[(c + 1) * LDT + r] = x.y;
-            Kt[(c + 2) * LDT + r] = x.z; Kt[(c + 3) * LDT + r] = x.w;
-        }
-        for (int e = tid; e < BK * (DV / 4); e += 256) {
-            const int r = e / (DV / 4), c = e % (DV / 4) * 4;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (j0 + r < hi) x = load4(kv + ((s.k0 + j0 + r) * H + h) * (NOPE + DV) + NOPE + c);
-            store4(Vs + r * DV + c, x);
-        }
-        __syncthreads();
+        const float *K = Ks + buf * BK * LDQ;
         float sc[4][4] = {};
-#pragma unroll 4
-        for (int c = 0; c < DQK; ++c) {
-            const float4 a = load4(Qt + c * LDT + 4 * tr), b = load4(Kt + c * LDT + 4 * tc);
-            const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll 2
+        for (int c = 0; c < DQK; c += 4) {
+            float4 a[4], b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[i] = load4(Qs + (4 * tr + i) * LDQ + c);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) b[k] = load4(K + (tc + 16 * k) * LDQ + c);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) sc[i][j] += av[i] * bv[j];
+                for (int k = 0; k < 4; ++k)
+                    sc[i][k] += a[i].x * b[k].x + a[i].y * b[k].y + a[i].z * b[k].z + a[i].w * b[k].w;
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t qi = i0 + 4 * tr + i;
+            const int64_t qi = u.i0 + 4 * tr + i;
             const int64_t end = p.causal ? qi + s.nk - s.nq + 1 : s.nk;   // keys it sees
             float top = m[i];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t kj = j0 + 4 * tc + j;
-                sc[i][j] = kj < end && kj < s.nk ? sc[i][j] * p.scale : -CUDART_INF_F;
-                top = fmaxf(top, sc[i][j]);
+            for (int k = 0; k < 4; ++k) {
+                const int kj = j0 + tc + 16 * k;
+                sc[i][k] = kj < end && kj < u.j1 ? sc[i][k] * sl : -CUDART_INF_F;
+                top = fmaxf(top, sc[i][k]);
             }
 #pragma unroll
             for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             const float ref = top == -CUDART_INF_F ? 0.f : top;
-            const float f = expf(m[i] - ref);
+            const float f = exp2f(m[i] - ref);
             float sum = 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                sc[i][j] = expf(sc[i][j] - ref);
-                sum += sc[i][j];
-                Pt[(4 * tc + j) * LDT + 4 * tr + i] = sc[i][j];
+            for (int k = 0; k < 4; ++k) {
+                sc[i][k] = exp2f(sc[i][k] - ref);
+                sum += sc[i][k];
+                Ps[(4 * tr + i) * LDP + tc + 16 * k] = sc[i][k];
             }
-            l[i] = l[i] * f + sum;                   // this thread's four columns
+            l[i] = l[i] * f + sum;                   // this thread's four keys
             m[i] = top;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[i][j] *= f;
+            for (int k = 0; k < 8; ++k) acc[i][k] *= f;
+        }
+        copy_wait<1>();                              // these values
+        __syncthreads();
+#pragma unroll 2
+        for (int k = 0; k < BK; k += 4) {
+            float4 a[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[i] = load4(Ps + (4 * tr + i) * LDP + k);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float4 v0 = load4(Vs + (k + e) * DV + 4 * tc), v1 = load4(Vs + (k + e) * DV + 64 + 4 * tc);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float w = e == 0 ? a[i].x : (e == 1 ? a[i].y : (e == 2 ? a[i].z : a[i].w));
+                    acc[i][0] += w * v0.x; acc[i][1] += w * v0.y; acc[i][2] += w * v0.z; acc[i][3] += w * v0.w;
+                    acc[i][4] += w * v1.x; acc[i][5] += w * v1.y; acc[i][6] += w * v1.z; acc[i][7] += w * v1.w;
+                }
+            }
         }
         __syncthreads();
-#pragma unroll 4
-        for (int j = 0; j < BK; ++j) {
-            const float4 a = load4(Pt + j * LDT + 4 * tr);
-            const float4 v0 = load4(Vs + j * DV + 4 * tc), v1 = load4(Vs + j * DV + 64 + 4 * tc);
-            const float av[4] = {a.x, a.y, a.z, a.w};
-            const float bv[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int k = 0; k < 8; ++k) acc[i][k] += av[i] * bv[k];
-        }
+        if (j0 + BK < u.j1) load_values(j0 + BK); else copy_commit();
     }
-    T *o = (T *)p.o;
+    copy_wait<0>();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         float sum = l[i];
 #pragma unroll
         for (int of = 1; of < 16; of <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, of);
-        const int qi = i0 + 4 * tr + i;
+        const int qi = u.i0 + 4 * tr + i;
         if (qi >= s.nq) continue;
-        const float r = sum > 0.f ? 1.f / sum : 0.f;
         const int64_t at = (s.q0 + qi) * H + h;
-        store4(o + at * DV + 4 * tc, make_float4(acc[i][0] * r, acc[i][1] * r, acc[i][2] * r, acc[i][3] * r));
-        store4(o + at * DV + 64 + 4 * tc, make_float4(acc[i][4] * r, acc[i][5] * r, acc[i][6] * r, acc[i][7] * r));
-        if (p.lse && tc == 0) p.lse[at] = sum > 0.f ? m[i] + logf(sum) : -CUDART_INF_F;
+        const bool whole = u.parts == 1;
+        const float r = whole ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
+        const int64_t to = whole ? at : (int64_t)blockIdx.z * p.Tq * H + at;
+        float *o = (whole ? (float *)p.o : sp.part) + to * DV;
+        store4(o + 4 * tc, make_float4(acc[i][0] * r, acc[i][1] * r, acc[i][2] * r, acc[i][3] * r));
+        store4(o + 64 + 4 * tc, make_float4(acc[i][4] * r, acc[i][5] * r, acc[i][6] * r, acc[i][7] * r));
+        if (tc == 0) {
+            if (!whole) *reinterpret_cast<float2 *>(sp.stat + 2 * to) = make_float2(m[i], sum);
+            else if (p.lse) p.lse[at] = sum > 0.f ? (m[i] + log2f(sum)) * CUDART_LN2_F : -CUDART_INF_F;
+        }
     }
+}
+
+// Joins the parts of (64 queries, head); a warp takes 8 queries, a lane 4 channels.
+__global__ void __launch_bounds__(PTHREADS) prefill_join_kernel(const PrefillArgs p, const PreSplit sp) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y;
+    PreUnit u;
+    if (!pre_unit(p, blockIdx.x, 0, sp.parts, u) || u.parts == 1) return;
+    for (int r = warp; r < BQ && u.i0 + r < u.s.nq; r += 8) {
+        const int64_t at = (u.s.q0 + u.i0 + r) * p.H + h, step = p.Tq * p.H;
+        float2 st[SPLITS];
+        float4 y[SPLITS];
+        float top = -CUDART_INF_F;
+#pragma unroll
+        for (int k = 0; k < SPLITS; ++k)
+            if (k < u.parts) {
+                st[k] = *reinterpret_cast<const float2 *>(sp.stat + 2 * (k * step + at));
+                y[k] = load4(sp.part + (k * step + at) * DV + 4 * lane);
+                top = fmaxf(top, st[k].x);
+            }
+        const float ref = top == -CUDART_INF_F ? 0.f : top;
+        float sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < SPLITS; ++k)
+            if (k < u.parts) {
+                const float f = exp2f(st[k].x - ref);
+                sum += f * st[k].y;
+                acc.x += f * y[k].x; acc.y += f * y[k].y; acc.z += f * y[k].z; acc.w += f * y[k].w;
+            }
+        const float f = sum > 0.f ? 1.f / sum : 0.f;
+        store4((float *)p.o + at * DV + 4 * lane, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
+        if (p.lse && lane == 0) p.lse[at] = sum > 0.f ? (top + log2f(sum)) * CUDART_LN2_F : -CUDART_INF_F;
+    }
+}
+
+// Parts per (queries, head) block: enough for about four blocks an SM.
+int prefill_parts(int32_t N, int64_t Tq, int32_t H) {
+    const int64_t blocks = (Tq / BQ + N) * H, want = (608 + blocks - 1) / blocks;
+    return (int)(want < 1 ? 1 : (want > SPLITS ? SPLITS : want));
 }
 
 // ---- absorbed form --------------------------------------------------------------
@@ -158,11 +249,6 @@ __global__ void __launch_bounds__(256) prefill_simt_kernel(const PrefillArgs p) 
 constexpr int HG = 8, TT = 32, LDR = ROW + 4, DTHREADS = 256;
 constexpr int DEC_FLOATS = HG * ROW + TT * LDR + 8 * TT * HG + TT * HG + HG;
 constexpr int DEC_CTAS = 320;                   // per launch, up to two per SM
-
-__device__ __forceinline__ void copy16_or_zero(float *dst, const float *src, bool copy) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
-                 :: "r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src), "r"(copy ? 16 : 0) : "memory");
-}
 
 __global__ void __launch_bounds__(DTHREADS, 2) decode_simt_kernel(const SplitParams p, const float *q,
                                                                   const float *cache) {
@@ -275,23 +361,33 @@ __global__ void __launch_bounds__(DTHREADS, 2) decode_simt_kernel(const SplitPar
     } while (w.next(p, share));
 }
 
-template <typename T>
-cudaError_t run_prefill(const PrefillArgs &a, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(prefill_simt_kernel<T>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         PRE_FLOATS * (int)sizeof(float));
-    if (e != cudaSuccess) return e;
-    const int64_t tiles = (a.Tq + BQ - 1) / BQ + a.N;      // at most
-    prefill_simt_kernel<T><<<dim3((unsigned)tiles, a.H), 256, PRE_FLOATS * sizeof(float), st>>>(a);
-    return cudaGetLastError();
-}
-
 }  // namespace
 
 uint64_t decode_simt_workspace_bytes(int32_t H) { return ws_bytes(split_plan(H, HG, DEC_CTAS)); }
 
+uint64_t prefill_simt_workspace_bytes(int32_t N, int64_t Tq, int32_t H) {
+    const int parts = prefill_parts(N, Tq, H);
+    return parts == 1 ? 0 : 256 + (uint64_t)parts * Tq * H * (DV + 2) * sizeof(float);
+}
+
 cudaError_t launch_prefill_simt(const PrefillArgs &a, cudaStream_t st) {
-    return run_prefill<float>(a, st);
+    cudaError_t e = cudaFuncSetAttribute(prefill_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         PRE_FLOATS * (int)sizeof(float));
+    if (e != cudaSuccess) return e;
+    PreSplit sp;
+    sp.parts = prefill_parts(a.N, a.Tq, a.H);
+    sp.part = reinterpret_cast<float *>((uint8_t *)a.ws + 256);
+    sp.stat = sp.part + (int64_t)sp.parts * a.Tq * a.H * DV;
+    if (sp.parts > 1) {                     // no wait here can give up: the status is clear
+        e = cudaMemsetAsync(a.ws, 0, sizeof(int32_t), st);
+        if (e != cudaSuccess) return e;
+    }
+    const unsigned tiles = (unsigned)(a.Tq / BQ + a.N);     // at most
+    prefill_simt_kernel<<<dim3(tiles, a.H, sp.parts), PTHREADS, PRE_FLOATS * sizeof(float), st>>>(a, sp);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || sp.parts == 1) return e;
+    prefill_join_kernel<<<dim3(tiles, a.H), PTHREADS, 0, st>>>(a, sp);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_decode_simt(const DecodeArgs &a, cudaStream_t st) {

@@ -75,13 +75,13 @@ def test_prefill_refusals(lib, kw, expect):
 
 
 def test_prefill_workspace(lib):
-    need = kda.kda_mla_prefill_workspace_size(3, 1000, 4, torch.bfloat16)
-    if need:
-        assert _prefill(lib, N=3, Tq=1000, H=4, ws=None) == BAD
-        assert _prefill(lib, N=3, Tq=1000, H=4, wsb=need - 1) == BAD
-        assert _prefill(lib, N=3, Tq=1000, H=4, ws=P + 8) == BAD
-    assert kda.kda_mla_prefill_workspace_size(0, 1000, 4, torch.bfloat16) == 0
-    assert kda.kda_mla_prefill_workspace_size(3, 1000, 4, torch.float32) == 0
+    for code, dt in enumerate((torch.bfloat16, torch.float32)):
+        need = kda.kda_mla_prefill_workspace_size(3, 1000, 4, dt)
+        if need:
+            assert _prefill(lib, N=3, Tq=1000, H=4, dtype=code, ws=None) == BAD
+            assert _prefill(lib, N=3, Tq=1000, H=4, dtype=code, wsb=need - 1) == BAD
+            assert _prefill(lib, N=3, Tq=1000, H=4, dtype=code, ws=P + 8) == BAD
+        assert kda.kda_mla_prefill_workspace_size(0, 1000, 4, dt) == 0
 
 
 def _decode(lib, **kw):
