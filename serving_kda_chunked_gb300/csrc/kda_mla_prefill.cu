@@ -11,6 +11,11 @@
 // products run while the other tile's softmax does, and each key tile of 128
 // tokens is read once for both.
 //
+// CTAs take (256 queries, head) pairs, those with the most keys first.  Where
+// there are few pairs, their keys are cut into parts of at most an SM's share of
+// all key tiles; parts leave unnormalised results that a join kernel adds up in
+// a fixed order.
+//
 // Tensor memory (all 512 columns): scores of A and B (128 columns each), their
 // outputs (128 each).  The weights P replace the scores they come from, as
 // bf16 pairs, and are the A operand of the output product straight from
@@ -28,7 +33,6 @@
 #include "kda_mla_tc.cuh"
 
 #include <float.h>
-#include <math_constants.h>
 #include <mutex>
 
 namespace kda {
@@ -45,11 +49,36 @@ static_assert(SM_BYTES <= 232448, "shared memory");
 constexpr uint32_t S_COL = 0, O_COL = 256;                  // + 128 for tile B
 constexpr float RESCALE = 8.f;
 
-// workspace: [0] status, [1] entries; then the offsets of the sequences' first
-// entries, then the entries (sequence, block of 256 queries), most keys first
-constexpr uint32_t WS_BASE = 256;
-__host__ __device__ inline uint64_t ws_list(int N) {
-    return (WS_BASE + 4ull * ((uint64_t)N + 1) + 15) / 16 * 16;
+constexpr int MAX_SMS = 160;
+constexpr int SLOTS = 2 * MAX_SMS;           // parts with results of their own, over all heads
+constexpr int CUTS = MAX_SMS;                // blocks that are cut, over all heads
+constexpr int MIN_PART = 4;                  // key tiles that are worth a part
+
+// A block of up to 256 queries of a sequence, or a part of its keys; one CTA per
+// head.  Everything a CTA needs in one read.
+struct __align__(16) Entry {
+    int32_t row0, rows;                      // first query among all, queries
+    int32_t key0, keys;                      // first key of the part among all, the sequence's keys from there
+    int32_t off;                             // query row0 + r sees keys up to key0 + r + off
+    int32_t nA, nB;                          // key tiles of the part that tile A and tile B need
+    int32_t base, part, parts;               // slot of the block's first part, over all heads; -1 if whole
+    int32_t pad[2];
+};
+// workspace: header | first block of each sequence | entries, most keys first |
+// blocks that are cut (as their first part) | partial results per slot:
+// [256][2] (maximum in log2 units, sum) and [256][128]
+struct Header { int32_t status, entries, cut; };
+struct Layout { uint64_t base, entries, cut, stat, part, bytes; };
+__host__ __device__ inline Layout layout(int64_t N, int64_t Tq) {
+    const uint64_t cap = (uint64_t)Tq / ROWS + N;
+    Layout l;
+    l.base = 256;
+    l.entries = (l.base + 4 * ((uint64_t)N + 1) + 255) / 256 * 256;
+    l.cut = l.entries + (cap + SLOTS) * sizeof(Entry);
+    l.stat = l.cut + CUTS * sizeof(Entry);
+    l.part = l.stat + (uint64_t)SLOTS * ROWS * 8;
+    l.bytes = l.part + (uint64_t)SLOTS * ROWS * DV * 4;
+    return l;
 }
 
 struct PreParams {
@@ -57,39 +86,30 @@ struct PreParams {
     const int32_t *cu_q, *cu_k;
     __nv_bfloat16 *o;
     float *lse;
-    int32_t *ws;
+    Header *head;
+    int32_t *base;
+    Entry *entries, *cut;
+    float2 *stat;
+    float *part;
     int64_t Tq, Tk;
     int32_t N, H, causal, negative;   // negative: the scale is; scale_log2 is its magnitude
     float scale_log2;
     int32_t force_timeout;
 };
 
-__device__ __forceinline__ int2 *list_of(const PreParams &p) {
-    return reinterpret_cast<int2 *>(reinterpret_cast<uint8_t *>(p.ws) + ws_list(p.N));
-}
-// Keys that row i (of nq) sees, and key tiles that the rows up to `last` need.
-__device__ __forceinline__ int keys_seen(const SeqSpan &s, int i, int causal) {
-    if (!causal) return s.nk;
-    const int64_t e = (int64_t)i + s.nk - s.nq + 1;
-    return e < 0 ? 0 : (e > s.nk ? s.nk : (int)e);
-}
-__device__ __forceinline__ int key_tiles(const SeqSpan &s, int row0, int rows, int causal) {
-    if (row0 >= s.nq) return 0;
-    const int last = min(row0 + rows, s.nq) - 1;
-    return (keys_seen(s, last, causal) + BK - 1) / BK;
-}
-
-// Lists the blocks of queries, those with the most keys first (CTAs start in
-// list order, so the longest do not end last), and clears the status.  At most
-// `cap` of them: offsets that overlap or run backwards lose the rest.
-__global__ void __launch_bounds__(1024) plan_kernel(const PreParams p, int cap) {
+// Lists the blocks of queries and the parts of them, those with the most keys
+// first (CTAs start in list order, so the longest do not end last), and clears
+// the status.  At most `cap` blocks: offsets that overlap or run backwards lose
+// the rest.
+__global__ void __launch_bounds__(1024) plan_kernel(const PreParams p, int cap, int sms, int may_cut) {
     constexpr int NB = 1024;
-    __shared__ int start[NB + 1];
+    __shared__ int start[NB];
     __shared__ int64_t warp_tot[32];
+    __shared__ int64_t work;
+    __shared__ int blocks, slots, cuts, listed;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int32_t *base = p.ws + WS_BASE / 4;
     auto block_scan = [&](int64_t x) -> int64_t {           // inclusive
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -99,51 +119,100 @@ __global__ void __launch_bounds__(1024) plan_kernel(const PreParams p, int cap) 
         __syncthreads();
         if (lane == 31) warp_tot[warp] = x;
         __syncthreads();
-        for (int w = 0; w < warp; ++w) x += warp_tot[w];
-        return x;
+        if (warp == 0) {
+            int64_t t = warp_tot[lane];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, t, o);
+                if (lane >= o) t += y;
+            }
+            warp_tot[lane] = t;
+        }
+        __syncthreads();
+        return x + (warp > 0 ? warp_tot[warp - 1] : 0);
     };
+    auto count = [&](int n) { return (seq_span(p.cu_q, p.cu_k, n, p.Tq, p.Tk).nq + ROWS - 1) / ROWS; };
     const int per = (p.N + 1023) / 1024;
     const int n0 = min(p.N, tid * per), n1 = min(p.N, n0 + per);
     int64_t mine = 0;
-    for (int n = n0; n < n1; ++n) mine += (seq_span(p.cu_q, p.cu_k, n, p.Tq, p.Tk).nq + ROWS - 1) / ROWS;
+    for (int n = n0; n < n1; ++n) mine += count(n);
     int64_t at = block_scan(mine) - mine;
     for (int n = n0; n < n1; ++n) {
-        base[n] = (int)(at < cap ? at : cap);
-        at += (seq_span(p.cu_q, p.cu_k, n, p.Tq, p.Tk).nq + ROWS - 1) / ROWS;
+        p.base[n] = (int)(at < cap ? at : cap);
+        at += count(n);
     }
     start[tid] = 0;
-    if (tid == 1023) {
-        const int all = (int)(at < cap ? at : cap);
-        base[p.N] = all;
-        p.ws[0] = 0;
-        p.ws[1] = all;
-        start[NB] = all;
-    }
+    if (tid == 1023) blocks = (int)(at < cap ? at : cap);
+    if (tid == 0) { work = 0; slots = 0; cuts = 0; listed = 0; }
     __syncthreads();
-    const int E = start[NB];
-    auto entry = [&](int e, int &bin) -> int2 {
+    const int E = blocks;
+    auto entry = [&](int e) {
         int lo = 0, hi = p.N - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (base[mid] <= e) lo = mid; else hi = mid - 1;
+            if (p.base[mid] <= e) lo = mid; else hi = mid - 1;
         }
-        const int qb = e - base[lo];
         const SeqSpan s = seq_span(p.cu_q, p.cu_k, lo, p.Tq, p.Tk);
-        bin = NB - 1 - min(key_tiles(s, qb * ROWS, ROWS, p.causal), NB - 1);
-        return make_int2(lo, qb);
+        const int i0 = (e - p.base[lo]) * ROWS;
+        Entry x;
+        x.row0 = (int)s.q0 + i0;
+        x.rows = min(ROWS, s.nq - i0);
+        x.key0 = (int)s.k0;
+        x.keys = s.nk;
+        x.off = p.causal ? i0 + s.nk - s.nq : s.nk - 1;
+        auto need = [&](int r0) {            // key tiles for the rows r0 .. r0 + 127
+            const int64_t seen = (int64_t)min(r0 + BQ, x.rows) + x.off;
+            return r0 >= x.rows || seen < 0 ? 0 : (int)(((seen < x.keys ? seen : x.keys) + BK - 1) / BK);
+        };
+        x.nA = need(0);
+        x.nB = need(BQ);
+        x.base = -1; x.part = 0; x.parts = 1;
+        return x;
     };
-    int bin;
-    for (int e = tid; e < E; e += 1024) { entry(e, bin); atomicAdd(&start[bin], 1); }
+    auto tiles_of = [](const Entry &x) { return max(x.nA, x.nB); };
+    // key tiles of all blocks, for one head
+    mine = 0;
+    for (int e = tid; e < E; e += 1024) mine += tiles_of(entry(e));
+    const int64_t sum = block_scan(mine);
+    if (tid == 1023) work = sum;
     __syncthreads();
-    const int count = start[tid];
-    const int incl = (int)block_scan(count);
-    start[tid] = incl - count;
-    __syncthreads();
-    int2 *list = list_of(p);
+    // Where the CTAs are few, a block with more key tiles than an SM's share is cut
+    // into parts of at most that: over all heads fewer than `sms` blocks and
+    // 2 sms parts.
+    int64_t share = (work * p.H + sms - 1) / sms;
+    if (share < MIN_PART) share = MIN_PART;
+    auto parts_of = [&](int tiles) { return may_cut && tiles > share ? (int)((tiles + share - 1) / share) : 1; };
+    auto bin_of = [&](int tiles) { return NB - 1 - min(tiles, NB - 1); };
     for (int e = tid; e < E; e += 1024) {
-        const int2 x = entry(e, bin);
-        list[atomicAdd(&start[bin], 1)] = x;
+        const int tiles = tiles_of(entry(e)), parts = parts_of(tiles);
+        for (int k = 0; k < parts; ++k)
+            atomicAdd(&start[bin_of((int)((int64_t)tiles * (k + 1) / parts - (int64_t)tiles * k / parts))], 1);
     }
+    __syncthreads();
+    const int c = start[tid];
+    const int incl = (int)block_scan(c);
+    start[tid] = incl - c;
+    if (tid == 1023) listed = incl;
+    __syncthreads();
+    for (int e = tid; e < E; e += 1024) {
+        const Entry whole = entry(e);
+        const int tiles = tiles_of(whole), parts = parts_of(tiles);
+        const int base = parts > 1 ? atomicAdd(&slots, parts) : -1;
+        for (int k = 0; k < parts; ++k) {
+            const int t0 = (int)((int64_t)tiles * k / parts), t1 = (int)((int64_t)tiles * (k + 1) / parts);
+            Entry x = whole;
+            x.key0 += t0 * BK;
+            x.keys -= t0 * BK;
+            x.off -= t0 * BK;
+            x.nA = max(min(x.nA, t1) - t0, 0);
+            x.nB = max(min(x.nB, t1) - t0, 0);
+            x.base = base; x.part = k; x.parts = parts;
+            p.entries[atomicAdd(&start[bin_of(t1 - t0)], 1)] = x;
+            if (parts > 1 && k == 0) p.cut[atomicAdd(&cuts, 1)] = x;
+        }
+    }
+    __syncthreads();
+    if (tid == 0) { p.head->status = 0; p.head->entries = listed; p.head->cut = cuts; }
 }
 
 __device__ __forceinline__ void mma_f16_tmem_a(uint32_t d, uint32_t a, uint64_t b, uint32_t id,
@@ -200,6 +269,12 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    // the first CTAs set up while the plan is still being made; of the later ones,
+    // those that the plan has no entry for end at once
+    if (blockIdx.x >= MAX_SMS) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if ((int)(blockIdx.x / p.H) >= p.head->entries) return;
+    }
     if (tid == 0) {
         for (int i = 0; i < 26; ++i) mbar_init(&full[i], i >= 20 && i < 24 ? 4 : 1);
         mbar_fence_init();
@@ -223,12 +298,9 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
         if (tid == 0 && !mbar_wait(drain, 0, 64)) *fail = FAIL_TIMEOUT;
         __syncthreads();
     }
-    if (e < p.ws[1] && !forced) {
-        const int2 ent = list_of(p)[e];
-        const SeqSpan s = seq_span(p.cu_q, p.cu_k, ent.x, p.Tq, p.Tk);
-        const int i0 = ent.y * ROWS;
-        const int nA = key_tiles(s, i0, BQ, p.causal), nB = key_tiles(s, i0 + BQ, BQ, p.causal);
-        const int n = max(nA, nB);
+    const Entry ent = p.entries[e];          // read beside the count
+    if (e < p.head->entries && !forced) {
+        const int nA = ent.nA, nB = ent.nB, n = max(nA, nB);
         if (warp == W_LOAD) {
             bool ok = true;
             int q = 0;                                      // blocks asked for
@@ -236,16 +308,16 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
                 if (elect_one()) {
                     if (nA > 0) {
                         mbar_arrive_expect_tx(&q_full[0], 3 * BLOCK);
-                        tma4(smb + SM_Q, &p.tm_q, 0, (int)s.q0 + i0, 0, h, &q_full[0]);
+                        tma4(smb + SM_Q, &p.tm_q, 0, ent.row0, 0, h, &q_full[0]);
                     }
                     if (nB > 0) {
                         mbar_arrive_expect_tx(&q_full[1], 3 * BLOCK);
-                        tma4(smb + SM_Q + 3 * BLOCK, &p.tm_q, 0, (int)s.q0 + i0 + BQ, 0, h, &q_full[1]);
+                        tma4(smb + SM_Q + 3 * BLOCK, &p.tm_q, 0, ent.row0 + BQ, 0, h, &q_full[1]);
                     }
                 }
                 __syncwarp();
                 for (int j = 0; ok && j < n; ++j) {
-                    const int t = (int)s.k0 + j * BK;
+                    const int t = ent.key0 + j * BK;
 #pragma unroll
                     for (int b = 0; b < PER; ++b) {
                         const int slot = q % RING;
@@ -338,9 +410,9 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
             // ---- softmax: two threads a row, each half of a key tile's columns ----
             const int x = warp >> 3, half = warp >> 2 & 1;  // tile, columns 64 half ..
             const int row = tid & 127;                      // row of the tile
-            const int i = i0 + x * BQ + row;                // query of the sequence
+            const int i = x * BQ + row;                     // query of the block
             const int nX = x ? nB : nA;
-            const int end = i < s.nq ? keys_seen(s, i, p.causal) : s.nk;
+            const int end = i < ent.rows ? min(i + ent.off + 1, ent.keys) : ent.keys;   // keys it sees
             // keys that every row of this warp sees
             const int warp_end = __reduce_min_sync(0xffffffffu, end);
             const uint32_t t_s = tmem_at(tmem, warp, S_COL + 128 * x);
@@ -385,7 +457,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
                 const bool stop = bar_or(pair, 64, !ok);
                 const float top = fmaxf(part, *theirs);
                 if (stop) { ok = false; break; }
-                const int valid = s.nk - j * BK;            // keys of the sequence in this tile
+                const int valid = ent.keys - j * BK;            // keys of the sequence in this tile
                 if (valid < BK) {
                     // values behind the sequence's end hold anything: zero them
                     // (each tile for its own product)
@@ -448,10 +520,12 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
             const float part = l2.x + l2.y;
             *mine = part;
             ok = !bar_or(pair, 64, !ok);
-            if (ok && i0 + x * BQ < s.nq) {
+            if (ok && x * BQ < ent.rows) {
                 const float l = part + *theirs;
-                const float r = l > 0.f ? 1.f / l : 0.f;
-                const int64_t at = (s.q0 + i) * p.H + h;
+                const bool whole = ent.base < 0;
+                const float r = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+                const int64_t at = (int64_t)(ent.row0 + i) * p.H + h;
+                const int64_t pr = ((int64_t)(ent.base + ent.part) * p.H + h) * ROWS + i;
                 fence_after_sync();
 #pragma unroll
                 for (int c = 0; c < 64; c += 16) {
@@ -464,31 +538,69 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
 #pragma unroll
                         for (int k = 0; k < 16; ++k) y[k] = 0.f;
                     }
-                    if (i < s.nq) {
+                    if (i < ent.rows && whole) {
                         uint32_t w[8];
 #pragma unroll
                         for (int k = 0; k < 8; ++k) w[k] = pack_bf(y[2 * k] * r, y[2 * k + 1] * r);
                         uint4 *to = reinterpret_cast<uint4 *>(p.o + at * DV + 64 * half + c);
                         to[0] = make_uint4(w[0], w[1], w[2], w[3]);
                         to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                    } else if (i < ent.rows) {
+                        float *to = p.part + pr * DV + 64 * half + c;
+#pragma unroll
+                        for (int k = 0; k < 16; k += 4) store4(to + k, make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]));
                     }
                 }
-                if (p.lse && half == 0 && i < s.nq)
-                    p.lse[at] = l > 0.f ? (m * sc + log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
+                if (half == 0 && i < ent.rows) {
+                    if (!whole) p.stat[pr] = make_float2(m * sc, l);
+                    else if (p.lse) p.lse[at] = l > 0.f ? (m * sc + log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
+                }
             }
         }
     }
     fence_before_sync();
     __syncthreads();
-    if (tid == 0 && *fail) atomicExch(p.ws, *fail);
+    if (tid == 0 && *fail) atomicExch(&p.head->status, *fail);
     if (warp == W_MMA) tmem_dealloc<512>(tmem);
+}
+
+// Adds up the parts of the blocks that are cut: a warp takes a query of a head,
+// a lane 4 channels.
+__global__ void __launch_bounds__(256) prefill_join_kernel(const PreParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int cuts = p.head->cut, lane = threadIdx.x & 31;
+    if (p.head->status) return;              // a CTA gave up: o stays as it is
+    const int total = cuts * p.H * (ROWS / 8);      // cuts x H is at most MAX_SMS
+    for (int job = blockIdx.x; job < total; job += gridDim.x) {
+        const int h = job / (ROWS / 8) % p.H, r = job % (ROWS / 8) * 8 + (threadIdx.x >> 5);
+        const Entry x = p.cut[job / (ROWS / 8) / p.H];
+        if (r >= x.rows) continue;
+        auto row_of = [&](int k) { return ((int64_t)(x.base + k) * p.H + h) * ROWS + r; };
+        float top = -CUDART_INF_F;
+        for (int k = lane; k < x.parts; k += 32) top = fmaxf(top, p.stat[row_of(k)].x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float ref = top == -CUDART_INF_F ? 0.f : top;
+        float sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = 0; k < x.parts; ++k) {
+            const float2 st = p.stat[row_of(k)];
+            const float4 y = load4(p.part + row_of(k) * DV + 4 * lane);
+            const float f = ex2(st.x - ref);
+            sum += f * st.y;
+            acc.x += f * y.x; acc.y += f * y.y; acc.z += f * y.z; acc.w += f * y.w;
+        }
+        const float f = sum > 0.f ? 1.f / sum : 0.f;
+        const int64_t at = (int64_t)(x.row0 + r) * p.H + h;
+        store4(p.o + at * DV + 4 * lane, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
+        if (p.lse && lane == 0) p.lse[at] = sum > 0.f ? (top + log2f(sum)) * CUDART_LN2_F : -CUDART_INF_F;
+    }
 }
 
 }  // namespace
 
-uint64_t prefill_tc_workspace_bytes(int32_t N, int64_t Tq) {
-    return ws_list(N) + 8ull * ((uint64_t)Tq / ROWS + N);
-}
+uint64_t prefill_tc_workspace_bytes(int32_t N, int64_t Tq) { return layout(N, Tq).bytes; }
 
 cudaError_t launch_prefill_tc(const PrefillArgs &a, cudaStream_t st) {
     static std::mutex mu;
@@ -520,7 +632,14 @@ cudaError_t launch_prefill_tc(const PrefillArgs &a, cudaStream_t st) {
             return cudaErrorInvalidValue;
     }
     p.cu_q = a.cu_q; p.cu_k = a.cu_k; p.o = (__nv_bfloat16 *)a.o; p.lse = a.lse;
-    p.ws = static_cast<int32_t *>(a.ws);
+    const Layout l = layout(a.N, a.Tq);
+    uint8_t *ws = static_cast<uint8_t *>(a.ws);
+    p.head = reinterpret_cast<Header *>(ws);
+    p.base = reinterpret_cast<int32_t *>(ws + l.base);
+    p.entries = reinterpret_cast<Entry *>(ws + l.entries);
+    p.cut = reinterpret_cast<Entry *>(ws + l.cut);
+    p.stat = reinterpret_cast<float2 *>(ws + l.stat);
+    p.part = reinterpret_cast<float *>(ws + l.part);
     p.Tq = a.Tq; p.Tk = a.Tk; p.N = a.N; p.H = a.H; p.causal = a.causal;
     // a negative scale flips the scores' sign; a zero one makes them (almost) equal
     const float s2 = a.scale * 1.4426950408889634f;
@@ -536,13 +655,30 @@ cudaError_t launch_prefill_tc(const PrefillArgs &a, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const int cap = (int)(a.Tq / ROWS + a.N);
-    e = cudaLaunchKernelEx(&cfg, plan_kernel, p, cap);
+    int sms = 1;
+    e = sm_count(&sms);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3((unsigned)cap * (unsigned)a.H);
+    if (sms > MAX_SMS) sms = MAX_SMS;
+    const int64_t cap = a.Tq / ROWS + a.N;                  // blocks of queries, at most
+    // Cutting pays where (queries / 256) x heads leaves the SMs fewer than two
+    // CTAs each: two sequences of up to 3000 queries over up to 8000 keys, one
+    // head: 106 us whole, 47 us cut; one prompt of 4096 tokens, four heads: 60 and
+    // 46 us.  Where nothing is cut after all it costs 3 to 5 us (a join kernel and
+    // CTAs with nothing to do), and with more CTAs the longest-first order balances
+    // by itself (8 packed prompts, 864 CTAs: 125 us).
+    const bool may_cut = a.Tq / ROWS * a.H < 2 * sms && a.H < 2 * sms && a.Tk > MIN_PART * BK;
+    e = cudaLaunchKernelEx(&cfg, plan_kernel, p, (int)cap, sms, (int)may_cut);
+    if (e != cudaSuccess) return e;
+    // a CTA per block and head, and one for each further part
+    cfg.gridDim = dim3((unsigned)(cap * a.H + (may_cut ? SLOTS : 0)));
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = SM_BYTES;
-    return cudaLaunchKernelEx(&cfg, prefill_kernel, p);
+    e = cudaLaunchKernelEx(&cfg, prefill_kernel, p);
+    if (e != cudaSuccess || !may_cut) return e;
+    cfg.gridDim = dim3(8 * (unsigned)sms);                  // all resident: without a cut they end at once
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, prefill_join_kernel, p);
 }
 
 }  // namespace mla

@@ -145,6 +145,19 @@ def test_prefill(dtype, causal, case):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("lens", [
+    [(1, 6000)], [(129, 5000)], [(300, 2500), (2, 1100)], [(1000, 1000), (40, 900)],
+    [(256, 256 + 128 * k) for k in (1, 3, 7, 12)],
+])
+def test_prefill_few_queries_many_keys(dtype, lens):
+    """Few blocks of queries: their keys are cut into parts and joined."""
+    for causal in (True, False):
+        q, kv, kr, cu_q, cu_k = _prefill_inputs(lens, 2, dtype, seed=len(lens))
+        o, lse = _call_prefill(q, kv, kr, cu_q, cu_k, causal)
+        _check_prefill(lens, q, kv, kr, causal, dtype, o, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_prefill_other_scales(dtype):
     lens = [(150, 200)]
     for scale in (0.0, -0.05, 0.5):
