@@ -297,61 +297,64 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                                     *reinterpret_cast<uint4 *>(r + ch * 1024 + e * 16) = make_uint4(0, 0, 0, 0);
                         }
                     }
-                    // maximum over the warp's 16 tokens: each exchange halves the
-                    // heads a lane keeps, lane bits 4, 3, 2 choosing bits of v
-                    float t[V];
-#pragma unroll
-                    for (int v = 0; v < V; ++v) t[v] = fmaxf(x[(v >> 1) * 4 + (v & 1)], x[(v >> 1) * 4 + 2 + (v & 1)]);
-                    int keep = 0;
-#pragma unroll
-                    for (int bit = 16, half = V / 2; bit >= 4; bit >>= 1, half >>= 1) {
-                        if (half >= 1) {
-                            const bool up = lane & bit;
-#pragma unroll
-                            for (int v = 0; v < V / 2; ++v)
-                                if (v < half) {
-                                    const float give = up ? t[v] : t[v + half], have = up ? t[v + half] : t[v];
-                                    t[v] = fmaxf(have, __shfl_xor_sync(0xffffffffu, give, bit));
-                                }
-                            keep += up ? half : 0;
-                        } else {
-                            t[0] = fmaxf(t[0], __shfl_xor_sync(0xffffffffu, t[0], bit));
-                        }
-                    }
-                    float *rd = red_w + (k & 1) * 4 * NW;
-                    rd[w4 * NW + (keep >> 1) * 8 + 2 * (lane & 3) + (keep & 1)] = t[0];
-                    stop = bar_or(bar, 128, !ok);
-                    if (stop) break;
-                    bool grow = false;
-                    float mx[V];
-#pragma unroll
-                    for (int v = 0; v < V; v += 2) {
-                        const int at = (v >> 1) * 8 + 2 * (lane & 3);
-                        float2 y = *reinterpret_cast<const float2 *>(rd + at);
-#pragma unroll
-                        for (int q = 1; q < 4; ++q) {
-                            const float2 z = *reinterpret_cast<const float2 *>(rd + q * NW + at);
-                            y.x = fmaxf(y.x, z.x); y.y = fmaxf(y.y, z.y);
-                        }
-                        mx[v] = y.x; mx[v + 1] = y.y;
-                        grow |= y.x > m[v] + RESCALE || y.y > m[v + 1] + RESCALE;
-                    }
                     // The reference maximum is raised only when a score exceeds it by
                     // more than 2^8: until then weights stay below 2^8, which float32
-                    // sums and bf16 weights hold as well as ones below 1, and the
-                    // output in tensor memory need not be rescaled.  All warps of the
-                    // warpgroup see the same maxima and decide alike.
-                    if (__any_sync(0xffffffffu, grow)) {
-                        const bool scale_o = i > w.lo;
+                    // sums and bf16 weights hold as well as ones below 1, and neither
+                    // need the warps tell each other their maxima nor the output in
+                    // tensor memory be rescaled.
+                    bool raise = i == w.lo;
+                    if (!raise) {
+                        bool over = !ok;
 #pragma unroll
-                        for (int v = 0; v < V; ++v) {
-                            const float to = fmaxf(m[v], mx[v]);
-                            const float f = to == -CUDART_INF_F ? 1.f : ex2(m[v] - to);
-                            l[v] *= f;
-                            m[v] = to;
-                            if (w4 == 0 && lane < 4) ca[(v >> 1) * 8 + 2 * lane + (v & 1)] = f;
+                        for (int e = 0; e < NW / 2; ++e) over |= x[e] > m[(e >> 2) * 2 + (e & 1)] + RESCALE;
+                        raise = bar_or(bar, 128, over);
+                    }
+                    if (raise) {
+                        // maximum over the warp's 16 tokens: each exchange halves the
+                        // heads a lane keeps, lane bits 4, 3, 2 choosing bits of v
+                        float t[V];
+#pragma unroll
+                        for (int v = 0; v < V; ++v) t[v] = fmaxf(x[(v >> 1) * 4 + (v & 1)], x[(v >> 1) * 4 + 2 + (v & 1)]);
+                        int keep = 0;
+#pragma unroll
+                        for (int bit = 16, half = V / 2; bit >= 4; bit >>= 1, half >>= 1) {
+                            if (half >= 1) {
+                                const bool up = lane & bit;
+#pragma unroll
+                                for (int v = 0; v < V / 2; ++v)
+                                    if (v < half) {
+                                        const float give = up ? t[v] : t[v + half], have = up ? t[v + half] : t[v];
+                                        t[v] = fmaxf(have, __shfl_xor_sync(0xffffffffu, give, bit));
+                                    }
+                                keep += up ? half : 0;
+                            } else {
+                                t[0] = fmaxf(t[0], __shfl_xor_sync(0xffffffffu, t[0], bit));
+                            }
                         }
-                        if (scale_o) {
+                        float *rd = red_w + (k & 1) * 4 * NW;
+                        rd[w4 * NW + (keep >> 1) * 8 + 2 * (lane & 3) + (keep & 1)] = t[0];
+                        stop = bar_or(bar, 128, !ok);
+                        if (stop) break;
+#pragma unroll
+                        for (int v = 0; v < V; v += 2) {
+                            const int at = (v >> 1) * 8 + 2 * (lane & 3);
+                            float2 y = *reinterpret_cast<const float2 *>(rd + at);
+#pragma unroll
+                            for (int q = 1; q < 4; ++q) {
+                                const float2 z = *reinterpret_cast<const float2 *>(rd + q * NW + at);
+                                y.x = fmaxf(y.x, z.x); y.y = fmaxf(y.y, z.y);
+                            }
+                            const float top[2] = {y.x, y.y};
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const float to = fmaxf(m[v + j], top[j]);
+                                const float f = to == -CUDART_INF_F ? 1.f : ex2(m[v + j] - to);
+                                l[v + j] *= f;
+                                m[v + j] = to;
+                                if (w4 == 0 && lane < 4) ca[at + j] = f;
+                            }
+                        }
+                        if (i > w.lo) {
                             ok = wait_or_fail(o_full, (k - 1) & 1, fail);
                             bar_sync(bar, 128);             // ca
                             fence_after_sync();
