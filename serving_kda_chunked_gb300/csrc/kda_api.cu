@@ -350,7 +350,7 @@ kda_status kda_mla_prefill(const void *q, const void *kv, const void *k_r, const
     const uint64_t need = kda_mla_prefill_workspace_size(N, Tq, H, dtype);
     if (need && (!workspace || workspace_bytes < need || !aligned16(workspace)))
         return KDA_ERR_INVALID_ARG;
-    if (H > 65535 || (Tq / 64 + N) * (int64_t)H > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
+    if (H > 65535 || (Tq / 32 + N) * (int64_t)H > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
     const kda_status dst = check_device_ptrs({q, kv, k_r, cu_q, cu_k, o, lse, need ? workspace : nullptr});
     if (dst != KDA_OK) return dst;
     kda::mla::PrefillArgs a;

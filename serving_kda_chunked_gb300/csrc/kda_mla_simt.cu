@@ -19,14 +19,25 @@ __device__ __forceinline__ float warp_sum(float x) {
 }
 
 // ---- expanded form -------------------------------------------------------------
-// One block per (64 queries of a sequence, head, part of their keys); 256
-// threads, each a 4 x 4 piece of the 64 x 64 scores and a 4 x 8 piece of the
-// 64 x 128 output: 64 FMAs for 12 shared-memory wavefronts, so the FMA pipes
-// bound it.  Keys arrive with asynchronous copies one tile ahead, values while
-// the scores are computed.  With few (queries, head) blocks the keys are cut
-// into up to SPLITS parts, whose unnormalised results a second kernel joins.
-constexpr int BQ = 64, BK = 64, LDQ = DQK + 4, LDP = BK + 4, SPLITS = 8, PTHREADS = 256;
-constexpr int PRE_FLOATS = (BQ + 2 * BK) * LDQ + BK * DV + BQ * LDP;
+// One block per (32 queries of a sequence, head, part of their keys), four warps.
+// A 16-byte shared-memory read of a warp costs four wavefronts, shared addresses
+// or not, so a thread needs large pieces: in the scores a warp takes 48 of the
+// 192 channels of the whole 32 x 32 tile (8 x 4 a thread: 128 FMAs for 12 reads)
+// and the warps' sums are added in shared memory; in the output a warp takes 8
+// of the tile's 32 keys for the whole 32 x 128 (8 x 16 a thread: 128 FMAs for 6
+// reads), and the warps' outputs are added once, at the end.  Keys arrive with
+// asynchronous copies one tile ahead, values while the scores are computed; two
+// blocks an SM fill each other's gaps.  (With 4 x 4 and 2 x 4 pieces, shared
+// memory held three prompts up to 777 tokens with four heads at 95 and 92 us.)
+// With few (queries, head) blocks the keys are cut into up to SPLITS parts,
+// whose unnormalised results a second kernel joins.
+constexpr int BQ = 32, BK = 32, LDQ = DQK + 4, LDP = BQ + 4, SPLITS = 8, PTHREADS = 128;
+constexpr int PRE_FLOATS = (BQ + 2 * BK) * LDQ + BK * DV + BK * LDP + BQ;
+// partial scores of a warp: element (row, key)
+__device__ __forceinline__ int red_at(int w, int row, int key) {
+    return w * (BQ * 36 + 32) + row * 36 + (row >> 3) * 8 + key;
+}
+static_assert(4 * (BQ * 36 + 32) <= BK * LDQ && 4 * BQ * DV <= (BQ + 2 * BK) * LDQ, "reused buffers");
 
 __device__ __forceinline__ void copy16_or_zero(float *dst, const float *src, bool copy) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
@@ -39,36 +50,58 @@ template <int N> __device__ __forceinline__ void copy_wait() {
 
 struct PreSplit { float *part, *stat; int parts; };     // [parts][Tq][H]: output (128), then maximum and sum
 
-// What a block works on: sequence span, first query, keys of its part.
+// What a block works on: sequence span, first query, keys of its part.  A warp
+// looks at 32 sequences at a time.
 struct PreUnit { SeqSpan s; int i0, j0, j1, parts; };
 __device__ __forceinline__ bool pre_unit(const PrefillArgs &p, int tile, int part, int parts, PreUnit &u) {
-    int n = 0;
-    for (; n < p.N; ++n) {               // every sequence has ceil(nq / 64) tiles
-        u.s = seq_span(p.cu_q, p.cu_k, n, p.Tq, p.Tk);
-        const int tiles = (u.s.nq + BQ - 1) / BQ;
-        if (tile < tiles) break;
-        tile -= tiles;
+    const int lane = threadIdx.x & 31;
+    bool found = false;
+    for (int n0 = 0; n0 < p.N && !found; n0 += 32) {     // every sequence has ceil(nq / 32) tiles
+        SeqSpan s{0, 0, 0, 0};
+        if (n0 + lane < p.N) s = seq_span(p.cu_q, p.cu_k, n0 + lane, p.Tq, p.Tk);
+        const int64_t mine = (s.nq + BQ - 1) / BQ;
+        int64_t incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        const uint32_t in = __ballot_sync(0xffffffffu, tile < incl);
+        if (in) {
+            const int l = __ffs(in) - 1;
+            u.s.q0 = __shfl_sync(0xffffffffu, s.q0, l);
+            u.s.k0 = __shfl_sync(0xffffffffu, s.k0, l);
+            u.s.nq = __shfl_sync(0xffffffffu, s.nq, l);
+            u.s.nk = __shfl_sync(0xffffffffu, s.nk, l);
+            tile -= (int)__shfl_sync(0xffffffffu, incl - mine, l);
+            found = true;
+        } else {
+            tile -= (int)__shfl_sync(0xffffffffu, incl, 31);
+        }
     }
-    if (n == p.N) return false;
+    if (!found) return false;
     u.i0 = tile * BQ;
     const int last = min(u.i0 + BQ, u.s.nq) - 1;         // keys seen by the tile's last query
     const int64_t seen = p.causal ? (int64_t)last + u.s.nk - u.s.nq + 1 : u.s.nk;
     const int hi = seen < 0 ? 0 : (seen > u.s.nk ? u.s.nk : (int)seen);
     int len = ((hi + parts - 1) / parts + BK - 1) / BK * BK;
-    len = max(len, 2 * BK);              // a part is worth two tiles at least
+    len = max(len, 4 * BK);              // a part is worth four tiles at least
     u.parts = max(1, (hi + len - 1) / len);
     u.j0 = part * len;
     u.j1 = min(hi, u.j0 + len);
     return part < u.parts;
 }
 
-__global__ void __launch_bounds__(PTHREADS) prefill_simt_kernel(const PrefillArgs p, const PreSplit sp) {
+__global__ void __launch_bounds__(PTHREADS, 2) prefill_simt_kernel(const PrefillArgs p, const PreSplit sp) {
     extern __shared__ __align__(16) float smf[];
-    float *Qs = smf;                       // [64][LDQ]
-    float *Ks = Qs + BQ * LDQ;             // [2][64][LDQ]
-    float *Vs = Ks + 2 * BK * LDQ;         // [64][128]
-    float *Ps = Vs + BK * DV;              // [64 queries][LDP]
+    float *Qs = smf;                       // [32][LDQ]
+    float *Ks = Qs + BQ * LDQ;             // [2][32][LDQ]
+    float *Vs = Ks + 2 * BK * LDQ;         // [32][128]
+    float *Pt = Vs + BK * DV;              // [32 keys][LDP], query fastest
+    float *fs = Pt + BK * LDP;             // [32] factors per query
     const int tid = threadIdx.x, h = blockIdx.y, H = p.H;
+    if (sp.parts > 1 && tid == 0 && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
+        *static_cast<int32_t *>(p.ws) = 0;  // no wait here can give up: the call's status is clear
     PreUnit u;                             // long blocks first: the last queries see the most keys
     if (!pre_unit(p, gridDim.x - 1 - blockIdx.x, blockIdx.z, sp.parts, u)) return;
     const SeqSpan s = u.s;
@@ -101,141 +134,178 @@ __global__ void __launch_bounds__(PTHREADS) prefill_simt_kernel(const PrefillArg
         load_keys(u.j0, 0);
         load_values(u.j0);
     }
-    const int tr = tid / 16, tc = tid % 16;          // rows 4 tr .., keys tc + 16 k
+    const int lane = tid & 31, warp = tid >> 5;
+    const int lr = lane / 8, lc = lane % 8;          // rows 8 lr .., keys lc + 8 k or channels 32 g + 4 lc ..
+    const int row = tid / 4, part = tid % 4;         // softmax: keys 8 part .. of a row
     const float sl = p.scale * 1.4426950408889634f;
-    float m[4], l[4], acc[4][8];
+    const int64_t qi = u.i0 + row;
+    const int64_t end = p.causal ? qi + s.nk - s.nq + 1 : s.nk;           // keys the row sees
+    float m = -CUDART_INF_F, l = 0.f, acc[8][16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        m[i] = -CUDART_INF_F; l[i] = 0.f;
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
-    }
+        for (int j = 0; j < 16; ++j) acc[i][j] = 0.f;
     int buf = 0;
     for (int j0 = u.j0; j0 < u.j1; j0 += BK, buf ^= 1) {
         if (j0 + BK < u.j1) load_keys(j0 + BK, buf ^ 1); else copy_commit();
         copy_wait<2>();                              // these keys (and the queries)
         __syncthreads();
-        const float *K = Ks + buf * BK * LDQ;
-        float sc[4][4] = {};
+        float *K = Ks + buf * BK * LDQ;
+        float sc[8][4] = {};
 #pragma unroll 2
-        for (int c = 0; c < DQK; c += 4) {
-            float4 a[4], b[4];
+        for (int c = warp * 48; c < warp * 48 + 48; c += 4) {
+            float4 a[8], b[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) a[i] = load4(Qs + (4 * tr + i) * LDQ + c);
+            for (int i = 0; i < 8; ++i) a[i] = load4(Qs + (8 * lr + i) * LDQ + c);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) b[k] = load4(K + (tc + 16 * k) * LDQ + c);
+            for (int k = 0; k < 4; ++k) b[k] = load4(K + (lc + 8 * k) * LDQ + c);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 8; ++i)
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    sc[i][k] += a[i].x * b[k].x + a[i].y * b[k].y + a[i].z * b[k].z + a[i].w * b[k].w;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t qi = u.i0 + 4 * tr + i;
-            const int64_t end = p.causal ? qi + s.nk - s.nq + 1 : s.nk;   // keys it sees
-            float top = m[i];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int kj = j0 + tc + 16 * k;
-                sc[i][k] = kj < end && kj < u.j1 ? sc[i][k] * sl : -CUDART_INF_F;
-                top = fmaxf(top, sc[i][k]);
-            }
-#pragma unroll
-            for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float ref = top == -CUDART_INF_F ? 0.f : top;
-            const float f = exp2f(m[i] - ref);
-            float sum = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                sc[i][k] = exp2f(sc[i][k] - ref);
-                sum += sc[i][k];
-                Ps[(4 * tr + i) * LDP + tc + 16 * k] = sc[i][k];
-            }
-            l[i] = l[i] * f + sum;                   // this thread's four keys
-            m[i] = top;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) acc[i][k] *= f;
-        }
-        copy_wait<1>();                              // these values
-        __syncthreads();
-#pragma unroll 2
-        for (int k = 0; k < BK; k += 4) {
-            float4 a[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) a[i] = load4(Ps + (4 * tr + i) * LDP + k);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float4 v0 = load4(Vs + (k + e) * DV + 4 * tc), v1 = load4(Vs + (k + e) * DV + 64 + 4 * tc);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float w = e == 0 ? a[i].x : (e == 1 ? a[i].y : (e == 2 ? a[i].z : a[i].w));
-                    acc[i][0] += w * v0.x; acc[i][1] += w * v0.y; acc[i][2] += w * v0.z; acc[i][3] += w * v0.w;
-                    acc[i][4] += w * v1.x; acc[i][5] += w * v1.y; acc[i][6] += w * v1.z; acc[i][7] += w * v1.w;
+                for (int k = 0; k < 4; ++k) {
+                    sc[i][k] += a[i].x * b[k].x;
+                    sc[i][k] += a[i].y * b[k].y;
+                    sc[i][k] += a[i].z * b[k].z;
+                    sc[i][k] += a[i].w * b[k].w;
                 }
+        }
+        __syncthreads();                             // these keys have been read: their place takes the sums
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) K[red_at(warp, 8 * lr + i, lc + 8 * k)] = sc[i][k];
+        __syncthreads();
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+            float4 y = load4(K + red_at(0, row, 8 * part + e));
+#pragma unroll
+            for (int w = 1; w < 4; ++w) {
+                const float4 z = load4(K + red_at(w, row, 8 * part + e));
+                y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;
             }
+            x[e] = y.x; x[e + 1] = y.y; x[e + 2] = y.z; x[e + 3] = y.w;
+        }
+        float top = -CUDART_INF_F;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int kj = j0 + 8 * part + e;
+            x[e] = kj < end && kj < u.j1 ? x[e] * sl : -CUDART_INF_F;
+            top = fmaxf(top, x[e]);
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // raised only by more than 2^8, so that the outputs are rarely rescaled
+        const bool raise = top > m + 8.f;
+        const float to = raise ? top : m, ref = to == -CUDART_INF_F ? 0.f : to;
+        const float f = raise ? exp2f(m - ref) : 1.f;
+        m = to;
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float w = exp2f(x[e] - ref);
+            sum += w;
+            Pt[(8 * part + e) * LDP + row] = w;
+        }
+        l = l * f + sum;                             // this thread's eight keys
+        if (part == 0) fs[row] = f;
+        copy_wait<1>();                              // these values
+        if (__syncthreads_or(raise)) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float g = fs[8 * lr + i];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) acc[i][k] *= g;
+            }
+        }
+#pragma unroll 2
+        for (int k = warp * 8; k < warp * 8 + 8; ++k) {
+            const float4 a0 = load4(Pt + k * LDP + 8 * lr), a1 = load4(Pt + k * LDP + 8 * lr + 4);
+            const float w[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+            float4 v[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) v[g] = load4(Vs + k * DV + 32 * g + 4 * lc);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    acc[i][4 * g] += w[i] * v[g].x; acc[i][4 * g + 1] += w[i] * v[g].y;
+                    acc[i][4 * g + 2] += w[i] * v[g].z; acc[i][4 * g + 3] += w[i] * v[g].w;
+                }
         }
         __syncthreads();
         if (j0 + BK < u.j1) load_values(j0 + BK); else copy_commit();
     }
     copy_wait<0>();
+    __syncthreads();
+    // the four warps' outputs, over the queries and keys
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float sum = l[i];
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int of = 1; of < 16; of <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, of);
-        const int qi = u.i0 + 4 * tr + i;
-        if (qi >= s.nq) continue;
-        const int64_t at = (s.q0 + qi) * H + h;
-        const bool whole = u.parts == 1;
-        const float r = whole ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
-        const int64_t to = whole ? at : (int64_t)blockIdx.z * p.Tq * H + at;
-        float *o = (whole ? (float *)p.o : sp.part) + to * DV;
-        store4(o + 4 * tc, make_float4(acc[i][0] * r, acc[i][1] * r, acc[i][2] * r, acc[i][3] * r));
-        store4(o + 64 + 4 * tc, make_float4(acc[i][4] * r, acc[i][5] * r, acc[i][6] * r, acc[i][7] * r));
-        if (tc == 0) {
-            if (!whole) *reinterpret_cast<float2 *>(sp.stat + 2 * to) = make_float2(m[i], sum);
-            else if (p.lse) p.lse[at] = sum > 0.f ? (m[i] + log2f(sum)) * CUDART_LN2_F : -CUDART_INF_F;
+        for (int g = 0; g < 4; ++g)
+            store4(smf + (warp * BQ + 8 * lr + i) * DV + 32 * g + 4 * lc,
+                   make_float4(acc[i][4 * g], acc[i][4 * g + 1], acc[i][4 * g + 2], acc[i][4 * g + 3]));
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    const bool whole = u.parts == 1;
+    const int64_t at = (s.q0 + qi) * H + h, to = whole ? at : (int64_t)blockIdx.z * p.Tq * H + at;
+    if (part == 0 && qi < s.nq) {
+        if (!whole) *reinterpret_cast<float2 *>(sp.stat + 2 * to) = make_float2(m, l);
+        else if (p.lse) p.lse[at] = l > 0.f ? (m + log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
+    }
+    if (part == 0) fs[row] = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+    __syncthreads();
+    for (int e = tid; e < BQ * DV / 4; e += PTHREADS) {
+        const int r = e / (DV / 4), c = e % (DV / 4) * 4;
+        if (u.i0 + r >= s.nq) break;                 // rows ascend
+        float4 y = load4(smf + r * DV + c);
+#pragma unroll
+        for (int w = 1; w < 4; ++w) {
+            const float4 z = load4(smf + (w * BQ + r) * DV + c);
+            y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;
         }
+        const float g = fs[r];
+        const int64_t out = (whole ? 0 : (int64_t)blockIdx.z * p.Tq * H) + (s.q0 + u.i0 + r) * H + h;
+        store4((whole ? (float *)p.o : sp.part) + out * DV + c, make_float4(y.x * g, y.y * g, y.z * g, y.w * g));
     }
 }
 
-// Joins the parts of (64 queries, head); a warp takes 8 queries, a lane 4 channels.
-__global__ void __launch_bounds__(PTHREADS) prefill_join_kernel(const PrefillArgs p, const PreSplit sp) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y;
+// Joins the parts of (32 queries, head); a warp takes a query, a lane 4 channels.
+__global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillArgs p, const PreSplit sp) {
+    const int lane = threadIdx.x & 31, r = blockIdx.z * 8 + (threadIdx.x >> 5), h = blockIdx.y;
     PreUnit u;
-    if (!pre_unit(p, blockIdx.x, 0, sp.parts, u) || u.parts == 1) return;
-    for (int r = warp; r < BQ && u.i0 + r < u.s.nq; r += 8) {
-        const int64_t at = (u.s.q0 + u.i0 + r) * p.H + h, step = p.Tq * p.H;
-        float2 st[SPLITS];
-        float4 y[SPLITS];
-        float top = -CUDART_INF_F;
+    if (!pre_unit(p, blockIdx.x, 0, sp.parts, u) || u.parts == 1 || u.i0 + r >= u.s.nq) return;
+    const int64_t at = (u.s.q0 + u.i0 + r) * p.H + h, step = p.Tq * p.H;
+    float2 st[SPLITS];
+    float4 y[SPLITS];
+    float top = -CUDART_INF_F;
 #pragma unroll
-        for (int k = 0; k < SPLITS; ++k)
-            if (k < u.parts) {
-                st[k] = *reinterpret_cast<const float2 *>(sp.stat + 2 * (k * step + at));
-                y[k] = load4(sp.part + (k * step + at) * DV + 4 * lane);
-                top = fmaxf(top, st[k].x);
-            }
-        const float ref = top == -CUDART_INF_F ? 0.f : top;
-        float sum = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < SPLITS; ++k)
+        if (k < u.parts) {
+            st[k] = *reinterpret_cast<const float2 *>(sp.stat + 2 * (k * step + at));
+            y[k] = load4(sp.part + (k * step + at) * DV + 4 * lane);
+        }
 #pragma unroll
-        for (int k = 0; k < SPLITS; ++k)
-            if (k < u.parts) {
-                const float f = exp2f(st[k].x - ref);
-                sum += f * st[k].y;
-                acc.x += f * y[k].x; acc.y += f * y[k].y; acc.z += f * y[k].z; acc.w += f * y[k].w;
-            }
-        const float f = sum > 0.f ? 1.f / sum : 0.f;
-        store4((float *)p.o + at * DV + 4 * lane, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
-        if (p.lse && lane == 0) p.lse[at] = sum > 0.f ? (top + log2f(sum)) * CUDART_LN2_F : -CUDART_INF_F;
-    }
+    for (int k = 0; k < SPLITS; ++k)
+        if (k < u.parts) top = fmaxf(top, st[k].x);
+    const float ref = top == -CUDART_INF_F ? 0.f : top;
+    float sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < SPLITS; ++k)
+        if (k < u.parts) {
+            const float f = exp2f(st[k].x - ref);
+            sum += f * st[k].y;
+            acc.x += f * y[k].x; acc.y += f * y[k].y; acc.z += f * y[k].z; acc.w += f * y[k].w;
+        }
+    const float f = sum > 0.f ? 1.f / sum : 0.f;
+    store4((float *)p.o + at * DV + 4 * lane, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
+    if (p.lse && lane == 0) p.lse[at] = sum > 0.f ? (top + log2f(sum)) * CUDART_LN2_F : -CUDART_INF_F;
 }
 
-// Parts per (queries, head) block: enough for about four blocks an SM.
+// Parts per (queries, head) block: enough for about eight blocks an SM.
 int prefill_parts(int32_t N, int64_t Tq, int32_t H) {
-    const int64_t blocks = (Tq / BQ + N) * H, want = (608 + blocks - 1) / blocks;
+    const int64_t blocks = (Tq / BQ + N) * H, want = (1216 + blocks - 1) / blocks;
     return (int)(want < 1 ? 1 : (want > SPLITS ? SPLITS : want));
 }
 
@@ -378,15 +448,11 @@ cudaError_t launch_prefill_simt(const PrefillArgs &a, cudaStream_t st) {
     sp.parts = prefill_parts(a.N, a.Tq, a.H);
     sp.part = reinterpret_cast<float *>((uint8_t *)a.ws + 256);
     sp.stat = sp.part + (int64_t)sp.parts * a.Tq * a.H * DV;
-    if (sp.parts > 1) {                     // no wait here can give up: the status is clear
-        e = cudaMemsetAsync(a.ws, 0, sizeof(int32_t), st);
-        if (e != cudaSuccess) return e;
-    }
     const unsigned tiles = (unsigned)(a.Tq / BQ + a.N);     // at most
     prefill_simt_kernel<<<dim3(tiles, a.H, sp.parts), PTHREADS, PRE_FLOATS * sizeof(float), st>>>(a, sp);
     e = cudaGetLastError();
     if (e != cudaSuccess || sp.parts == 1) return e;
-    prefill_join_kernel<<<dim3(tiles, a.H), PTHREADS, 0, st>>>(a, sp);
+    prefill_join_kernel<<<dim3(tiles, a.H, BQ / 8), 256, 0, st>>>(a, sp);
     return cudaGetLastError();
 }
 
