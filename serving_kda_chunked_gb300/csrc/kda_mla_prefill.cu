@@ -39,22 +39,32 @@ namespace kda {
 namespace mla {
 namespace {
 
-constexpr int BQ = 128, BK = 128, ROWS = 2 * BQ;            // rows a tile, keys a tile, rows a CTA
-constexpr int THREADS = 576, W_MMA = 16, W_LOAD = 17;
-constexpr uint32_t BLOCK = 16384;
+constexpr int BQ = 128;                                     // rows a tile
+constexpr uint32_t QBLOCK = BQ * 128;                       // 64 channels of a query tile
 constexpr int RING = 8, PER = 5;                            // blocks in the ring, blocks a key tile
-constexpr uint32_t SM_Q = 0, SM_RING = 6 * BLOCK, SM_MISC = SM_RING + RING * BLOCK,
-                   SM_SWAP = SM_MISC + 256, SM_BYTES = SM_SWAP + 4 * 128 * 4;
-static_assert(SM_BYTES <= 232448, "shared memory");
-constexpr uint32_t S_COL = 0, O_COL = 256;                  // + 128 for tile B
+
+// TILES = 2: as above.  TILES = 1, for short sequences: one query tile, key tiles
+// of 64, one softmax thread a row, two CTAs an SM.  Nothing overlaps inside such a
+// CTA, but one CTA's start and end run beside the other's products; with few key
+// tiles these cost more than the lost overlap and the second reading of the keys.
+template <int TILES> struct Cfg {
+    static constexpr int ROWS = TILES * BQ, BK = 64 * TILES;
+    static constexpr int SPLIT = TILES;                     // softmax threads a row; each has 64 of a key tile's columns
+    static constexpr int W_MMA = 4 * SPLIT * TILES, W_LOAD = W_MMA + 1, THREADS = 32 * (W_LOAD + 1);
+    static constexpr uint32_t BLOCK = BK * 128;             // 64 channels of a key tile, or BK / 2 tokens of a value tile
+    static constexpr uint32_t SM_RING = TILES * 3 * QBLOCK, SM_MISC = SM_RING + RING * BLOCK,
+                              SM_SWAP = SM_MISC + 256, SM_BYTES = SM_SWAP + (SPLIT == 2 ? 2 * TILES * BQ * 4 : 0);
+    static constexpr uint32_t O_COL = BQ * TILES, TCOLS = 256 * TILES;   // scores of tile x at column 128 x
+};
+static_assert(Cfg<2>::SM_BYTES <= 232448 && 2 * (Cfg<1>::SM_BYTES + 1024) <= 233472, "shared memory");
 constexpr float RESCALE = 8.f;
 
 constexpr int MAX_SMS = 160;
 constexpr int SLOTS = 2 * MAX_SMS;           // parts with results of their own, over all heads
 constexpr int CUTS = MAX_SMS;                // blocks that are cut, over all heads
-constexpr int MIN_PART = 4;                  // key tiles that are worth a part
+constexpr int MIN_PART = 512;                // keys that are worth a part
 
-// A block of up to 256 queries of a sequence, or a part of its keys; one CTA per
+// A block of up to ROWS queries of a sequence, or a part of its keys; one CTA per
 // head.  Everything a CTA needs in one read.
 struct __align__(16) Entry {
     int32_t row0, rows;                      // first query among all, queries
@@ -66,18 +76,18 @@ struct __align__(16) Entry {
 };
 // workspace: header | first block of each sequence | entries, most keys first |
 // blocks that are cut (as their first part) | partial results per slot:
-// [256][2] (maximum in log2 units, sum) and [256][128]
+// [ROWS][2] (maximum in log2 units, sum) and [ROWS][128]
 struct Header { int32_t status, entries, cut; };
 struct Layout { uint64_t base, entries, cut, stat, part, bytes; };
 __host__ __device__ inline Layout layout(int64_t N, int64_t Tq) {
-    const uint64_t cap = (uint64_t)Tq / ROWS + N;
+    const uint64_t cap = (uint64_t)Tq / BQ + N;             // blocks of either size, at most
     Layout l;
     l.base = 256;
     l.entries = (l.base + 4 * ((uint64_t)N + 1) + 255) / 256 * 256;
     l.cut = l.entries + (cap + SLOTS) * sizeof(Entry);
     l.stat = l.cut + CUTS * sizeof(Entry);
-    l.part = l.stat + (uint64_t)SLOTS * ROWS * 8;
-    l.bytes = l.part + (uint64_t)SLOTS * ROWS * DV * 4;
+    l.part = l.stat + (uint64_t)SLOTS * 2 * BQ * 8;
+    l.bytes = l.part + (uint64_t)SLOTS * 2 * BQ * DV * 4;
     return l;
 }
 
@@ -101,8 +111,9 @@ struct PreParams {
 // first (CTAs start in list order, so the longest do not end last), and clears
 // the status.  At most `cap` blocks: offsets that overlap or run backwards lose
 // the rest.
+template <int TILES>
 __global__ void __launch_bounds__(1024) plan_kernel(const PreParams p, int cap, int sms, int may_cut) {
-    constexpr int NB = 1024;
+    constexpr int ROWS = Cfg<TILES>::ROWS, BK = Cfg<TILES>::BK, NB = 1024;
     __shared__ int start[NB];
     __shared__ int64_t warp_tot[32];
     __shared__ int64_t work;
@@ -180,7 +191,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const PreParams p, int cap, 
     // into parts of at most that: over all heads fewer than `sms` blocks and
     // 2 sms parts.
     int64_t share = (work * p.H + sms - 1) / sms;
-    if (share < MIN_PART) share = MIN_PART;
+    if (share < MIN_PART / BK) share = MIN_PART / BK;
     auto parts_of = [&](int tiles) { return may_cut && tiles > share ? (int)((tiles + share - 1) / share) : 1; };
     auto bin_of = [&](int tiles) { return NB - 1 - min(tiles, NB - 1); };
     for (int e = tid; e < E; e += 1024) {
@@ -254,9 +265,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
-__global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_constant__ PreParams p) {
+template <int TILES>
+__global__ void __launch_bounds__(Cfg<TILES>::THREADS, 3 - TILES) prefill_kernel(const __grid_constant__ PreParams p) {
+    using G = Cfg<TILES>;
+    constexpr int BK = G::BK, ROWS = G::ROWS, SPLIT = G::SPLIT, W_MMA = G::W_MMA, W_LOAD = G::W_LOAD;
+    constexpr uint32_t BLOCK = G::BLOCK, SM_Q = 0, SM_RING = G::SM_RING, O_COL = G::O_COL;
     extern __shared__ __align__(1024) uint8_t sm[];
-    uint64_t *full = reinterpret_cast<uint64_t *>(sm + SM_MISC);    // [8] ring block loaded
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm + G::SM_MISC);    // [8] ring block loaded
     uint64_t *empty = full + RING;                          // [8] ring block read
     uint64_t *q_full = full + 16;                           // [2] query tiles
     uint64_t *s_full = full + 18;                           // [2] scores
@@ -265,13 +280,13 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(full + 26);
     volatile int *fail = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
-    float *swap = reinterpret_cast<float *>(sm + SM_SWAP);  // [2 tiles][2 halves][128 rows]
+    float *swap = reinterpret_cast<float *>(sm + G::SM_SWAP);  // [2 tiles][2 halves][128 rows]
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     // the first CTAs set up while the plan is still being made; of the later ones,
     // those that the plan has no entry for end at once
-    if (blockIdx.x >= MAX_SMS) {
+    if (blockIdx.x >= MAX_SMS * (3 - TILES)) {
         asm volatile("griddepcontrol.wait;" ::: "memory");
         if ((int)(blockIdx.x / p.H) >= p.head->entries) return;
     }
@@ -280,7 +295,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
         mbar_fence_init();
         *fail = 0;
     }
-    if (warp == W_MMA) tmem_alloc<512>(tmem_slot);
+    if (warp == W_MMA) tmem_alloc<G::TCOLS>(tmem_slot);
     if (warp == W_LOAD && lane == 0) {
         prefetch_map(&p.tm_q); prefetch_map(&p.tm_k); prefetch_map(&p.tm_v); prefetch_map(&p.tm_r);
     }
@@ -307,12 +322,12 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
             if (n > 0) {
                 if (elect_one()) {
                     if (nA > 0) {
-                        mbar_arrive_expect_tx(&q_full[0], 3 * BLOCK);
+                        mbar_arrive_expect_tx(&q_full[0], 3 * QBLOCK);
                         tma4(smb + SM_Q, &p.tm_q, 0, ent.row0, 0, h, &q_full[0]);
                     }
                     if (nB > 0) {
-                        mbar_arrive_expect_tx(&q_full[1], 3 * BLOCK);
-                        tma4(smb + SM_Q + 3 * BLOCK, &p.tm_q, 0, ent.row0 + BQ, 0, h, &q_full[1]);
+                        mbar_arrive_expect_tx(&q_full[1], 3 * QBLOCK);
+                        tma4(smb + SM_Q + 3 * QBLOCK, &p.tm_q, 0, ent.row0 + BQ, 0, h, &q_full[1]);
                     }
                 }
                 __syncwarp();
@@ -328,7 +343,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
                             mbar_arrive_expect_tx(&full[slot], BLOCK);
                             if (b < 2) tma4(dst, &p.tm_k, 0, t, b, h, &full[slot]);
                             else if (b == 2) tma4(dst, &p.tm_r, 0, t, 0, 0, &full[slot]);
-                            else tma4(dst, &p.tm_v, 0, t + (b - 3) * 64, 2, h, &full[slot]);
+                            else tma4(dst, &p.tm_v, 0, t + (b - 3) * (BK / 2), 2, h, &full[slot]);
                         }
                         __syncwarp();
                         ++q;
@@ -342,13 +357,13 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
             }
         } else if (warp == W_MMA) {
             if (elect_one()) {
-                constexpr uint32_t id_s = idesc(128, 128, FMT_BF16, FMT_BF16, 0, 0);
+                constexpr uint32_t id_s = idesc(128, BK, FMT_BF16, FMT_BF16, 0, 0);
                 constexpr uint32_t id_o = idesc(128, 128, FMT_BF16, FMT_BF16, 0, 1);
                 bool ok = true;
                 auto landed = [&](uint32_t q) { ok &= wait_one(&full[q % RING], (q / RING) & 1); };  // ring block q
                 // S of tile x, step j
                 auto scores = [&](uint32_t x, uint32_t j, bool first, bool last) {
-                    const uint64_t dq = sdesc_k_sw128(smb + SM_Q + x * 3 * BLOCK);
+                    const uint64_t dq = sdesc_k_sw128(smb + SM_Q + x * 3 * QBLOCK);
 #pragma unroll
                     for (uint32_t b = 0; b < 3; ++b) {
                         const uint32_t q = PER * j + b;
@@ -356,7 +371,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
                         const uint64_t dk = sdesc_k_sw128(smb + SM_RING + q % RING * BLOCK);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma_f16(tmem + S_COL + 128 * x, sdesc_add(dq, b * BLOCK + k * 32),
+                            mma_f16(tmem + 128 * x, sdesc_add(dq, b * QBLOCK + k * 32),
                                     sdesc_add(dk, k * 32), id_s, b > 0 || k > 0);
                         if (last) mma_commit(&empty[q % RING]);
                     }
@@ -368,29 +383,32 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
                     for (uint32_t b = 0; b < 2; ++b) {
                         const uint32_t q = PER * j + 3 + b;
                         if (first) landed(q);
-                        ok &= wait_one(&p_full[2 * x + b], j & 1);
+                        if (b < SPLIT) ok &= wait_one(&p_full[2 * x + b], j & 1);
                         fence_after_sync();
-                        // values [2 chunks of 64 channels][64 tokens][128 bytes]: MN-major B
-                        const uint64_t dv = sdesc(smb + SM_RING + q % RING * BLOCK, 8192, 1024, LAYOUT_SW128);
+                        // values [2 chunks of 64 channels][BK / 2 tokens][128 bytes]: MN-major B
+                        const uint64_t dv = sdesc(smb + SM_RING + q % RING * BLOCK, BLOCK / 2, 1024, LAYOUT_SW128);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_f16_tmem_a(tmem + O_COL + 128 * x, tmem + S_COL + 128 * x + (b * 4 + k) * 8,
+                        for (int k = 0; k < BK / 32; ++k)
+                            mma_f16_tmem_a(tmem + O_COL + 128 * x, tmem + 128 * x + (b * (BK / 32) + k) * 8,
                                            sdesc_add(dv, k * 2048), id_o, j > 0 || b > 0 || k > 0);
                         if (last) mma_commit(&empty[q % RING]);
                     }
                 };
-                const uint32_t both = min(nA, nB);
+                uint32_t both = 0;
                 if (nA > 0) ok &= wait_one(&q_full[0], 0);
                 if (nB > 0) ok &= wait_one(&q_full[1], 0);
-                for (uint32_t j = 0; ok && j < both; ++j) { // S_A(j) O_B(j-1) S_B(j) O_A(j)
-                    scores(0, j, true, false);
-                    if (j > 0) outputs(1, j - 1, false, true);
-                    scores(1, j, false, true);
-                    outputs(0, j, true, false);
+                if constexpr (TILES == 2) {
+                    both = min(nA, nB);
+                    for (uint32_t j = 0; ok && j < both; ++j) {     // S_A(j) O_B(j-1) S_B(j) O_A(j)
+                        scores(0, j, true, false);
+                        if (j > 0) outputs(1, j - 1, false, true);
+                        scores(1, j, false, true);
+                        outputs(0, j, true, false);
+                    }
+                    if (ok && both > 0) outputs(1, both - 1, false, true);
                 }
-                if (ok && both > 0) outputs(1, both - 1, false, true);
                 for (uint32_t j = both; ok && j < n; ++j) { // steps that only one tile has
-                    if (nB > nA) {
+                    if (TILES == 2 && nB > nA) {
                         scores(1, j, true, true);
                         outputs(1, j, true, true);
                     } else {
@@ -407,17 +425,20 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
             }
             __syncwarp();
         } else {
-            // ---- softmax: two threads a row, each half of a key tile's columns ----
-            const int x = warp >> 3, half = warp >> 2 & 1;  // tile, columns 64 half ..
+            // ---- softmax: SPLIT threads a row, each 64 of a key tile's columns ----
+            constexpr int OC = DV / SPLIT;                  // output columns a thread
+            const int x = SPLIT == 2 ? warp >> 3 : 0;       // tile
+            const int half = SPLIT == 2 ? warp >> 2 & 1 : 0;    // columns 64 half ..
             const int row = tid & 127;                      // row of the tile
             const int i = x * BQ + row;                     // query of the block
             const int nX = x ? nB : nA;
             const int end = i < ent.rows ? min(i + ent.off + 1, ent.keys) : ent.keys;   // keys it sees
             // keys that every row of this warp sees
             const int warp_end = __reduce_min_sync(0xffffffffu, end);
-            const uint32_t t_s = tmem_at(tmem, warp, S_COL + 128 * x);
-            const uint32_t t_o = tmem_at(tmem, warp, O_COL + 128 * x + 64 * half);
+            const uint32_t t_s = tmem_at(tmem, warp, 128 * x);
+            const uint32_t t_o = tmem_at(tmem, warp, O_COL + 128 * x + OC * half);
             const uint32_t pair = 1 + 4 * x + (warp & 3);   // named barrier of the rows' two warps
+            // what the row's two threads tell one another (SPLIT == 2)
             float *mine = swap + (2 * x + half) * 128 + row, *theirs = swap + (2 * x + 1 - half) * 128 + row;
             const float sc = p.scale_log2;
             float m = -CUDART_INF_F;                        // unscaled
@@ -453,18 +474,25 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
                 const float part = max3(t0, t1, fmaxf(t2, t3));
                 // The other half's maximum.  It is read before the other thread's
                 // next write: that follows the next scores, which follow this P.
-                *mine = part;
-                const bool stop = bar_or(pair, 64, !ok);
-                const float top = fmaxf(part, *theirs);
+                float top = part;
+                bool stop;
+                if constexpr (SPLIT == 2) {
+                    *mine = part;
+                    stop = bar_or(pair, 64, !ok);
+                    top = fmaxf(part, *theirs);
+                } else {
+                    stop = !ok;                             // the same for the whole warp
+                }
                 if (stop) { ok = false; break; }
                 const int valid = ent.keys - j * BK;            // keys of the sequence in this tile
                 if (valid < BK) {
                     // values behind the sequence's end hold anything: zero them
                     // (each tile for its own product)
-                    const int q = PER * j + 3 + (row >> 6), slot = q % RING;
+                    const int token = row % BK, chunk = SPLIT == 2 ? half : row / BK;
+                    const int q = PER * j + 3 + token / (BK / 2), slot = q % RING;
                     ok = wait_or_fail(&full[slot], (q / RING) & 1, fail);
-                    if (row >= valid) {
-                        uint8_t *r = sm + SM_RING + slot * BLOCK + half * 8192 + (row & 63) * 128;
+                    if (token >= valid) {
+                        uint8_t *r = sm + SM_RING + slot * BLOCK + chunk * (BLOCK / 2) + token % (BK / 2) * 128;
 #pragma unroll
                         for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(r + c * 16) = make_uint4(0, 0, 0, 0);
                     }
@@ -480,7 +508,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
                     m = to;
                     l2.x *= f; l2.y *= f;
                     if (j > 0) {
-                        for (int c = 0; c < 64; c += 16) {
+                        for (int c = 0; c < OC; c += 16) {
                             float y[16];
                             tmem_ld16(t_o + c, y);
                             tmem_wait_ld();
@@ -518,17 +546,20 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
             }
             if (ok && nX > 0) ok = wait_or_fail(o_full, 0, fail);
             const float part = l2.x + l2.y;
-            *mine = part;
-            ok = !bar_or(pair, 64, !ok);
+            float l = part;
+            if constexpr (SPLIT == 2) {
+                *mine = part;
+                ok = !bar_or(pair, 64, !ok);
+                l += *theirs;
+            }
             if (ok && x * BQ < ent.rows) {
-                const float l = part + *theirs;
                 const bool whole = ent.base < 0;
                 const float r = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
                 const int64_t at = (int64_t)(ent.row0 + i) * p.H + h;
                 const int64_t pr = ((int64_t)(ent.base + ent.part) * p.H + h) * ROWS + i;
                 fence_after_sync();
 #pragma unroll
-                for (int c = 0; c < 64; c += 16) {
+                for (int c = 0; c < OC; c += 16) {
                     float y[16];
                     if (nX > 0) {
                         tmem_ld16(t_o + c, y);
@@ -542,11 +573,11 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
                         uint32_t w[8];
 #pragma unroll
                         for (int k = 0; k < 8; ++k) w[k] = pack_bf(y[2 * k] * r, y[2 * k + 1] * r);
-                        uint4 *to = reinterpret_cast<uint4 *>(p.o + at * DV + 64 * half + c);
+                        uint4 *to = reinterpret_cast<uint4 *>(p.o + at * DV + OC * half + c);
                         to[0] = make_uint4(w[0], w[1], w[2], w[3]);
                         to[1] = make_uint4(w[4], w[5], w[6], w[7]);
                     } else if (i < ent.rows) {
-                        float *to = p.part + pr * DV + 64 * half + c;
+                        float *to = p.part + pr * DV + OC * half + c;
 #pragma unroll
                         for (int k = 0; k < 16; k += 4) store4(to + k, make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]));
                     }
@@ -561,12 +592,14 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
     fence_before_sync();
     __syncthreads();
     if (tid == 0 && *fail) atomicExch(&p.head->status, *fail);
-    if (warp == W_MMA) tmem_dealloc<512>(tmem);
+    if (warp == W_MMA) tmem_dealloc<G::TCOLS>(tmem);
 }
 
 // Adds up the parts of the blocks that are cut: a warp takes a query of a head,
 // a lane 4 channels.
+template <int TILES>
 __global__ void __launch_bounds__(256) prefill_join_kernel(const PreParams p) {
+    constexpr int ROWS = Cfg<TILES>::ROWS;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int cuts = p.head->cut, lane = threadIdx.x & 31;
     if (p.head->status) return;              // a CTA gave up: o stays as it is
@@ -598,11 +631,8 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const PreParams p) {
     }
 }
 
-}  // namespace
-
-uint64_t prefill_tc_workspace_bytes(int32_t N, int64_t Tq) { return layout(N, Tq).bytes; }
-
-cudaError_t launch_prefill_tc(const PrefillArgs &a, cudaStream_t st) {
+template <int TILES> cudaError_t launch(const PrefillArgs &a, cudaStream_t st) {
+    using G = Cfg<TILES>;
     static std::mutex mu;
     static bool ready[64] = {false};
     int dev = 0;
@@ -612,8 +642,8 @@ cudaError_t launch_prefill_tc(const PrefillArgs &a, cudaStream_t st) {
     {
         std::lock_guard<std::mutex> lock(mu);
         if (!ready[dev]) {
-            e = cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)SM_BYTES);
+            e = cudaFuncSetAttribute(prefill_kernel<TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)G::SM_BYTES);
             if (e != cudaSuccess) return e;
             ready[dev] = true;
         }
@@ -625,7 +655,7 @@ cudaError_t launch_prefill_tc(const PrefillArgs &a, cudaStream_t st) {
     if (!map4(&p.tm_q, a.q, qd, qs, qb)) return cudaErrorInvalidValue;
     if (Tk > 0) {      // without keys no tile is loaded
         const uint64_t kd[4] = {64, Tk, 4, H}, ks[3] = {H * (NOPE + DV) * 2, 128, (NOPE + DV) * 2};
-        const uint32_t kb[4] = {64, BK, 1, 1}, vb[4] = {64, 64, 2, 1};
+        const uint32_t kb[4] = {64, G::BK, 1, 1}, vb[4] = {64, G::BK / 2, 2, 1};
         const uint64_t rd[4] = {64, Tk, 1, 1}, rs[3] = {ROPE * 2, ROPE * 2, ROPE * 2};
         if (!map4(&p.tm_k, a.kv, kd, ks, kb) || !map4(&p.tm_v, a.kv, kd, ks, vb) ||
             !map4(&p.tm_r, a.k_r, rd, rs, kb))
@@ -659,26 +689,37 @@ cudaError_t launch_prefill_tc(const PrefillArgs &a, cudaStream_t st) {
     e = sm_count(&sms);
     if (e != cudaSuccess) return e;
     if (sms > MAX_SMS) sms = MAX_SMS;
-    const int64_t cap = a.Tq / ROWS + a.N;                  // blocks of queries, at most
+    const int64_t cap = a.Tq / G::ROWS + a.N;                  // blocks of queries, at most
     // Cutting pays where (queries / 256) x heads leaves the SMs fewer than two
     // CTAs each: two sequences of up to 3000 queries over up to 8000 keys, one
     // head: 106 us whole, 47 us cut; one prompt of 4096 tokens, four heads: 60 and
     // 46 us.  Where nothing is cut after all it costs 3 to 5 us (a join kernel and
     // CTAs with nothing to do), and with more CTAs the longest-first order balances
     // by itself (8 packed prompts, 864 CTAs: 125 us).
-    const bool may_cut = a.Tq / ROWS * a.H < 2 * sms && a.H < 2 * sms && a.Tk > MIN_PART * BK;
-    e = cudaLaunchKernelEx(&cfg, plan_kernel, p, (int)cap, sms, (int)may_cut);
+    const bool may_cut = a.Tq / G::ROWS * a.H < 2 * sms && a.H < 2 * sms && a.Tk > MIN_PART;
+    e = cudaLaunchKernelEx(&cfg, plan_kernel<TILES>, p, (int)cap, sms, (int)may_cut);
     if (e != cudaSuccess) return e;
     // a CTA per block and head, and one for each further part
     cfg.gridDim = dim3((unsigned)(cap * a.H + (may_cut ? SLOTS : 0)));
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = SM_BYTES;
-    e = cudaLaunchKernelEx(&cfg, prefill_kernel, p);
+    cfg.blockDim = dim3(G::THREADS);
+    cfg.dynamicSmemBytes = G::SM_BYTES;
+    e = cudaLaunchKernelEx(&cfg, prefill_kernel<TILES>, p);
     if (e != cudaSuccess || !may_cut) return e;
     cfg.gridDim = dim3(8 * (unsigned)sms);                  // all resident: without a cut they end at once
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, prefill_join_kernel, p);
+    return cudaLaunchKernelEx(&cfg, prefill_join_kernel<TILES>, p);
+}
+
+}  // namespace
+
+uint64_t prefill_tc_workspace_bytes(int32_t N, int64_t Tq) { return layout(N, Tq).bytes; }
+
+cudaError_t launch_prefill_tc(const PrefillArgs &a, cudaStream_t st) {
+    // One tile where sequences have up to 512 keys on average.  Packed prompts, 16
+    // heads, one tile and two: 64 of up to 300 tokens 65 and 90 us, 32 of 200 to 600
+    // 90 and 105, 32 of 600 to 1200 233 and 233, 32 of 1500 to 2500 840 and 696.
+    return a.Tk <= 512 * (int64_t)a.N ? launch<1>(a, st) : launch<2>(a, st);
 }
 
 }  // namespace mla

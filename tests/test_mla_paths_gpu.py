@@ -1,0 +1,172 @@
+"""Latent attention on the GPU: both forms of the bf16 prefill kernel over the
+same sequences, and the bounded waits.
+
+The prefill takes one query tile a CTA where sequences have up to 512 keys on
+average and two otherwise.  Here the same odd lengths run through both: with a
+sequence of one query over many keys beside them the average is above that,
+with one-token sequences beside them below it.  Tolerances are those of
+``test_mla_gpu.py``, for the same reasons.
+
+``libkda_faultinj.so`` is the same source with a hook that makes every CTA wait
+on a barrier that nothing arrives at, with a limit of 64 polls, before it
+issues any copy or MMA: nothing is in flight when the wait gives up.
+"""
+import ctypes
+
+import pytest
+import torch
+
+import serving_kda_chunked_gb300 as kda
+from test_mla_gpu import (DEV, SC, _call_decode, _call_prefill, _check_decode, _check_prefill,
+                          _decode_inputs, _prefill_inputs)
+
+pytestmark = pytest.mark.gpu
+
+ODD = [
+    [(64, 64), (1, 1), (63, 63), (65, 65)],
+    [(127, 127), (128, 128), (129, 129)],
+    [(255, 255), (256, 256), (257, 257), (0, 0), (3, 3)],
+    [(100, 300), (7, 133), (256, 511), (130, 700)],
+    [(300, 100), (5, 0), (200, 1), (64, 63), (0, 40)],
+    [(384, 384), (385, 1025)],
+    [(1, 6000)],
+    [(300, 2500), (130, 1100)],
+]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def fi():
+    from serving_kda_chunked_gb300 import build
+    build.build()
+    main = kda.load()
+    lib = ctypes.CDLL(build.FAULTINJ_LIB)
+    for name in ("kda_mla_prefill", "kda_mla_decode", "kda_mla_check"):
+        getattr(lib, name).argtypes = getattr(main, name).argtypes
+        getattr(lib, name).restype = ctypes.c_int
+    lib.kda_test_force_timeout.argtypes = [ctypes.c_int32]
+    lib.kda_test_force_timeout.restype = None
+    return lib
+
+
+def _mean_above(lens):
+    """The lengths, and one query over enough keys for a mean above 512."""
+    return lens + [(1, 513 * (len(lens) + 1))]
+
+
+def _mean_below(lens):
+    return lens + [(1, 1)] * (sum(k for _, k in lens) // 511 + 1)
+
+
+@pytest.mark.parametrize("beside", [_mean_above, _mean_below])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("case", range(len(ODD)))
+def test_prefill_odd_lengths_in_both_forms(case, causal, beside):
+    lens = beside(ODD[case])
+    q, kv, kr, cu_q, cu_k = _prefill_inputs(lens, 3, "bf16", seed=100 + case)
+    o, lse = _call_prefill(q, kv, kr, cu_q, cu_k, causal)
+    _check_prefill(lens, q, kv, kr, causal, "bf16", o, lse)
+
+
+@pytest.mark.parametrize("beside", [_mean_above, _mean_below])
+def test_prefill_unseen_values_in_both_forms(beside):
+    """NaN and infinities in the middle sequence, and behind the last key."""
+    lens = [(50, 50), (90, 90), (130, 130)]
+    more = beside(lens)
+    q, kv, kr, cu_q, cu_k = _prefill_inputs(more, 2, "bf16", seed=106, tail=70)
+    kv[50:140] = float("nan")
+    kr[50:140] = float("inf")
+    q[50:140] = float("nan")
+    o, lse = _call_prefill(q, kv, kr, cu_q, cu_k, True)
+    _check_prefill(more, q, kv, kr, True, "bf16", o, lse, skip=(1,))
+
+
+@pytest.mark.parametrize("n", [400, 1200])
+def test_prefill_growing_and_falling_scores_in_both_forms(n):
+    lens = [(n, n)]
+    q, kv, kr, cu_q, cu_k = _prefill_inputs(lens, 1, "bf16", seed=105)
+    q[:] = 0
+    q[..., 0] = 4.0
+    kv[..., :128] = 0
+    for step in (1.0, -2.0):
+        kv[:, 0, 0] = (torch.arange(n, device=DEV) * step).to(q.dtype)
+        o, lse = _call_prefill(q, kv, kr, cu_q, cu_k, False, scale=0.25)
+        _check_prefill(lens, q, kv, kr, False, "bf16", o, lse, scale=0.25)
+
+
+def test_prefill_many_short_sequences_repeat():
+    """More CTAs than are resident at once; the same bits every time."""
+    lens = [((37 * i) % 300, (37 * i) % 300 + (i % 5)) for i in range(90)]
+    q, kv, kr, cu_q, cu_k = _prefill_inputs(lens, 8, "bf16", seed=110)
+    o, lse = _call_prefill(q, kv, kr, cu_q, cu_k, True)
+    for _ in range(3):
+        o2, lse2 = _call_prefill(q, kv, kr, cu_q, cu_k, True)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    h = q.shape[1] - 1          # one head against the plain computation
+    _check_prefill(lens, q[:, h:], kv[:, h:], kr, True, "bf16", o[:, h:], lse[:, h:])
+
+
+# ---- bounded waits -----------------------------------------------------------------
+
+def _stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+@pytest.mark.parametrize("lens", [
+    [(130, 130), (70, 300)],        # one query tile a CTA
+    [(600, 700)],                   # two
+    [(300, 2500)],                  # keys cut into parts
+])
+def test_prefill_forced_timeout(fi, lens):
+    q, kv, kr, cu_q, cu_k = _prefill_inputs(lens, 2, "bf16", seed=120)
+    need = kda.kda_mla_prefill_workspace_size(len(lens), q.shape[0], 2, q.dtype)
+    ws = torch.full((need,), 0xA5, dtype=torch.uint8, device=DEV)
+    o = torch.full(q.shape[:2] + (128,), 12345.0, dtype=q.dtype, device=DEV)
+    lse = torch.full(q.shape[:2], 12345.0, device=DEV)
+
+    def call():
+        return fi.kda_mla_prefill(q.data_ptr(), kv.data_ptr(), kr.data_ptr(), cu_q.data_ptr(),
+                                  cu_k.data_ptr(), len(lens), q.shape[0], kv.shape[0], 2, 128, 64,
+                                  128, kda.KDA_BF16, SC, 1, o.data_ptr(), lse.data_ptr(),
+                                  ws.data_ptr(), need, _stream())
+
+    sentinel = o.clone()
+    fi.kda_test_force_timeout(1)
+    try:
+        st = call()
+    finally:
+        fi.kda_test_force_timeout(0)
+    assert st == kda.KDA_OK                     # the launch itself succeeds
+    assert fi.kda_mla_check(ws.data_ptr(), _stream()) == kda.KDA_ERR_TIMEOUT
+    assert torch.equal(o, sentinel) and bool((lse == 12345.0).all())
+    assert call() == kda.KDA_OK                 # and the next call is a normal one
+    assert fi.kda_mla_check(ws.data_ptr(), _stream()) == kda.KDA_OK
+    _check_prefill(lens, q, kv, kr, True, "bf16", o, lse)
+
+
+@pytest.mark.parametrize("H", [2, 20, 64])
+@pytest.mark.parametrize("lens", [[1], [70, 300, 5], [6000]])
+def test_decode_forced_timeout(fi, H, lens):
+    q, cache, table, n = _decode_inputs(lens, H, 32, "bf16", seed=121)
+    need = kda.kda_mla_decode_workspace_size(len(lens), H, q.dtype)
+    ws = torch.full((need,), 0xA5, dtype=torch.uint8, device=DEV)
+    o = torch.full((len(lens), H, 512), 12345.0, dtype=q.dtype, device=DEV)
+    lse = torch.full((len(lens), H), 12345.0, device=DEV)
+
+    def call():
+        return fi.kda_mla_decode(q.data_ptr(), cache.data_ptr(), table.data_ptr(), n.data_ptr(),
+                                 len(lens), H, cache.shape[0], 32, table.shape[1], 512, 64,
+                                 kda.KDA_BF16, SC, o.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+                                 need, _stream())
+
+    sentinel = o.clone()
+    fi.kda_test_force_timeout(1)
+    try:
+        st = call()
+    finally:
+        fi.kda_test_force_timeout(0)
+    assert st == kda.KDA_OK
+    assert fi.kda_mla_check(ws.data_ptr(), _stream()) == kda.KDA_ERR_TIMEOUT
+    assert torch.equal(o, sentinel) and bool((lse == 12345.0).all())
+    assert call() == kda.KDA_OK
+    assert fi.kda_mla_check(ws.data_ptr(), _stream()) == kda.KDA_OK
+    _check_decode(q, cache, table, n, "bf16", o, lse)
