@@ -43,10 +43,13 @@ constexpr int BQ = 128;                                     // rows a tile
 constexpr uint32_t QBLOCK = BQ * 128;                       // 64 channels of a query tile
 constexpr int RING = 8, PER = 5;                            // blocks in the ring, blocks a key tile
 
-// TILES = 2: as above.  TILES = 1, for short sequences: one query tile, key tiles
-// of 64, one softmax thread a row, two CTAs an SM.  Nothing overlaps inside such a
-// CTA, but one CTA's start and end run beside the other's products; with few key
-// tiles these cost more than the lost overlap and the second reading of the keys.
+// TILES = 2: as above.  TILES = 1: one query tile, key tiles of 64 whose scores
+// take turns in two places (S(0) S(1) O(0) S(2) O(1) ...: the products of the
+// next scores run during a tile's softmax), one softmax thread a row, two CTAs an
+// SM.  It reads the keys twice as often and its score products are 128 x 64,
+// bound by their operands in shared memory; but one CTA's start and end run beside
+// the other's products.  With one place for the scores 195 prompts of 400 tokens
+// took the same time, 8 of up to 2048 131 us (115).
 template <int TILES> struct Cfg {
     static constexpr int ROWS = TILES * BQ, BK = 64 * TILES;
     static constexpr int SPLIT = TILES;                     // softmax threads a row; each has 64 of a key tile's columns
@@ -273,10 +276,11 @@ __global__ void __launch_bounds__(Cfg<TILES>::THREADS, 3 - TILES) prefill_kernel
     extern __shared__ __align__(1024) uint8_t sm[];
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + G::SM_MISC);    // [8] ring block loaded
     uint64_t *empty = full + RING;                          // [8] ring block read
-    uint64_t *q_full = full + 16;                           // [2] query tiles
+    uint64_t *q_full = full + 16;                           // [TILES] query tiles
     uint64_t *s_full = full + 18;                           // [2] scores
     uint64_t *p_full = full + 20;                           // [2][2] halves of P
     uint64_t *o_full = full + 24, *drain = full + 25;       // all outputs
+    uint64_t *o_step = full + 17;                           // TILES == 1: the output products of a step
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(full + 26);
     volatile int *fail = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -362,7 +366,9 @@ __global__ void __launch_bounds__(Cfg<TILES>::THREADS, 3 - TILES) prefill_kernel
                 bool ok = true;
                 auto landed = [&](uint32_t q) { ok &= wait_one(&full[q % RING], (q / RING) & 1); };  // ring block q
                 // S of tile x, step j
+                // TILES == 1: scores of even steps in columns 0 .., of odd ones in 64 ..
                 auto scores = [&](uint32_t x, uint32_t j, bool first, bool last) {
+                    const uint32_t at = TILES == 2 ? 128 * x : 64 * (j & 1);
                     const uint64_t dq = sdesc_k_sw128(smb + SM_Q + x * 3 * QBLOCK);
 #pragma unroll
                     for (uint32_t b = 0; b < 3; ++b) {
@@ -371,25 +377,27 @@ __global__ void __launch_bounds__(Cfg<TILES>::THREADS, 3 - TILES) prefill_kernel
                         const uint64_t dk = sdesc_k_sw128(smb + SM_RING + q % RING * BLOCK);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma_f16(tmem + 128 * x, sdesc_add(dq, b * QBLOCK + k * 32),
+                            mma_f16(tmem + at, sdesc_add(dq, b * QBLOCK + k * 32),
                                     sdesc_add(dk, k * 32), id_s, b > 0 || k > 0);
                         if (last) mma_commit(&empty[q % RING]);
                     }
-                    mma_commit(&s_full[x]);
+                    mma_commit(&s_full[TILES == 2 ? x : j & 1]);
                 };
                 // O of tile x, step j, as the halves of P arrive
                 auto outputs = [&](uint32_t x, uint32_t j, bool first, bool last) {
+                    const uint32_t at = TILES == 2 ? 128 * x : 64 * (j & 1);
 #pragma unroll
                     for (uint32_t b = 0; b < 2; ++b) {
                         const uint32_t q = PER * j + 3 + b;
                         if (first) landed(q);
-                        if (b < SPLIT) ok &= wait_one(&p_full[2 * x + b], j & 1);
+                        if (TILES == 2) ok &= wait_one(&p_full[2 * x + b], j & 1);
+                        else if (b == 0) ok &= wait_one(&p_full[j & 1], j >> 1 & 1);
                         fence_after_sync();
                         // values [2 chunks of 64 channels][BK / 2 tokens][128 bytes]: MN-major B
                         const uint64_t dv = sdesc(smb + SM_RING + q % RING * BLOCK, BLOCK / 2, 1024, LAYOUT_SW128);
 #pragma unroll
                         for (int k = 0; k < BK / 32; ++k)
-                            mma_f16_tmem_a(tmem + O_COL + 128 * x, tmem + 128 * x + (b * (BK / 32) + k) * 8,
+                            mma_f16_tmem_a(tmem + O_COL + 128 * x, tmem + at + (b * (BK / 32) + k) * 8,
                                            sdesc_add(dv, k * 2048), id_o, j > 0 || b > 0 || k > 0);
                         if (last) mma_commit(&empty[q % RING]);
                     }
@@ -407,14 +415,18 @@ __global__ void __launch_bounds__(Cfg<TILES>::THREADS, 3 - TILES) prefill_kernel
                     }
                     if (ok && both > 0) outputs(1, both - 1, false, true);
                 }
-                for (uint32_t j = both; ok && j < n; ++j) { // steps that only one tile has
-                    if (TILES == 2 && nB > nA) {
-                        scores(1, j, true, true);
-                        outputs(1, j, true, true);
-                    } else {
-                        scores(0, j, true, true);
+                if constexpr (TILES == 1) {                 // S(0) S(1) O(0) S(2) O(1) ...
+                    if (ok && n > 0) scores(0, 0, true, true);
+                    for (uint32_t j = 0; ok && j < n; ++j) {
+                        if (j + 1 < n) scores(0, j + 1, true, true);
                         outputs(0, j, true, true);
+                        mma_commit(o_step);
                     }
+                }
+                for (uint32_t j = both; TILES == 2 && ok && j < n; ++j) {   // steps that only one tile has
+                    const uint32_t x = nB > nA;
+                    scores(x, j, true, true);
+                    outputs(x, j, true, true);
                 }
                 mma_commit(o_full);
                 if (!ok) {     // MMAs in flight end before tensor memory is freed
@@ -435,7 +447,7 @@ __global__ void __launch_bounds__(Cfg<TILES>::THREADS, 3 - TILES) prefill_kernel
             const int end = i < ent.rows ? min(i + ent.off + 1, ent.keys) : ent.keys;   // keys it sees
             // keys that every row of this warp sees
             const int warp_end = __reduce_min_sync(0xffffffffu, end);
-            const uint32_t t_s = tmem_at(tmem, warp, 128 * x);
+            const uint32_t t_s0 = tmem_at(tmem, warp, 128 * x);
             const uint32_t t_o = tmem_at(tmem, warp, O_COL + 128 * x + OC * half);
             const uint32_t pair = 1 + 4 * x + (warp & 3);   // named barrier of the rows' two warps
             // what the row's two threads tell one another (SPLIT == 2)
@@ -445,7 +457,9 @@ __global__ void __launch_bounds__(Cfg<TILES>::THREADS, 3 - TILES) prefill_kernel
             float2 l2 = make_float2(0.f, 0.f);
             bool ok = true;
             for (int j = 0; j < nX; ++j) {
-                ok = wait_or_fail(&s_full[x], j & 1, fail);
+                const uint32_t t_s = TILES == 2 ? t_s0 : t_s0 + 64 * (j & 1);
+                ok = TILES == 2 ? wait_or_fail(&s_full[x], j & 1, fail)
+                                : wait_or_fail(&s_full[j & 1], j >> 1 & 1, fail);
                 fence_after_sync();
                 float v[64];
                 tmem_ld32(t_s + 64 * half, v);
@@ -507,6 +521,11 @@ __global__ void __launch_bounds__(Cfg<TILES>::THREADS, 3 - TILES) prefill_kernel
                     const float f = to == -CUDART_INF_F ? 1.f : ex2((m - to) * sc);
                     m = to;
                     l2.x *= f; l2.y *= f;
+                    if (TILES == 1 && j > 0) {              // the output is not being added to
+                        ok = wait_or_fail(o_step, (j - 1) & 1, fail);
+                        if (!ok) break;
+                        fence_after_sync();
+                    }
                     if (j > 0) {
                         for (int c = 0; c < OC; c += 16) {
                             float y[16];
@@ -541,7 +560,7 @@ __global__ void __launch_bounds__(Cfg<TILES>::THREADS, 3 - TILES) prefill_kernel
                 tmem_wait_st();
                 fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[2 * x + half]);
+                if (lane == 0) mbar_arrive(&p_full[TILES == 2 ? 2 * x + half : j & 1]);
                 l2 = add2(l2, add2(a0, a1));
             }
             if (ok && nX > 0) ok = wait_or_fail(o_full, 0, fail);
@@ -716,10 +735,24 @@ template <int TILES> cudaError_t launch(const PrefillArgs &a, cudaStream_t st) {
 uint64_t prefill_tc_workspace_bytes(int32_t N, int64_t Tq) { return layout(N, Tq).bytes; }
 
 cudaError_t launch_prefill_tc(const PrefillArgs &a, cudaStream_t st) {
-    // One tile where sequences have up to 512 keys on average.  Packed prompts, 16
-    // heads, one tile and two: 64 of up to 300 tokens 65 and 90 us, 32 of 200 to 600
-    // 90 and 105, 32 of 600 to 1200 233 and 233, 32 of 1500 to 2500 840 and 696.
-    return a.Tk <= 512 * (int64_t)a.N ? launch<1>(a, st) : launch<2>(a, st);
+    // One tile where a CTA's start and end are much of its time (few keys or few
+    // queries a sequence) or where the SMs get few CTAs; two where the products
+    // decide.  In us, one tile and two, 16 heads where not said otherwise:
+    //   64 prompts of up to 300 tokens                 62 and 89
+    //   195 of 400, 8 heads                           272 and 292
+    //   38 of 64 after 4000                           144 and 164
+    //   1 of 2048                                      37 and 50
+    //   8 of up to 2048, 32 heads                     115 and 130
+    //   11 of 900, 31 heads (work 3600)               181 and 173
+    //   4 of 2560, 30 heads (work 5100)               235 and 227
+    //   1 of 8192, 32 heads (work 28000)              489 and 430
+    int sms = 1;
+    const cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    const double q = (double)a.Tq / a.N, k = (double)a.Tk / a.N;
+    // keys that a block of 256 queries meets, times blocks an SM
+    const double work = (a.causal ? k - q / 2 : k) * a.Tq / 256 * a.H / sms;
+    return q <= 128 || k <= 640 || work <= 4000 ? launch<1>(a, st) : launch<2>(a, st);
 }
 
 }  // namespace mla

@@ -1,11 +1,10 @@
 """Latent attention on the GPU: both forms of the bf16 prefill kernel over the
 same sequences, and the bounded waits.
 
-The prefill takes one query tile a CTA where sequences have up to 512 keys on
-average and two otherwise.  Here the same odd lengths run through both: with a
-sequence of one query over many keys beside them the average is above that,
-with one-token sequences beside them below it.  Tolerances are those of
-``test_mla_gpu.py``, for the same reasons.
+The prefill takes one query tile a CTA for little work or short sequences and
+two otherwise.  Here the same odd lengths run through both: alone, and beside a
+long prompt with many heads, of which two are compared with the plain
+computation.  Tolerances are those of ``test_mla_gpu.py``, for the same reasons.
 
 ``libkda_faultinj.so`` is the same source with a hook that makes every CTA wait
 on a barrier that nothing arrives at, with a limit of 64 polls, before it
@@ -48,49 +47,58 @@ def fi():
     return lib
 
 
-def _mean_above(lens):
-    """The lengths, and one query over enough keys for a mean above 512."""
-    return lens + [(1, 513 * (len(lens) + 1))]
+LONG = (9000, 9000)
 
 
-def _mean_below(lens):
-    return lens + [(1, 1)] * (sum(k for _, k in lens) // 511 + 1)
+def _alone_and_beside(lens):
+    """(lengths, heads, sequences that are not compared) for one tile a CTA, and for two."""
+    return [(lens, 3, ()), (lens + [LONG], 64, (len(lens),))]
 
 
-@pytest.mark.parametrize("beside", [_mean_above, _mean_below])
+def _check_two_heads(lens, q, kv, kr, causal, o, lse, **kw):
+    for h in {0, q.shape[1] - 1}:
+        _check_prefill(lens, q[:, h:h + 1], kv[:, h:h + 1], kr, causal, "bf16", o[:, h:h + 1],
+                       lse[:, h:h + 1], **kw)
+
+
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("case", range(len(ODD)))
-def test_prefill_odd_lengths_in_both_forms(case, causal, beside):
-    lens = beside(ODD[case])
-    q, kv, kr, cu_q, cu_k = _prefill_inputs(lens, 3, "bf16", seed=100 + case)
-    o, lse = _call_prefill(q, kv, kr, cu_q, cu_k, causal)
-    _check_prefill(lens, q, kv, kr, causal, "bf16", o, lse)
+def test_prefill_odd_lengths_in_both_forms(case, causal):
+    for lens, H, skip in _alone_and_beside(ODD[case]):
+        q, kv, kr, cu_q, cu_k = _prefill_inputs(lens, H, "bf16", seed=100 + case)
+        o, lse = _call_prefill(q, kv, kr, cu_q, cu_k, causal)
+        _check_two_heads(lens, q, kv, kr, causal, o, lse, skip=skip)
 
 
-@pytest.mark.parametrize("beside", [_mean_above, _mean_below])
-def test_prefill_unseen_values_in_both_forms(beside):
-    """NaN and infinities in the middle sequence, and behind the last key."""
-    lens = [(50, 50), (90, 90), (130, 130)]
-    more = beside(lens)
-    q, kv, kr, cu_q, cu_k = _prefill_inputs(more, 2, "bf16", seed=106, tail=70)
-    kv[50:140] = float("nan")
-    kr[50:140] = float("inf")
-    q[50:140] = float("nan")
+@pytest.mark.parametrize("lens,H", [([(300, 30000), (140, 9000)], 32), ([(700, 12000)], 20)])
+def test_prefill_two_tiles_cut(lens, H):
+    q, kv, kr, cu_q, cu_k = _prefill_inputs(lens, H, "bf16", seed=130)
     o, lse = _call_prefill(q, kv, kr, cu_q, cu_k, True)
-    _check_prefill(more, q, kv, kr, True, "bf16", o, lse, skip=(1,))
+    _check_two_heads(lens, q, kv, kr, True, o, lse)
 
 
-@pytest.mark.parametrize("n", [400, 1200])
-def test_prefill_growing_and_falling_scores_in_both_forms(n):
-    lens = [(n, n)]
-    q, kv, kr, cu_q, cu_k = _prefill_inputs(lens, 1, "bf16", seed=105)
-    q[:] = 0
-    q[..., 0] = 4.0
-    kv[..., :128] = 0
-    for step in (1.0, -2.0):
-        kv[:, 0, 0] = (torch.arange(n, device=DEV) * step).to(q.dtype)
-        o, lse = _call_prefill(q, kv, kr, cu_q, cu_k, False, scale=0.25)
-        _check_prefill(lens, q, kv, kr, False, "bf16", o, lse, scale=0.25)
+def test_prefill_unseen_values_in_both_forms():
+    """NaN and infinities in the middle sequence, and behind the last key."""
+    for lens, H, skip in _alone_and_beside([(50, 50), (90, 90), (130, 130)]):
+        q, kv, kr, cu_q, cu_k = _prefill_inputs(lens, H, "bf16", seed=106, tail=70)
+        kv[50:140] = float("nan")
+        kr[50:140] = float("inf")
+        q[50:140] = float("nan")
+        o, lse = _call_prefill(q, kv, kr, cu_q, cu_k, True)
+        _check_two_heads(lens, q, kv, kr, True, o, lse, skip=(1,) + skip)
+
+
+def test_prefill_growing_and_falling_scores_in_both_forms():
+    n = 400
+    for lens, H, skip in _alone_and_beside([(n, n)]):
+        q, kv, kr, cu_q, cu_k = _prefill_inputs(lens, H, "bf16", seed=105)
+        q[:] = 0
+        q[..., 0] = 4.0
+        kv[..., :128] = 0
+        for step in (1.0, -2.0):
+            kv[:n, :, 0] = (torch.arange(n, device=DEV) * step).to(q.dtype)[:, None]
+            o, lse = _call_prefill(q, kv, kr, cu_q, cu_k, False, scale=0.25)
+            _check_two_heads(lens, q, kv, kr, False, o, lse, scale=0.25, skip=skip)
 
 
 def test_prefill_many_short_sequences_repeat():
@@ -101,8 +109,7 @@ def test_prefill_many_short_sequences_repeat():
     for _ in range(3):
         o2, lse2 = _call_prefill(q, kv, kr, cu_q, cu_k, True)
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
-    h = q.shape[1] - 1          # one head against the plain computation
-    _check_prefill(lens, q[:, h:], kv[:, h:], kr, True, "bf16", o[:, h:], lse[:, h:])
+    _check_two_heads(lens, q, kv, kr, True, o, lse)
 
 
 # ---- bounded waits -----------------------------------------------------------------
@@ -111,21 +118,22 @@ def _stream():
     return torch.cuda.current_stream().cuda_stream
 
 
-@pytest.mark.parametrize("lens", [
-    [(130, 130), (70, 300)],        # one query tile a CTA
-    [(600, 700)],                   # two
-    [(300, 2500)],                  # keys cut into parts
+@pytest.mark.parametrize("lens,H", [
+    ([(130, 130), (70, 300)], 2),           # one query tile a CTA
+    ([(300, 2500)], 2),                     # with the keys cut into parts
+    ([(300, 300), LONG], 64),               # two query tiles
+    ([(700, 12000)], 20),                   # with the keys cut into parts
 ])
-def test_prefill_forced_timeout(fi, lens):
-    q, kv, kr, cu_q, cu_k = _prefill_inputs(lens, 2, "bf16", seed=120)
-    need = kda.kda_mla_prefill_workspace_size(len(lens), q.shape[0], 2, q.dtype)
+def test_prefill_forced_timeout(fi, lens, H):
+    q, kv, kr, cu_q, cu_k = _prefill_inputs(lens, H, "bf16", seed=120)
+    need = kda.kda_mla_prefill_workspace_size(len(lens), q.shape[0], H, q.dtype)
     ws = torch.full((need,), 0xA5, dtype=torch.uint8, device=DEV)
     o = torch.full(q.shape[:2] + (128,), 12345.0, dtype=q.dtype, device=DEV)
     lse = torch.full(q.shape[:2], 12345.0, device=DEV)
 
     def call():
         return fi.kda_mla_prefill(q.data_ptr(), kv.data_ptr(), kr.data_ptr(), cu_q.data_ptr(),
-                                  cu_k.data_ptr(), len(lens), q.shape[0], kv.shape[0], 2, 128, 64,
+                                  cu_k.data_ptr(), len(lens), q.shape[0], kv.shape[0], H, 128, 64,
                                   128, kda.KDA_BF16, SC, 1, o.data_ptr(), lse.data_ptr(),
                                   ws.data_ptr(), need, _stream())
 
@@ -140,7 +148,7 @@ def test_prefill_forced_timeout(fi, lens):
     assert torch.equal(o, sentinel) and bool((lse == 12345.0).all())
     assert call() == kda.KDA_OK                 # and the next call is a normal one
     assert fi.kda_mla_check(ws.data_ptr(), _stream()) == kda.KDA_OK
-    _check_prefill(lens, q, kv, kr, True, "bf16", o, lse)
+    _check_two_heads(lens, q, kv, kr, True, o, lse, skip=[n for n, x in enumerate(lens) if x == LONG])
 
 
 @pytest.mark.parametrize("H", [2, 20, 64])
