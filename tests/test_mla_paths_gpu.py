@@ -178,3 +178,21 @@ def test_decode_forced_timeout(fi, H, lens):
     assert call() == kda.KDA_OK
     assert fi.kda_mla_check(ws.data_ptr(), _stream()) == kda.KDA_OK
     _check_decode(q, cache, table, n, "bf16", o, lse)
+
+
+# ---- the example -------------------------------------------------------------------
+
+@pytest.mark.parametrize("heads,prompts,steps", [(16, (700, 64, 1500), 4), (3, (1, 130), 70)])
+def test_example_layer(heads, prompts, steps):
+    """The example's two forms agree.  Either rounds the keys or the queries, the
+    values, the weights, the latent outputs and the answers to bf16: about six
+    independent errors of at most 2^-8 of an answer's magnitude, of which the
+    largest of some thousand answers takes four times the mean."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "latent_attention.py")
+    spec = importlib.util.spec_from_file_location("latent_attention", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    assert module.run(heads, prompts, steps) <= 4 * 6 ** 0.5 * 2.0 ** -8
