@@ -9,6 +9,8 @@ loading fails with an error -- there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -433,17 +435,39 @@ MLA_LATENT, MLA_ROPE, MLA_NOPE, MLA_DV = 512, 64, 128, 128
 _MLA_ROW, _MLA_QK = MLA_LATENT + MLA_ROPE, MLA_NOPE + MLA_ROPE
 _MLA_SCALE = _MLA_QK ** -0.5
 _mla = None
+_calls = None
 
 
 def _mla_lib():
-    """The latent-attention entry points, bound once: a decode step launches
-    them every few tens of microseconds, so the checks and the marshalling in
-    front of them are kept short (raw addresses, one comparison per property,
-    no device or stream objects where the current ones are meant)."""
+    """The library, bound once."""
     global _mla
     if _mla is None:
         _mla = load()
     return _mla
+
+
+def _mla_calls():
+    """The latent-attention calls in their common form, compiled
+    (``csrc/py_mla.cpp``): a decode step launches them every few tens of
+    microseconds.  They give NotImplemented for what is not of that form; the
+    functions below then check and marshal it themselves."""
+    global _calls
+    if _calls is None:
+        from .build import CALLS_LIB
+        if not os.path.exists(CALLS_LIB):
+            raise RuntimeError(
+                "%s is not built; build it with `python -m serving_kda_chunked_gb300.build`"
+                % os.path.basename(CALLS_LIB))
+        lib = _mla_lib()
+        spec = importlib.util.spec_from_loader(
+            "_kda_torch", importlib.machinery.ExtensionFileLoader("_kda_torch", CALLS_LIB))
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
+            "kda_mla_append", "kda_mla_prefill", "kda_mla_prefill_workspace_size", "kda_mla_decode",
+            "kda_mla_decode_workspace_size")), KdaError)
+        _calls = module
+    return _calls
 
 
 def _first(name, t, ndim):
@@ -534,6 +558,11 @@ def kda_mla_append(c, k_r, slots, cache, *, positions=None, rope=None, interleav
     them; ``q_r`` [T, H, 64] (strided) is rotated into ``q_out`` (allocated if
     omitted).  Returns q_out (None without q_r).
     """
+    if stream is None:
+        done = (_calls or _mla_calls()).append(c, k_r, slots, cache, positions, rope, interleaved,
+                                               k_out, q_r, q_out)
+        if done is not NotImplemented:
+            return done
     dt, dev = _first("c", c, 2)
     T = c.shape[0]
     pc = _need("c", c, dt, (T, MLA_LATENT), dev, True)
@@ -599,6 +628,11 @@ def kda_mla_prefill(q, kv, k_r, cu_q, cu_k, *, scale=None, causal=True, o=None, 
     queries are the last tokens of their sequence's keys.  Returns
     (o [Tq, H, 128], lse [Tq, H] fp32).
     """
+    if stream is None:
+        done = (_calls or _mla_calls()).prefill(q, kv, k_r, cu_q, cu_k, scale, causal, o, lse,
+                                                workspace)
+        if done is not NotImplemented:
+            return done
     dt, dev = _first("q", q, 3)
     Tq, H, _ = q.shape
     pq = _need("q", q, dt, (Tq, H, _MLA_QK), dev)
@@ -629,6 +663,10 @@ def kda_mla_decode(q, cache, table, seq_lens, *, scale=None, o=None, lse=None, w
     ``scale`` defaults to 192 ** -0.5, that of the expanded heads.  Returns
     (o [B, H, 512], lse [B, H] fp32).
     """
+    if stream is None:
+        done = (_calls or _mla_calls()).decode(q, cache, table, seq_lens, scale, o, lse, workspace)
+        if done is not NotImplemented:
+            return done
     dt, dev = _first("q", q, 3)
     B, H, _ = q.shape
     pq = _need("q", q, dt, (B, H, _MLA_ROW), dev)

@@ -6,7 +6,9 @@ The same sources compiled with ``-DKDA_FAULT_INJECTION`` give
 ``libkda_faultinj.so``, a test-only copy of the library whose
 ``kda_test_force_timeout`` makes the prefill's bounded device wait give up on
 purpose (the tests use it to check the timeout path); both are built in one
-parallel pass.  Usage: ``python -m serving_kda_chunked_gb300.build [--force]``.
+parallel pass, and with them ``_kda_torch-<torch version>.so``: the calls of
+``csrc/py_mla.cpp``, compiled by the host compiler against the headers of the
+torch that is imported.  Usage: ``python -m serving_kda_chunked_gb300.build [--force]``.
 """
 from __future__ import annotations
 
@@ -15,6 +17,9 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
+
+import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -22,6 +27,8 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libkda.so")
 FAULTINJ_LIB = os.path.join(HERE, "libkda_faultinj.so")
+CALLS_SRC = os.path.join(CSRC, "py_mla.cpp")
+CALLS_LIB = os.path.join(HERE, "_kda_torch-%s.so" % torch.__version__)
 VARIANTS = ((LIB, "", []), (FAULTINJ_LIB, "faultinj", ["-DKDA_FAULT_INJECTION"]))
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -40,17 +47,30 @@ def nvcc() -> str:
     return p
 
 
+def _calls_command(out: str) -> list[str]:
+    tdir = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    cmd = [shutil.which(os.environ.get("CXX", "g++")) or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch.compiled_with_cxx11_abi(),
+           "-I", INCLUDE]
+    for inc in (sysconfig.get_paths()["include"], os.path.join(tdir, "include"),
+                os.path.join(cuda, "include")):
+        cmd += ["-isystem", inc]
+    return cmd + [CALLS_SRC, "-o", out, "-L" + os.path.join(tdir, "lib"), "-ltorch_python",
+                  "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+
+
 def sources() -> list[str]:
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
 def _deps() -> list[str]:
-    return (sources() + glob.glob(os.path.join(CSRC, "*.cuh"))
+    return (sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [CALLS_SRC]
             + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
-    for lib, _, _ in VARIANTS:
+    for lib in [lib for lib, _, _ in VARIANTS] + [CALLS_LIB]:
         if not os.path.exists(lib):
             return False
         t = os.path.getmtime(lib)
@@ -65,6 +85,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     cc = nvcc()
     procs = []
     links = []
+    calls_tmp = CALLS_LIB + ".tmp.%d" % os.getpid()
+    cmd = _calls_command(calls_tmp)
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    procs.append((CALLS_SRC, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     for lib, sub, vflags in VARIANTS:
         bdir = os.path.join(BUILD, sub) if sub else BUILD
         os.makedirs(bdir, exist_ok=True)
@@ -89,7 +114,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
             print(text, flush=True)
     if failed:
         msg = "\n".join("%s:\n%s" % (s, t) for s, t in failed)
-        raise RuntimeError("nvcc failed:\n" + msg)
+        raise RuntimeError("compiling failed:\n" + msg)
+    os.replace(calls_tmp, CALLS_LIB)
     for lib, objs in links:
         tmp = lib + ".tmp.%d" % os.getpid()
         cmd = [cc, *ARCH, "-shared", "-cudart", "shared", *objs, "-o", tmp]

@@ -180,6 +180,75 @@ def test_decode_forced_timeout(fi, H, lens):
     _check_decode(q, cache, table, n, "bf16", o, lse)
 
 
+# ---- the compiled calls and the interpreted ones -------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_calls_with_and_without_a_stream_agree(dtype):
+    """Without a stream the compiled calls run; with one the interpreted checks do."""
+    here = torch.cuda.current_stream()
+    lens = [(70, 70), (3, 40)]
+    q, kv, kr, cu_q, cu_k = _prefill_inputs(lens, 2, dtype, seed=140)
+    for kw in ({}, {"scale": 0.25, "causal": False}, {"scale": 1}):
+        a = kda.kda_mla_prefill(q, kv, kr, cu_q, cu_k, **kw)
+        b = kda.kda_mla_prefill(q, kv, kr, cu_q, cu_k, stream=here, **kw)
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    o, lse = torch.empty_like(a[0]), torch.empty_like(a[1])
+    got = kda.kda_mla_prefill(q, kv, kr, cu_q, cu_k, o=o, lse=lse)
+    assert got[0] is o and got[1] is lse
+
+    qd, cache, table, n = _decode_inputs([5, 90], 3, 16, dtype, seed=141)
+    a = kda.kda_mla_decode(qd, cache, table, n)
+    b = kda.kda_mla_decode(qd, cache, table, n, stream=here)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+    c = torch.randn(6, 640, device=DEV).to(q.dtype)
+    slots = torch.arange(6, dtype=torch.int32, device=DEV)
+    rope = torch.randn(8, 64, device=DEV)
+    qr = torch.randn(6, 2, 96, device=DEV).to(q.dtype)[..., :64]
+    caches, outs = [], []
+    for kw in ({}, {"stream": here}):
+        cache = torch.zeros(2, 16, 576, dtype=q.dtype, device=DEV)
+        k_out = torch.empty(6, 64, dtype=q.dtype, device=DEV)
+        outs.append((kda.kda_mla_append(c[:, :512], c[:, 512:576], slots, cache, positions=slots, rope=rope,
+                                        interleaved=True, k_out=k_out, q_r=qr, **kw), k_out, cache))
+        assert kda.kda_mla_append(c[:, :512], c[:, 512:576], slots, cache.clone(), **kw) is None
+    assert all(torch.equal(x, y) for x, y in zip(*outs))
+
+
+def test_wrong_arguments_on_the_gpu():
+    q, kv, kr, cu_q, cu_k = _prefill_inputs([(20, 20)], 2, "bf16", seed=142)
+    small = torch.empty(16, dtype=torch.uint8, device=DEV)
+    with pytest.raises(kda.KdaError):
+        kda.kda_mla_prefill(q, kv, kr, cu_q, cu_k, workspace=small)
+    with pytest.raises(ValueError, match="contiguous"):
+        kda.kda_mla_prefill(q.transpose(0, 1).contiguous().transpose(0, 1), kv, kr, cu_q, cu_k)
+    with pytest.raises(ValueError, match="k_r"):
+        kda.kda_mla_prefill(q, kv, kr[:-1], cu_q, cu_k)
+    with pytest.raises(ValueError, match="cu_k"):
+        kda.kda_mla_prefill(q, kv, kr, cu_q, cu_k.long())
+    with pytest.raises(TypeError, match="lse"):
+        kda.kda_mla_prefill(q, kv, kr, cu_q, cu_k, lse=3)
+    with pytest.raises(kda.KdaError):
+        kda.kda_mla_prefill(q, kv, kr, cu_q, cu_k, scale=float("nan"))
+
+    qd, cache, table, n = _decode_inputs([5, 90], 3, 16, "bf16", seed=143)
+    with pytest.raises(kda.KdaError):
+        kda.kda_mla_decode(qd, cache, table, n, workspace=small)
+    with pytest.raises(ValueError, match="seq_lens"):
+        kda.kda_mla_decode(qd, cache, table, n.cpu())
+    with pytest.raises(ValueError, match="o must"):
+        kda.kda_mla_decode(qd, cache, table, n, o=torch.empty(2, 3, 512, device=DEV))
+    with pytest.raises(ValueError, match="rope go together"):
+        kda.kda_mla_append(kv[:, 0].repeat(1, 2), kr, torch.arange(20, dtype=torch.int32, device=DEV),
+                           cache, rope=torch.empty(4, 64, device=DEV))
+    with pytest.raises(ValueError, match="q_out needs"):
+        kda.kda_mla_append(kv[:, 0].repeat(1, 2), kr, torch.arange(20, dtype=torch.int32, device=DEV), cache,
+                           q_out=torch.empty(20, 2, 64, dtype=torch.bfloat16, device=DEV))
+    for page in (8, 48):        # a page the library does not have
+        with pytest.raises(kda.KdaError):
+            kda.kda_mla_decode(qd, torch.zeros(3, page, 576, dtype=torch.bfloat16, device=DEV), table, n)
+
+
 # ---- the example -------------------------------------------------------------------
 
 @pytest.mark.parametrize("heads,prompts,steps", [(16, (700, 64, 1500), 4), (3, (1, 130), 70)])
