@@ -311,22 +311,22 @@ int prefill_parts(int32_t N, int64_t Tq, int32_t H) {
 
 // ---- absorbed form --------------------------------------------------------------
 // Shares and joins as in kda_mla_split.cuh, two CTAs per SM, groups of 8 heads,
-// tiles of 32 tokens.  A tile's rows go to shared memory (padded, so that 32
-// lanes read 32 rows without conflicts); a warp computes the scores of its 72
-// of the 576 channels (lane = token) for all heads, one warp per head takes the
-// softmax, and a thread owns 2 of the 512 output channels of all 8 heads.
-// Shared-memory reads bound it: 12 wavefronts for 32 FMAs in the scores.
-constexpr int HG = 8, TT = 32, LDR = ROW + 4, DTHREADS = 256;
-constexpr int DEC_FLOATS = HG * ROW + TT * LDR + 8 * TT * HG + TT * HG + HG;
+// tiles of 32 tokens.  A tile's rows go to shared memory (padded, so that the
+// lanes' reads meet different banks); a warp computes the scores of its 72 of the
+// 576 channels for all tokens and heads, one warp per head takes the softmax, and
+// a thread owns 4 of the 512 output channels of all 8 heads, for half the tokens.
+// Shared-memory reads bound it: 3840 wavefronts a tile for 2200 cycles of FMAs.
+constexpr int HG = 8, TT = 32, LDR = ROW + 4, LDS = TT + 4, DTHREADS = 256;
+constexpr int DEC_FLOATS = HG * LDR + TT * LDR + 8 * HG * LDS + TT * HG + HG;
 constexpr int DEC_CTAS = 320;                   // per launch, up to two per SM
 
 __global__ void __launch_bounds__(DTHREADS, 2) decode_simt_kernel(const SplitParams p, const float *q,
                                                                   const float *cache) {
     extern __shared__ __align__(16) float smf[];
-    float *qs = smf;                        // [8][576]
-    float *rows = qs + HG * ROW;            // [32][LDR]
-    float *red = rows + TT * LDR;           // [8 warps][8 heads][32 tokens]
-    float *ps = red + 8 * TT * HG;          // [32 tokens][8 heads]
+    float *qs = smf;                        // [8][LDR]
+    float *rows = qs + HG * LDR;            // [32][LDR]
+    float *red = rows + TT * LDR;           // [8 warps][8 heads][LDS]
+    float *ps = red + 8 * HG * LDS;         // [32 tokens][8 heads]
     float *fs = ps + TT * HG;               // rescale factor per head
     __shared__ ShareScratch<DTHREADS> scratch;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -344,11 +344,12 @@ __global__ void __launch_bounds__(DTHREADS, 2) decode_simt_kernel(const SplitPar
         __syncthreads();
         for (int e = tid; e < HG * ROW / 4; e += DTHREADS) {
             const int r = e / (ROW / 4), c = e % (ROW / 4) * 4;
-            store4(qs + r * ROW + c, r < nh ? load4(q + ((int64_t)w.b * p.H + h0 + r) * ROW + c)
+            store4(qs + r * LDR + c, r < nh ? load4(q + ((int64_t)w.b * p.H + h0 + r) * ROW + c)
                                             : make_float4(0.f, 0.f, 0.f, 0.f));
         }
         float m = -CUDART_INF_F, l = 0.f;   // of head `warp`, this lane's tokens
-        float acc[HG][2] = {};
+        float4 acc[HG] = {};                // channels 4 (tid % 128) .., tokens of half tid / 128
+        const int ch = 4 * (tid & 127), half = tid >> 7;
         for (int64_t i = w.lo; i < w.hi; ++i) {
             const int64_t t = i * TT;
             // lane = token: its row of the cache, or none
@@ -367,23 +368,42 @@ __global__ void __launch_bounds__(DTHREADS, 2) decode_simt_kernel(const SplitPar
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
             __syncthreads();
-            float sc[HG] = {};
-#pragma unroll 6
-            for (int c = warp * (ROW / 8); c < (warp + 1) * (ROW / 8); c += 4) {
-                const float4 x = load4(rows + lane * LDR + c);
+            // A lane takes 4 tokens x 4 heads of half the warp's channels: 8 reads
+            // of 16 bytes for 64 products (a token and 8 heads a lane: 9 for 32,
+            // and shared memory bounds it: 16 sequences of up to 2000 tokens, 8
+            // heads, 24 us in place of 23; of 8000 tokens, 109 and 105).
+            const int tg = lane >> 2, hg = lane >> 1 & 1, cs = lane & 1;
+            float sc[4][4] = {};
+#pragma unroll 3
+            for (int g = 0; g < ROW / 64; ++g) {
+                const int c = ((warp * (ROW / 64) + g) * 2 + cs) * 4;
+                float4 x[4];
 #pragma unroll
-                for (int h = 0; h < HG; ++h) {
-                    const float4 y = load4(qs + h * ROW + c);
-                    sc[h] += x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
+                for (int i = 0; i < 4; ++i) x[i] = load4(rows + (4 * tg + i) * LDR + c);
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const float4 y = load4(qs + (4 * hg + h) * LDR + c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        sc[i][h] += x[i].x * y.x + x[i].y * y.y + x[i].z * y.z + x[i].w * y.w;
                 }
             }
+            // the lanes of the two halves of the channels keep two heads each
 #pragma unroll
-            for (int h = 0; h < HG; ++h) red[(warp * HG + h) * TT + lane] = sc[h];
+            for (int h = 0; h < 2; ++h) {
+                float z[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float give = cs ? sc[i][h] : sc[i][h + 2], have = cs ? sc[i][h + 2] : sc[i][h];
+                    z[i] = have + __shfl_xor_sync(0xffffffffu, give, 1);
+                }
+                store4(red + (warp * HG + 4 * hg + 2 * cs + h) * LDS + 4 * tg, make_float4(z[0], z[1], z[2], z[3]));
+            }
             __syncthreads();
             {                               // head `warp`, token `lane`
                 float x = 0.f;
 #pragma unroll
-                for (int v = 0; v < 8; ++v) x += red[(v * HG + warp) * TT + lane];
+                for (int v = 0; v < 8; ++v) x += red[(v * HG + warp) * LDS + lane];
                 x = at >= 0 ? x * p.scale_log2 : -CUDART_INF_F;
                 const float top = fmaxf(m, warp_max(x));
                 const float ref = top == -CUDART_INF_F ? 0.f : top;
@@ -395,14 +415,20 @@ __global__ void __launch_bounds__(DTHREADS, 2) decode_simt_kernel(const SplitPar
             }
             __syncthreads();
 #pragma unroll
-            for (int h = 0; h < HG; ++h) { acc[h][0] *= fs[h]; acc[h][1] *= fs[h]; }
-#pragma unroll 8
-            for (int r = 0; r < TT; ++r) {
-                const float2 v = *reinterpret_cast<const float2 *>(rows + r * LDR + 2 * tid);
+            for (int h = 0; h < HG; ++h) {
+                const float f = fs[h];
+                acc[h].x *= f; acc[h].y *= f; acc[h].z *= f; acc[h].w *= f;
+            }
+#pragma unroll 4
+            for (int r = half * (TT / 2); r < (half + 1) * (TT / 2); ++r) {
+                const float4 v = load4(rows + r * LDR + ch);
                 const float4 a = load4(ps + r * HG), c = load4(ps + r * HG + 4);
                 const float e[HG] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
 #pragma unroll
-                for (int h = 0; h < HG; ++h) { acc[h][0] += e[h] * v.x; acc[h][1] += e[h] * v.y; }
+                for (int h = 0; h < HG; ++h) {
+                    acc[h].x += e[h] * v.x; acc[h].y += e[h] * v.y;
+                    acc[h].z += e[h] * v.z; acc[h].w += e[h] * v.w;
+                }
             }
         }
         // the segment's end
@@ -418,15 +444,22 @@ __global__ void __launch_bounds__(DTHREADS, 2) decode_simt_kernel(const SplitPar
                 *reinterpret_cast<float2 *>(p.stat + (slot * HG + warp) * 2) = make_float2(m, l);
             }
         }
-        __syncthreads();                    // fs has been read
+        __syncthreads();                    // fs and the rows have been read
         if (lane == 0) fs[warp] = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+        // the halves of the tokens: each thread gives the other one four heads
+#pragma unroll
+        for (int h = 0; h < HG; ++h)
+            if (h / 4 != half) store4(rows + h * LDR + ch, acc[h]);
         __syncthreads();
 #pragma unroll
         for (int h = 0; h < HG; ++h)
-            if (h < nh) {
+            if (h / 4 == half && h < nh) {
                 float *to = whole ? (float *)p.o + ((int64_t)w.b * p.H + h0 + h) * LATENT
                                   : p.part + (slot * HG + h) * LATENT;
-                *reinterpret_cast<float2 *>(to + 2 * tid) = make_float2(acc[h][0] * fs[h], acc[h][1] * fs[h]);
+                const float4 x = load4(rows + h * LDR + ch);
+                const float f = fs[h];
+                store4(to + ch, make_float4((acc[h].x + x.x) * f, (acc[h].y + x.y) * f, (acc[h].z + x.z) * f,
+                                            (acc[h].w + x.w) * f));
             }
     } while (w.next(p, share));
 }
