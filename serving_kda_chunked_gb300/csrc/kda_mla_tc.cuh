@@ -37,6 +37,11 @@ __device__ __forceinline__ void tma4(uint32_t dst, const CUtensorMap *m, int c0,
                  :: "r"(dst), "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(mbar))
                  : "memory");
 }
+// The same box to L2 only.
+__device__ __forceinline__ void tma4_prefetch(const CUtensorMap *m, int c0, int c1, int c2, int c3) {
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];"
+                 :: "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(c3) : "memory");
+}
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *m) {
     asm volatile("prefetch.tensormap [%0];" :: "l"(m) : "memory");
 }
