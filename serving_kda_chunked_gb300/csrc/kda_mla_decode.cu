@@ -37,6 +37,7 @@ namespace {
 constexpr int TOK = 64, CHUNKS = ROW / 64;                  // tokens a tile, 128-byte chunks a row
 constexpr uint32_t GROUP = CHUNKS * 1024;                   // 8 tokens
 constexpr uint32_t STAGE = 8 * GROUP;
+constexpr int OVER = 2;                                     // tiles' time to begin and end a sequence
 constexpr int THREADS = 320, W_MMA = 8, W_LOAD = 9;
 constexpr int MAX_CTAS = 160;                               // per launch, up to one wave
 constexpr float RESCALE = 8.f;                              // see the softmax below
@@ -119,7 +120,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     fence_before_sync();
-    const Share share = find_share<TOK, THREADS, N, __nv_bfloat16>(p, *scratch);
+    const Share share = find_share<TOK, OVER, THREADS, N, __nv_bfloat16>(p, *scratch);
     fence_after_sync();
     const uint32_t tmem = warp_uniform(*tmem_slot);
     const uint32_t smb = warp_uniform(smem_addr(sm));
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
     }
 
     if (share.busy && !forced) {
-        Walk<TOK> w;
+        Walk<TOK, OVER> w;
         w.start(p, share);
         if (warp == W_LOAD) {
             // ---- loads: the table is read 32 entries at a time; what a tile

@@ -318,6 +318,7 @@ int prefill_parts(int32_t N, int64_t Tq, int32_t H) {
 // Shared-memory reads bound it: 3840 wavefronts a tile for 2200 cycles of FMAs.
 constexpr int HG = 8, TT = 32, LDR = ROW + 4, LDS = TT + 4, DTHREADS = 256;
 constexpr int DEC_FLOATS = HG * LDR + TT * LDR + 8 * HG * LDS + TT * HG + HG;
+constexpr int OVER = 1;                         // tiles' time to begin and end a sequence
 constexpr int DEC_CTAS = 320;                   // per launch, up to two per SM
 
 __global__ void __launch_bounds__(DTHREADS, 2) decode_simt_kernel(const SplitParams p, const float *q,
@@ -333,10 +334,10 @@ __global__ void __launch_bounds__(DTHREADS, 2) decode_simt_kernel(const SplitPar
     const int h0 = blockIdx.x % p.groups * HG, nh = min(HG, p.H - h0);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Share share = find_share<TT, DTHREADS, HG, float>(p, scratch);
+    const Share share = find_share<TT, OVER, DTHREADS, HG, float>(p, scratch);
     if (tid == 0) p.status[blockIdx.x] = 0;
     if (!share.busy) return;
-    Walk<TT> w;
+    Walk<TT, OVER> w;
     w.start(p, share);
     const int shift = 31 - __clz(p.page);
     do {

@@ -265,3 +265,17 @@ def test_example_layer(heads, prompts, steps):
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)
     assert module.run(heads, prompts, steps) <= 4 * 6 ** 0.5 * 2.0 ** -8
+
+
+# ---- shares of many sequences ---------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("lens", [
+    [1] * 400, [65, 0, 0, 1, 64, 63] * 30, [5000] + [3] * 50, [3] * 50 + [5000], [129] * 151, [1, 20000, 1],
+])
+def test_decode_shares(dtype, lens):
+    """Every token in exactly one share, whatever the lengths."""
+    H = 2
+    q, cache, table, n = _decode_inputs(lens, H, 32, dtype, seed=150)
+    o, lse = _call_decode(q, cache, table, n)
+    _check_decode(q, cache, table, n, dtype, o, lse)
