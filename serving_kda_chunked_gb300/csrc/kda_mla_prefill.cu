@@ -329,10 +329,6 @@ __global__ void __launch_bounds__(Cfg<TILES>::THREADS, 3 - TILES) prefill_kernel
                         mbar_arrive_expect_tx(&q_full[0], 3 * QBLOCK);
                         tma4(smb + SM_Q, &p.tm_q, 0, ent.row0, 0, h, &q_full[0]);
                     }
-                    if (nB > 0) {
-                        mbar_arrive_expect_tx(&q_full[1], 3 * QBLOCK);
-                        tma4(smb + SM_Q + 3 * QBLOCK, &p.tm_q, 0, ent.row0 + BQ, 0, h, &q_full[1]);
-                    }
                 }
                 __syncwarp();
                 for (int j = 0; ok && j < n; ++j) {
@@ -348,6 +344,10 @@ __global__ void __launch_bounds__(Cfg<TILES>::THREADS, 3 - TILES) prefill_kernel
                             if (b < 2) tma4(dst, &p.tm_k, 0, t, b, h, &full[slot]);
                             else if (b == 2) tma4(dst, &p.tm_r, 0, t, 0, 0, &full[slot]);
                             else tma4(dst, &p.tm_v, 0, t + (b - 3) * (BK / 2), 2, h, &full[slot]);
+                            if (j == 0 && b == 2 && nB > 0) {       // not before what tile A begins with
+                                mbar_arrive_expect_tx(&q_full[1], 3 * QBLOCK);
+                                tma4(smb + SM_Q + 3 * QBLOCK, &p.tm_q, 0, ent.row0 + BQ, 0, h, &q_full[1]);
+                            }
                         }
                         __syncwarp();
                         ++q;
@@ -404,16 +404,17 @@ __global__ void __launch_bounds__(Cfg<TILES>::THREADS, 3 - TILES) prefill_kernel
                 };
                 uint32_t both = 0;
                 if (nA > 0) ok &= wait_one(&q_full[0], 0);
-                if (nB > 0) ok &= wait_one(&q_full[1], 0);
                 if constexpr (TILES == 2) {
                     both = min(nA, nB);
                     for (uint32_t j = 0; ok && j < both; ++j) {     // S_A(j) O_B(j-1) S_B(j) O_A(j)
                         scores(0, j, true, false);
                         if (j > 0) outputs(1, j - 1, false, true);
+                        else ok &= wait_one(&q_full[1], 0);
                         scores(1, j, false, true);
                         outputs(0, j, true, false);
                     }
                     if (ok && both > 0) outputs(1, both - 1, false, true);
+                    if (both == 0 && nB > 0) ok &= wait_one(&q_full[1], 0);
                 }
                 if constexpr (TILES == 1) {                 // S(0) S(1) O(0) S(2) O(1) ...
                     if (ok && n > 0) scores(0, 0, true, true);
