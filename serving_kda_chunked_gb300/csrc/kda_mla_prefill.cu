@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const PreParams p, int cap, 
     constexpr int ROWS = Cfg<TILES>::ROWS, BK = Cfg<TILES>::BK, NB = 1024;
     __shared__ int start[NB];
     __shared__ int64_t warp_tot[32];
-    __shared__ int64_t work;
+    __shared__ unsigned long long work;
     __shared__ int blocks, slots, cuts, listed;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -184,21 +184,28 @@ __global__ void __launch_bounds__(1024) plan_kernel(const PreParams p, int cap, 
         return x;
     };
     auto tiles_of = [](const Entry &x) { return max(x.nA, x.nB); };
+    // a thread's first block, which is mostly its only one, is worked out once
+    Entry own = {};
+    if (tid < E) own = entry(tid);
+    auto get = [&](int e) { return e == tid ? own : entry(e); };
     // key tiles of all blocks, for one head
-    mine = 0;
-    for (int e = tid; e < E; e += 1024) mine += tiles_of(entry(e));
-    const int64_t sum = block_scan(mine);
-    if (tid == 1023) work = sum;
-    __syncthreads();
+    if (may_cut) {
+        unsigned long long tiles = 0;
+        for (int e = tid; e < E; e += 1024) tiles += tiles_of(get(e));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+        if (lane == 0 && tiles) atomicAdd(&work, tiles);
+        __syncthreads();
+    }
     // Where the CTAs are few, a block with more key tiles than an SM's share is cut
     // into parts of at most that: over all heads fewer than `sms` blocks and
     // 2 sms parts.
-    int64_t share = (work * p.H + sms - 1) / sms;
+    int64_t share = may_cut ? ((int64_t)work * p.H + sms - 1) / sms : 0;
     if (share < MIN_PART / BK) share = MIN_PART / BK;
     auto parts_of = [&](int tiles) { return may_cut && tiles > share ? (int)((tiles + share - 1) / share) : 1; };
     auto bin_of = [&](int tiles) { return NB - 1 - min(tiles, NB - 1); };
     for (int e = tid; e < E; e += 1024) {
-        const int tiles = tiles_of(entry(e)), parts = parts_of(tiles);
+        const int tiles = tiles_of(get(e)), parts = parts_of(tiles);
         for (int k = 0; k < parts; ++k)
             atomicAdd(&start[bin_of((int)((int64_t)tiles * (k + 1) / parts - (int64_t)tiles * k / parts))], 1);
     }
@@ -209,7 +216,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const PreParams p, int cap, 
     if (tid == 1023) listed = incl;
     __syncthreads();
     for (int e = tid; e < E; e += 1024) {
-        const Entry whole = entry(e);
+        const Entry whole = get(e);
         const int tiles = tiles_of(whole), parts = parts_of(tiles);
         const int base = parts > 1 ? atomicAdd(&slots, parts) : -1;
         for (int k = 0; k < parts; ++k) {
