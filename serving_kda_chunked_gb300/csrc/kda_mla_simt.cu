@@ -7,6 +7,15 @@ namespace kda {
 namespace mla {
 namespace {
 
+// Two float32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)),
+          "l"(reinterpret_cast<uint64_t &>(c)));
+    return d;
+}
 __device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
@@ -29,6 +38,8 @@ __device__ __forceinline__ float warp_sum(float x) {
 // asynchronous copies one tile ahead, values while the scores are computed; two
 // blocks an SM fill each other's gaps.  (With 4 x 4 and 2 x 4 pieces, shared
 // memory held three prompts up to 777 tokens with four heads at 95 and 92 us.)
+// The output's FMAs go two an instruction: 74 us in place of 78.  In the scores
+// that takes 32 more sums or 4 more reads: 80 and 78 us.
 // With few (queries, head) blocks the keys are cut into up to SPLITS parts,
 // whose unnormalised results a second kernel joins.
 constexpr int BQ = 32, BK = 32, LDQ = DQK + 4, LDP = BQ + 4, SPLITS = 8, PTHREADS = 128;
@@ -100,6 +111,8 @@ __global__ void __launch_bounds__(PTHREADS, 2) prefill_simt_kernel(const Prefill
     float *Pt = Vs + BK * DV;              // [32 keys][LDP], query fastest
     float *fs = Pt + BK * LDP;             // [32] factors per query
     const int tid = threadIdx.x, h = blockIdx.y, H = p.H;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (sp.parts > 1 && tid == 0 && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
         *static_cast<int32_t *>(p.ws) = 0;  // no wait here can give up: the call's status is clear
     PreUnit u;                             // long blocks first: the last queries see the most keys
@@ -140,7 +153,8 @@ __global__ void __launch_bounds__(PTHREADS, 2) prefill_simt_kernel(const Prefill
     const float sl = p.scale * 1.4426950408889634f;
     const int64_t qi = u.i0 + row;
     const int64_t end = p.causal ? qi + s.nk - s.nq + 1 : s.nk;           // keys the row sees
-    float m = -CUDART_INF_F, l = 0.f, acc[8][16];
+    alignas(16) float acc[8][16];
+    float m = -CUDART_INF_F, l = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -226,12 +240,15 @@ __global__ void __launch_bounds__(PTHREADS, 2) prefill_simt_kernel(const Prefill
 #pragma unroll
             for (int g = 0; g < 4; ++g) v[g] = load4(Vs + k * DV + 32 * g + 4 * lc);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 8; ++i) {
+                const float2 ww = make_float2(w[i], w[i]);
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    acc[i][4 * g] += w[i] * v[g].x; acc[i][4 * g + 1] += w[i] * v[g].y;
-                    acc[i][4 * g + 2] += w[i] * v[g].z; acc[i][4 * g + 3] += w[i] * v[g].w;
+                    float2 &lo = *reinterpret_cast<float2 *>(&acc[i][4 * g]), &hi = *reinterpret_cast<float2 *>(&acc[i][4 * g + 2]);
+                    lo = fma2(ww, make_float2(v[g].x, v[g].y), lo);
+                    hi = fma2(ww, make_float2(v[g].z, v[g].w), hi);
                 }
+            }
         }
         __syncthreads();
         if (j0 + BK < u.j1) load_values(j0 + BK); else copy_commit();
@@ -273,6 +290,7 @@ __global__ void __launch_bounds__(PTHREADS, 2) prefill_simt_kernel(const Prefill
 // Joins the parts of (32 queries, head); a warp takes a query, a lane 4 channels.
 __global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillArgs p, const PreSplit sp) {
     const int lane = threadIdx.x & 31, r = blockIdx.z * 8 + (threadIdx.x >> 5), h = blockIdx.y;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     PreUnit u;
     if (!pre_unit(p, blockIdx.x, 0, sp.parts, u) || u.parts == 1 || u.i0 + r >= u.s.nq) return;
     const int64_t at = (u.s.q0 + u.i0 + r) * p.H + h, step = p.Tq * p.H;
@@ -315,7 +333,9 @@ int prefill_parts(int32_t N, int64_t Tq, int32_t H) {
 // lanes' reads meet different banks); a warp computes the scores of its 72 of the
 // 576 channels for all tokens and heads, one warp per head takes the softmax, and
 // a thread owns 4 of the 512 output channels of all 8 heads, for half the tokens.
-// Shared-memory reads bound it: 3840 wavefronts a tile for 2200 cycles of FMAs.
+// Shared-memory reads bound it: 3840 wavefronts a tile, with copies and sums 5100,
+// for 1700 cycles of FMAs (16 sequences of 8000 tokens, 8 heads: 89 us, 97 with
+// one FMA an instruction in the output; HBM would take 44).
 constexpr int HG = 8, TT = 32, LDR = ROW + 4, LDS = TT + 4, DTHREADS = 256;
 constexpr int DEC_FLOATS = HG * LDR + TT * LDR + 8 * HG * LDS + TT * HG + HG;
 constexpr int OVER = 1;                         // tiles' time to begin and end a sequence
@@ -349,7 +369,7 @@ __global__ void __launch_bounds__(DTHREADS, 2) decode_simt_kernel(const SplitPar
                                             : make_float4(0.f, 0.f, 0.f, 0.f));
         }
         float m = -CUDART_INF_F, l = 0.f;   // of head `warp`, this lane's tokens
-        float4 acc[HG] = {};                // channels 4 (tid % 128) .., tokens of half tid / 128
+        float2 acc[HG][2] = {};             // channels 4 (tid % 128) .., tokens of half tid / 128
         const int ch = 4 * (tid & 127), half = tid >> 7;
         for (int64_t i = w.lo; i < w.hi; ++i) {
             const int64_t t = i * TT;
@@ -418,7 +438,7 @@ __global__ void __launch_bounds__(DTHREADS, 2) decode_simt_kernel(const SplitPar
 #pragma unroll
             for (int h = 0; h < HG; ++h) {
                 const float f = fs[h];
-                acc[h].x *= f; acc[h].y *= f; acc[h].z *= f; acc[h].w *= f;
+                acc[h][0].x *= f; acc[h][0].y *= f; acc[h][1].x *= f; acc[h][1].y *= f;
             }
 #pragma unroll 4
             for (int r = half * (TT / 2); r < (half + 1) * (TT / 2); ++r) {
@@ -427,8 +447,9 @@ __global__ void __launch_bounds__(DTHREADS, 2) decode_simt_kernel(const SplitPar
                 const float e[HG] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
 #pragma unroll
                 for (int h = 0; h < HG; ++h) {
-                    acc[h].x += e[h] * v.x; acc[h].y += e[h] * v.y;
-                    acc[h].z += e[h] * v.z; acc[h].w += e[h] * v.w;
+                    const float2 ee = make_float2(e[h], e[h]);
+                    acc[h][0] = fma2(ee, make_float2(v.x, v.y), acc[h][0]);
+                    acc[h][1] = fma2(ee, make_float2(v.z, v.w), acc[h][1]);
                 }
             }
         }
@@ -450,7 +471,7 @@ __global__ void __launch_bounds__(DTHREADS, 2) decode_simt_kernel(const SplitPar
         // the halves of the tokens: each thread gives the other one four heads
 #pragma unroll
         for (int h = 0; h < HG; ++h)
-            if (h / 4 != half) store4(rows + h * LDR + ch, acc[h]);
+            if (h / 4 != half) store4(rows + h * LDR + ch, make_float4(acc[h][0].x, acc[h][0].y, acc[h][1].x, acc[h][1].y));
         __syncthreads();
 #pragma unroll
         for (int h = 0; h < HG; ++h)
@@ -459,8 +480,8 @@ __global__ void __launch_bounds__(DTHREADS, 2) decode_simt_kernel(const SplitPar
                                   : p.part + (slot * HG + h) * LATENT;
                 const float4 x = load4(rows + h * LDR + ch);
                 const float f = fs[h];
-                store4(to + ch, make_float4((acc[h].x + x.x) * f, (acc[h].y + x.y) * f, (acc[h].z + x.z) * f,
-                                            (acc[h].w + x.w) * f));
+                store4(to + ch, make_float4((acc[h][0].x + x.x) * f, (acc[h][0].y + x.y) * f,
+                                            (acc[h][1].x + x.z) * f, (acc[h][1].y + x.w) * f));
             }
     } while (w.next(p, share));
 }
@@ -483,11 +504,22 @@ cudaError_t launch_prefill_simt(const PrefillArgs &a, cudaStream_t st) {
     sp.part = reinterpret_cast<float *>((uint8_t *)a.ws + 256);
     sp.stat = sp.part + (int64_t)sp.parts * a.Tq * a.H * DV;
     const unsigned tiles = (unsigned)(a.Tq / BQ + a.N);     // at most
-    prefill_simt_kernel<<<dim3(tiles, a.H, sp.parts), PTHREADS, PRE_FLOATS * sizeof(float), st>>>(a, sp);
-    e = cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(tiles, a.H, sp.parts);
+    cfg.blockDim = dim3(PTHREADS);
+    cfg.dynamicSmemBytes = PRE_FLOATS * sizeof(float);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, prefill_simt_kernel, a, sp);
     if (e != cudaSuccess || sp.parts == 1) return e;
-    prefill_join_kernel<<<dim3(tiles, a.H, BQ / 8), 256, 0, st>>>(a, sp);
-    return cudaGetLastError();
+    cfg.gridDim = dim3(tiles, a.H, BQ / 8);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, prefill_join_kernel, a, sp);
 }
 
 cudaError_t launch_decode_simt(const DecodeArgs &a, cudaStream_t st) {
