@@ -57,7 +57,7 @@ def _calls_command(out: str) -> list[str]:
                 os.path.join(cuda, "include")):
         cmd += ["-isystem", inc]
     return cmd + [CALLS_SRC, "-o", out, "-L" + os.path.join(tdir, "lib"), "-ltorch_python",
-                  "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+                  "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
 
 
 def sources() -> list[str]:

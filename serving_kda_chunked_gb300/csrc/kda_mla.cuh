@@ -59,6 +59,16 @@ inline cudaError_t sm_count(int *nsm) {
     return e != cudaSuccess ? e : cudaDeviceGetAttribute(nsm, cudaDevAttrMultiProcessorCount, dev);
 }
 
+// Two float32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)),
+          "l"(reinterpret_cast<uint64_t &>(c)));
+    return d;
+}
+
 // Queries [bos, eos) of sequence n and its keys, from clamped offsets.
 struct SeqSpan { int64_t q0, k0; int nq, nk; };
 __device__ __forceinline__ SeqSpan seq_span(const int32_t *cu_q, const int32_t *cu_k, int n,

@@ -3,9 +3,9 @@
 //
 // A decode step's kernels take about 10 us.  Interpreted checks, three
 // allocations through Python's argument parser and a call with 18 converted
-// arguments took 25 us in front of them; the same here takes 11 us, and 5 where
-// the caller gives the outputs and the workspace.  An append (2 us on the GPU)
-// went from 15 to 4 us.
+// arguments took 25 us in front of them; the same here takes 8 us (11 with
+// at::empty), and 5 where the caller gives the outputs and the workspace.  An
+// append (2 us on the GPU) went from 15 to 4 us.
 //
 // Whatever is not of the common form (another type, shape, device or stream, an
 // argument that is wrong) gives NotImplemented before anything is launched: the
@@ -14,7 +14,8 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -67,8 +68,8 @@ struct Call {
         return ok ? &t : nullptr;
     }
     at::Tensor make(at::ScalarType of, std::initializer_list<int64_t> shape) const {
-        return at::empty(at::IntArrayRef(shape.begin(), shape.size()),
-                         at::TensorOptions().dtype(of).device(at::Device(at::kCUDA, dev)));
+        return at::Tensor(at::detail::empty_cuda(at::IntArrayRef(shape.begin(), shape.size()), of,
+                                                 at::Device(at::kCUDA, dev), std::nullopt));
     }
     // An output: the caller's, or a new one.
     at::Tensor out(PyObject *o, at::ScalarType of, std::initializer_list<int64_t> shape) {
@@ -104,20 +105,24 @@ PyObject *pair(const at::Tensor &a, const at::Tensor &b) {
     return t;
 }
 
-// The workspace: the caller's, or a new one of `need` bytes.
+// The workspace: the caller's, or one of `need` bytes until the call returns (the
+// allocator hands it out again in the stream's order).
 struct Scratch {
-    at::Tensor t;
+    c10::DataPtr own;
+    void *data = nullptr;
     uint64_t bytes = 0;
     void get(Call &c, PyObject *o, uint64_t need) {
         if (!c.ok) return;
         if (o == Py_None) {
-            if (need) t = c.make(at::kByte, {(int64_t)need});
+            if (!need) return;
+            own = c10::cuda::CUDACachingAllocator::get()->allocate(need);
+            data = own.get();
+            bytes = need;
         } else if (const at::Tensor *w = c.need(o, at::kByte, {-1})) {
-            t = *w;
+            data = w->data_ptr();
+            bytes = (uint64_t)w->numel();
         }
-        bytes = t.defined() ? (uint64_t)t.numel() : 0;
     }
-    void *data() const { return t.defined() ? t.data_ptr() : nullptr; }
 };
 
 // prefill(q, kv, k_r, cu_q, cu_k, scale, causal, o, lse, workspace)
@@ -149,7 +154,7 @@ PyObject *prefill(PyObject *, PyObject *const *a, Py_ssize_t n) {
     Py_BEGIN_ALLOW_THREADS
     st = prefill_fn(q->data_ptr(), kv->data_ptr(), kr->data_ptr(), cq->data_ptr<int32_t>(),
                     ck->data_ptr<int32_t>(), (int32_t)N, Tq, Tk, (int32_t)H, NOPE, ROPE, DV, c.code(), scale,
-                    causal, o.data_ptr(), lse.data_ptr<float>(), w.data(), w.bytes, stream);
+                    causal, o.data_ptr(), lse.data_ptr<float>(), w.data, w.bytes, stream);
     Py_END_ALLOW_THREADS
     return st == KDA_OK ? pair(o, lse) : failed("kda_mla_prefill", st);
     END_HANDLE_TH_ERRORS
@@ -179,7 +184,7 @@ PyObject *decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
     st = decode_fn(q->data_ptr(), cache->data_ptr(), table->data_ptr<int32_t>(), lens->data_ptr<int32_t>(),
                    (int32_t)B, (int32_t)H, (int32_t)cache->size(0), (int32_t)cache->size(1),
                    (int32_t)table->size(1), LATENT, ROPE, c.code(), scale, o.data_ptr(),
-                   lse.data_ptr<float>(), w.data(), w.bytes, stream);
+                   lse.data_ptr<float>(), w.data, w.bytes, stream);
     Py_END_ALLOW_THREADS
     return st == KDA_OK ? pair(o, lse) : failed("kda_mla_decode", st);
     END_HANDLE_TH_ERRORS
