@@ -65,6 +65,7 @@ constexpr float RESCALE = 8.f;
 constexpr int MAX_SMS = 160;
 constexpr int SLOTS = 2 * MAX_SMS;           // parts with results of their own, over all heads
 constexpr int CUTS = MAX_SMS;                // blocks that are cut, over all heads
+constexpr int MAX_TAIL = 320;                // blocks of a call whose last round is looked at
 constexpr int MIN_PART = 512;                // keys that are worth a part
 
 // A block of up to ROWS queries of a sequence, or a part of its keys; one CTA per
@@ -120,7 +121,8 @@ __global__ void __launch_bounds__(1024) plan_kernel(const PreParams p, int cap, 
     __shared__ int start[NB];
     __shared__ int64_t warp_tot[32];
     __shared__ unsigned long long work;
-    __shared__ int blocks, slots, cuts, listed;
+    __shared__ int blocks, slots, cuts, listed, longest, first_work;
+    __shared__ int sizes[MAX_TAIL];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -157,7 +159,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const PreParams p, int cap, 
     }
     start[tid] = 0;
     if (tid == 1023) blocks = (int)(at < cap ? at : cap);
-    if (tid == 0) { work = 0; slots = 0; cuts = 0; listed = 0; }
+    if (tid == 0) { work = 0; slots = 0; cuts = 0; listed = 0; longest = 0; first_work = 0; }
     __syncthreads();
     const int E = blocks;
     auto entry = [&](int e) {
@@ -191,10 +193,17 @@ __global__ void __launch_bounds__(1024) plan_kernel(const PreParams p, int cap, 
     // key tiles of all blocks, for one head
     if (may_cut) {
         unsigned long long tiles = 0;
-        for (int e = tid; e < E; e += 1024) tiles += tiles_of(get(e));
+        int most = 0;
+        for (int e = tid; e < E; e += 1024) {
+            const int t = tiles_of(get(e));
+            tiles += t;
+            most = max(most, t);
+            if (TILES == 2 && e < MAX_TAIL) sizes[e] = t;
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
-        if (lane == 0 && tiles) atomicAdd(&work, tiles);
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 0 && tiles) { atomicAdd(&work, tiles); atomicMax(&longest, most); }
         __syncthreads();
     }
     // Where the CTAs are few, a block with more key tiles than an SM's share is cut
@@ -202,7 +211,38 @@ __global__ void __launch_bounds__(1024) plan_kernel(const PreParams p, int cap, 
     // 2 sms parts.
     int64_t share = may_cut ? ((int64_t)work * p.H + sms - 1) / sms : 0;
     if (share < MIN_PART / BK) share = MIN_PART / BK;
-    auto parts_of = [&](int tiles) { return may_cut && tiles > share ? (int)((tiles + share - 1) / share) : 1; };
+    // Without such blocks the last round of CTAs can leave many SMs idle: those
+    // blocks that do not fill a round, the ones with the fewest keys, are cut into
+    // up to 4 parts if that ends sooner (4 prompts of up to 512 queries after up to
+    // 7700 tokens, 224 CTAs: 191 us, 213 without; with lengths that differ more the
+    // longest-first order fills the SMs by itself, and looking costs 1 us).
+    const int rounds = TILES == 2 && may_cut && longest <= min(share, (int64_t)1 << 20) && E <= MAX_TAIL ? E * p.H / sms : 0;
+    const int whole = rounds * sms / p.H;                   // blocks that stay whole
+    const int full = whole * p.H - (rounds - 1) * sms;      // SMs that run `rounds` of them, not one fewer
+    int rank = 0, cut_into = 1;
+    const bool tail = whole > 0 && E > whole && full > 0;
+    if (tail) {
+        if (tid < E)
+            for (int i = 0; i < E; ++i) rank += sizes[i] > sizes[tid] || (sizes[i] == sizes[tid] && i < tid);
+        if (tid < E && rank < whole) atomicAdd(&first_work, sizes[tid]);
+        __syncthreads();
+        // a lane tries lane + 1 parts, all blocks as long as the mean of their kind
+        const int parts = lane + 1, rest = (E - whole) * p.H;
+        const int w = first_work / whole, t = (int)(work - first_work) / (E - whole);
+        const int q = max((t + parts - 1) / parts, 1);
+        int end = 1 << 30;
+        if (parts == 1 || (parts <= 4 && q >= MIN_PART / BK && rest * parts <= SLOTS)) {
+            int i = 0;
+            while (full * i + (sms - full) * ((w + i * q) / q) < rest * parts) ++i;
+            end = rounds * w + i * q + (parts > 1 ? 4 : 0); // the join costs about four key tiles' time
+        }
+        const int best = __reduce_min_sync(0xffffffffu, end);
+        cut_into = __ffs(__ballot_sync(0xffffffffu, best == end));
+    }
+    auto parts_of = [&](int tiles) {
+        if (tail) return rank < whole ? 1 : max(min(cut_into, tiles), 1);
+        return may_cut && tiles > share ? (int)((tiles + share - 1) / share) : 1;
+    };
     auto bin_of = [&](int tiles) { return NB - 1 - min(tiles, NB - 1); };
     for (int e = tid; e < E; e += 1024) {
         const int tiles = tiles_of(get(e)), parts = parts_of(tiles);
@@ -713,7 +753,7 @@ template <int TILES> cudaError_t launch(const PrefillArgs &a, cudaStream_t st) {
     // head: 106 us whole, 47 us cut; one prompt of 4096 tokens, four heads: 60 and
     // 46 us.  Where nothing is cut after all it costs 3 to 5 us (a join kernel and
     // CTAs with nothing to do), and with more CTAs the longest-first order balances
-    // by itself (8 packed prompts, 864 CTAs: 125 us).
+    // by itself.
     const bool may_cut = a.Tq / G::ROWS * a.H < 2 * sms && a.H < 2 * sms && a.Tk > MIN_PART;
     e = cudaLaunchKernelEx(&cfg, plan_kernel<TILES>, p, (int)cap, sms, (int)may_cut);
     if (e != cudaSuccess) return e;

@@ -70,11 +70,18 @@ def test_prefill_odd_lengths_in_both_forms(case, causal):
         _check_two_heads(lens, q, kv, kr, causal, o, lse, skip=skip)
 
 
-@pytest.mark.parametrize("lens,H", [([(300, 30000), (140, 9000)], 32), ([(700, 12000)], 20)])
+@pytest.mark.parametrize("lens,H", [
+    ([(300, 30000), (140, 9000)], 32), ([(700, 12000)], 20),
+    ([(256, 4000)] * 6 + [(255, 3777)], 32),        # the last round of CTAs is cut
+    ([(256, 4000)] * 11, 16),
+])
 def test_prefill_two_tiles_cut(lens, H):
+    """Keys cut into parts, the same bits every time."""
     q, kv, kr, cu_q, cu_k = _prefill_inputs(lens, H, "bf16", seed=130)
     o, lse = _call_prefill(q, kv, kr, cu_q, cu_k, True)
     _check_two_heads(lens, q, kv, kr, True, o, lse)
+    o2, lse2 = _call_prefill(q, kv, kr, cu_q, cu_k, True)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
 def test_prefill_unseen_values_in_both_forms():
