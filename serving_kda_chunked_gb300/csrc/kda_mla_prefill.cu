@@ -63,6 +63,27 @@ template <int TILES> struct Cfg {
 static_assert(Cfg<2>::SM_BYTES <= 232448 && 2 * (Cfg<1>::SM_BYTES + 1024) <= 233472, "shared memory");
 constexpr float RESCALE = 8.f;
 
+// Which value row of a key tile a softmax thread zeroes where it lies behind the
+// sequence's end: (token, chunk of 64 channels).  The output product reads the value
+// tile in two blocks of BK / 2 tokens, all channels.  With two halves it begins with
+// block b once the warps of half b have arrived on p_full[2 x + b], so that half
+// zeroes the whole of that block; with one, all warps arrive before either block.
+struct ValueRow { int token, chunk; };
+__host__ __device__ constexpr ValueRow unseen_row(int row, int half) { return {64 * half + (row & 63), row >> 6}; }
+template <int TILES> constexpr bool zeroed_before_read() {
+    using G = Cfg<TILES>;
+    bool done[2][G::BK] = {};
+    for (int half = 0; half < G::SPLIT; ++half)
+        for (int row = 0; row < BQ; ++row) {
+            const ValueRow r = unseen_row(row, half);
+            if (G::SPLIT == 1 || r.token / (G::BK / 2) == half) done[r.chunk][r.token] = true;
+        }
+    for (int t = 0; t < G::BK; ++t)
+        if (!done[0][t] || !done[1][t]) return false;
+    return true;
+}
+static_assert(zeroed_before_read<1>() && zeroed_before_read<2>(), "a product would read values that are not zeroed yet");
+
 constexpr int MAX_SMS = 160;
 constexpr int SLOTS = 2 * MAX_SMS;           // parts with results of their own, over all heads
 constexpr int CUTS = MAX_SMS;                // blocks that are cut, over all heads
@@ -541,12 +562,12 @@ __global__ void __launch_bounds__(Cfg<TILES>::THREADS, 3 - TILES) prefill_kernel
                 const int valid = ent.keys - j * BK;            // keys of the sequence in this tile
                 if (valid < BK) {
                     // values behind the sequence's end hold anything: zero them
-                    // (each tile for its own product)
-                    const int token = row % BK, chunk = SPLIT == 2 ? half : row / BK;
-                    const int q = PER * j + 3 + token / (BK / 2), slot = q % RING;
+                    // (each tile for its own product; the arrival below releases them)
+                    const ValueRow v0 = unseen_row(row, half);
+                    const int q = PER * j + 3 + v0.token / (BK / 2), slot = q % RING;
                     ok = wait_or_fail(&full[slot], (q / RING) & 1, fail);
-                    if (token >= valid) {
-                        uint8_t *r = sm + SM_RING + slot * BLOCK + chunk * (BLOCK / 2) + token % (BK / 2) * 128;
+                    if (v0.token >= valid) {
+                        uint8_t *r = sm + SM_RING + slot * BLOCK + v0.chunk * (BLOCK / 2) + v0.token % (BK / 2) * 128;
 #pragma unroll
                         for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(r + c * 16) = make_uint4(0, 0, 0, 0);
                     }

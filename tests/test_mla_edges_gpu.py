@@ -1,0 +1,54 @@
+"""Latent attention on the GPU: what lies beside the keys that are seen, and
+what a caller may leave out.  Plain computations and tolerances are those of
+``test_mla_gpu.py``.
+"""
+import pytest
+import torch
+
+import serving_kda_chunked_gb300 as kda
+from test_mla_gpu import _call_prefill, _prefill_inputs
+from test_mla_paths_gpu import LONG, _check_two_heads
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from serving_kda_chunked_gb300 import build
+    build.build()
+    kda.load()
+
+
+# ---- values behind a sequence's end -----------------------------------------------
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("long,H", [((), 3), ((LONG,), 64)])      # one query tile a CTA, and two
+def test_prefill_last_tile_followed_by_nan(long, H, causal):
+    """Last key tiles of 1 to 127 keys, each followed by a sequence of NaN and
+    infinities: neither reaches the outputs, and the bits are the same every time."""
+    ends = [(1, 129), (200, 161), (191, 191), (63, 63), (300, 1), (70, 192), (130, 193), (255, 255)]
+    lens = [x for e in ends for x in (e, (5, 130))] + list(long)
+    q, kv, kr, cu_q, cu_k = _prefill_inputs(lens, H, "bf16", seed=160, tail=70)
+    at_k = 0
+    for n, (_, nk) in enumerate(lens):
+        if n % 2 and n < 2 * len(ends):
+            kv[at_k:at_k + nk] = float("nan")
+            kv[at_k:at_k + nk:3] = float("inf")
+            kr[at_k:at_k + nk] = float("inf")
+        at_k += nk
+    skip = [2 * n + 1 for n in range(len(ends))] + [2 * len(ends)] * len(long)
+    o, lse = _call_prefill(q, kv, kr, cu_q, cu_k, causal)
+    _check_two_heads(lens, q, kv, kr, causal, o, lse, skip=skip)
+    a = 0
+    for n, (nq, _) in enumerate(lens):
+        if n not in skip:
+            assert bool(torch.isfinite(o[a:a + nq]).all())
+        a += nq
+    bits = o.view(torch.int16).clone()
+    for _ in range(30):
+        o2, _ = _call_prefill(q, kv, kr, cu_q, cu_k, causal)
+        a = 0
+        for n, (nq, _) in enumerate(lens):
+            if n not in skip:
+                assert torch.equal(o2[a:a + nq].view(torch.int16), bits[a:a + nq])
+            a += nq
