@@ -5,6 +5,11 @@ Every step of the computation runs in the CUDA kernels behind the C ABI in
 allocates outputs that the caller did not provide, and passes raw device
 pointers plus the current CUDA stream.  If the compiled library is missing,
 loading fails with an error -- there is no fallback implementation.
+
+With ``stream=`` a call runs on that stream.  The caller orders it behind what
+writes its inputs and in front of what reads its outputs, as with any work on
+several streams; memory that the call allocates itself, and memory that is let
+go of while the call is still to run, is taken care of here.
 """
 from __future__ import annotations
 
@@ -131,6 +136,45 @@ def _stream(stream, device=None):
     elif device is not None and stream.device != torch.device(device):
         raise ValueError("stream is on %s, the tensors on %s" % (stream.device, device))
     return ctypes.c_void_p(int(stream.cuda_stream))
+
+
+def _other_stream(stream, device):
+    """``stream`` where the call runs beside the current stream of ``device``,
+    else None."""
+    if stream is None:
+        return None
+    if stream.device != device:
+        raise ValueError("stream is on %s, the tensors on %s" % (stream.device, device))
+    if int(stream.cuda_stream) == torch._C._cuda_getCurrentRawStream(device.index):
+        return None
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream.cuda_stream), device=device)
+    return stream
+
+
+def _empty(shape, dtype, device, side, returned=True):
+    """New memory of a call that runs on ``side`` (None: on the current stream).
+
+    It comes from that stream's memory: a block of the current stream may still
+    be in use there, and would be handed out there again once the call lets go
+    of it, in both cases beside the call's kernels.  What is returned to the
+    caller is recorded with the current stream as well."""
+    if side is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(side):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _record(side, *tensors):
+    """The caller's tensors are in use on ``side`` too: the allocator does not
+    hand their memory out again before the call has run."""
+    if side is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(side)
 
 
 def _same_device(device, **tensors):
@@ -506,12 +550,7 @@ def _need(name, t, dtype, shape, dev, rows=False):
 
 def _call(fn, dev, stream, *args):
     """Call on device ``dev`` and ``stream`` (default: its current stream)."""
-    if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(dev)
-    elif stream.device.index != dev:
-        raise ValueError("stream is on %s, the tensors on cuda:%d" % (stream.device, dev))
-    else:
-        raw = int(stream.cuda_stream)
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream.cuda_stream)
     if torch.cuda.current_device() == dev:
         st = getattr(_mla_lib(), fn)(*args, raw)
     else:
@@ -521,22 +560,27 @@ def _call(fn, dev, stream, *args):
         raise KdaError(fn, st)
 
 
-def _given(name, t, dtype, shape, dev, device):
-    """(tensor, address) of an output or a workspace; allocated when omitted."""
+def _given(name, t, dtype, shape, dev, device, side):
+    """(tensor, address) of an output; allocated when omitted."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=device)
+        t = _empty(shape, dtype, device, side)
         return t, t.data_ptr()
-    return t, _need(name, t, dtype, shape, dev)
+    address = _need(name, t, dtype, shape, dev)
+    _record(side, t)
+    return t, address
 
 
-def _scratch(workspace, need, dev, device):
+def _scratch(workspace, need, dev, device, side):
     """(tensor, address, bytes) of the workspace; allocated when omitted."""
     if workspace is not None:
         n = workspace.numel() if isinstance(workspace, torch.Tensor) else 0
-        return workspace, _need("workspace", workspace, torch.uint8, (n,), dev), n
+        address = _need("workspace", workspace, torch.uint8, (n,), dev)
+        _record(side, workspace)
+        return workspace, address, n
     if not need:
         return None, None, 0
-    return _given("workspace", None, torch.uint8, (need,), dev, device) + (need,)
+    workspace = _empty((need,), torch.uint8, device, side, returned=False)
+    return workspace, workspace.data_ptr(), need
 
 
 def _cache_shape(cache):
@@ -570,6 +614,7 @@ def kda_mla_append(c, k_r, slots, cache, *, positions=None, rope=None, interleav
     ps = _need("slots", slots, torch.int32, (T,), dev)
     cs = _cache_shape(cache)
     pcache = _need("cache", cache, dt, cs, dev)
+    side = _other_stream(stream, c.device)
     pp = pr = pko = pq = pqo = None
     max_pos = kos = H = qt = qh = ot = oh = 0
     if (rope is None) != (positions is None):
@@ -585,13 +630,15 @@ def kda_mla_append(c, k_r, slots, cache, *, positions=None, rope=None, interleav
         H = q_r.shape[1] if isinstance(q_r, torch.Tensor) and q_r.dim() == 3 else -1
         pq = _need("q_r", q_r, dt, (T, H, MLA_ROPE), dev, True)
         if q_out is None:
-            q_out, pqo = _given("q_out", None, dt, (T, H, MLA_ROPE), dev, c.device)
+            q_out, pqo = _given("q_out", None, dt, (T, H, MLA_ROPE), dev, c.device, side)
         else:
             pqo = _need("q_out", q_out, dt, (T, H, MLA_ROPE), dev, True)
+            _record(side, q_out)
         qt, qh, _ = q_r.stride()
         ot, oh, _ = q_out.stride()
     elif q_out is not None:
         raise ValueError("q_out needs q_r")
+    _record(side, c, k_r, slots, cache, positions, rope, k_out, q_r)
     _call("kda_mla_append", dev, stream, pc, c.stride(0), pk, k_r.stride(0), ps, pp, pr, max_pos,
           1 if interleaved else 0, T, pcache, cs[0], cs[1], MLA_LATENT, MLA_ROPE, _DTYPE_CODE[dt],
           pko, kos, pq, qt, qh, H, pqo, ot, oh)
@@ -643,11 +690,13 @@ def kda_mla_prefill(q, kv, k_r, cu_q, cu_k, *, scale=None, causal=True, o=None, 
     pcq = _need("cu_q", cu_q, torch.int32, (N + 1,), dev)
     pck = _need("cu_k", cu_k, torch.int32, (N + 1,), dev)
     device = q.device
-    o, po = _given("o", o, dt, (Tq, H, MLA_DV), dev, device)
-    lse, pl = _given("lse", lse, torch.float32, (Tq, H), dev, device)
+    side = _other_stream(stream, device)
+    o, po = _given("o", o, dt, (Tq, H, MLA_DV), dev, device, side)
+    lse, pl = _given("lse", lse, torch.float32, (Tq, H), dev, device, side)
     code = _DTYPE_CODE[dt]
     need = _mla_lib().kda_mla_prefill_workspace_size(N, Tq, H, code)
-    workspace, pw, nw = _scratch(workspace, need, dev, device)
+    workspace, pw, nw = _scratch(workspace, need, dev, device, side)
+    _record(side, q, kv, k_r, cu_q, cu_k)
     _call("kda_mla_prefill", dev, stream, pq, pkv, pk, pcq, pck, N, Tq, Tk, H, MLA_NOPE, MLA_ROPE,
           MLA_DV, code, _MLA_SCALE if scale is None else scale, 1 if causal else 0, po, pl, pw, nw)
     return o, lse
@@ -676,11 +725,13 @@ def kda_mla_decode(q, cache, table, seq_lens, *, scale=None, o=None, lse=None, w
     pt = _need("table", table, torch.int32, (B, width), dev)
     pn = _need("seq_lens", seq_lens, torch.int32, (B,), dev)
     device = q.device
-    o, po = _given("o", o, dt, (B, H, MLA_LATENT), dev, device)
-    lse, pl = _given("lse", lse, torch.float32, (B, H), dev, device)
+    side = _other_stream(stream, device)
+    o, po = _given("o", o, dt, (B, H, MLA_LATENT), dev, device, side)
+    lse, pl = _given("lse", lse, torch.float32, (B, H), dev, device, side)
     code = _DTYPE_CODE[dt]
     need = _mla_lib().kda_mla_decode_workspace_size(B, H, code)
-    workspace, pw, nw = _scratch(workspace, need, dev, device)
+    workspace, pw, nw = _scratch(workspace, need, dev, device, side)
+    _record(side, q, cache, table, seq_lens)
     _call("kda_mla_decode", dev, stream, pq, pc, pt, pn, B, H, cs[0], cs[1], width, MLA_LATENT,
           MLA_ROPE, code, _MLA_SCALE if scale is None else scale, po, pl, pw, nw)
     return o, lse
