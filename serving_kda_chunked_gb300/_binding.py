@@ -235,21 +235,24 @@ def _prefill(fn, gate_shape, q, k, v, g, beta, cu_seqlens, S0, chunk, o, S_T, wo
     N = cu_seqlens.shape[0] - 1
     if S0 is not None:
         _check_cuda("S0", S0, torch.float32, (N, H, dk, dv))
+    side = _other_stream(stream, q.device)
+    brought = (q, k, v, g, beta, cu_seqlens, S0, o, S_T, workspace)
     if o is None:
-        o = torch.empty((T, H, dv), dtype=q.dtype, device=q.device)
+        o = _empty((T, H, dv), q.dtype, q.device, side)
     _check_cuda("o", o, q.dtype, (T, H, dv))
     if S_T is None:
-        S_T = torch.empty((N, H, dk, dv), dtype=torch.float32, device=q.device)
+        S_T = _empty((N, H, dk, dv), torch.float32, q.device, side)
     _check_cuda("S_T", S_T, torch.float32, (N, H, dk, dv))
     need = kda_prefill_workspace_size(N, T, H, dk, dv, q.dtype, chunk)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty((need,), torch.uint8, q.device, side, returned=False)
     ws_bytes = 0
     if workspace is not None:
         _check_cuda("workspace", workspace, torch.uint8)
         ws_bytes = workspace.numel()
     _same_device(q.device, k=k, v=v, g=g, beta=beta, cu_seqlens=cu_seqlens, S0=S0, o=o,
                  S_T=S_T, workspace=workspace)
+    _record(side, *brought)
     with torch.cuda.device(q.device):
         st = getattr(load(), fn)(
             _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0), _ptr(cu_seqlens),
@@ -310,9 +313,13 @@ def kda_prefill_chunked_host(q, k, v, g, beta, cu_seqlens, S0=None, *, chunk: in
     _check_host("S_T", S_T, torch.float32, (N, H, dk, dv))
     if workspace is None:
         need = kda_prefill_host_workspace_size(N, T, H, dk, dv, q.dtype, chunk)
-        dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    _check_cuda("workspace", workspace, torch.uint8)
+        dev = torch.device("cuda" if device is None else device)
+        if dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        workspace = _empty((max(need, 1),), torch.uint8, dev, _other_stream(stream, dev), returned=False)
+    else:
+        _check_cuda("workspace", workspace, torch.uint8)
+        _record(_other_stream(stream, workspace.device), workspace)
     with torch.cuda.device(workspace.device):
         st = load().kda_prefill_chunked_host(
             _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0), _ptr(cu_seqlens),
@@ -347,14 +354,17 @@ def kda_prefill_chunked_noalloc(q, k, v, g, beta, cu_seqlens, S0=None, *, chunk:
     N = cu_seqlens.shape[0] - 1
     if S0 is not None:
         _check_cuda("S0", S0, torch.float32, (N, H, dk, dv))
+    side = _other_stream(stream, q.device)
+    brought = (q, k, v, g, beta, cu_seqlens, S0, o, S_T)
     if o is None:
-        o = torch.empty((T, H, dv), dtype=q.dtype, device=q.device)
+        o = _empty((T, H, dv), q.dtype, q.device, side)
     _check_cuda("o", o, q.dtype, (T, H, dv))
     if S_T is None:
-        S_T = torch.empty((N, H, dk, dv), dtype=torch.float32, device=q.device)
+        S_T = _empty((N, H, dk, dv), torch.float32, q.device, side)
     _check_cuda("S_T", S_T, torch.float32, (N, H, dk, dv))
     _same_device(q.device, k=k, v=v, g=g, beta=beta, cu_seqlens=cu_seqlens, S0=S0, o=o,
                  S_T=S_T)
+    _record(side, *brought)
     with torch.cuda.device(q.device):
         st = load().kda_prefill_chunked_noalloc(
             _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0), _ptr(cu_seqlens),
@@ -399,10 +409,13 @@ def _decode(fn, gate_shape, q, k, v, g, beta, S, o, stream):
     _check_cuda("g", g, torch.float32, gate_shape(B, H, dk))
     _check_cuda("beta", beta, torch.float32, (B, H))
     _check_cuda("S", S, torch.float32, (B, H, dk, dv))
+    side = _other_stream(stream, q.device)
+    brought = (q, k, v, g, beta, S, o)
     if o is None:
-        o = torch.empty((B, H, dv), dtype=q.dtype, device=q.device)
+        o = _empty((B, H, dv), q.dtype, q.device, side)
     _check_cuda("o", o, q.dtype, (B, H, dv))
     _same_device(q.device, k=k, v=v, g=g, beta=beta, S=S, o=o)
+    _record(side, *brought)
     with torch.cuda.device(q.device):
         st = getattr(load(), fn)(
             _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S), B, H, dk, dv,
@@ -443,10 +456,13 @@ def _decode_pooled(fn, gate_shape, q, k, v, g, beta, S_pool, slots, o, stream):
     if S_pool.dim() != 4 or tuple(S_pool.shape[1:]) != (H, dk, dv):
         raise ValueError("S_pool must have shape [P, %d, %d, %d]" % (H, dk, dv))
     _check_cuda("slots", slots, torch.int32, (B,))
+    side = _other_stream(stream, q.device)
+    brought = (q, k, v, g, beta, S_pool, slots, o)
     if o is None:
-        o = torch.empty((B, H, dv), dtype=q.dtype, device=q.device)
+        o = _empty((B, H, dv), q.dtype, q.device, side)
     _check_cuda("o", o, q.dtype, (B, H, dv))
     _same_device(q.device, k=k, v=v, g=g, beta=beta, S_pool=S_pool, slots=slots, o=o)
+    _record(side, *brought)
     with torch.cuda.device(q.device):
         st = getattr(load(), fn)(
             _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S_pool), _ptr(slots),

@@ -7,6 +7,7 @@ import gc
 import pytest
 import torch
 
+import kda_inputs as ki
 import serving_kda_chunked_gb300 as kda
 from test_mla_gpu import _decode_inputs, _gen, _prefill_inputs, _rand
 
@@ -50,7 +51,29 @@ def _mla_append(dtype):
     return (c, kr, slots, pos, rope, q), call, []
 
 
-CALLS = {"kda_mla_prefill": _mla_prefill, "kda_mla_decode": _mla_decode, "kda_mla_append": _mla_append}
+def _kda_prefill(dtype):
+    d = 128 if dtype == "bf16" else 64
+    inp = ki.prefill_inputs(ki.PrefillConfig("streams", H=4, d=d, dtype=dtype, T=700, s0_std=0.1), device=DEV, seed=173)
+    inputs = tuple(inp[n] for n in ("q", "k", "v", "g", "beta", "cu_seqlens", "S0"))
+    return inputs, lambda *a, **kw: kda.kda_prefill_chunked(*a, **kw), [
+        kda.kda_prefill_workspace_size(1, 700, 4, d, d, inputs[0].dtype)]
+
+
+def _kda_decode(dtype):
+    inp = ki.decode_inputs(ki.DecodeConfig("streams", B=5, H=4, d=128, steps=1, dtype=dtype), device=DEV, seed=174)
+    inputs = tuple(inp[n][0] for n in ("q", "k", "v", "g", "beta")) + (inp["S0"],)
+
+    def call(*a, **kw):
+        S = a[-1].clone()
+        if "stream" in kw:
+            kw["stream"].wait_stream(torch.cuda.current_stream())
+        return kda.kda_decode_step(*a[:-1], S, **kw), S
+    return inputs, call, []
+
+
+CALLS = {"kda_mla_prefill": _mla_prefill, "kda_mla_decode": _mla_decode, "kda_mla_append": _mla_append,
+         "kda_prefill_chunked": _kda_prefill, "kda_decode_step": _kda_decode}
+UPDATE = ("kda_mla_append", "kda_decode_step")       # these write a copy made on the current stream
 
 
 def _equal(a, b):
@@ -89,7 +112,7 @@ def test_other_stream_is_busy(name, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
-@pytest.mark.parametrize("name", [n for n in sorted(CALLS) if n != "kda_mla_append"])
+@pytest.mark.parametrize("name", [n for n in sorted(CALLS) if n not in UPDATE])
 def test_current_stream_is_busy(name, dtype):
     """What the current stream still has to write into memory that it has let
     go of does not meet the call's."""

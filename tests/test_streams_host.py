@@ -146,3 +146,52 @@ def test_latent_attention_refuses_another_devices_stream(gpu):
         with pytest.raises(ValueError, match="stream is on"):
             getattr(b, name)(*args, **kw, stream=Elsewhere(5))
     assert not gpu.made and not gpu.runs
+
+
+# ---- the KDA calls -----------------------------------------------------------------
+
+def _kda_calls():
+    def prefill(gate):
+        return (_make(6, 2, 64, dtype=BF), _make(6, 2, 64, dtype=BF), _make(6, 2, 64, dtype=BF), gate,
+                _make(6, 2), _make(3, dtype=I32), _make(2, 2, 64, 64))
+
+    def decode(gate, states, *slots):
+        return (_make(3, 2, 64, dtype=BF), _make(3, 2, 64, dtype=BF), _make(3, 2, 64, dtype=BF), gate,
+                _make(3, 2), _make(states, 2, 64, 64), *slots)
+
+    pool = ("o",)
+    return {
+        "kda_prefill_chunked": (prefill(_make(6, 2, 64)), ("o", "S_T", "workspace")),
+        "kda_gdn_prefill_chunked": (prefill(_make(6, 2)), ("o", "S_T", "workspace")),
+        "kda_prefill_chunked_noalloc": (prefill(_make(6, 2, 64)), ("o", "S_T")),
+        "kda_decode_step": (decode(_make(3, 2, 64), 3), pool),
+        "kda_gdn_decode_step": (decode(_make(3, 2), 3), pool),
+        "kda_decode_step_pooled": (decode(_make(3, 2, 64), 5, _make(3, dtype=I32)), pool),
+        "kda_gdn_decode_step_pooled": (decode(_make(3, 2), 5, _make(3, dtype=I32)), pool),
+    }
+
+
+@pytest.mark.parametrize("name", sorted(_kda_calls()))
+def test_kda_on_another_stream(gpu, name):
+    args, new = _kda_calls()[name]
+    _check(gpu, name, args, {}, new, new)
+
+
+def test_kda_from_host_memory_on_another_stream(gpu):
+    def host(*shape, dtype=F32):
+        return torch.zeros(shape, dtype=dtype)
+
+    args = (host(6, 2, 64, dtype=BF), host(6, 2, 64, dtype=BF), host(6, 2, 64, dtype=BF), host(6, 2, 64),
+            host(6, 2), host(3, dtype=I32), host(2, 2, 64, 64))
+    kw = {"o": host(6, 2, 64, dtype=BF), "S_T": host(2, 2, 64, 64)}
+    for device in (None, "cuda", "cuda:0", DEVICE):
+        gpu.made.clear()
+        b.kda_prefill_chunked_host(*args, **kw, device=device, stream=gpu.side)
+        (workspace, stream), = gpu.made
+        assert stream is gpu.side and "recorded" not in workspace.__dict__ and gpu.runs[-1] == 77
+    mine = _make(4096, dtype=torch.uint8)
+    b.kda_prefill_chunked_host(*args, **kw, workspace=mine, stream=gpu.side)
+    assert mine.__dict__.get("recorded") == [gpu.side]
+    gpu.made.clear()
+    b.kda_prefill_chunked_host(*args, **kw)
+    assert [s for _, s in gpu.made] == [gpu.here] and gpu.runs[-1] == 0
