@@ -361,7 +361,8 @@ __global__ void __launch_bounds__(Cfg<TILES>::THREADS, 3 - TILES) prefill_kernel
     }
     if (warp == W_MMA) tmem_alloc<G::TCOLS>(tmem_slot);
     if (warp == W_LOAD && lane == 0) {
-        prefetch_map(&p.tm_q); prefetch_map(&p.tm_k); prefetch_map(&p.tm_v); prefetch_map(&p.tm_r);
+        prefetch_map(&p.tm_q);
+        if (p.Tk > 0) { prefetch_map(&p.tm_k); prefetch_map(&p.tm_v); prefetch_map(&p.tm_r); }   // else there are none
     }
     fence_before_sync();
     __syncthreads();
@@ -728,12 +729,12 @@ template <int TILES> cudaError_t launch(const PrefillArgs &a, cudaStream_t st) {
             ready[dev] = true;
         }
     }
-    PreParams p;
+    PreParams p = {};
     const uint64_t H = (uint64_t)a.H, Tq = (uint64_t)a.Tq, Tk = (uint64_t)a.Tk;
     const uint64_t qd[4] = {64, Tq, 3, H}, qs[3] = {H * DQK * 2, 128, DQK * 2};
     const uint32_t qb[4] = {64, BQ, 3, 1};
     if (!map4(&p.tm_q, a.q, qd, qs, qb)) return cudaErrorInvalidValue;
-    if (Tk > 0) {      // without keys no tile is loaded
+    if (Tk > 0) {      // without keys no tile is loaded, and no map is looked at
         const uint64_t kd[4] = {64, Tk, 4, H}, ks[3] = {H * (NOPE + DV) * 2, 128, (NOPE + DV) * 2};
         const uint32_t kb[4] = {64, G::BK, 1, 1}, vb[4] = {64, G::BK / 2, 2, 1};
         const uint64_t rd[4] = {64, Tk, 1, 1}, rs[3] = {ROPE * 2, ROPE * 2, ROPE * 2};

@@ -52,3 +52,16 @@ def test_prefill_last_tile_followed_by_nan(long, H, causal):
             if n not in skip:
                 assert torch.equal(o2[a:a + nq].view(torch.int16), bits[a:a + nq])
             a += nq
+
+
+# ---- nothing to see ----------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("lens,H", [([(1, 0)], 1), ([(300, 0), (0, 0), (40, 0)], 5), ([(2000, 0)] * 9, 64)])
+def test_prefill_without_any_key(lens, H, dtype):
+    """No sequence of the call has a key, and the key tensors have no rows."""
+    q, kv, kr, cu_q, cu_k = _prefill_inputs(lens, H, dtype, seed=161)
+    assert kv.shape[0] == 0 and kr.shape[0] == 0
+    for causal in (True, False):
+        o, lse = _call_prefill(q, kv, kr, cu_q, cu_k, causal)
+        assert bool((o == 0).all()) and bool((lse == -float("inf")).all())
