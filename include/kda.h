@@ -431,7 +431,9 @@ kda_status kda_mla_append(const void *c, int64_t c_stride, const void *k_r,
  *   o          [Tq, H, 128]  outputs (written)
  *   lse        [Tq, H]       float32 (written), or NULL
  *   workspace  device scratch of kda_mla_prefill_workspace_size(N, Tq, H,
- *              dtype) bytes, 16-byte aligned; may be NULL when that is 0
+ *              dtype) bytes, 16-byte aligned; may be NULL when that is 0.  One
+ *              that is passed all the same takes the call's status (its first
+ *              4 bytes, if it has them) and is otherwise left alone
  *
  * bf16 runs on the tensor cores, fp32 on the CUDA cores.  Calls that share a
  * workspace must not overlap on the GPU.  Tokens outside every [cu_q[n],
@@ -487,8 +489,10 @@ uint64_t kda_mla_decode_workspace_size(int32_t B, int32_t H, int32_t dtype);
  * kda_prefill_check for kda_mla_prefill and kda_mla_decode: synchronise
  * `stream` and report the device-side status of the last call that used
  * `workspace` (KDA_ERR_TIMEOUT: a bounded wait gave up and outputs are
- * incomplete).  A NULL workspace (a call that needed none) reports the
- * stream's status only.
+ * incomplete).  Every call that launches something and was passed a workspace of
+ * 4 bytes or more writes its status there, whether or not it needs the
+ * workspace; the no-ops (Tq = 0, B = 0) leave it as it was.  A NULL workspace
+ * (a call that needed none) reports the stream's status only.
  */
 kda_status kda_mla_check(const void *workspace, void *stream);
 

@@ -348,10 +348,12 @@ kda_status kda_mla_prefill(const void *q, const void *kv, const void *k_r, const
         !aligned4(cu_q) || !aligned4(cu_k))
         return KDA_ERR_INVALID_ARG;
     const uint64_t need = kda_mla_prefill_workspace_size(N, Tq, H, dtype);
-    if (need && (!workspace || workspace_bytes < need || !aligned16(workspace)))
-        return KDA_ERR_INVALID_ARG;
+    if (need && (!workspace || workspace_bytes < need)) return KDA_ERR_INVALID_ARG;
+    // one that the call does not need still takes the call's status
+    if (workspace_bytes < sizeof(int32_t)) workspace = nullptr;
+    if (!aligned16(workspace)) return KDA_ERR_INVALID_ARG;
     if (H > 65535 || (Tq / 32 + N) * (int64_t)H > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
-    const kda_status dst = check_device_ptrs({q, kv, k_r, cu_q, cu_k, o, lse, need ? workspace : nullptr});
+    const kda_status dst = check_device_ptrs({q, kv, k_r, cu_q, cu_k, o, lse, workspace});
     if (dst != KDA_OK) return dst;
     kda::mla::PrefillArgs a;
     a.q = q; a.kv = kv; a.k_r = k_r; a.cu_q = cu_q; a.cu_k = cu_k; a.o = o; a.lse = lse;

@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(PTHREADS, 2) prefill_simt_kernel(const Prefill
     const int tid = threadIdx.x, h = blockIdx.y, H = p.H;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (sp.parts > 1 && tid == 0 && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
+    if (p.ws && tid == 0 && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
         *static_cast<int32_t *>(p.ws) = 0;  // no wait here can give up: the call's status is clear
     PreUnit u;                             // long blocks first: the last queries see the most keys
     if (!pre_unit(p, gridDim.x - 1 - blockIdx.x, blockIdx.z, sp.parts, u)) return;

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import serving_kda_chunked_gb300 as kda
-from test_mla_gpu import _call_prefill, _prefill_inputs
+from test_mla_gpu import DEV, DT, _call_decode, _call_prefill, _decode_inputs, _gen, _prefill_inputs, _rand
 from test_mla_paths_gpu import LONG, _check_two_heads
 
 pytestmark = pytest.mark.gpu
@@ -65,3 +65,26 @@ def test_prefill_without_any_key(lens, H, dtype):
     for causal in (True, False):
         o, lse = _call_prefill(q, kv, kr, cu_q, cu_k, causal)
         assert bool((o == 0).all()) and bool((lse == -float("inf")).all())
+
+
+# ---- the status of a call that was handed a workspace ------------------------------
+
+@pytest.mark.parametrize("lens,H", [([(6400, 6400)], 8), ([(70, 70), (0, 9), (33, 100)], 600)])
+def test_check_of_a_workspace_that_fp32_does_not_need(lens, H):
+    """One buffer for all calls, fresh from the allocator: a call that needs
+    none of it reports its own status, too."""
+    q, kv, kr, cu_q, cu_k = _prefill_inputs(lens, H, "fp32", seed=162)
+    assert kda.kda_mla_prefill_workspace_size(len(lens), q.shape[0], H, torch.float32) == 0
+    ref = kda.kda_mla_prefill(q, kv, kr, cu_q, cu_k)
+    for size in (4, 256, 1 << 20):
+        for kw in ({}, {"stream": torch.cuda.current_stream()}):
+            ws = torch.full((size,), 0xA5, dtype=torch.uint8, device=q.device)
+            got = kda.kda_mla_prefill(q, kv, kr, cu_q, cu_k, workspace=ws, **kw)
+            assert kda.kda_mla_check(ws) == kda.KDA_OK
+            assert all(torch.equal(x, y) for x, y in zip(got, ref))
+            assert bool((ws[4:] == 0xA5).all())
+    # too small for a status word: left alone
+    ws = torch.full((4,), 0xA5, dtype=torch.uint8, device=q.device)
+    kda.kda_mla_prefill(q, kv, kr, cu_q, cu_k, workspace=ws[:3])
+    torch.cuda.synchronize()
+    assert bool((ws == 0xA5).all())
