@@ -370,7 +370,8 @@ kda_status kda_gdn_decode_step_pooled(const void *q, const void *k, const void *
  *   - lse is the natural logarithm of the sum of exp(s), float32; it lets a
  *     caller merge results over parts of the keys.  A query that sees no key
  *     gets o = 0 and lse = -inf.
- *   - Inputs that a query can see are finite.  What it cannot see by length
+ *   - Inputs that a query can see are finite.  Where it sees a NaN, or one of its
+ *     scores is +infinity in float32, its o and lse are NaN.  What it cannot see by length
  *     or by sequence (cache rows behind a length, other sequences' tokens)
  *     may hold anything, infinities and NaN included.
  */

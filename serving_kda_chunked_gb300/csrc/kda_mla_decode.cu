@@ -446,11 +446,10 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                 if (wt < NW) {
                     const float sum = rd[wt] + rd[NW + wt] + rd[2 * NW + wt] + rd[3 * NW + wt];
                     const float top = cb[wt];
-                    ca[wt] = whole ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
+                    ca[wt] = whole ? inverse_of(sum) : 1.f;
                     if (whole) {
                         if (p.lse && n0 + wt < nh)
-                            p.lse[(int64_t)w.b * p.H + h0 + n0 + wt] =
-                                sum > 0.f ? (top + log2f(sum)) * CUDART_LN2_F : -CUDART_INF_F;
+                            p.lse[(int64_t)w.b * p.H + h0 + n0 + wt] = lse_of(top, sum);
                     } else {
                         float2 *to = reinterpret_cast<float2 *>(p.stat + slot * N * 2) + n0 + wt;
                         *to = make_float2(top, sum);

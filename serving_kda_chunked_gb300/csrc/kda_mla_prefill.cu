@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(Cfg<TILES>::THREADS, 3 - TILES) prefill_kernel
             }
             if (ok && x * BQ < ent.rows) {
                 const bool whole = ent.base < 0;
-                const float r = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+                const float r = whole ? inverse_of(l) : 1.f;
                 const int64_t at = (int64_t)(ent.row0 + i) * p.H + h;
                 const int64_t pr = ((int64_t)(ent.base + ent.part) * p.H + h) * ROWS + i;
                 fence_after_sync();
@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(Cfg<TILES>::THREADS, 3 - TILES) prefill_kernel
                 }
                 if (half == 0 && i < ent.rows) {
                     if (!whole) p.stat[pr] = make_float2(m * sc, l);
-                    else if (p.lse) p.lse[at] = l > 0.f ? (m * sc + log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
+                    else if (p.lse) p.lse[at] = lse_of(m * sc, l);
                 }
             }
         }
@@ -705,10 +705,10 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const PreParams p) {
             sum += f * st.y;
             acc.x += f * y.x; acc.y += f * y.y; acc.z += f * y.z; acc.w += f * y.w;
         }
-        const float f = sum > 0.f ? 1.f / sum : 0.f;
+        const float f = inverse_of(sum);
         const int64_t at = (int64_t)(x.row0 + r) * p.H + h;
         store4(p.o + at * DV + 4 * lane, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
-        if (p.lse && lane == 0) p.lse[at] = sum > 0.f ? (top + log2f(sum)) * CUDART_LN2_F : -CUDART_INF_F;
+        if (p.lse && lane == 0) p.lse[at] = lse_of(top, sum);
     }
 }
 

@@ -259,9 +259,9 @@ __global__ void __launch_bounds__(PTHREADS, 2) prefill_simt_kernel(const Prefill
     const int64_t at = (s.q0 + qi) * H + h, to = whole ? at : (int64_t)blockIdx.z * p.Tq * H + at;
     if (part == 0 && qi < s.nq) {
         if (!whole) *reinterpret_cast<float2 *>(sp.stat + 2 * to) = make_float2(m, l);
-        else if (p.lse) p.lse[at] = l > 0.f ? (m + log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
+        else if (p.lse) p.lse[at] = lse_of(m, l);
     }
-    if (part == 0) fs[row] = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+    if (part == 0) fs[row] = whole ? inverse_of(l) : 1.f;
     __syncthreads();
     for (int e = tid; e < BQ * DV / 4; e += PTHREADS) {
         const int r = e / (DV / 4), c = e % (DV / 4) * 4;
@@ -307,9 +307,9 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillArgs p, 
             sum += f * st[k].y;
             acc.x += f * y[k].x; acc.y += f * y[k].y; acc.z += f * y[k].z; acc.w += f * y[k].w;
         }
-    const float f = sum > 0.f ? 1.f / sum : 0.f;
+    const float f = inverse_of(sum);
     store4((float *)p.o + at * DV + 4 * lane, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
-    if (p.lse && lane == 0) p.lse[at] = sum > 0.f ? (top + log2f(sum)) * CUDART_LN2_F : -CUDART_INF_F;
+    if (p.lse && lane == 0) p.lse[at] = lse_of(top, sum);
 }
 
 // Parts per (queries, head) block: enough for about eight blocks an SM.
@@ -450,15 +450,13 @@ __global__ void __launch_bounds__(DTHREADS, 2) decode_simt_kernel(const SplitPar
         const int64_t slot = w.slot();
         if (lane == 0 && warp < nh) {
             if (whole) {
-                if (p.lse)
-                    p.lse[(int64_t)w.b * p.H + h0 + warp] =
-                        l > 0.f ? (m + log2f(l)) * CUDART_LN2_F : -CUDART_INF_F;
+                if (p.lse) p.lse[(int64_t)w.b * p.H + h0 + warp] = lse_of(m, l);
             } else {
                 *reinterpret_cast<float2 *>(p.stat + (slot * HG + warp) * 2) = make_float2(m, l);
             }
         }
         __syncthreads();                    // fs and the rows have been read
-        if (lane == 0) fs[warp] = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+        if (lane == 0) fs[warp] = whole ? inverse_of(l) : 1.f;
         // the halves of the tokens: each thread gives the other one four heads
 #pragma unroll
         for (int h = 0; h < HG; ++h)

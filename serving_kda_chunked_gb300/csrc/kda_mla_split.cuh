@@ -25,6 +25,14 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// What a softmax's sum and maximum (in log2 units) give: the factor of the output, and
+// the lse.  A sum of 0 says that nothing was seen; one that is NaN (NaN was seen, or a
+// score overflowed) stays NaN in both.
+__device__ __forceinline__ float inverse_of(float sum) { return sum == 0.f ? 0.f : 1.f / sum; }
+__device__ __forceinline__ float lse_of(float top, float sum) {
+    return sum == 0.f ? -CUDART_INF_F : (top + log2f(sum)) * CUDART_LN2_F;
+}
+
 // What the share of a CTA starts in: sequence b, which the starts of the shares
 // first .. last cut; b < 0 marks an idle CTA.
 struct Meta { int32_t b, first, last; };
@@ -206,12 +214,11 @@ __global__ void __launch_bounds__(256, 4) join_kernel(const SplitParams p, int c
     const int block = (c - m.first) * gridDim.x + blockIdx.x, blocks = (pieces - 1) * gridDim.x;
     auto write = [&](int item, float4 acc, float top, float sum, int bad) {
         if (__any_sync(0xffffffffu, bad)) return;           // a share that gave up: o stays as it is
-        const float r = sum > 0.f ? 1.f / sum : 0.f;
+        const float r = inverse_of(sum);
         const int64_t at = (int64_t)m.b * p.H + group * N + (item >> 2);
         store4((To *)p.o + at * LATENT + (item & 3) * 128 + 4 * lane,
                make_float4(acc.x * r, acc.y * r, acc.z * r, acc.w * r));
-        if (p.lse && (item & 3) == 0 && lane == 0)
-            p.lse[at] = sum > 0.f ? (top + log2f(sum)) * CUDART_LN2_F : -CUDART_INF_F;
+        if (p.lse && (item & 3) == 0 && lane == 0) p.lse[at] = lse_of(top, sum);
     };
     if (pieces <= 8) {
         for (int item = block * 8 + warp; item < 4 * nh; item += 8 * blocks) {

@@ -88,3 +88,47 @@ def test_check_of_a_workspace_that_fp32_does_not_need(lens, H):
     kda.kda_mla_prefill(q, kv, kr, cu_q, cu_k, workspace=ws[:3])
     torch.cuda.synchronize()
     assert bool((ws == 0xA5).all())
+
+
+# ---- scores that are not numbers ---------------------------------------------------
+
+def _spoil(how, query, key):
+    """NaN in a key, or finite values whose product overflows float32."""
+    if how == "nan":
+        key[..., 3] = float("nan")
+    else:
+        query[..., 3] = 1e30
+        key[..., 3] = 1e30
+
+
+@pytest.mark.parametrize("how", ["nan", "overflow"])
+@pytest.mark.parametrize("dtype,lens,H", [
+    ("bf16", [(100, 130), (90, 90)], 3),                       # one query tile a CTA
+    ("bf16", [(1, 6000), (3, 3)], 2),                          # its keys cut into parts
+    ("bf16", [(300, 300), LONG], 64),                          # two query tiles
+    ("bf16", [(300, 30000), (140, 9000)], 32),                 # their keys cut into parts
+    ("fp32", [(100, 130), (90, 90)], 3),                       # keys cut into parts
+    ("fp32", [(3000, 300), (90, 90)], 16),                     # and whole
+])
+def test_prefill_lse_of_scores_that_are_not_numbers(dtype, lens, H, how):
+    """The first sequence sees such a score in every query: its outputs and
+    their lse are NaN (-inf says that nothing was seen); the second's are not."""
+    q, kv, kr, cu_q, cu_k = _prefill_inputs(lens, H, dtype, seed=163)
+    nq, nk = lens[0]
+    _spoil(how, q[:nq, :, 128:], kr[nk // 2])
+    o, lse = _call_prefill(q, kv, kr, cu_q, cu_k, False)
+    assert bool(torch.isnan(o[:nq]).all()) and bool(torch.isnan(lse[:nq]).all())
+    assert bool(torch.isfinite(o[nq:]).all()) and bool(torch.isfinite(lse[nq:]).all())
+
+
+@pytest.mark.parametrize("how", ["nan", "overflow"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("lens,H", [([17, 64], 5), ([40] * 300 + [3], 20), ([300] * 40, 33), ([20000, 900], 16)])
+def test_decode_lse_of_scores_that_are_not_numbers(lens, H, dtype, how):
+    """The same for single tokens: sequences in one share, in a few and in many."""
+    q, cache, table, n = _decode_inputs(lens, H, 64, dtype, seed=164)
+    t = lens[0] // 2
+    _spoil(how, q[0, :, 512:], cache[table[0, t // 64], t % 64, 512:])
+    o, lse = _call_decode(q, cache, table, n)
+    assert bool(torch.isnan(o[0]).all()) and bool(torch.isnan(lse[0]).all())
+    assert bool(torch.isfinite(o[1:]).all()) and bool(torch.isfinite(lse[1:]).all())
