@@ -132,3 +132,67 @@ def test_decode_lse_of_scores_that_are_not_numbers(lens, H, dtype, how):
     o, lse = _call_decode(q, cache, table, n)
     assert bool(torch.isnan(o[0]).all()) and bool(torch.isnan(lse[0]).all())
     assert bool(torch.isfinite(o[1:]).all()) and bool(torch.isfinite(lse[1:]).all())
+
+
+# ---- graphs ------------------------------------------------------------------------
+
+@pytest.mark.parametrize("given", [True, False])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_calls_replay_in_a_cuda_graph(dtype, given):
+    """Append, prompts and single tokens captured together, with outputs and
+    workspaces of the caller or taken during the capture, and replayed on other
+    inputs: the bits of the calls made one by one."""
+    g = _gen(165)
+    H, T, page = 8, 500, 64
+    dt = DT[dtype]
+    cu = torch.tensor([0, 200, 500], dtype=torch.int32, device=DEV)
+    table = torch.tensor([[3, 0, 5, 1, -1], [2, 7, 4, 6, 8]], dtype=torch.int32, device=DEV)
+    lens = torch.tensor([200, 300], dtype=torch.int32, device=DEV)
+    at = torch.cat([torch.arange(200), torch.arange(300)]).to(DEV)
+    slots = (table[(torch.arange(T, device=DEV) >= 200).long(), at // page] * page + at % page).to(torch.int32)
+    rope = torch.randn(320, 64, generator=g, device=DEV)
+
+    def draw():
+        return [_rand(g, dt, *s) for s in ((T, 512), (T, 64), (T, H, 192), (T, H, 256), (2, H, 576))]
+
+    x = draw()
+    cache = torch.zeros(9, page, 576, dtype=dt, device=DEV)
+    k_out = torch.zeros(T, 64, dtype=dt, device=DEV)
+    kw_p, kw_d = {}, {}
+    if given:
+        kw_p = {"o": torch.empty(T, H, 128, dtype=dt, device=DEV), "lse": torch.empty(T, H, device=DEV),
+                "workspace": torch.empty(max(4, kda.kda_mla_prefill_workspace_size(2, T, H, dt)),
+                                         dtype=torch.uint8, device=DEV)}
+        kw_d = {"o": torch.empty(2, H, 512, dtype=dt, device=DEV), "lse": torch.empty(2, H, device=DEV),
+                "workspace": torch.empty(kda.kda_mla_decode_workspace_size(2, H, dt), dtype=torch.uint8, device=DEV)}
+
+    def work():
+        c, kr, q, kv, qd = x
+        q_out = kda.kda_mla_append(c, kr, slots, cache, positions=at.to(torch.int32), rope=rope, k_out=k_out,
+                                   q_r=q[..., 128:])
+        o, lse = kda.kda_mla_prefill(q, kv, k_out, cu, cu, **kw_p)
+        od, lsed = kda.kda_mla_decode(qd, cache, table, lens, **kw_d)
+        return q_out, o, lse, od, lsed
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        work()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = work()
+    for _ in range(3):
+        for old, new in zip(x, draw()):
+            old.copy_(new)
+        cache.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out] + [cache.clone(), k_out.clone()]
+        for ws in (kw_p, kw_d):
+            assert not given or kda.kda_mla_check(ws["workspace"]) == kda.KDA_OK
+        cache.zero_()
+        want = [t.clone() for t in work()] + [cache, k_out]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
