@@ -401,8 +401,9 @@ kda_status kda_gdn_decode_step_pooled(const void *q, const void *k, const void *
  *
  * (a, b) -> (a cos - b sin, a sin + b cos) in float32, rounded once.  Strides
  * are multiples of 16 bytes (so that views of a projection's output can be
- * passed as they are).  T = 0 is a valid no-op.  Outputs must not overlap
- * inputs otherwise.
+ * passed as they are); those of k_out and q_out keep the rows of 64 apart
+ * (strides that make them overlap are rejected).  T = 0 is a valid no-op.
+ * Outputs must not overlap inputs otherwise.
  */
 kda_status kda_mla_append(const void *c, int64_t c_stride, const void *k_r,
                           int64_t k_r_stride, const int32_t *slots,

@@ -11,6 +11,18 @@ namespace {
 inline bool aligned16(const void *p) { return p == nullptr || ((uintptr_t)p & 15u) == 0; }
 inline bool aligned4(const void *p) { return p == nullptr || ((uintptr_t)p & 3u) == 0; }
 inline bool page_ok(int32_t page) { return page == 16 || page == 32 || page == 64 || page == 128; }
+// Whether any two of the rows of `row` elements at t * a + h * b, t < T, h < H, overlap
+// (strides >= 0): exact, so that any layout with separate rows is taken.
+bool rows_overlap(int64_t T, int64_t a, int64_t H, int64_t b, int64_t row) {
+    if ((T > 1 && a < row) || (H > 1 && b < row)) return true;
+    if (T <= 1 || H <= 1) return false;
+    if (a >= (__int128)(H - 1) * b + row || b >= (__int128)(T - 1) * a + row) return false;   // one inside the other
+    for (int64_t h = 1; h < H; ++h) {                       // rows (t, 0) and (0, h), nearest t
+        const __int128 at = (__int128)h * b, t = at / a;
+        if ((t < T && at - t * a < row) || (t + 1 < T && (t + 1) * a - at < row)) return true;
+    }
+    return false;
+}
 inline bool head_ok(int32_t dk, int32_t dv) { return dk == dv && (dk == 64 || dk == 128); }
 
 kda_status cuda_status(cudaError_t e) {
@@ -309,6 +321,9 @@ kda_status kda_mla_append(const void *c, int64_t c_stride, const void *k_r, int6
     for (int64_t x : {c_stride, k_r_stride, k_out ? k_out_stride : 0, q_r ? q_token_stride : 0,
                       q_r ? q_head_stride : 0, q_r ? qo_token_stride : 0, q_r ? qo_head_stride : 0})
         if (x < 0 || x % piece != 0) return KDA_ERR_INVALID_ARG;
+    if ((k_out && rows_overlap(T, k_out_stride, 1, 0, rope_dim)) ||
+        (q_out && rows_overlap(T, qo_token_stride, H, qo_head_stride, rope_dim)))
+        return KDA_ERR_INVALID_ARG;                         // whose store comes last would be open
     const kda_status dst = check_device_ptrs({c, k_r, slots, positions, rope, cache, k_out, q_r, q_out});
     if (dst != KDA_OK) return dst;
     kda::mla::AppendArgs a;
