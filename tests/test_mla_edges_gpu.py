@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import serving_kda_chunked_gb300 as kda
-from test_mla_gpu import DEV, DT, _call_decode, _call_prefill, _decode_inputs, _gen, _prefill_inputs, _rand
+from test_mla_gpu import DEV, DT, _call_decode, _call_prefill, _check_prefill, _decode_inputs, _gen, _prefill_inputs, _rand
 from test_mla_paths_gpu import LONG, _check_two_heads
 
 pytestmark = pytest.mark.gpu
@@ -132,6 +132,44 @@ def test_decode_lse_of_scores_that_are_not_numbers(lens, H, dtype, how):
     o, lse = _call_decode(q, cache, table, n)
     assert bool(torch.isnan(o[0]).all()) and bool(torch.isnan(lse[0]).all())
     assert bool(torch.isfinite(o[1:]).all()) and bool(torch.isfinite(lse[1:]).all())
+
+
+# ---- without rotation, and long keys -----------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,H,page", [(1, 1, 16), (37, 5, 32), (300, 32, 64), (65, 130, 128), (2500, 3, 64)])
+def test_append_without_rotation(dtype, T, H, page):
+    """Layers without position rotation: every value arrives as it was, out of
+    strided views, with padding tokens in between."""
+    g = _gen(166 + T)
+    P = -(-T // page) + 2
+    down = _rand(g, DT[dtype], T, 576 + 64)
+    c, kr = down[:, :512], down[:, 512:576]
+    q = _rand(g, DT[dtype], T, H, 192)[..., 128:]
+    q_abs = torch.full((T, H, 576), 3.0, dtype=DT[dtype], device=DEV)
+    k_out = torch.full((T, 128), 5.0, dtype=DT[dtype], device=DEV)
+    cache = torch.full((P, page, 576), 7.0, dtype=DT[dtype], device=DEV)
+    slots = torch.randperm(P * page, generator=g, device=DEV)[:T].to(torch.int32)
+    if T > 10:
+        slots[3], slots[4], slots[T - 1] = -1, P * page, -(1 << 31)
+    kda.kda_mla_append(c, kr, slots, cache, k_out=k_out[:, 64:], q_r=q, q_out=q_abs[..., 512:])
+    assert torch.equal(k_out[:, 64:], kr) and torch.equal(q_abs[..., 512:], q)
+    assert bool((q_abs[..., :512] == 3.0).all()) and bool((k_out[:, :64] == 5.0).all())
+    want = torch.full_like(cache, 7.0).view(-1, 576)
+    put = [t for t in range(T) if 0 <= int(slots[t]) < P * page]
+    want[slots[put].long()] = torch.cat([c, kr], 1)[put]
+    assert torch.equal(cache.view(-1, 576), want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_prefill_keys_past_32_bits(dtype):
+    """A few queries after 1 Mi tokens, the longest context of the library, with
+    key and value tensors of more than 2^31 elements."""
+    lens, H = [(3, 1 << 20), (2, 700)], 9
+    q, kv, kr, cu_q, cu_k = _prefill_inputs(lens, H, dtype, seed=167)
+    assert kv.numel() > 1 << 31
+    o, lse = _call_prefill(q, kv, kr, cu_q, cu_k, True)
+    _check_prefill(lens, q[:, H - 1:], kv[:, H - 1:], kr, True, dtype, o[:, H - 1:], lse[:, H - 1:])
 
 
 # ---- graphs ------------------------------------------------------------------------
