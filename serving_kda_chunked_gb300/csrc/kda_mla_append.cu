@@ -7,7 +7,7 @@
 // hold whole rotation pairs, loaded before either is stored by the same thread,
 // which makes in-place rotation safe.  The queries' parts are 128-byte pieces
 // of longer rows on both sides, so the memory sees no long runs: 65,536 tokens
-// move at 4.9 TB/s (128 us instead of 145 us where both sides are dense).
+// take 156 us = 4.57 TB/s (138 us = 5.2 TB/s where both sides are dense).
 // Measured and rejected: two or four tokens or heads a thread at a time (168 to
 // 300 us and 162 to 174 us), 16-byte units with the pair's other half fetched
 // from a neighbouring lane (177 us), registers cut to 40 (216 us).
@@ -168,8 +168,8 @@ cudaError_t launch(const AppendArgs &a, cudaStream_t st) {
     if (chunks > 65535) return cudaErrorInvalidValue;
     const int threads = (int)((items + chunks - 1) / chunks + 31) / 32 * 32;
     // up to 6144 threads an SM, about five times what is resident: 65,536 tokens
-    // of 32 heads take 157 us with a grid of 1536 threads an SM, 145 us with
-    // this one, 152 us with a block per token
+    // of 32 heads take 166 us with a grid of 1536 threads an SM, 156 us with
+    // this one, 171 us with a block per token
     int64_t blocks = (int64_t)nsm * 6144 / (threads * chunks);
     blocks = blocks < 1 ? 1 : (blocks < a.T ? blocks : a.T);
     cudaLaunchConfig_t cfg = {};

@@ -8,8 +8,8 @@
 // operations a token, 60 per byte at H = 32, a fifth of what the tensor cores
 // do in that time: HBM.  So a tile of 64 tokens is brought to shared memory
 // once and serves as the keys and as the values.  Measured: 256 sequences of up to
-// 8192 tokens, 32 heads, 201 us = 6.3 TB/s; one of 1 Mi tokens 180 us = 6.7 TB/s, what
-// a copy reaches; 48 of up to 9001, 128 heads (two groups of 64 read each tile), 83 us.
+// 8192 tokens, 32 heads, 203 us = 6.3 TB/s; one of 1 Mi tokens 183 us = 6.6 TB/s, 99 % of
+// what a copy reaches; 48 of up to 9001, 128 heads (two groups of 64 read each tile), 83 us.
 //
 // Both products are transposed: S^T [64 tokens x N heads] = C Q^T and
 // O^T [512 x N heads] = C^T P, so that the tokens or latent channels are the

@@ -10,7 +10,8 @@
 // queries of one head as two tiles (A, B) of 128 rows, so that one tile's
 // products run while the other tile's softmax does, and each key tile of 128
 // tokens is read once for both.  Measured: a prompt of 8192 tokens, 32 heads, 421 us
-// = 1.63 PFLOP/s of the pairs that are seen (tensor pipe 71% busy; softmax between).
+// = 1.63 PFLOP/s of the pairs that are seen, 465 to 477 us under the power cap (tensor
+// pipe 71% busy; softmax between).
 //
 // CTAs take (256 queries, head) pairs, those with the most keys first.  Where
 // there are few pairs, the keys of those above an SM's share of all key tiles, or
@@ -50,7 +51,7 @@ constexpr int RING = 8, PER = 5;                            // blocks in the rin
 // SM.  It reads the keys twice as often and its score products are 128 x 64,
 // bound by their operands in shared memory; but one CTA's start and end run beside
 // the other's products.  With one place for the scores 195 prompts of 400 tokens
-// took the same time, 8 of up to 2048 131 us (115).
+// took the same time, 8 of up to 2048 131 us (then 115).
 template <int TILES> struct Cfg {
     static constexpr int ROWS = TILES * BQ, BK = 64 * TILES;
     static constexpr int SPLIT = TILES;                     // softmax threads a row; each has 64 of a key tile's columns
@@ -799,15 +800,19 @@ uint64_t prefill_tc_workspace_bytes(int32_t N, int64_t Tq) { return layout(N, Tq
 cudaError_t launch_prefill_tc(const PrefillArgs &a, cudaStream_t st) {
     // One tile where a CTA's start and end are much of its time (few keys or few
     // queries a sequence) or where the SMs get few CTAs; two where the products
-    // decide.  In us, one tile and two, 16 heads where not said otherwise:
-    //   64 prompts of up to 300 tokens                 62 and 89
-    //   195 of 400, 8 heads                           272 and 292
-    //   38 of 64 after 4000                           144 and 164
-    //   1 of 2048                                      37 and 50
-    //   8 of up to 2048, 32 heads                     115 and 130
-    //   11 of 900, 31 heads (work 3600)               181 and 173
-    //   4 of 2560, 30 heads (work 5100)               235 and 227
-    //   1 of 8192, 32 heads (work 28000)              489 and 430
+    // decide.  In us, one tile and two, 16 heads where not said otherwise, all
+    // under the power cap:
+    //   64 prompts of up to 300 tokens                 69 and 95
+    //   195 of 400, 8 heads                           269 and 284
+    //   38 of 64 after 4000                           204 and 227
+    //   1 of 2048 (work 860)                           44 and 52
+    //   8 of up to 2048, 32 heads (work 2450)         117 and 125
+    //   11 of 900, 31 heads (work 3550)               185 and 172
+    //   4 of 2560, 30 heads (work 10100)              236 and 227
+    //   1 of 8192, 32 heads (work 27600)              512 and 465
+    // 11 of 900 is on the wrong side of the rule, which loses 8 % there.  Between
+    // work 2450 and 3550 nothing is measured, nor how far ragged lengths move the
+    // point: the host knows the sums of the lengths only.
     int sms = 1;
     const cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess) return e;

@@ -1,6 +1,7 @@
 // kda_mla_simt.cu -- latent attention of fp32 tensors on the CUDA cores: the
 // expanded form in tiles with a running maximum and sum, and the absorbed form.
-// (tf32 tensor-core products keep 11 of the 24 bits.)
+// (A tf32 tensor-core product keeps 11 of the 24 bits.  Three products of operands
+// split in two would keep nearly all; that has not been built.)
 #include "kda_mla_split.cuh"
 
 namespace kda {
