@@ -488,7 +488,155 @@ kda_status kda_mla_decode(const void *q, const void *cache, const int32_t *table
 uint64_t kda_mla_decode_workspace_size(int32_t B, int32_t H, int32_t dtype);
 
 /*
- * kda_prefill_check for kda_mla_prefill and kda_mla_decode: synchronise
+ * Drafted tokens.  A step of one token a sequence reads a whole state or cache
+ * for it; T drafted tokens cost the same bytes.  Four operators take a tree of
+ * drafted tokens through a model and settle what stays of it:
+ *   - kda_tree_step: a KDA (kda_gdn_tree_step: Gated DeltaNet) layer's outputs
+ *     for all nodes of a tree, the state left as it is;
+ *   - kda_mla_tree_decode: absorbed latent attention of all nodes over the
+ *     paged cache, to which the nodes' rows have been appended;
+ *   - kda_tree_verify: which nodes the target model accepts, and the token
+ *     behind the last one, from given random numbers;
+ *   - kda_tree_commit: the state advanced along the accepted path.  The latent
+ *     cache needs no operator of its own: kda_mla_append puts the accepted
+ *     nodes' rows to their final slots, with slot -1 for the others.
+ *
+ * Conventions in addition to those at the top of this file
+ *   - A sequence has T nodes, 1 <= T <= 64.  parents [B, T] int32 holds, for
+ *     node i, an earlier node (0 <= parent < i), or -1 where the node follows the
+ *     committed tokens; any other value makes it a padding node, and so are
+ *     the nodes behind one.  Several nodes may have -1.  A node's path is itself and its
+ *     ancestors, in the order of their index.
+ *   - Padding nodes' inputs may hold anything; their outputs are 0 (lse -inf).
+ *   - Neither parents nor slots nor lengths are read on the host, and no value
+ *     in them leads outside the buffers.  Equal inputs give equal bits.
+ */
+
+/*
+ * kda_tree_step -- outputs of a KDA layer for a tree of drafted tokens.
+ *
+ *   q, k       [B, T, H, dk]     v, o  [B, T, H, dv]    dtype
+ *   g          [B, T, H, dk]     float32 log-gates (kda_gdn_tree_step: [B, T, H])
+ *   beta       [B, T, H]         float32
+ *   S          [P, H, dk, dv]    float32 states, read only
+ *   slots      [B]               int32, state of each sequence, or NULL (P = B and
+ *                                sequence b has state b); a value outside [0, P)
+ *                                skips the sequence (its o rows are zeroed)
+ *   parents    [B, T]            int32
+ *   dk, dv     64 or 128, dk == dv
+ *
+ * Row (b, i) of o is what kda_decode_step gives for node i after the decode
+ * steps of its ancestors, started from the state.  bf16: the product of the nodes'
+ * rows with the state takes both rounded to tf32 (11 bits), sums are float32;
+ * fp32: float32 throughout.  B = 0 is a valid no-op.
+ */
+kda_status kda_tree_step(const void *q, const void *k, const void *v,
+                         const float *g, const float *beta, const float *S,
+                         const int32_t *slots, int32_t P, const int32_t *parents,
+                         int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv,
+                         int32_t dtype, void *o, void *stream);
+kda_status kda_gdn_tree_step(const void *q, const void *k, const void *v,
+                             const float *g, const float *beta, const float *S,
+                             const int32_t *slots, int32_t P,
+                             const int32_t *parents, int32_t B, int32_t T,
+                             int32_t H, int32_t dk, int32_t dv, int32_t dtype,
+                             void *o, void *stream);
+
+/*
+ * kda_tree_commit -- the states advanced along a path of nodes, as by one
+ * kda_decode_step a node.
+ *
+ *   k, v, g, beta, slots  as for kda_tree_step; the slots in [0, P) must be
+ *                         distinct
+ *   S          [P, H, dk, dv]    float32 states, updated in place
+ *   path       [B, T]            int32, nodes in their order up to the first value
+ *                                outside [0, T); a sequence without any keeps its
+ *                                state (it is neither read nor written)
+ */
+kda_status kda_tree_commit(const void *k, const void *v, const float *g,
+                           const float *beta, float *S, const int32_t *slots,
+                           int32_t P, const int32_t *path, int32_t B, int32_t T,
+                           int32_t H, int32_t dk, int32_t dv, int32_t dtype,
+                           void *stream);
+kda_status kda_gdn_tree_commit(const void *k, const void *v, const float *g,
+                               const float *beta, float *S,
+                               const int32_t *slots, int32_t P,
+                               const int32_t *path, int32_t B, int32_t T,
+                               int32_t H, int32_t dk, int32_t dv, int32_t dtype,
+                               void *stream);
+
+/*
+ * kda_mla_tree_decode -- kda_mla_decode for the nodes of a tree.
+ *
+ *   q          [B, T, H, 576]    T * H <= 65535
+ *   ctx_lens   [B]               int32, tokens in front of the tree, clamped into
+ *                                [0, max_pages * page]; node i's row is that of token
+ *                                ctx_lens[b] + i (nodes behind the table's end have none)
+ *   parents    [B, T]            int32
+ *   o          [B, T, H, 512]    lse [B, T, H] float32, or NULL
+ *   cache, table, scale, workspace   as for kda_mla_decode
+ *
+ * A node sees the tokens in front of the tree, its ancestors and itself.  What
+ * no node sees by length, by a hidden page or as padding may hold anything; the row of
+ * a node that is not padding is finite even for nodes that do not see it.
+ */
+kda_status kda_mla_tree_decode(const void *q, const void *cache,
+                               const int32_t *table, const int32_t *ctx_lens,
+                               const int32_t *parents, int32_t B, int32_t T,
+                               int32_t H, int32_t n_pages, int32_t page,
+                               int32_t max_pages, int32_t latent,
+                               int32_t rope_dim, int32_t dtype, float scale,
+                               void *o, float *lse, void *workspace,
+                               uint64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace kda_mla_tree_decode needs.  Host arithmetic. */
+uint64_t kda_mla_tree_decode_workspace_size(int32_t B, int32_t T, int32_t H,
+                                            int32_t dtype);
+
+/*
+ * kda_tree_verify -- which drafted tokens are accepted, so that the tokens of
+ * a sequence are distributed as the target's own.
+ *
+ *   target     [B, T, V]   dtype    row i: the target's probabilities for what follows
+ *                                   node i; rows are target_stride >= V elements apart
+ *   draft      [B, T, V]   dtype    row i: the probabilities from which node i's
+ *                                   children were drawn, independently of one another
+ *                                   (draft_stride); NULL: the children were chosen, not
+ *                                   drawn
+ *   tokens     [B, T]      int32    node i's token; one outside [0, V) is never
+ *                                   accepted (tokens[b][0] is not looked at)
+ *   parents    [B, T]      int32    node 0 is the last committed token and has -1; with
+ *                                   any other value the sequence is skipped
+ *   uniform    [B, T]      float32  random numbers in [0, 1): one for node i's test,
+ *                                   and uniform[b][0] for the last token
+ *   path       [B, T]      int32    (written) the accepted nodes in order, node 0 first,
+ *                                   then -1
+ *   count      [B]         int32    (written) how many there are
+ *   next       [B]         int32    (written) the token behind them
+ *
+ * From node 0 on, with p and q the target's and the draft's row at the node, the
+ * children are tried in the order of their index: with R = p and S = 1, child x is
+ * accepted if uniform q(x) S < R(x), and the walk goes on there.  Else
+ * R = max(R / S - q, 0) and S = the sum of R, and the next child is tried.
+ * Without draft probabilities q is 1 at the child's token and 0 elsewhere, and a
+ * rejection takes the token out of R and its probability out of S.  When no
+ * child is left, next is the first token at which the running sum of R exceeds
+ * uniform[b][0] times all of it (the last token with R > 0 where none does); where
+ * nothing is left of R, R = p.  Skipped sequences have path -1, count 0 and next -1;
+ * a target row without a positive value gives next = -1.
+ *
+ * Probabilities are finite and >= 0.  Sums over V and comparisons are held in pairs
+ * of floats and float64, so that results do not depend on the order of a sum.
+ */
+kda_status kda_tree_verify(const void *target, int64_t target_stride,
+                           const void *draft, int64_t draft_stride,
+                           const int32_t *tokens, const int32_t *parents,
+                           const float *uniform, int32_t B, int32_t T,
+                           int32_t V, int32_t dtype, int32_t *path,
+                           int32_t *count, int32_t *next, void *stream);
+
+/*
+ * kda_prefill_check for kda_mla_prefill, kda_mla_decode and kda_mla_tree_decode: synchronise
  * `stream` and report the device-side status of the last call that used
  * `workspace` (KDA_ERR_TIMEOUT: a bounded wait gave up and outputs are
  * incomplete).  Every call that launches something and was passed a workspace of

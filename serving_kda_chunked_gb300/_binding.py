@@ -106,6 +106,20 @@ def load() -> ctypes.CDLL:
         lib.kda_mla_decode.restype = ctypes.c_int
         lib.kda_mla_decode_workspace_size.argtypes = [i32, i32, i32]
         lib.kda_mla_decode_workspace_size.restype = u64
+        lib.kda_mla_tree_decode.argtypes = [
+            vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, i32, f32, vp, vp, vp, u64, vp]
+        lib.kda_mla_tree_decode.restype = ctypes.c_int
+        lib.kda_mla_tree_decode_workspace_size.argtypes = [i32, i32, i32, i32]
+        lib.kda_mla_tree_decode_workspace_size.restype = u64
+        for fn in (lib.kda_tree_step, lib.kda_gdn_tree_step):
+            fn.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32, vp, vp]
+            fn.restype = ctypes.c_int
+        for fn in (lib.kda_tree_commit, lib.kda_gdn_tree_commit):
+            fn.argtypes = [vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32, vp]
+            fn.restype = ctypes.c_int
+        lib.kda_tree_verify.argtypes = [
+            vp, i64, vp, i64, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp]
+        lib.kda_tree_verify.restype = ctypes.c_int
         lib.kda_mla_check.argtypes = [vp, vp]
         lib.kda_mla_check.restype = ctypes.c_int
         lib.kda_status_string.argtypes = [i32]
@@ -751,3 +765,152 @@ def kda_mla_decode(q, cache, table, seq_lens, *, scale=None, o=None, lse=None, w
     _call("kda_mla_decode", dev, stream, pq, pc, pt, pn, B, H, cs[0], cs[1], width, MLA_LATENT,
           MLA_ROPE, code, _MLA_SCALE if scale is None else scale, po, pl, pw, nw)
     return o, lse
+
+
+def kda_mla_tree_decode_workspace_size(B, T, H, dtype) -> int:
+    """Workspace bytes ``kda_mla_tree_decode`` needs."""
+    code = _DTYPE_CODE[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
+    return int(_mla_lib().kda_mla_tree_decode_workspace_size(B, T, H, code))
+
+
+def kda_mla_tree_decode(q, cache, table, ctx_lens, parents, *, scale=None, o=None, lse=None,
+                        workspace=None, stream=None):
+    """Absorbed latent attention of a tree of drafted tokens per sequence
+    over the paged cache (``kda_mla_tree_decode`` in kda.h).
+
+    q [B, T, H, 576], cache [n_pages, page, 576], both bf16 or fp32; table
+    [B, max_pages], ctx_lens [B] (tokens in front of the tree, whose rows are
+    those of tokens ctx_lens .. ctx_lens + T - 1) and parents [B, T] int32 on
+    the device.  Returns (o [B, T, H, 512], lse [B, T, H] fp32).
+    """
+    dt, dev = _first("q", q, 4)
+    B, T, H, _ = q.shape
+    pq = _need("q", q, dt, (B, T, H, _MLA_ROW), dev)
+    cs = _cache_shape(cache)
+    pc = _need("cache", cache, dt, cs, dev)
+    width = table.shape[1] if isinstance(table, torch.Tensor) and table.dim() == 2 else -1
+    pt = _need("table", table, torch.int32, (B, width), dev)
+    pn = _need("ctx_lens", ctx_lens, torch.int32, (B,), dev)
+    pp = _need("parents", parents, torch.int32, (B, T), dev)
+    device = q.device
+    side = _other_stream(stream, device)
+    o, po = _given("o", o, dt, (B, T, H, MLA_LATENT), dev, device, side)
+    lse, pl = _given("lse", lse, torch.float32, (B, T, H), dev, device, side)
+    code = _DTYPE_CODE[dt]
+    need = _mla_lib().kda_mla_tree_decode_workspace_size(B, T, H, code)
+    workspace, pw, nw = _scratch(workspace, need, dev, device, side)
+    _record(side, q, cache, table, ctx_lens, parents)
+    _call("kda_mla_tree_decode", dev, stream, pq, pc, pt, pn, pp, B, T, H, cs[0], cs[1], width,
+          MLA_LATENT, MLA_ROPE, code, _MLA_SCALE if scale is None else scale, po, pl, pw, nw)
+    return o, lse
+
+
+def _tree_inputs(k, v, g, beta, S, slots, scalar_gate):
+    """What a tree's step and commit check alike: type, device, sizes and addresses."""
+    dt, dev = _first("k", k, 4)
+    B, T, H, dk = k.shape
+    dv = v.shape[-1] if isinstance(v, torch.Tensor) and v.dim() else -1
+    pk = _need("k", k, dt, (B, T, H, dk), dev)
+    pv = _need("v", v, dt, (B, T, H, dv), dev)
+    pg = _need("g", g, torch.float32, (B, T, H) if scalar_gate else (B, T, H, dk), dev)
+    pb = _need("beta", beta, torch.float32, (B, T, H), dev)
+    P = B
+    ps = None
+    if slots is not None:
+        P = S.shape[0] if isinstance(S, torch.Tensor) and S.dim() else -1
+        ps = _need("slots", slots, torch.int32, (B,), dev)
+    pS = _need("S", S, torch.float32, (P, H, dk, dv), dev)
+    return dt, dev, (B, T, H, dk, dv), P, (pk, pv, pg, pb, pS, ps)
+
+
+def _tree_step(fn, scalar_gate, q, k, v, g, beta, S, parents, slots, o, stream):
+    dt, dev, sizes, P, (pk, pv, pg, pb, pS, ps) = _tree_inputs(k, v, g, beta, S, slots, scalar_gate)
+    B, T, H, dk, dv = sizes
+    pq = _need("q", q, dt, (B, T, H, dk), dev)
+    pp = _need("parents", parents, torch.int32, (B, T), dev)
+    device = k.device
+    side = _other_stream(stream, device)
+    o, po = _given("o", o, dt, (B, T, H, dv), dev, device, side)
+    _record(side, q, k, v, g, beta, S, parents, slots)
+    _call(fn, dev, stream, pq, pk, pv, pg, pb, pS, ps, P, pp, B, T, H, dk, dv, _DTYPE_CODE[dt], po)
+    return o
+
+
+def kda_tree_step(q, k, v, g, beta, S, parents, *, slots=None, o=None, stream=None):
+    """A KDA layer's outputs for a tree of drafted tokens per sequence; the
+    states are read only (``kda_tree_step`` in kda.h).
+
+    q, k [B, T, H, dk], v [B, T, H, dv] (bf16 or fp32); g [B, T, H, dk] and
+    beta [B, T, H] fp32; parents [B, T] int32; S [B, H, dk, dv] fp32, or with
+    ``slots`` [B] int32 a pool [P, H, dk, dv].  Returns o [B, T, H, dv].
+    """
+    return _tree_step("kda_tree_step", False, q, k, v, g, beta, S, parents, slots, o, stream)
+
+
+def kda_gdn_tree_step(q, k, v, g, beta, S, parents, *, slots=None, o=None, stream=None):
+    """A Gated DeltaNet layer's outputs for a tree of drafted tokens
+    (``kda_gdn_tree_step`` in kda.h): as ``kda_tree_step`` with g [B, T, H]."""
+    return _tree_step("kda_gdn_tree_step", True, q, k, v, g, beta, S, parents, slots, o, stream)
+
+
+def _tree_commit(fn, scalar_gate, k, v, g, beta, S, path, slots, stream):
+    dt, dev, sizes, P, (pk, pv, pg, pb, pS, ps) = _tree_inputs(k, v, g, beta, S, slots, scalar_gate)
+    B, T, H, dk, dv = sizes
+    pp = _need("path", path, torch.int32, (B, T), dev)
+    _record(_other_stream(stream, k.device), k, v, g, beta, S, path, slots)
+    _call(fn, dev, stream, pk, pv, pg, pb, pS, ps, P, pp, B, T, H, dk, dv, _DTYPE_CODE[dt])
+
+
+def kda_tree_commit(k, v, g, beta, S, path, *, slots=None, stream=None):
+    """States advanced in place along the accepted path of a tree of drafted
+    tokens (``kda_tree_commit`` in kda.h).
+
+    k, v, g, beta, S and ``slots`` as for ``kda_tree_step``; path [B, T] int32
+    holds nodes up to the first value outside [0, T) (``kda_tree_verify``'s).
+    """
+    _tree_commit("kda_tree_commit", False, k, v, g, beta, S, path, slots, stream)
+
+
+def kda_gdn_tree_commit(k, v, g, beta, S, path, *, slots=None, stream=None):
+    """Gated DeltaNet states advanced along the accepted path
+    (``kda_gdn_tree_commit`` in kda.h): as ``kda_tree_commit`` with g [B, T, H]."""
+    _tree_commit("kda_gdn_tree_commit", True, k, v, g, beta, S, path, slots, stream)
+
+
+def _vocabulary(name, t, dt, B, T, V, dev):
+    """(address, elements between rows) of probabilities [B, T, V], whose rows
+    may be the front of longer ones."""
+    address = _need(name, t, dt, (B, T, V), dev, True)
+    row = t.stride(1) if T > 1 else (t.stride(0) if B > 1 else V)
+    if B > 1 and t.stride(0) != T * row:
+        raise ValueError("%s must have evenly spaced rows, got strides %s" % (name, t.stride()))
+    return address, row
+
+
+def kda_tree_verify(target, tokens, parents, uniform, *, draft=None, path=None, count=None,
+                    next_token=None, stream=None):
+    """Which drafted tokens the target model accepts, and the token behind
+    the last of them (``kda_tree_verify`` in kda.h).
+
+    target [B, T, V] probabilities (bf16 or fp32) of what follows each node;
+    ``draft`` [B, T, V] those from which a node's children were drawn, None
+    where they were chosen; rows of both may be the front of longer ones.
+    tokens, parents [B, T] int32; uniform [B, T] fp32 random numbers.  Returns
+    (path [B, T], count [B], next_token [B]), all int32.
+    """
+    dt, dev = _first("target", target, 3)
+    B, T, V = target.shape
+    pt, ts = _vocabulary("target", target, dt, B, T, V, dev)
+    pd, ds = _vocabulary("draft", draft, dt, B, T, V, dev) if draft is not None else (None, 0)
+    px = _need("tokens", tokens, torch.int32, (B, T), dev)
+    pp = _need("parents", parents, torch.int32, (B, T), dev)
+    pu = _need("uniform", uniform, torch.float32, (B, T), dev)
+    device = target.device
+    side = _other_stream(stream, device)
+    path, ppath = _given("path", path, torch.int32, (B, T), dev, device, side)
+    count, pcount = _given("count", count, torch.int32, (B,), dev, device, side)
+    next_token, pnext = _given("next_token", next_token, torch.int32, (B,), dev, device, side)
+    _record(side, target, draft, tokens, parents, uniform)
+    _call("kda_tree_verify", dev, stream, pt, ts, pd, ds, px, pp, pu, B, T, V, _DTYPE_CODE[dt],
+          ppath, pcount, pnext)
+    return path, count, next_token

@@ -2,6 +2,7 @@
 #include "../../include/kda.h"
 #include "kda_internal.cuh"
 #include "kda_mla.cuh"
+#include "kda_tree.cuh"
 
 #include <initializer_list>
 #include <math.h>
@@ -128,6 +129,51 @@ kda_status decode_impl(const void *q, const void *k, const void *v, const float 
     a.slots = pooled ? slots : nullptr; a.P = P;
     a.scalar_gate = scalar_gate;
     return cuda_status(kda::launch_decode(a, (cudaStream_t)stream));
+}
+
+// What a step and a commit over a tree of drafted tokens share: sizes and the state.
+kda_status tree_sizes(int32_t P, int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, int32_t dtype, bool pooled) {
+    if (B < 0 || T <= 0 || H <= 0 || dk <= 0 || dv <= 0 || (B > 0 && P <= 0)) return KDA_ERR_INVALID_ARG;
+    if (dtype != KDA_BF16 && dtype != KDA_FP32) return KDA_ERR_INVALID_ARG;
+    if (!pooled && P != B) return KDA_ERR_INVALID_ARG;
+    if (!head_ok(dk, dv) || T > kda::tree::MAX_NODES) return KDA_ERR_UNSUPPORTED;
+    if ((int64_t)B * H > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+kda_status tree_step_impl(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                          const float *S, const int32_t *slots, int32_t P, const int32_t *parents, int32_t B,
+                          int32_t T, int32_t H, int32_t dk, int32_t dv, int32_t dtype, void *o,
+                          bool scalar_gate, void *stream) {
+    const kda_status sizes = tree_sizes(P, B, T, H, dk, dv, dtype, slots != nullptr);
+    if (sizes != KDA_OK || B == 0) return sizes;
+    if (!q || !k || !v || !g || !beta || !S || !parents || !o) return KDA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !(scalar_gate ? aligned4(g) : aligned16(g)) ||
+        !aligned16(S) || !aligned16(o) || !aligned4(beta) || !aligned4(slots) || !aligned4(parents))
+        return KDA_ERR_INVALID_ARG;
+    const kda_status dst = check_device_ptrs({q, k, v, g, beta, S, slots, parents, o});
+    if (dst != KDA_OK) return dst;
+    kda::tree::StepArgs a;
+    a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.S = S; a.slots = slots; a.parents = parents;
+    a.o = o; a.P = P; a.B = B; a.T = T; a.H = H; a.d = dk; a.dtype = dtype; a.scalar_gate = scalar_gate;
+    return cuda_status(kda::tree::launch_step(a, (cudaStream_t)stream));
+}
+
+kda_status tree_commit_impl(const void *k, const void *v, const float *g, const float *beta, float *S,
+                            const int32_t *slots, int32_t P, const int32_t *path, int32_t B, int32_t T,
+                            int32_t H, int32_t dk, int32_t dv, int32_t dtype, bool scalar_gate, void *stream) {
+    const kda_status sizes = tree_sizes(P, B, T, H, dk, dv, dtype, slots != nullptr);
+    if (sizes != KDA_OK || B == 0) return sizes;
+    if (!k || !v || !g || !beta || !S || !path) return KDA_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !(scalar_gate ? aligned4(g) : aligned16(g)) || !aligned16(S) ||
+        !aligned4(beta) || !aligned4(slots) || !aligned4(path))
+        return KDA_ERR_INVALID_ARG;
+    const kda_status dst = check_device_ptrs({k, v, g, beta, S, slots, path});
+    if (dst != KDA_OK) return dst;
+    kda::tree::CommitArgs a;
+    a.k = k; a.v = v; a.g = g; a.beta = beta; a.S = S; a.slots = slots; a.path = path;
+    a.P = P; a.B = B; a.T = T; a.H = H; a.d = dk; a.dtype = dtype; a.scalar_gate = scalar_gate;
+    return cuda_status(kda::tree::launch_commit(a, (cudaStream_t)stream));
 }
 
 }  // namespace
@@ -415,6 +461,92 @@ kda_status kda_mla_decode(const void *q, const void *cache, const int32_t *table
                                          : kda::mla::launch_decode_simt(a, (cudaStream_t)stream));
 }
 
+uint64_t kda_mla_tree_decode_workspace_size(int32_t B, int32_t T, int32_t H, int32_t dtype) {
+    if (T <= 0 || T > kda::tree::MAX_NODES || H <= 0 || H > 65535) return 0;
+    return kda_mla_decode_workspace_size(B, T * H, dtype);
+}
+
+kda_status kda_mla_tree_decode(const void *q, const void *cache, const int32_t *table,
+                               const int32_t *ctx_lens, const int32_t *parents, int32_t B, int32_t T,
+                               int32_t H, int32_t n_pages, int32_t page, int32_t max_pages,
+                               int32_t latent, int32_t rope_dim, int32_t dtype, float scale, void *o,
+                               float *lse, void *workspace, uint64_t workspace_bytes, void *stream) {
+    if (B < 0 || T <= 0 || H <= 0 || n_pages <= 0 || page <= 0 || max_pages < 0 || latent <= 0 || rope_dim <= 0)
+        return KDA_ERR_INVALID_ARG;
+    if (dtype != KDA_BF16 && dtype != KDA_FP32) return KDA_ERR_INVALID_ARG;
+    if (!isfinite(scale)) return KDA_ERR_INVALID_ARG;
+    if (latent != kda::mla::LATENT || rope_dim != kda::mla::ROPE || !page_ok(page) ||
+        T > kda::tree::MAX_NODES || B > 65535 || H > 65535 || (int64_t)T * H > 65535 ||
+        (int64_t)n_pages * page > 0x7fffffffLL || (int64_t)max_pages * page > 0x7fffffffLL)
+        return KDA_ERR_UNSUPPORTED;
+    if (B == 0) return KDA_OK;
+    if (!q || !cache || (max_pages > 0 && !table) || !ctx_lens || !parents || !o) return KDA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(cache) || !aligned4(table) || !aligned4(ctx_lens) || !aligned4(parents) ||
+        !aligned16(o) || !aligned4(lse))
+        return KDA_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < kda_mla_tree_decode_workspace_size(B, T, H, dtype) ||
+        !aligned16(workspace))
+        return KDA_ERR_INVALID_ARG;
+    const kda_status dst = check_device_ptrs({q, cache, table, ctx_lens, parents, o, lse, workspace});
+    if (dst != KDA_OK) return dst;
+    kda::mla::DecodeArgs a;
+    a.q = q; a.cache = cache; a.table = table; a.seq_lens = ctx_lens; a.o = o; a.lse = lse;
+    a.ws = workspace; a.B = B; a.H = T * H; a.n_pages = n_pages; a.page = page;
+    a.max_pages = max_pages; a.dtype = dtype; a.scale = scale;
+    a.parents = parents; a.T = T; a.heads = H;
+    return cuda_status(dtype == KDA_BF16 ? kda::mla::launch_decode_tc(a, (cudaStream_t)stream)
+                                         : kda::mla::launch_decode_simt(a, (cudaStream_t)stream));
+}
+
+kda_status kda_tree_step(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                         const float *S, const int32_t *slots, int32_t P, const int32_t *parents, int32_t B,
+                         int32_t T, int32_t H, int32_t dk, int32_t dv, int32_t dtype, void *o, void *stream) {
+    return tree_step_impl(q, k, v, g, beta, S, slots, P, parents, B, T, H, dk, dv, dtype, o, false, stream);
+}
+
+kda_status kda_gdn_tree_step(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                             const float *S, const int32_t *slots, int32_t P, const int32_t *parents,
+                             int32_t B, int32_t T, int32_t H, int32_t dk, int32_t dv, int32_t dtype, void *o,
+                             void *stream) {
+    return tree_step_impl(q, k, v, g, beta, S, slots, P, parents, B, T, H, dk, dv, dtype, o, true, stream);
+}
+
+kda_status kda_tree_commit(const void *k, const void *v, const float *g, const float *beta, float *S,
+                           const int32_t *slots, int32_t P, const int32_t *path, int32_t B, int32_t T,
+                           int32_t H, int32_t dk, int32_t dv, int32_t dtype, void *stream) {
+    return tree_commit_impl(k, v, g, beta, S, slots, P, path, B, T, H, dk, dv, dtype, false, stream);
+}
+
+kda_status kda_gdn_tree_commit(const void *k, const void *v, const float *g, const float *beta, float *S,
+                               const int32_t *slots, int32_t P, const int32_t *path, int32_t B, int32_t T,
+                               int32_t H, int32_t dk, int32_t dv, int32_t dtype, void *stream) {
+    return tree_commit_impl(k, v, g, beta, S, slots, P, path, B, T, H, dk, dv, dtype, true, stream);
+}
+
+kda_status kda_tree_verify(const void *target, int64_t target_stride, const void *draft,
+                           int64_t draft_stride, const int32_t *tokens, const int32_t *parents,
+                           const float *uniform, int32_t B, int32_t T, int32_t V, int32_t dtype,
+                           int32_t *path, int32_t *count, int32_t *next, void *stream) {
+    if (B < 0 || T <= 0 || V <= 0) return KDA_ERR_INVALID_ARG;
+    if (dtype != KDA_BF16 && dtype != KDA_FP32) return KDA_ERR_INVALID_ARG;
+    if (T > kda::tree::MAX_NODES || (int64_t)B * 8 > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
+    if (B == 0) return KDA_OK;
+    if (!target || !tokens || !parents || !uniform || !path || !count || !next) return KDA_ERR_INVALID_ARG;
+    const int64_t rows = (int64_t)B * T - 1, most = (int64_t)1 << 60;
+    for (int64_t x : {target_stride, draft ? draft_stride : target_stride})
+        if (x < V || (rows > 0 && x > most / rows)) return KDA_ERR_INVALID_ARG;
+    if (!aligned16(target) || !aligned16(draft) || !aligned4(tokens) || !aligned4(parents) ||
+        !aligned4(uniform) || !aligned4(path) || !aligned4(count) || !aligned4(next))
+        return KDA_ERR_INVALID_ARG;
+    const kda_status dst = check_device_ptrs({target, draft, tokens, parents, uniform, path, count, next});
+    if (dst != KDA_OK) return dst;
+    kda::tree::VerifyArgs a;
+    a.target = target; a.draft = draft; a.tokens = tokens; a.parents = parents; a.uniform = uniform;
+    a.path = path; a.count = count; a.next = next; a.target_stride = target_stride;
+    a.draft_stride = draft ? draft_stride : 0; a.B = B; a.T = T; a.V = V; a.dtype = dtype;
+    return cuda_status(kda::tree::launch_verify(a, (cudaStream_t)stream));
+}
+
 kda_status kda_mla_check(const void *workspace, void *stream) {
     return kda_prefill_check(workspace, stream);
 }
@@ -432,6 +564,6 @@ const char *kda_status_string(int32_t status) {
     }
 }
 
-int32_t kda_abi_version(void) { return (2 << 16) | 5; }
+int32_t kda_abi_version(void) { return (2 << 16) | 6; }
 
 }  // extern "C"

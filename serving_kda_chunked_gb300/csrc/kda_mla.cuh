@@ -40,6 +40,10 @@ struct DecodeArgs {
     void *ws;
     int32_t B, H, n_pages, page, max_pages, dtype;
     float scale;
+    // A tree of T drafted tokens a sequence: H counts the rows of all of them, row
+    // t * heads + h; seq_lens are the tokens in front of the tree.
+    const int32_t *parents = nullptr;
+    int32_t T = 0, heads = 0;
 };
 
 cudaError_t launch_append(const AppendArgs &a, cudaStream_t st);

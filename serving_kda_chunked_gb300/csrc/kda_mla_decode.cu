@@ -29,6 +29,7 @@
 // issue; warp 9: loads.
 #include "kda_mla_split.cuh"
 #include "kda_mla_tc.cuh"
+#include "kda_tree.cuh"
 
 #include <mutex>
 
@@ -88,7 +89,9 @@ __device__ __forceinline__ void st_cols(uint32_t a, const float (&v)[8]) {
 __device__ __forceinline__ void ld_cols(uint32_t a, float (&v)[16]) { tmem_ld16(a, v); }
 __device__ __forceinline__ void st_cols(uint32_t a, const float (&v)[16]) { tmem_st16(a, v); }
 
-template <int N>
+// TREE: the rows are the heads of a tree's nodes (kda_mla_tree_decode); a node's rows see
+// the tokens in front of the tree, the node and its ancestors.
+template <int N, bool TREE>
 __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constant__ DecParams p) {
     using L = Smem<N>;
     constexpr uint32_t TCOLS = N == 64 ? 512 : 256;
@@ -156,6 +159,15 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                 __syncwarp();
                 ++seg;
                 const int32_t *tab = p.table + (int64_t)w.b * p.max_pages;
+                uint64_t nodes = 0;                                        // that are not padding
+                int64_t front = 0;
+                if constexpr (TREE) {
+                    front = seq_front(p, w.b);
+                    const int32_t *par = p.parents + (int64_t)w.b * p.T;
+                    const uint32_t lo = __ballot_sync(0xffffffffu, lane < p.T && tree::ancestors(par, lane));
+                    const uint32_t hi = __ballot_sync(0xffffffffu, lane + 32 < p.T && tree::ancestors(par, lane + 32));
+                    nodes = (uint64_t)hi << 32 | lo;
+                }
                 // first row / 8 of this lane's box of 32, and of the next 32
                 auto boxes = [&](int64_t i) {
                     const int64_t t = i * TOK + ((int64_t)lane << psh);
@@ -180,6 +192,11 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                     }
                     const int64_t left = w.len - i * TOK;
                     if (left < TOK) mask &= (1ull << left) - 1;
+                    if constexpr (TREE) {
+                        const int64_t d = i * TOK - front;                 // node of the tile's first token
+                        if (d >= 0) mask &= d < 64 ? nodes >> d : 0ull;
+                        else if (d > -64) mask &= nodes << -d | ((1ull << -d) - 1);
+                    }
                     if (k >= 2) ok = wait_or_fail(&empty[st], ((k >> 1) & 1) ^ 1, fail);
                     if (!ok) break;
                     if (elect_one()) {
@@ -289,6 +306,19 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
             const int row = 16 * w4 + (lane >> 2);          // this thread's tokens: row, row + 8
             do {
                 float m[V], l[V];                           // heads 8 (v / 2) + 2 (lane % 4) + v % 2
+                // lane: what nodes lane and lane + 32 see; which of the warpgroup's rows are padding's
+                uint64_t sees = 0, sees32 = 0;
+                uint32_t pad = 0;
+                int64_t front = 0;
+                if constexpr (TREE) {
+                    const int32_t *par = p.parents + (int64_t)w.b * p.T;
+                    front = seq_front(p, w.b);
+                    if (lane < p.T) sees = tree::ancestors(par, lane);
+                    if (lane + 32 < p.T) sees32 = tree::ancestors(par, lane + 32);
+                    const uint32_t lo = __ballot_sync(0xffffffffu, sees != 0), hi = __ballot_sync(0xffffffffu, sees32 != 0);
+                    const int t = min((h0 + n0 + lane) / p.heads, p.T - 1);
+                    pad = __ballot_sync(0xffffffffu, !((t < 32 ? lo : hi) >> (t & 31) & 1));
+                }
 #pragma unroll
                 for (int v = 0; v < V; ++v) { m[v] = -CUDART_INF_F; l[v] = 0.f; }
                 for (int64_t i = w.lo; i < w.hi; ++i, ++k) {
@@ -305,6 +335,21 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
 #pragma unroll
                     for (int e = 0; e < NW / 2; ++e)
                         x[e] = (e & 2 ? see1 : see0) ? x[e] * p.scale_log2 : -CUDART_INF_F;
+                    if constexpr (TREE) {
+                        const int64_t d = i * TOK - front;
+                        if (d > -TOK) {                     // the tile has nodes
+                            const int d0 = (int)d + row, d1 = d0 + 8;
+#pragma unroll
+                            for (int v = 0; v < V; ++v) {
+                                const int col = n0 + 8 * (v >> 1) + 2 * (lane & 3) + (v & 1);
+                                const int t = min((h0 + col) / p.heads, p.T - 1);
+                                const uint64_t a = __shfl_sync(0xffffffffu, sees, t & 31), c = __shfl_sync(0xffffffffu, sees32, t & 31);
+                                const uint64_t mine = t < 32 ? a : c;
+                                if (d0 >= 0 && !(d0 < 64 && (mine >> d0 & 1))) x[(v >> 1) * 4 + (v & 1)] = -CUDART_INF_F;
+                                if (d1 >= 0 && !(d1 < 64 && (mine >> d1 & 1))) x[(v >> 1) * 4 + 2 + (v & 1)] = -CUDART_INF_F;
+                            }
+                        }
+                    }
                     if (vm != ~0ull) {
                         // rows that are not seen hold anything: zero them as values
                         const int t = tid >> 2;
@@ -444,8 +489,9 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                 const int64_t slot = w.slot();
                 bar_sync(bar, 128);
                 if (wt < NW) {
-                    const float sum = rd[wt] + rd[NW + wt] + rd[2 * NW + wt] + rd[3 * NW + wt];
-                    const float top = cb[wt];
+                    float sum = rd[wt] + rd[NW + wt] + rd[2 * NW + wt] + rd[3 * NW + wt];
+                    float top = cb[wt];
+                    if (TREE && (pad >> wt & 1)) { sum = 0.f; top = -CUDART_INF_F; }
                     ca[wt] = whole ? inverse_of(sum) : 1.f;
                     if (whole) {
                         if (p.lse && n0 + wt < nh)
@@ -468,6 +514,11 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                         ld_cols(tmem_at(tmem, warp, O_COL + mb * N + n), y);
                         tmem_wait_ld();
                         reg_fence(y);
+                        if constexpr (TREE) {               // a padding node's queries hold anything
+#pragma unroll
+                            for (int e = 0; e < EC; ++e)
+                                if (pad >> (c + e) & 1) y[e] = 0.f;
+                        }
                         if (whole) {
                             __nv_bfloat16 *to = (__nv_bfloat16 *)p.o + ((int64_t)w.b * p.H + h0 + n) * LATENT + ch;
 #pragma unroll
@@ -496,7 +547,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
 // Heads a CTA: the fewest that hold all H, else 64 a group.
 SplitPlan plan_of(int32_t H, int nsm) { return split_plan(H, H <= 16 ? 16 : (H <= 32 ? 32 : 64), nsm); }
 
-template <int N>
+template <int N, bool TREE>
 cudaError_t run(const DecodeArgs &a, const SplitPlan &pl, cudaStream_t st) {
     static std::mutex mu;
     static bool ready[64] = {false};
@@ -507,7 +558,7 @@ cudaError_t run(const DecodeArgs &a, const SplitPlan &pl, cudaStream_t st) {
     {
         std::lock_guard<std::mutex> lock(mu);
         if (!ready[dev]) {
-            e = cudaFuncSetAttribute(decode_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            e = cudaFuncSetAttribute(decode_kernel<N, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      (int)Smem<N>::BYTES);
             if (e != cudaSuccess) return e;
             ready[dev] = true;
@@ -524,7 +575,7 @@ cudaError_t run(const DecodeArgs &a, const SplitPlan &pl, cudaStream_t st) {
     if (!map4(&p.tm_c, a.cache, cd, cs, cb) || !map4(&p.tm_q, a.q, qd, qs, qb))
         return cudaErrorInvalidValue;
     p.force_timeout = fault_force_timeout();
-    return launch_split<N, __nv_bfloat16>(decode_kernel<N>, p, pl, THREADS, Smem<N>::BYTES, a.ws, st);
+    return launch_split<N, __nv_bfloat16>(decode_kernel<N, TREE>, p, pl, THREADS, Smem<N>::BYTES, a.ws, st);
 }
 
 }  // namespace
@@ -539,10 +590,15 @@ cudaError_t launch_decode_tc(const DecodeArgs &a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (nsm > MAX_CTAS) nsm = MAX_CTAS;
     const SplitPlan pl = plan_of(a.H, nsm);
+    if (a.parents) switch (pl.N) {
+    case 16: return run<16, true>(a, pl, st);
+    case 32: return run<32, true>(a, pl, st);
+    default: return run<64, true>(a, pl, st);
+    }
     switch (pl.N) {
-    case 16: return run<16>(a, pl, st);
-    case 32: return run<32>(a, pl, st);
-    default: return run<64>(a, pl, st);
+    case 16: return run<16, false>(a, pl, st);
+    case 32: return run<32, false>(a, pl, st);
+    default: return run<64, false>(a, pl, st);
     }
 }
 

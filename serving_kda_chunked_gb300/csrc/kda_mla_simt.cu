@@ -3,6 +3,7 @@
 // (A tf32 tensor-core product keeps 11 of the 24 bits.  Three products of operands
 // split in two would keep nearly all; that has not been built.)
 #include "kda_mla_split.cuh"
+#include "kda_tree.cuh"
 
 namespace kda {
 namespace mla {
@@ -333,6 +334,8 @@ constexpr int DEC_FLOATS = HG * LDR + TT * LDR + 8 * HG * LDS + TT * HG + HG;
 constexpr int OVER = 1;                         // tiles' time to begin and end a sequence
 constexpr int DEC_CTAS = 320;                   // per launch, up to two per SM
 
+// TREE: see kda_mla_decode.cu.
+template <bool TREE>
 __global__ void __launch_bounds__(DTHREADS, 2) decode_simt_kernel(const SplitParams p, const float *q,
                                                                   const float *cache) {
     extern __shared__ __align__(16) float smf[];
@@ -361,6 +364,10 @@ __global__ void __launch_bounds__(DTHREADS, 2) decode_simt_kernel(const SplitPar
                                             : make_float4(0.f, 0.f, 0.f, 0.f));
         }
         float m = -CUDART_INF_F, l = 0.f;   // of head `warp`, this lane's tokens
+        const int32_t *par = TREE ? p.parents + (int64_t)w.b * p.T : nullptr;
+        const int64_t front = TREE ? seq_front(p, w.b) : 0;
+        const int node = TREE ? (h0 + warp) / p.heads : 0;
+        const uint64_t sees = TREE && node < p.T ? tree::ancestors(par, node) : 0;
         float2 acc[HG][2] = {};             // channels 4 (tid % 128) .., tokens of half tid / 128
         const int ch = 4 * (tid & 127), half = tid >> 7;
         for (int64_t i = w.lo; i < w.hi; ++i) {
@@ -371,6 +378,15 @@ __global__ void __launch_bounds__(DTHREADS, 2) decode_simt_kernel(const SplitPar
                 const int pg = tab[(t + lane) >> shift];
                 if (pg >= 0 && pg < p.n_pages) at = (pg << shift) + ((int)(t + lane) & (p.page - 1));
             }
+            bool see = !TREE || sees;
+            if constexpr (TREE) {
+                const int64_t d = t + lane - front;
+                if (d >= 0) {               // a row that no node has is left out, and zero
+                    if (d >= p.T || !tree::ancestors(par, (int)d)) at = -1;
+                    see = d < p.T && (sees >> d & 1);
+                }
+            }
+            see = see && at >= 0;
             __syncthreads();                // the previous tile has been read
 #pragma unroll
             for (int r = 0; r < TT / 8; ++r) {              // a warp copies rows warp, warp + 8, ...
@@ -417,7 +433,7 @@ __global__ void __launch_bounds__(DTHREADS, 2) decode_simt_kernel(const SplitPar
                 float x = 0.f;
 #pragma unroll
                 for (int v = 0; v < 8; ++v) x += red[(v * HG + warp) * LDS + lane];
-                x = at >= 0 ? x * p.scale_log2 : -CUDART_INF_F;
+                x = see ? x * p.scale_log2 : -CUDART_INF_F;
                 const float top = fmaxf(m, warp_max(x));
                 const float ref = top == -CUDART_INF_F ? 0.f : top;
                 const float f = exp2f(m - ref), e = exp2f(x - ref);
@@ -516,13 +532,13 @@ cudaError_t launch_decode_simt(const DecodeArgs &a, cudaStream_t st) {
     int nsm = 1;
     cudaError_t e = sm_count(&nsm);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(decode_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 DEC_FLOATS * (int)sizeof(float));
+        e = cudaFuncSetAttribute(a.parents ? decode_simt_kernel<true> : decode_simt_kernel<false>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, DEC_FLOATS * (int)sizeof(float));
     if (e != cudaSuccess) return e;
     const SplitPlan pl = split_plan(a.H, HG, 2 * nsm < DEC_CTAS ? 2 * nsm : DEC_CTAS);
     SplitParams p;
     split_params(p, a, pl);
-    return launch_split<HG, float>(decode_simt_kernel, p, pl, DTHREADS, DEC_FLOATS * sizeof(float), a.ws, st,
+    return launch_split<HG, float>(a.parents ? decode_simt_kernel<true> : decode_simt_kernel<false>, p, pl, DTHREADS, DEC_FLOATS * sizeof(float), a.ws, st,
                                    (const float *)a.q, (const float *)a.cache);
 }
 

@@ -46,11 +46,18 @@ struct SplitParams {
     float *part, *stat;        // two slots per CTA: [N][512], and [N][2] (maximum in log2 units, sum)
     int32_t B, H, n_pages, page, max_pages, groups;
     float scale_log2;
+    const int32_t *parents;    // drafted trees: [B, T], and the heads of a node (else NULL, 0, 0)
+    int32_t T, heads;
 };
 
-__device__ __forceinline__ int64_t seq_len(const SplitParams &p, int b) {
+// Tokens in front of a sequence's tree, and all of its tokens (without trees the same).
+__device__ __forceinline__ int64_t seq_front(const SplitParams &p, int b) {
     const int64_t cap = (int64_t)p.max_pages * p.page, n = p.seq_lens[b];
     return n < 0 ? 0 : (n > cap ? cap : n);
+}
+__device__ __forceinline__ int64_t seq_len(const SplitParams &p, int b) {
+    const int64_t cap = (int64_t)p.max_pages * p.page, n = seq_front(p, b) + p.T;
+    return n > cap ? cap : n;
 }
 template <int TOK> __device__ __forceinline__ int64_t tiles_of(int64_t len) { return (len + TOK - 1) / TOK; }
 template <int TOK, int OVER> __device__ __forceinline__ int64_t units_of(int64_t len) {
@@ -326,6 +333,7 @@ inline void split_params(SplitParams &p, const DecodeArgs &a, const SplitPlan &s
     p.part = reinterpret_cast<float *>(ws + ws_part(s));
     p.B = a.B; p.H = a.H; p.n_pages = a.n_pages; p.page = a.page; p.max_pages = a.max_pages;
     p.groups = s.groups;
+    p.parents = a.parents; p.T = a.T; p.heads = a.heads;
     p.scale_log2 = a.scale * 1.4426950408889634f;
 }
 
