@@ -521,7 +521,7 @@ def _mla_lib():
 
 
 def _mla_calls():
-    """The latent-attention calls in their common form, compiled
+    """The latent-attention calls and those for drafted tokens in their common form, compiled
     (``csrc/py_mla.cpp``): a decode step launches them every few tens of
     microseconds.  They give NotImplemented for what is not of that form; the
     functions below then check and marshal it themselves."""
@@ -537,9 +537,11 @@ def _mla_calls():
             "_kda_torch", importlib.machinery.ExtensionFileLoader("_kda_torch", CALLS_LIB))
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
-        module.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
+        module.bind(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
             "kda_mla_append", "kda_mla_prefill", "kda_mla_prefill_workspace_size", "kda_mla_decode",
-            "kda_mla_decode_workspace_size")), KdaError)
+            "kda_mla_decode_workspace_size", "kda_mla_tree_decode", "kda_mla_tree_decode_workspace_size",
+            "kda_tree_step", "kda_gdn_tree_step", "kda_tree_commit", "kda_gdn_tree_commit",
+            "kda_tree_verify")), KdaError)
         _calls = module
     return _calls
 
@@ -783,6 +785,10 @@ def kda_mla_tree_decode(q, cache, table, ctx_lens, parents, *, scale=None, o=Non
     those of tokens ctx_lens .. ctx_lens + T - 1) and parents [B, T] int32 on
     the device.  Returns (o [B, T, H, 512], lse [B, T, H] fp32).
     """
+    if stream is None:
+        done = (_calls or _mla_calls()).tree_decode(q, cache, table, ctx_lens, parents, scale, o, lse, workspace)
+        if done is not NotImplemented:
+            return done
     dt, dev = _first("q", q, 4)
     B, T, H, _ = q.shape
     pq = _need("q", q, dt, (B, T, H, _MLA_ROW), dev)
@@ -824,6 +830,10 @@ def _tree_inputs(k, v, g, beta, S, slots, scalar_gate):
 
 
 def _tree_step(fn, scalar_gate, q, k, v, g, beta, S, parents, slots, o, stream):
+    if stream is None:
+        done = (_calls or _mla_calls()).tree_step(scalar_gate, q, k, v, g, beta, S, parents, slots, o)
+        if done is not NotImplemented:
+            return done
     dt, dev, sizes, P, (pk, pv, pg, pb, pS, ps) = _tree_inputs(k, v, g, beta, S, slots, scalar_gate)
     B, T, H, dk, dv = sizes
     pq = _need("q", q, dt, (B, T, H, dk), dev)
@@ -854,6 +864,9 @@ def kda_gdn_tree_step(q, k, v, g, beta, S, parents, *, slots=None, o=None, strea
 
 
 def _tree_commit(fn, scalar_gate, k, v, g, beta, S, path, slots, stream):
+    if stream is None:
+        if (_calls or _mla_calls()).tree_commit(scalar_gate, k, v, g, beta, S, path, slots) is not NotImplemented:
+            return
     dt, dev, sizes, P, (pk, pv, pg, pb, pS, ps) = _tree_inputs(k, v, g, beta, S, slots, scalar_gate)
     B, T, H, dk, dv = sizes
     pp = _need("path", path, torch.int32, (B, T), dev)
@@ -898,6 +911,10 @@ def kda_tree_verify(target, tokens, parents, uniform, *, draft=None, path=None, 
     tokens, parents [B, T] int32; uniform [B, T] fp32 random numbers.  Returns
     (path [B, T], count [B], next_token [B]), all int32.
     """
+    if stream is None:
+        done = (_calls or _mla_calls()).tree_verify(target, tokens, parents, uniform, draft, path, count, next_token)
+        if done is not NotImplemented:
+            return done
     dt, dev = _first("target", target, 3)
     B, T, V = target.shape
     pt, ts = _vocabulary("target", target, dt, B, T, V, dev)

@@ -1,5 +1,6 @@
-// py_mla.cpp -- the Python calls of the latent-attention operators in their
-// common form: exact torch tensors on the current device, on its current stream.
+// py_mla.cpp -- the Python calls of the latent-attention operators and of those for
+// drafted tokens in their common form: exact torch tensors on the current device, on
+// its current stream.
 //
 // A decode step's kernels take about 10 us.  Interpreted checks, three
 // allocations through Python's argument parser and a call with 18 converted
@@ -35,6 +36,11 @@ decltype(&kda_mla_prefill) prefill_fn;
 decltype(&kda_mla_prefill_workspace_size) prefill_ws_fn;
 decltype(&kda_mla_decode) decode_fn;
 decltype(&kda_mla_decode_workspace_size) decode_ws_fn;
+decltype(&kda_mla_tree_decode) tree_decode_fn;
+decltype(&kda_mla_tree_decode_workspace_size) tree_decode_ws_fn;
+decltype(&kda_tree_step) step_fn[2];                // KDA, Gated DeltaNet
+decltype(&kda_tree_commit) commit_fn[2];
+decltype(&kda_tree_verify) verify_fn;
 PyObject *error_class;                              // KdaError(function, status)
 
 // The arguments of one call; `ok` turns false at the first that does not fit.
@@ -236,27 +242,187 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// bind(addresses of the five C entry points, KdaError)
+// tree_decode(q, cache, table, ctx_lens, parents, scale, o, lse, workspace)
+PyObject *tree_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 9) return not_handled();
+    Call c;
+    const at::Tensor *q = c.first(a[0], 4);
+    if (!q) return not_handled();
+    const int64_t B = q->size(0), T = q->size(1), H = q->size(2);
+    c.need(a[0], c.type, {B, T, H, ROW});
+    const at::Tensor *cache = c.need(a[1], c.type, {-1, -1, ROW});
+    const at::Tensor *table = c.need(a[2], at::kInt, {B, -1});
+    const at::Tensor *lens = c.need(a[3], at::kInt, {B});
+    const at::Tensor *parents = c.need(a[4], at::kInt, {B, T});
+    const float scale = c.scale(a[5]);
+    const at::Tensor o = c.out(a[6], c.type, {B, T, H, LATENT});
+    const at::Tensor lse = c.out(a[7], at::kFloat, {B, T, H});
+    Scratch w;
+    w.get(c, a[8], c.ok ? tree_decode_ws_fn((int32_t)B, (int32_t)T, (int32_t)H, c.code()) : 0);
+    if (!c.ok) return not_handled();
+    kda_status st;
+    void *stream = c.stream();
+    Py_BEGIN_ALLOW_THREADS
+    st = tree_decode_fn(q->data_ptr(), cache->data_ptr(), table->data_ptr<int32_t>(), lens->data_ptr<int32_t>(),
+                        parents->data_ptr<int32_t>(), (int32_t)B, (int32_t)T, (int32_t)H, (int32_t)cache->size(0),
+                        (int32_t)cache->size(1), (int32_t)table->size(1), LATENT, ROPE, c.code(), scale,
+                        o.data_ptr(), lse.data_ptr<float>(), w.data, w.bytes, stream);
+    Py_END_ALLOW_THREADS
+    return st == KDA_OK ? pair(o, lse) : failed("kda_mla_tree_decode", st);
+    END_HANDLE_TH_ERRORS
+}
+
+// What a step and a commit over a tree share.
+struct Tree {
+    const at::Tensor *k = nullptr, *v = nullptr, *g = nullptr, *beta = nullptr, *S = nullptr, *slots = nullptr;
+    int64_t B = 0, T = 0, H = 0, dk = 0, dv = 0, P = 0;
+    bool get(Call &c, bool scalar, PyObject *k_, PyObject *v_, PyObject *g_, PyObject *beta_, PyObject *S_, PyObject *slots_) {
+        k = c.first(k_, 4);
+        if (!k) return false;
+        B = k->size(0); T = k->size(1); H = k->size(2); dk = k->size(3);
+        c.need(k_, c.type, {B, T, H, dk});
+        v = c.need(v_, c.type, {B, T, H, -1});
+        if (!c.ok) return false;
+        dv = v->size(3);
+        g = scalar ? c.need(g_, at::kFloat, {B, T, H}) : c.need(g_, at::kFloat, {B, T, H, dk});
+        beta = c.need(beta_, at::kFloat, {B, T, H});
+        P = B;
+        if (slots_ != Py_None) {
+            slots = c.need(slots_, at::kInt, {B});
+            P = -1;
+        }
+        S = c.need(S_, at::kFloat, {P, H, dk, dv});
+        if (c.ok) P = S->size(0);
+        return c.ok;
+    }
+    const int32_t *slot_ptr() const { return slots ? slots->data_ptr<int32_t>() : nullptr; }
+};
+
+// tree_step(scalar gate, q, k, v, g, beta, S, parents, slots, o)
+PyObject *tree_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 10) return not_handled();
+    const bool scalar = a[0] == Py_True;
+    Call c;
+    Tree t;
+    if (!t.get(c, scalar, a[2], a[3], a[4], a[5], a[6], a[8])) return not_handled();
+    const at::Tensor *q = c.need(a[1], c.type, {t.B, t.T, t.H, t.dk});
+    const at::Tensor *parents = c.need(a[7], at::kInt, {t.B, t.T});
+    const at::Tensor o = c.out(a[9], c.type, {t.B, t.T, t.H, t.dv});
+    if (!c.ok) return not_handled();
+    kda_status st;
+    void *stream = c.stream();
+    Py_BEGIN_ALLOW_THREADS
+    st = step_fn[scalar](q->data_ptr(), t.k->data_ptr(), t.v->data_ptr(), t.g->data_ptr<float>(),
+                         t.beta->data_ptr<float>(), t.S->data_ptr<float>(), t.slot_ptr(), (int32_t)t.P,
+                         parents->data_ptr<int32_t>(), (int32_t)t.B, (int32_t)t.T, (int32_t)t.H, (int32_t)t.dk,
+                         (int32_t)t.dv, c.code(), o.data_ptr(), stream);
+    Py_END_ALLOW_THREADS
+    if (st != KDA_OK) return failed(scalar ? "kda_gdn_tree_step" : "kda_tree_step", st);
+    if (a[9] != Py_None) { Py_INCREF(a[9]); return a[9]; }
+    return THPVariable_Wrap(o);
+    END_HANDLE_TH_ERRORS
+}
+
+// tree_commit(scalar gate, k, v, g, beta, S, path, slots)
+PyObject *tree_commit(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 8) return not_handled();
+    const bool scalar = a[0] == Py_True;
+    Call c;
+    Tree t;
+    if (!t.get(c, scalar, a[1], a[2], a[3], a[4], a[5], a[7])) return not_handled();
+    const at::Tensor *path = c.need(a[6], at::kInt, {t.B, t.T});
+    if (!c.ok) return not_handled();
+    kda_status st;
+    void *stream = c.stream();
+    Py_BEGIN_ALLOW_THREADS
+    st = commit_fn[scalar](t.k->data_ptr(), t.v->data_ptr(), t.g->data_ptr<float>(), t.beta->data_ptr<float>(),
+                           t.S->data_ptr<float>(), t.slot_ptr(), (int32_t)t.P, path->data_ptr<int32_t>(),
+                           (int32_t)t.B, (int32_t)t.T, (int32_t)t.H, (int32_t)t.dk, (int32_t)t.dv, c.code(), stream);
+    Py_END_ALLOW_THREADS
+    if (st != KDA_OK) return failed(scalar ? "kda_gdn_tree_commit" : "kda_tree_commit", st);
+    Py_RETURN_NONE;
+    END_HANDLE_TH_ERRORS
+}
+
+// tree_verify(target, tokens, parents, uniform, draft, path, count, next_token)
+PyObject *tree_verify(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 8) return not_handled();
+    Call c;
+    const at::Tensor *target = c.first(a[0], 3);
+    if (!target) return not_handled();
+    const int64_t B = target->size(0), T = target->size(1), V = target->size(2);
+    c.need(a[0], c.type, {B, T, V});                // rows of another stride go the other way
+    const at::Tensor *draft = a[4] == Py_None ? nullptr : c.need(a[4], c.type, {B, T, V});
+    const at::Tensor *tokens = c.need(a[1], at::kInt, {B, T});
+    const at::Tensor *parents = c.need(a[2], at::kInt, {B, T});
+    const at::Tensor *uniform = c.need(a[3], at::kFloat, {B, T});
+    const at::Tensor out[3] = {c.out(a[5], at::kInt, {B, T}), c.out(a[6], at::kInt, {B}), c.out(a[7], at::kInt, {B})};
+    if (!c.ok) return not_handled();
+    kda_status st;
+    void *stream = c.stream();
+    Py_BEGIN_ALLOW_THREADS
+    st = verify_fn(target->data_ptr(), V, draft ? draft->data_ptr() : nullptr, V, tokens->data_ptr<int32_t>(),
+                   parents->data_ptr<int32_t>(), uniform->data_ptr<float>(), (int32_t)B, (int32_t)T, (int32_t)V,
+                   c.code(), out[0].data_ptr<int32_t>(), out[1].data_ptr<int32_t>(), out[2].data_ptr<int32_t>(), stream);
+    Py_END_ALLOW_THREADS
+    if (st != KDA_OK) return failed("kda_tree_verify", st);
+    PyObject *t = PyTuple_New(3);
+    for (int i = 0; t && i < 3; ++i) {
+        PyObject *x = THPVariable_Wrap(out[i]);
+        if (!x) { Py_DECREF(t); return nullptr; }
+        PyTuple_SET_ITEM(t, i, x);
+    }
+    return t;
+    END_HANDLE_TH_ERRORS
+}
+
+// bind((addresses of the C entry points, in the order below), KdaError)
 PyObject *bind(PyObject *, PyObject *args) {
-    unsigned long long f[5];
-    PyObject *e;
-    if (!PyArg_ParseTuple(args, "KKKKKO", &f[0], &f[1], &f[2], &f[3], &f[4], &e)) return nullptr;
-    append_fn = reinterpret_cast<decltype(append_fn)>(f[0]);
-    prefill_fn = reinterpret_cast<decltype(prefill_fn)>(f[1]);
-    prefill_ws_fn = reinterpret_cast<decltype(prefill_ws_fn)>(f[2]);
-    decode_fn = reinterpret_cast<decltype(decode_fn)>(f[3]);
-    decode_ws_fn = reinterpret_cast<decltype(decode_ws_fn)>(f[4]);
+    PyObject *f, *e;
+    if (!PyArg_ParseTuple(args, "O!O", &PyTuple_Type, &f, &e)) return nullptr;
+    void *at[12];
+    if (PyTuple_GET_SIZE(f) != 12) {
+        PyErr_SetString(PyExc_ValueError, "bind takes 12 addresses");
+        return nullptr;
+    }
+    for (int i = 0; i < 12; ++i) {
+        at[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(f, i));
+        if (!at[i]) return nullptr;
+    }
+    append_fn = reinterpret_cast<decltype(append_fn)>(at[0]);
+    prefill_fn = reinterpret_cast<decltype(prefill_fn)>(at[1]);
+    prefill_ws_fn = reinterpret_cast<decltype(prefill_ws_fn)>(at[2]);
+    decode_fn = reinterpret_cast<decltype(decode_fn)>(at[3]);
+    decode_ws_fn = reinterpret_cast<decltype(decode_ws_fn)>(at[4]);
+    tree_decode_fn = reinterpret_cast<decltype(tree_decode_fn)>(at[5]);
+    tree_decode_ws_fn = reinterpret_cast<decltype(tree_decode_ws_fn)>(at[6]);
+    for (int i = 0; i < 2; ++i) {
+        step_fn[i] = reinterpret_cast<decltype(&kda_tree_step)>(at[7 + i]);
+        commit_fn[i] = reinterpret_cast<decltype(&kda_tree_commit)>(at[9 + i]);
+    }
+    verify_fn = reinterpret_cast<decltype(verify_fn)>(at[11]);
     Py_INCREF(e);
     Py_XDECREF(error_class);
     error_class = e;
     Py_RETURN_NONE;
 }
 
+template <PyObject *(*F)(PyObject *, PyObject *const *, Py_ssize_t)> PyCFunction fast() {
+    return reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(F));
+}
 PyMethodDef methods[] = {
     {"bind", bind, METH_VARARGS, nullptr},
-    {"append", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(append)), METH_FASTCALL, nullptr},
-    {"prefill", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(prefill)), METH_FASTCALL, nullptr},
-    {"decode", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(decode)), METH_FASTCALL, nullptr},
+    {"append", fast<append>(), METH_FASTCALL, nullptr},
+    {"prefill", fast<prefill>(), METH_FASTCALL, nullptr},
+    {"decode", fast<decode>(), METH_FASTCALL, nullptr},
+    {"tree_decode", fast<tree_decode>(), METH_FASTCALL, nullptr},
+    {"tree_step", fast<tree_step>(), METH_FASTCALL, nullptr},
+    {"tree_commit", fast<tree_commit>(), METH_FASTCALL, nullptr},
+    {"tree_verify", fast<tree_verify>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kda_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
