@@ -137,7 +137,7 @@ kda_status tree_sizes(int32_t P, int32_t B, int32_t T, int32_t H, int32_t dk, in
     if (dtype != KDA_BF16 && dtype != KDA_FP32) return KDA_ERR_INVALID_ARG;
     if (!pooled && P != B) return KDA_ERR_INVALID_ARG;
     if (!head_ok(dk, dv) || T > kda::tree::MAX_NODES) return KDA_ERR_UNSUPPORTED;
-    if ((int64_t)B * H > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
+    if ((int64_t)B * H * (dv / 64) > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 

@@ -9,40 +9,85 @@
 // Without draft probabilities q is a point mass at each child's token: R_j is p without
 // the rejected tokens and S_j = 1 - the sum of their p, no pass over V needed.
 //
-// A pass over V gives S_j: sum over p > c q of p, less c times that of q, both as
-// exact sums of pairs of floats, joined in float64 (in float32 a sum of 131,072 values
-// is off by more than the smallest tokens' probabilities, and the token that a random
-// number falls on would depend on the order of the sum; float64 throughout would take
-// four times HBM's time at this GPU's rate).  The last pass's sums over pieces of the
-// row say in which piece the random number falls, and only that piece is read again.
+// A pass over V gives S_j: sum over p > c q of p, less c times that of q, every sum a pair of
+// floats that keeps what its additions round off.  In float32 a sum of 131,072 values is
+// off by more than the smallest tokens' probabilities, and the token that a random number
+// falls on would depend on the order of the sum; a float64 operation of a warp takes 60
+// cycles of an SM here (a walk, three scans and the last piece's sums in float64 took 20,000
+// cycles beside a pass of 8,000).  Pairs hold 48 bits, for about ten float32 operations an
+// addition.  The last pass's sums over the warps' pieces of the row say in which piece the
+// random number falls, and only that one is read again.
 //
 // What bounds it: HBM, a row of p and one of q a sequence.  A cluster of CTAs takes a
 // sequence; all of its CTAs walk the tree alike and share each pass.
 #include "kda_tree.cuh"
 
-#include <math_constants.h>
 
 namespace kda {
 namespace tree {
 namespace {
 
-constexpr int THREADS = 512, WARPS = THREADS / 32, PIECES = 512, MAX_CLUSTER = 8;
+// With 512 threads and two CTAs an SM a batch of 256 trees over 131,072 tokens takes 100 us
+// (here 94), with 128 and eight 92, but single sequences 11 (here 8).
+constexpr int THREADS = 256, MIN_CTAS = 4, WARPS = THREADS / 32, MAX_CLUSTER = 8;
+constexpr int PER_LANE = MAX_CLUSTER * WARPS / 32;          // pieces a lane adds up
 
-// A sum of float32 values kept exact: hi + lo, the rounding of every addition to hi
-// goes to lo.
-struct Exact {
-    float hi = 0.f, lo = 0.f;
-    __device__ __forceinline__ void add(float x) {
-        const float s = __fadd_rn(hi, x), z = __fsub_rn(s, hi);
-        lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, z)), __fsub_rn(x, z)));
+// A number as the sum of two floats, lo below half a unit of hi's last place.
+struct Pair { float hi, lo; };
+
+__device__ __forceinline__ Pair two_sum(float a, float b) {                  // a + b, exact
+    const float s = __fadd_rn(a, b), z = __fsub_rn(s, a);
+    return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, z)), __fsub_rn(b, z))};
+}
+__device__ __forceinline__ Pair normal(float hi, float lo) {                 // |hi| >= |lo|
+    const float s = __fadd_rn(hi, lo);
+    return {s, __fsub_rn(lo, __fsub_rn(s, hi))};
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+    const Pair s = two_sum(a.hi, b.hi);
+    return normal(s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)));
+}
+__device__ __forceinline__ Pair operator-(Pair a, Pair b) { return a + Pair{-b.hi, -b.lo}; }
+__device__ __forceinline__ Pair operator*(Pair a, float b) {
+    const float p = __fmul_rn(a.hi, b);
+    return normal(p, __fmaf_rn(a.lo, b, __fmaf_rn(a.hi, b, -p)));
+}
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+    const float p = __fmul_rn(a.hi, b.hi);
+    return normal(p, __fmaf_rn(a.hi, b.lo, __fmaf_rn(a.lo, b.hi, __fmaf_rn(a.hi, b.hi, -p))));
+}
+__device__ __forceinline__ bool operator>(Pair a, Pair b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); }
+__device__ __forceinline__ Pair not_below_0(Pair a) { return a.hi > 0.f ? a : Pair{0.f, 0.f}; }
+
+// Two such sums of float32 values side by side, lo not yet below hi's last place.
+struct Sums {
+    float2 hi = {0.f, 0.f}, lo = {0.f, 0.f};
+    __device__ __forceinline__ void add(float2 x) {
+        const float2 s = add2(hi, x), z = sub2(s, hi);
+        lo = add2(lo, add2(sub2(hi, sub2(s, z)), sub2(x, z)));
         hi = s;
     }
-    __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
+    __device__ __forceinline__ Pair value() const { return normal(hi.x, lo.x) + normal(hi.y, lo.y); }
+    static __device__ __forceinline__ float2 add2(float2 a, float2 b) {
+        float2 d;
+        asm("add.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<uint64_t &>(d))
+            : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+        return d;
+    }
+    static __device__ __forceinline__ float2 sub2(float2 a, float2 b) {
+        float2 d;
+        asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<uint64_t &>(d))
+            : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+        return d;
+    }
 };
 
-__device__ __forceinline__ double warp_sum(double x) {
+__device__ __forceinline__ Pair shfl(Pair x, int from) {
+    return {__shfl_sync(0xffffffffu, x.hi, from), __shfl_sync(0xffffffffu, x.lo, from)};
+}
+__device__ __forceinline__ Pair warp_sum(Pair x) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    for (int o = 16; o > 0; o >>= 1) x = x + Pair{__shfl_xor_sync(0xffffffffu, x.hi, o), __shfl_xor_sync(0xffffffffu, x.lo, o)};
     return x;
 }
 
@@ -55,10 +100,10 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // x to the same variable of another CTA of the cluster
-__device__ __forceinline__ void store_to(double *p, uint32_t rank, double x) {
+__device__ __forceinline__ void store_to(Pair *p, uint32_t rank, Pair x) {
     uint32_t to;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
-    asm volatile("st.shared::cluster.f64 [%0], %1;" :: "r"(to), "d"(x) : "memory");
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" :: "r"(to), "f"(x.hi), "f"(x.lo) : "memory");
 }
 
 // Values e .. e + 3 of a row; those outside [0, V) are 0.  `wide`: in one load (the
@@ -75,20 +120,78 @@ template <typename Tp> __device__ __forceinline__ float4 values(const Tp *row, i
 
 struct State {                               // of the walk, alike in all CTAs of a cluster
     int cur, at, count, gone;                // node, next node to look at, path's length, tokens in `dead`
-    double c, left, total;                   // c_j, S_j, the last pass's sum
-    int last;                                // which of `totals` the last pass used
+    Pair c, left, total;                     // c_j, S_j, the last pass's sum
     bool summed;                             // the last pass was over this node's rows at c
     bool bare;                               // the residual was empty: the last token is drawn from p
     bool pass;                               // a pass is wanted now
 };
 
+// The rows of a pass.
+template <typename Tp> struct Rows {
+    const Tp *p, *q;                         // q NULL: R is p (without rejected tokens)
+    int lead;                                // values between the alignment boundary before the row and the row
+    bool wide;
+    Pair c;
+    int gone;
+    __device__ __forceinline__ Rows(const VerifyArgs &a, const State &st, int64_t b) {
+        const int64_t row = b * a.T + st.cur;
+        c = st.bare ? Pair{0.f, 0.f} : st.c;
+        gone = st.bare ? 0 : st.gone;
+        p = (const Tp *)a.target + row * a.target_stride;
+        q = a.draft && c.hi > 0.f ? (const Tp *)a.draft + row * a.draft_stride : nullptr;
+        lead = (int)((uintptr_t)p / sizeof(Tp) & 3);
+        wide = !q || (int)((uintptr_t)q / sizeof(Tp) & 3) == lead;
+    }
+};
+
+// R of the four values from e on, from their p and q.
+__device__ __forceinline__ Pair residual(float p, float q, Pair c) {
+    const Pair t = c * q, d = two_sum(p, -t.hi);
+    return not_below_0(normal(d.hi, __fsub_rn(d.lo, t.lo)));
+}
 template <typename Tp>
-__global__ void __launch_bounds__(THREADS, 2) verify_kernel(const VerifyArgs p, int cluster, int piece) {
+__device__ __forceinline__ void residual(const Rows<Tp> &w, int64_t e, int V, const int32_t *dead, Pair (&r)[4]) {
+    const float4 y = values(w.p, e, V, w.wide), z = w.q ? values(w.q, e, V, w.wide) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float yv[4] = {y.x, y.y, y.z, y.w}, zv[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        r[j] = w.q ? residual(yv[j], zv[j], w.c) : Pair{fmaxf(yv[j], 0.f), 0.f};
+        for (int d = 0; d < w.gone; ++d) if (dead[d] == e + j) r[j] = {0.f, 0.f};
+    }
+}
+
+// Inclusive sums over the lanes.
+__device__ __forceinline__ Pair warp_scan(Pair x, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const Pair y = {__shfl_up_sync(0xffffffffu, x.hi, o), __shfl_up_sync(0xffffffffu, x.lo, o)};
+        if (lane >= o) x = x + y;
+    }
+    return x;
+}
+
+// Where the running sum of a warp's values x (lane after lane) first exceeds goal - before:
+// the lane, and `before` moved to it.  Where it does not: the last lane whose x is not
+// 0 (-1: none), and `past` is set.
+__device__ __forceinline__ int find_lane(Pair x, Pair goal, Pair &before, bool &past, int lane) {
+    const Pair incl = warp_scan(x, lane);
+    const uint32_t some = __ballot_sync(0xffffffffu, x.hi > 0.f), hit = __ballot_sync(0xffffffffu, x.hi > 0.f && before + incl > goal);
+    past = !hit;
+    const int k = hit ? __ffs((int)hit) - 1 : (some ? 31 - __clz((int)some) : -1);
+    if (k >= 0) before = before + shfl(incl - x, k);
+    return k;
+}
+
+// `piece`: values of the row a warp takes in a pass, a multiple of 128; warp w of CTA r
+// has piece r * WARPS + w.
+template <typename Tp>
+__global__ void __launch_bounds__(THREADS, MIN_CTAS) verify_kernel(const VerifyArgs p, int cluster, int64_t piece) {
     __shared__ int32_t par[MAX_NODES], tok[MAX_NODES], path[MAX_NODES], dead[MAX_NODES];
     __shared__ float uni[MAX_NODES], px[MAX_NODES], qx[MAX_NODES];
-    __shared__ double sums[PIECES];          // R over this CTA's pieces of the row
-    __shared__ double totals[2][MAX_CLUSTER];
-    __shared__ double part[WARPS];
+    __shared__ Pair part[2][MAX_CLUSTER * WARPS];            // R over the pieces, of two passes in turn
+    __shared__ Pair sub[WARPS], sbefore;
+    __shared__ int spiece;
+    __shared__ bool spast;
     __shared__ State st;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster > 1 ? cluster_rank() : 0;
@@ -110,7 +213,8 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(const VerifyArgs p, 
     }
     if (tid == 0) {
         st.cur = 0; st.at = 1; st.count = 1; st.gone = 0;
-        st.c = 0.0; st.left = 1.0; st.total = 0.0;
+        st.c = st.total = {0.f, 0.f};
+        st.left = {1.f, 0.f};
         st.summed = st.bare = false;
         path[0] = 0;
     }
@@ -125,10 +229,11 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(const VerifyArgs p, 
     }
 
     if (cluster > 1) cluster_sync();                         // all CTAs are there to be written to
+    int last = 0;                                            // which of `part` the last pass used
     for (int round = 0;; ++round) {
         if (warp == 0) {                                     // the walk, up to a pass or its end
             int cur = st.cur, at = st.at, count = st.count, gone = st.gone;
-            double c = st.c, left = st.left;
+            Pair c = st.c, left = st.left;
             bool summed = st.summed, bare = st.bare, pass = false;
             while (!bare && !pass) {
                 const uint32_t lo = __ballot_sync(0xffffffffu, lane < T && lane >= at && par[lane] == cur);
@@ -137,28 +242,28 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(const VerifyArgs p, 
                 const int i = lo ? __ffs((int)lo) - 1 : 31 + __ffs((int)hi);
                 at = i + 1;
                 if (tok[i] < 0 || tok[i] >= V) continue;     // no token: as if the node were not there
-                const double P = px[i], q = qx[i];
+                const float P = px[i], q = qx[i];
                 bool was = false;
                 if (!draft) for (int j = 0; j < gone; ++j) was |= dead[j] == tok[i];
-                const double r = draft ? fmax(P - c * q, 0.0) : (was ? 0.0 : P);
-                if ((double)uni[i] * q * left < r) {
+                const Pair r = draft ? residual(P, q, c) : Pair{was ? 0.f : P, 0.f};
+                if (r > Pair{q, 0.f} * uni[i] * left) {
                     if (lane == 0) path[count] = i;
                     ++count;
                     cur = i;
-                    c = 0.0; left = 1.0; gone = 0;
+                    c = {0.f, 0.f}; left = {1.f, 0.f}; gone = 0;
                     summed = false;
                 } else if (draft) {
-                    c += left;
+                    c = c + left;
                     pass = true;
                 } else {
-                    left -= r;
+                    left = left - r;
                     if (lane == 0) dead[gone] = tok[i];
                     ++gone;
                     __syncwarp();
                 }
             }
             if (!pass && !summed) pass = true;               // for the last token
-            if (!pass && !bare && !(st.total > 0.0) && (c > 0.0 || gone)) bare = pass = true;
+            if (!pass && !bare && !(st.total.hi > 0.f) && (c.hi > 0.f || gone)) bare = pass = true;
             __syncwarp();
             if (lane == 0) {
                 st.cur = cur; st.at = at; st.count = count; st.gone = gone;
@@ -168,170 +273,185 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(const VerifyArgs p, 
         }
         __syncthreads();
         if (!st.pass) break;
-        const double c = st.bare ? 0.0 : st.c;
-        const int gone = st.bare ? 0 : st.gone;
-        const Tp *pr = target + (b * T + st.cur) * p.target_stride;
-        const Tp *qr = draft && c > 0.0 ? draft + (b * T + st.cur) * p.draft_stride : nullptr;
-        const int lead = (int)((uintptr_t)pr / sizeof(Tp) & 3);
-        const bool wide = !qr || (int)((uintptr_t)qr / sizeof(Tp) & 3) == lead;
-        const int pieces = (int)(((int64_t)V + lead + piece - 1) / piece), per = (pieces + cluster - 1) / cluster;
-        const int first = min(pieces, (int)rank * per), mine = min(pieces, first + per) - first;
-        const float cf = (float)c;
-        for (int k = warp; k < mine; k += WARPS) {
-            const int64_t e0 = (int64_t)(first + k) * piece - lead;
-            Exact sp, sq;
-            bool odd = false;                                // rejected tokens in this piece
-            for (int j = 0; j < gone; ++j) odd |= dead[j] >= e0 && dead[j] < e0 + piece;
-            for (int i = 0; i < piece; i += 512) {
+        const Rows<Tp> w(p, st, b);
+        const float cf = w.c.hi;
+        const int64_t e0 = ((int64_t)rank * WARPS + warp) * piece - w.lead;
+        const int64_t size = min(piece, (int64_t)V - e0);   // none or less where the row ends before
+        Pair s = {0.f, 0.f};
+        if (w.q) {
+            Sums sp, sq;
+            for (int64_t i = 0; i < size; i += 512) {
                 float4 y[4], z[4];
+                if (w.wide && i + 512 <= size && e0 + i >= 0) {   // all of it in the row: nothing between the loads
 #pragma unroll
-                for (int x = 0; x < 4; ++x) y[x] = values(pr, e0 + i + 128 * x + 4 * lane, V, wide);
-                if (qr) {
+                    for (int x = 0; x < 4; ++x) {
+                        y[x] = load4(w.p + e0 + i + 128 * x + 4 * lane);
+                        z[x] = load4(w.q + e0 + i + 128 * x + 4 * lane);
+                    }
+                } else {
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) z[x] = values(qr, e0 + i + 128 * x + 4 * lane, V, wide);
+                    for (int x = 0; x < 4; ++x) {
+                        const int64_t e = i + 128 * x < size ? e0 + i + 128 * x + 4 * lane : V;
+                        y[x] = values(w.p, e, V, w.wide);
+                        z[x] = values(w.q, e, V, w.wide);
+                    }
                 }
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const float yv[4] = {y[x].x, y[x].y, y[x].z, y[x].w};
-                    if (qr) {
-                        const float zv[4] = {z[x].x, z[x].y, z[x].z, z[x].w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            // a value this rounding puts on the other side counts for nothing
-                            const bool in = yv[j] > cf * zv[j];
-                            sp.add(in ? yv[j] : 0.f);
-                            sq.add(in ? zv[j] : 0.f);
-                        }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            float val = fmaxf(yv[j], 0.f);
-                            if (odd) for (int d = 0; d < gone; ++d) if (dead[d] == e0 + i + 128 * x + 4 * lane + j) val = 0.f;
-                            sp.add(val);
-                        }
-                    }
+                    // a value that this rounding puts on the other side counts for nothing
+                    const bool i0 = y[x].x > cf * z[x].x, i1 = y[x].y > cf * z[x].y, i2 = y[x].z > cf * z[x].z, i3 = y[x].w > cf * z[x].w;
+                    sp.add(make_float2(i0 ? y[x].x : 0.f, i1 ? y[x].y : 0.f));
+                    sq.add(make_float2(i0 ? z[x].x : 0.f, i1 ? z[x].y : 0.f));
+                    sp.add(make_float2(i2 ? y[x].z : 0.f, i3 ? y[x].w : 0.f));
+                    sq.add(make_float2(i2 ? z[x].z : 0.f, i3 ? z[x].w : 0.f));
                 }
             }
-            double s = sp.value();
-            if (qr) s -= c * sq.value();
-            s = warp_sum(s);
-            if (lane == 0) sums[k] = fmax(s, 0.0);
-        }
-        __syncthreads();
-        double s = 0.0;
-        for (int k = tid; k < mine; k += THREADS) s += sums[k];
-        s = warp_sum(s);
-        if (lane == 0) part[warp] = s;
-        __syncthreads();
-        if (tid < cluster) {                                 // this CTA's sum to all
-            double all = 0.0;
+            s = sp.value() - w.c * sq.value();
+        } else {
+            bool odd = false;                                // rejected tokens in this piece
+            for (int j = 0; j < w.gone; ++j) odd |= dead[j] >= e0 && dead[j] < e0 + size;
+            Sums sp;
+            for (int64_t i = 0; i < size; i += 1024) {
+                float4 y[8];
+                if (i + 1024 <= size && e0 + i >= 0) {
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) all += part[w];
-            if (cluster > 1) store_to(&totals[round & 1][rank], tid, all);
-            else totals[round & 1][0] = all;
+                    for (int x = 0; x < 8; ++x) y[x] = load4(w.p + e0 + i + 128 * x + 4 * lane);
+                } else
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) y[x] = values(w.p, i + 128 * x < size ? e0 + i + 128 * x + 4 * lane : V, V, w.wide);
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    if (odd)
+                        for (int d = 0; d < w.gone; ++d) {
+                            const int64_t at = dead[d] - (e0 + i + 128 * x + 4 * lane);
+                            if (at == 0) y[x].x = 0.f;
+                            if (at == 1) y[x].y = 0.f;
+                            if (at == 2) y[x].z = 0.f;
+                            if (at == 3) y[x].w = 0.f;
+                        }
+                    sp.add(make_float2(fmaxf(y[x].x, 0.f), fmaxf(y[x].y, 0.f)));
+                    sp.add(make_float2(fmaxf(y[x].z, 0.f), fmaxf(y[x].w, 0.f)));
+                }
+            }
+            s = sp.value();
         }
-        if (cluster > 1) cluster_sync(); else __syncthreads();
-        double total = 0.0;
-        for (int k = 0; k < cluster; ++k) total += totals[round & 1][k];
-        if (tid == 0) {
-            if (c > 0.0) st.left = total;
-            st.total = total;
-            st.summed = true;
-            st.last = round & 1;
+        s = not_below_0(warp_sum(s));
+        if (cluster > 1) {                                   // this piece's sum to all CTAs
+            if (lane < cluster) store_to(&part[round & 1][rank * WARPS + warp], lane, s);
+            cluster_sync();
+        } else {
+            if (lane == 0) part[round & 1][warp] = s;
+            __syncthreads();
         }
-        __syncthreads();
+        if (warp == 0) {
+            Pair total = {0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < PER_LANE; ++k)
+                if (PER_LANE * lane + k < cluster * WARPS) total = total + part[round & 1][PER_LANE * lane + k];
+            total = warp_sum(total);
+            if (lane == 0) {
+                if (w.q) st.left = total;
+                st.total = total;
+                st.summed = true;
+            }
+            __syncwarp();
+        }
+        last = round & 1;
     }
 
-    // the last token: the first at which the running sum of R exceeds u times all of it
-    const int now = st.last;
-    const double c = st.bare ? 0.0 : st.c;
-    const int gone = st.bare ? 0 : st.gone;
-    double before = 0.0;
-    int owner = -1, some = -1;
-    const double goal = (double)uni[0] * st.total;
-    {
-        double run = 0.0;
-        for (int k = 0; k < cluster; ++k) {
-            const double x = totals[now][k];
-            if (x > 0.0) some = k;
-            if (owner < 0 && x > 0.0 && run + x > goal) { owner = k; before = run; }
-            run += x;
-        }
-    }
-    const bool past = owner < 0;                             // u of 1 or more: the last token there is
-    if (past) owner = some;
+    // the last token: the first at which the running sum of R exceeds u times all of
+    // it, by piece, by a share of that, by value
     if (rank == 0) {
         if (tid < T) p.path[b * T + tid] = path[tid];
-        if (tid == 0) {
-            p.count[b] = st.count;
-            if (owner < 0) p.next[b] = -1;                   // a row of zeros
-        }
+        if (tid == 0) p.count[b] = st.count;
     }
-    if ((int)rank != owner || warp) return;
-    const Tp *pr = target + (b * T + st.cur) * p.target_stride;
-    const Tp *qr = draft && c > 0.0 ? draft + (b * T + st.cur) * p.draft_stride : nullptr;
-    const int lead = (int)((uintptr_t)pr / sizeof(Tp) & 3);
-    const bool wide = !qr || (int)((uintptr_t)qr / sizeof(Tp) & 3) == lead;
-    const int pieces = (int)(((int64_t)V + lead + piece - 1) / piece), per = (pieces + cluster - 1) / cluster;
-    const int first = min(pieces, (int)rank * per), mine = min(pieces, first + per) - first;
-    int k = -1, any = -1;
-    for (int k0 = 0; k0 < mine && k < 0; k0 += 32) {
-        const double x = k0 + lane < mine ? sums[k0 + lane] : 0.0;
-        double incl = x;
+    const Pair goal = st.total * uni[0];
+    if (warp == 0) {
+        Pair x[PER_LANE], sum = {0.f, 0.f}, before = {0.f, 0.f};
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
+        for (int k = 0; k < PER_LANE; ++k) {
+            x[k] = PER_LANE * lane + k < cluster * WARPS ? part[last][PER_LANE * lane + k] : Pair{0.f, 0.f};
+            sum = sum + x[k];
         }
-        const uint32_t there = __ballot_sync(0xffffffffu, x > 0.0);
-        const uint32_t hit = past ? 0u : __ballot_sync(0xffffffffu, x > 0.0 && before + incl > goal);
-        if (there) any = k0 + 31 - __clz((int)there);
-        if (hit) {
-            const int l = __ffs((int)hit) - 1;
-            k = k0 + l;
-            before += __shfl_sync(0xffffffffu, incl - x, l);
-        } else {
-            before += __shfl_sync(0xffffffffu, incl, 31);
+        bool past;
+        const int l = find_lane(sum, goal, before, past, lane);
+        if (lane == l) {
+            int k = 0;
+            Pair run = before;
+            if (past) {                                      // the last one that is not 0
+                for (int j = 0; j < PER_LANE; ++j) if (x[j].hi > 0.f) k = j;
+            } else {
+                bool hit = false;
+#pragma unroll
+                for (int j = 0; j < PER_LANE; ++j)
+                    if (!hit && x[j].hi > 0.f) {
+                        k = j;
+                        before = run;
+                        run = run + x[j];
+                        hit = run > goal;
+                    }
+            }
+            spiece = PER_LANE * lane + k;
+            sbefore = before;
+            spast = past;
         }
+        if (l < 0 && lane == 0) spiece = -1;
     }
-    const bool seek = k >= 0;                                // else the last token of the last piece
-    if (!seek) k = any;
-    const int64_t e0 = (int64_t)(first + k) * piece - lead;
+    __syncthreads();
+    if (spiece < 0) {                                        // a row of zeros
+        if (rank == 0 && tid == 0) p.next[b] = -1;
+        return;
+    }
+    if (spiece / WARPS != (int)rank) return;
+    const Rows<Tp> w(p, st, b);
+    const int64_t share = (piece / WARPS + 127) / 128 * 128; // of the piece, a warp
+    const int64_t e0 = (int64_t)spiece * piece - w.lead, end = min(e0 + piece, (int64_t)V);
+    {
+        Pair s = {0.f, 0.f};
+        const int64_t from = e0 + warp * share, to = min(from + share, end);
+        for (int64_t e = from + 4 * lane; e < to; e += 128) {
+            Pair r[4];
+            residual(w, e, V, dead, r);
+            s = s + ((r[0] + r[1]) + (r[2] + r[3]));
+        }
+        s = warp_sum(s);
+        if (lane == 0) sub[warp] = s;
+    }
+    __syncthreads();
+    Pair before = sbefore;
+    bool past;
+    const int x = find_lane(lane < WARPS ? sub[lane] : Pair{0.f, 0.f}, goal, before, past, lane);
+    if (warp != max(x, 0)) return;
+    const bool seek = !(spast || past);                      // (past: sums that differ in their last bits)
+    const int64_t from = e0 + warp * share, to = min(from + share, end);
     int64_t found = -1, tail = -1;
-    for (int i = 0; i < piece && found < 0; i += 128) {
-        const int64_t e = e0 + i + 4 * lane;
-        const float4 y = values(pr, e, V, wide), z = qr ? values(qr, e, V, wide) : make_float4(0.f, 0.f, 0.f, 0.f);
-        const float yv[4] = {y.x, y.y, y.z, y.w}, zv[4] = {z.x, z.y, z.z, z.w};
-        double r[4], incl = 0.0;
+    for (int64_t e1 = from; e1 < to && found < 0; e1 += 128) {
+        const int64_t e = e1 + 4 * lane;
+        Pair r[4] = {}, incl = {0.f, 0.f};
+        if (e < to) residual(w, e, V, dead, r);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            r[j] = fmax((double)yv[j] - c * (double)zv[j], 0.0);
-            for (int d = 0; d < gone; ++d) if (!draft && dead[d] == e + j) r[j] = 0.0;
-            if (r[j] > 0.0) tail = e + j;
-            incl += r[j];
+            if (r[j].hi > 0.f) tail = e + j;
+            incl = incl + r[j];
         }
-        const double own = incl;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double x = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += x;
-        }
+        const Pair own = incl;
+        incl = warp_scan(incl, lane);
         int64_t hit = -1;
-        double run = before + incl - own;
+        Pair run = before + (incl - own);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            run += r[j];
-            if (hit < 0 && r[j] > 0.0 && run > goal) hit = e + j;
+            run = run + r[j];
+            if (hit < 0 && r[j].hi > 0.f && run > goal) hit = e + j;
         }
         const uint32_t who = seek ? __ballot_sync(0xffffffffu, hit >= 0) : 0u;
         if (who) found = __shfl_sync(0xffffffffu, hit, __ffs((int)who) - 1);
-        before += __shfl_sync(0xffffffffu, incl, 31);
+        before = before + shfl(incl, 31);
     }
     if (found < 0) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
-            const int64_t x = __shfl_xor_sync(0xffffffffu, tail, o);
-            tail = x > tail ? x : tail;
+            const int64_t y = __shfl_xor_sync(0xffffffffu, tail, o);
+            tail = y > tail ? y : tail;
         }
         found = tail;
     }
@@ -339,13 +459,13 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(const VerifyArgs p, 
 }
 
 template <typename Tp> cudaError_t run(const VerifyArgs &a, cudaStream_t st) {
-    // CTAs a sequence: enough for two an SM, and few enough values each to be worth one
+    // CTAs a sequence: until there are four an SM, and no fewer than 2048 values each.  The
+    // batch of 256 trees: 148, 109, 94 and 100 us with 1, 2, 4 and 8; one sequence over 50,021
+    // tokens 19, 12.6, 10.2 and 8.2.
     int cluster = 1;
-    while (cluster < MAX_CLUSTER && (int64_t)a.B * cluster < 304 && (int64_t)cluster * 8192 < a.V) cluster *= 2;
-    // values a piece: 512, or as many as PIECES pieces a CTA need
-    const int64_t cap = (int64_t)PIECES * cluster;
-    int64_t piece = 512;
-    while ((((int64_t)a.V + 3 + piece - 1) / piece + cluster - 1) / cluster * cluster > cap) piece *= 2;
+    while (cluster < MAX_CLUSTER && (int64_t)a.B * cluster < 608 && (int64_t)cluster * 4096 <= a.V) cluster *= 2;
+    const int64_t pieces = (int64_t)cluster * WARPS;
+    const int64_t piece = ((int64_t)a.V + 3 + pieces * 128 - 1) / (pieces * 128) * 128;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.B * cluster));
     cfg.blockDim = dim3(THREADS);
@@ -359,7 +479,7 @@ template <typename Tp> cudaError_t run(const VerifyArgs &a, cudaStream_t st) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, verify_kernel<Tp>, a, cluster, (int)piece);
+    return cudaLaunchKernelEx(&cfg, verify_kernel<Tp>, a, cluster, piece);
 }
 
 }  // namespace
