@@ -164,8 +164,9 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                 if constexpr (TREE) {
                     front = seq_front(p, w.b);
                     const int32_t *par = p.parents + (int64_t)w.b * p.T;
-                    const uint32_t lo = __ballot_sync(0xffffffffu, lane < p.T && tree::ancestors(par, lane));
-                    const uint32_t hi = __ballot_sync(0xffffffffu, lane + 32 < p.T && tree::ancestors(par, lane + 32));
+                    uint64_t a, c;
+                    tree::all_ancestors(par, p.T, lane, a, c);
+                    const uint32_t lo = __ballot_sync(0xffffffffu, a != 0), hi = __ballot_sync(0xffffffffu, c != 0);
                     nodes = (uint64_t)hi << 32 | lo;
                 }
                 // first row / 8 of this lane's box of 32, and of the next 32
@@ -313,8 +314,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                 if constexpr (TREE) {
                     const int32_t *par = p.parents + (int64_t)w.b * p.T;
                     front = seq_front(p, w.b);
-                    if (lane < p.T) sees = tree::ancestors(par, lane);
-                    if (lane + 32 < p.T) sees32 = tree::ancestors(par, lane + 32);
+                    tree::all_ancestors(par, p.T, lane, sees, sees32);
                     const uint32_t lo = __ballot_sync(0xffffffffu, sees != 0), hi = __ballot_sync(0xffffffffu, sees32 != 0);
                     const int t = min((h0 + n0 + lane) / p.heads, p.T - 1);
                     pad = __ballot_sync(0xffffffffu, !((t < 32 ? lo : hi) >> (t & 31) & 1));

@@ -48,6 +48,19 @@ __device__ __forceinline__ void copy16(void *dst, const void *src) {
 }
 __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" :: "l"(p)); }
 
+// A row of bf16 as a lane loads it.
+template <int D> struct Raw { uint32_t x[D / 64]; };
+template <int D> __device__ __forceinline__ Raw<D> load_raw(const __nv_bfloat16 *p, int lane) {
+    Raw<D> r;
+    if constexpr (D == 128) {
+        const uint2 y = *reinterpret_cast<const uint2 *>(p + 4 * lane);
+        r.x[0] = y.x; r.x[1] = y.y;
+    } else {
+        r.x[0] = *reinterpret_cast<const uint32_t *>(p + 2 * lane);
+    }
+    return r;
+}
+
 // Channels a lane holds of a row of D: consecutive ones.
 template <int D> struct Row { float x[D / 32]; };
 template <int D, typename Tin> __device__ __forceinline__ Row<D> load_row(const Tin *p, int lane) {
@@ -61,110 +74,70 @@ template <int D, typename Tin> __device__ __forceinline__ Row<D> load_row(const 
     }
     return r;
 }
+template <int D> __device__ __forceinline__ void store_row(float *p, int lane, const Row<D> &r) {
+    if constexpr (D == 128) store4(p + 4 * lane, make_float4(r.x[0], r.x[1], r.x[2], r.x[3]));
+    else *reinterpret_cast<float2 *>(p + 2 * lane) = make_float2(r.x[0], r.x[1]);
+}
+template <int D> __device__ __forceinline__ Row<D> spread(float x) {
+    Row<D> r;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) r.x[c] = x;
+    return r;
+}
+template <int D> __device__ __forceinline__ Row<D> unpack(const Raw<D> &a) {
+    Row<D> r;
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+        const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&a.x[i]));
+        r.x[2 * i] = y.x;
+        r.x[2 * i + 1] = y.y;
+    }
+    return r;
+}
 
-// Up to 16 nodes: their rows come to shared memory, all at once.  More: from global memory
-// where they are used (two CTAs an SM would not fit beside them).
-template <int NT> constexpr bool STAGED = NT <= 16;
+constexpr float LOG2E = 1.4426950408889634f;
 
-// Shared memory: rows k e^gamma and q e^gamma, in their place after the product the
-// deltas (and fp32's outputs); A and P; masks, betas, parents.
+// Shared memory.  bf16: rows k e^gamma, q e^gamma and k e^-gamma (before them gamma, after the
+// product the deltas d); A and P, then M; masks, betas, parents.  With 64 nodes A and P take
+// the place of k e^-gamma, so that two CTAs fit an SM.  fp32: rows k e^gamma and q e^gamma,
+// after the product deltas and outputs; A and P; masks, betas; up to 16 nodes the inputs.
 template <int D, int NT> struct Smem {       // NT: nodes, a multiple of 8
-    static constexpr int LD = D + 16;        // two rows' quarter-warp reads meet different banks
-    static constexpr int LDU = D + 8;        // the deltas' rows: four rows' reads do
-    static constexpr int LDP = NT + 4;       // pairs of node r: ap[r * LDP + i]
-    static constexpr uint32_t KG = 0, QG = NT * LD * 4, AP = 2 * QG, MASK = AP + NT * LDP * 8, BETA = MASK + NT * 8,
-                              PAR = BETA + NT * 4, ROWS = PAR + NT * 4;
-    // staged: q, k, v, then gates
-    static constexpr uint32_t bytes(int e) { return ROWS + (STAGED<NT> ? NT * D * (3 * e + 4) : 0); }
+    static constexpr int LD = D + 4;         // eight rows' reads of four channels meet different banks
+    static constexpr int LDU = D + 8;        // the deltas' rows: four rows' reads of 32 columns do
+    static constexpr int LDS = D + 16;       // fp32: two rows' reads of 16 channels do
+    static constexpr int LDP = NT + 4;       // A and P of node r: pa[r * LDP + i], pp[r * LDP + i]
+    static constexpr bool OVER = NT == 64, STAGED = NT <= 16;
+    static constexpr uint32_t AP_BYTES = NT * LDP * 8;
+    // bf16 (the deltas' rows are longer, and may reach into those of q)
+    static constexpr uint32_t KG = 0, QG = NT * LD * 4, KI = 2 * QG, AP = OVER ? KI : 3 * QG, MASK = AP + (OVER && AP_BYTES < QG ? QG : AP_BYTES), BETA = MASK + NT * 8,
+                              UPS = BETA + NT * 4, TC_BYTES = UPS + 6 * NT + 16;
+    // fp32
+    static constexpr uint32_t SQG = NT * LDS * 4, SAP = 2 * SQG, SMASK = SAP + AP_BYTES, SBETA = SMASK + NT * 8, ROWS = SBETA + NT * 4,
+                              SIMT_BYTES = ROWS + (STAGED ? NT * D * 16 : 0);
 };
-// Warps a CTA: one for every 32 columns; from 32 nodes on two, which share the nodes.
-template <int D, int NT> struct Warps { static constexpr int COLS = D / 32, SPLIT = NT >= 32 ? 2 : 1, ALL = COLS * SPLIT; };
-// CTAs an SM that registers are shared out for (bf16, D = 128).
-template <int D, int NT> constexpr int resident(bool tc) { return !tc || D != 128 ? 1 : (NT == 8 ? 6 : (NT == 16 ? 5 : (NT == 32 ? 3 : 2))); }
+// Warps a CTA: one for every 32 columns; from 32 nodes on (D = 64: 16) two, which share the nodes.
+template <int D, int NT> struct Warps { static constexpr int COLS = D / 32, SPLIT = NT >= 32 || (D == 64 && NT == 16) ? 2 : 1, ALL = COLS * SPLIT; };
 
-template <int D, int NT, typename Tin>
-__global__ void
-__launch_bounds__(32 * Warps<D, NT>::ALL, resident<D, NT>(sizeof(Tin) == 2)) step_kernel(const StepArgs p) {
-    using L = Smem<D, NT>;
-    constexpr int LD = L::LD, LDU = L::LDU, LDP = L::LDP, C = D / 32;
-    constexpr int SPLIT = Warps<D, NT>::SPLIT, WARPS = Warps<D, NT>::ALL, THREADS = 32 * WARPS;
-    constexpr bool TC = sizeof(Tin) == 2;
-    extern __shared__ __align__(16) uint8_t sm[];
-    float *kg = reinterpret_cast<float *>(sm + L::KG), *qg = reinterpret_cast<float *>(sm + L::QG);
-    float2 *ap = reinterpret_cast<float2 *>(sm + L::AP);
-    uint64_t *mask = reinterpret_cast<uint64_t *>(sm + L::MASK);
-    float *beta = reinterpret_cast<float *>(sm + L::BETA);
-    int32_t *par = reinterpret_cast<int32_t *>(sm + L::PAR);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int b = blockIdx.x / p.H, h = blockIdx.x % p.H, T = p.T;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
-    const int64_t step = (int64_t)p.H * D;                              // between a head's nodes
-    const int64_t at0 = (int64_t)b * T * step + (int64_t)h * D;         // of node 0
-    const int64_t bt0 = (int64_t)b * T * p.H + h;
-    const Tin *q = (const Tin *)p.q + at0, *k = (const Tin *)p.k + at0, *v = (const Tin *)p.v + at0;
-    const float *g = p.scalar_gate ? p.g + bt0 : p.g + at0;
-    int64_t in = step, gs = p.scalar_gate ? p.H : step;                 // between nodes of the inputs, of the gates
-    Tin *o = (Tin *)p.o + at0;
-    int64_t slot = b;
-    if (tid < T) {
-        par[tid] = p.parents[(int64_t)b * T + tid];
-        beta[tid] = p.beta[bt0 + (int64_t)tid * p.H];
-    }
-    if constexpr (STAGED<NT>) {
-        Tin *rows = reinterpret_cast<Tin *>(sm + L::ROWS);
-        float *gates = reinterpret_cast<float *>(rows + 3 * NT * D);
-        constexpr int EL = 16 / sizeof(Tin), CH = D / EL;               // values and pieces of 16 bytes
-        for (int e = tid; e < T * CH; e += THREADS) {
-            const int r = e / CH, c = e % CH * EL;
-            copy16(rows + r * D + c, q + r * step + c);
-            copy16(rows + (NT + r) * D + c, k + r * step + c);
-            copy16(rows + (2 * NT + r) * D + c, v + r * step + c);
-        }
-        if (p.scalar_gate) {
-            if (tid < T) gates[tid] = g[tid * gs];
-            gs = 1;
-        } else {
-            for (int e = tid; e < T * (D / 4); e += THREADS) copy16(gates + 4 * e, g + e / (D / 4) * step + e % (D / 4) * 4);
-            gs = D;
-        }
-        q = rows; k = rows + NT * D; v = rows + 2 * NT * D; g = gates;
-        in = D;
-    }
-    if (p.slots) {
-        slot = p.slots[b];
-        if (slot < 0 || slot >= p.P) {
-            for (int e = tid; e < T * D; e += THREADS) o[e / D * step + e % D] = from_f32<Tin>(0.f);
-            if (STAGED<NT>) asm volatile("cp.async.wait_all;" ::: "memory");
-            return;
-        }
-    }
-    const float *S = p.S + (slot * p.H + h) * (D * D);
-    // the state starts on its way to L2 while gates and pairs are worked out
-    if (tid == 0) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" :: "l"(S), "r"(D * D * 4) : "memory");
-    if constexpr (!STAGED<NT>) {                         // the values start on their way to L2
-        constexpr int LINES = D * (int)sizeof(Tin) / 128;
-        for (int i = tid; i < T * LINES; i += THREADS) prefetch_l2((const char *)(v + i / LINES * step) + i % LINES * 128);
-    } else {
-        asm volatile("cp.async.wait_all;" ::: "memory");
-    }
-    __syncthreads();
-    if (tid < NT) mask[tid] = tid < T ? ancestors(par, tid) : 0;
-    __syncthreads();
-    // A warp a node: up its path, nearest ancestor first, with the gates between them
-    // summed on the way (differences of sums from the root would cancel); what the sum
-    // is at the end fades the rows that meet the state.  Four ancestors at a time, so that
-    // their loads are under way together and the sums over the lanes share exchanges.
+// A and P pair by pair, and the rows that meet the state, all in float32: a warp a node,
+// up its path, nearest ancestor first, with the gates between them summed on the way
+// (differences of sums from the root would cancel); what the sum is at the end fades the
+// rows.  Four ancestors at a time, so that their loads are under way together and the sums
+// over the lanes share exchanges.  in, gs: elements between nodes of k and q, of the gates.
+template <int D, int NT, int LD, int WARPS, typename Tin>
+__device__ __forceinline__ void pair_by_pair(const Tin *q, const Tin *k, const float *g, int64_t in, int64_t gs, bool scalar_gate,
+                                             const uint64_t *mask, const float *beta, float *kg, float *qg, float *pa, float *pp) {
+    constexpr int LDP = Smem<D, NT>::LDP, C = D / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int r = warp; r < NT; r += WARPS) {
         uint64_t m = mask[r];
+        const bool on = m != 0;
         Row<D> kr = {}, qr = {}, run = {};
-        if (m) {
+        if (on) {
             kr = load_row<D>(k + r * in, lane);
             qr = load_row<D>(q + r * in, lane);
         }
-        const float br = m ? beta[r] : 0.f;
-        const bool on = m != 0;
+        for (int i = lane; i < NT; i += 32) pa[r * LDP + i] = pp[r * LDP + i] = 0.f;
+        __syncwarp();
         while (m) {
             int at[4];
             Row<D> ki[4], gi[4];
@@ -175,7 +148,7 @@ __launch_bounds__(32 * Warps<D, NT>::ALL, resident<D, NT>(sizeof(Tin) == 2)) ste
                 if (m) {
                     m ^= 1ull << at[u];
                     ki[u] = load_row<D>(k + at[u] * in, lane);
-                    if (p.scalar_gate) {
+                    if (scalar_gate) {
                         const float x = g[at[u] * gs];
 #pragma unroll
                         for (int c = 0; c < C; ++c) gi[u].x[c] = x;
@@ -192,7 +165,7 @@ __launch_bounds__(32 * Warps<D, NT>::ALL, resident<D, NT>(sizeof(Tin) == 2)) ste
                     const float w = ki[u].x[c] * ex2(run.x[c]);
                     sum[2 * u] += kr.x[c] * w;
                     sum[2 * u + 1] += qr.x[c] * w;
-                    run.x[c] += gi[u].x[c] * 1.4426950408889634f;
+                    run.x[c] += gi[u].x[c] * LOG2E;
                 }
             // every exchange halves the sums a lane keeps
 #pragma unroll
@@ -209,122 +182,385 @@ __launch_bounds__(32 * Warps<D, NT>::ALL, resident<D, NT>(sizeof(Tin) == 2)) ste
             sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 1);
             const int u = lane >> 3, i = u == 0 ? at[0] : (u == 1 ? at[1] : (u == 2 ? at[2] : at[3]));
             if ((lane & 3) == 0 && i >= 0)
-                reinterpret_cast<float *>(ap + r * LDP + i)[lane >> 2 & 1] = lane & 4 ? sum[0] : br * sum[0];
+                (lane & 4 ? pp : pa)[r * LDP + i] = lane & 4 ? sum[0] : beta[r] * sum[0];
         }
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const float f = on ? ex2(run.x[c]) : 0.f;
             const float a = kr.x[c] * f, z = qr.x[c] * f;
-            kg[r * LD + C * lane + c] = TC ? to_tf32(a) : a;
-            qg[r * LD + C * lane + c] = TC ? to_tf32(z) : z;
+            kg[r * LD + C * lane + c] = sizeof(Tin) == 2 ? to_tf32(a) : a;
+            qg[r * LD + C * lane + c] = sizeof(Tin) == 2 ? to_tf32(z) : z;
         }
     }
+}
+
+// CTAs an SM that registers are shared out for (bf16, D = 128).
+template <int D, int NT> constexpr int resident() { return D != 128 ? 1 : (NT == 8 ? 6 : (NT == 16 ? 5 : (NT == 32 ? 3 : 2))); }
+// Beyond 2^-RANGE of decay from the root, e^-gamma and the products with it could leave float32.
+constexpr float RANGE = 100.f;
+
+template <int D, int NT>
+__global__ void __launch_bounds__(32 * Warps<D, NT>::ALL, resident<D, NT>()) step_tc_kernel(const StepArgs p) {
+    using L = Smem<D, NT>;
+    using Tin = __nv_bfloat16;
+    constexpr int LD = L::LD, LDU = L::LDU, LDP = L::LDP, C = D / 32;
+    constexpr int SPLIT = Warps<D, NT>::SPLIT, WARPS = Warps<D, NT>::ALL, THREADS = 32 * WARPS;
+    extern __shared__ __align__(16) uint8_t sm[];
+    float *kg = reinterpret_cast<float *>(sm + L::KG), *qg = reinterpret_cast<float *>(sm + L::QG), *ki = reinterpret_cast<float *>(sm + L::KI);
+    float *pa = reinterpret_cast<float *>(sm + L::AP), *pp = pa + NT * LDP;
+    uint64_t *mask = reinterpret_cast<uint64_t *>(sm + L::MASK);
+    float *beta = reinterpret_cast<float *>(sm + L::BETA);
+    int8_t *ups = reinterpret_cast<int8_t *>(sm + L::UPS);  // [round][node]: the node 2^round above
+    int *rounds = reinterpret_cast<int *>(sm + L::UPS + 6 * NT);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int b = blockIdx.x / p.H, h = blockIdx.x % p.H, T = p.T;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    const int64_t step = (int64_t)p.H * D;                              // between a head's nodes
+    const int64_t at0 = (int64_t)b * T * step + (int64_t)h * D;         // of node 0
+    const int64_t bt0 = (int64_t)b * T * p.H + h;
+    const Tin *q = (const Tin *)p.q + at0, *k = (const Tin *)p.k + at0, *v = (const Tin *)p.v + at0;
+    const float *g = p.scalar_gate ? p.g + bt0 : p.g + at0;
+    const int64_t gs = p.scalar_gate ? p.H : step;
+    Tin *o = (Tin *)p.o + at0;
+    int64_t slot = b;
+    if (p.slots) {
+        slot = p.slots[b];
+        if (slot < 0 || slot >= p.P) {
+            for (int e = tid; e < T * D; e += THREADS) o[e / D * step + e % D] = from_f32<Tin>(0.f);
+            return;
+        }
+    }
+    const float *S = p.S + (slot * p.H + h) * (D * D);
+    // values start on their way to L2, this warp's rows of k and q to registers, gates to shared
+    // memory; behind them the state to L2: in front of them it kept them waiting (batch of 256
+    // sequences with 8 nodes: 118 us, here 106; without 115)
+    constexpr int LINES = D * (int)sizeof(Tin) / 128;
+    for (int i = tid; i < T * LINES; i += THREADS) prefetch_l2((const char *)(v + i / LINES * step) + i % LINES * 128);
+    constexpr int MINE = NT / WARPS;                     // nodes warp, warp + WARPS, ...
+    Raw<D> kr[MINE], qr[MINE];
+#pragma unroll
+    for (int n = 0; n < MINE; ++n) {
+        const int r = warp + n * WARPS;
+        kr[n] = {}; qr[n] = {};
+        if (r < T) {
+            kr[n] = load_raw<D>(k + r * step, lane);
+            qr[n] = load_raw<D>(q + r * step, lane);
+        }
+    }
+    if (p.scalar_gate) {
+#pragma unroll
+        for (int n = 0; n < MINE; ++n) {
+            const int r = warp + n * WARPS;
+            if (r < T) {
+                const float x = g[r * gs];
+                store_row<D>(kg + r * LD, lane, spread<D>(x));
+            }
+        }
+    } else {
+        for (int e = tid; e < T * (D / 4); e += THREADS)
+            copy16(kg + e / (D / 4) * LD + e % (D / 4) * 4, g + e / (D / 4) * step + e % (D / 4) * 4);
+    }
+    if (warp == 0) {
+        uint64_t x, y;
+        const int n = all_ancestors(p.parents + (int64_t)b * T, T, lane, x, y, [&](int round, int up0, int up1) {
+            if (lane < NT) ups[round * NT + lane] = (int8_t)up0;
+            if (NT > 32) ups[round * NT + lane + 32] = (int8_t)up1;
+        });
+        if (lane < NT) mask[lane] = x;
+        if (NT > 32) mask[lane + 32] = y;
+        if (lane == 0) *rounds = n;
+    }
+    if (tid < T) beta[tid] = p.beta[bt0 + (int64_t)tid * p.H];
+    if (tid == 0) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" :: "l"(S), "r"(D * D * 4) : "memory");
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    // gamma: every round adds up twice as far a stretch of the paths, from one buffer to
+    // the other; a warp its rows
+    float *was = kg, *now = ki;
+    for (int k = 0; k < *rounds; ++k) {
+#pragma unroll
+        for (int n = 0; n < MINE; ++n) {
+            const int r = warp + n * WARPS, up = ups[k * NT + r];
+            Row<D> x = load_row<D>(was + r * LD, lane);
+            if (up >= 0) {
+                const Row<D> y = load_row<D>(was + up * LD, lane);
+#pragma unroll
+                for (int c = 0; c < C; ++c) x.x[c] += y.x[c];
+            }
+            store_row<D>(now + r * LD, lane, x);
+        }
+        __syncthreads();
+        float *z = was;
+        was = now;
+        now = z;
+    }
+    Row<D> gm[MINE];                                     // in log2 units
+    bool far = false;
+#pragma unroll
+    for (int n = 0; n < MINE; ++n) {
+        const int r = warp + n * WARPS;
+        gm[n] = load_row<D>(was + r * LD, lane);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            gm[n].x[c] = mask[r] ? gm[n].x[c] * LOG2E : 0.f;
+            far |= !(gm[n].x[c] >= -RANGE);              // (or a gate that is not a number)
+        }
+    }
+    const int gq = lane >> 2, c4 = lane & 3, cols = 32 * (warp / SPLIT);
+    if (__syncthreads_or(far)) {
+        pair_by_pair<D, NT, LD, WARPS>(q, k, g, step, gs, p.scalar_gate, mask, beta, kg, qg, pa, pp);
+        __syncthreads();
+    } else {
+#pragma unroll
+        for (int n = 0; n < MINE; ++n) {
+            const int r = warp + n * WARPS;
+            const bool on = mask[r] != 0;
+            Row<D> a = unpack<D>(kr[n]), z = unpack<D>(qr[n]), i;
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const float f = ex2(gm[n].x[c]);
+                i.x[c] = on ? to_tf32(a.x[c] * ex2(-gm[n].x[c])) : 0.f;
+                a.x[c] = on ? to_tf32(a.x[c] * f) : 0.f;
+                z.x[c] = on ? to_tf32(z.x[c] * f) : 0.f;
+            }
+            store_row<D>(kg + r * LD, lane, a);
+            store_row<D>(qg + r * LD, lane, z);
+            store_row<D>(ki + r * LD, lane, i);
+        }
+        __syncthreads();
+        // A and P of 8 nodes a warp: e^(gamma_r - gamma_i) is the product of the two rows' factors.
+        constexpr int TILES = (NT / 8 + WARPS - 1) / WARPS;
+        float pr[TILES][NT / 8][4] = {};
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) {
+            const int tile = warp + t * WARPS;
+            if (tile >= NT / 8) break;
+#pragma unroll 4
+            for (int s = 0; s < D / 8; ++s) {
+                const float *a = kg + (8 * tile + gq) * LD + 8 * s + c4, *c = qg + (8 * tile + gq) * LD + 8 * s + c4;
+                const float a0 = a[0], a1 = c[0], a2 = a[4], a3 = c[4];
+#pragma unroll
+                for (int j = 0; j < NT / 8; ++j)
+                    if (j <= tile) {                     // nodes see earlier ones only
+                        const float *x = ki + (8 * j + gq) * LD + 8 * s + c4;
+                        mma_tf32(pr[t][j], a0, a1, a2, a3, x[0], x[4]);
+                    }
+            }
+        }
+        if constexpr (L::OVER) __syncthreads();
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) {
+            const int tile = warp + t * WARPS;
+            if (tile >= NT / 8) break;
+            const int r = 8 * tile + gq;
+            const uint64_t m = mask[r];
+            const float br = m ? beta[r] : 0.f;
+#pragma unroll
+            for (int j = 0; j < NT / 8; ++j) {           // zeros where r does not see a node
+                const int i = 8 * j + 2 * c4;
+                const bool s0 = m >> i & 1, s1 = m >> (i + 1) & 1;
+                *reinterpret_cast<float2 *>(pa + r * LDP + i) = make_float2(s0 ? br * pr[t][j][0] : 0.f, s1 ? br * pr[t][j][1] : 0.f);
+                *reinterpret_cast<float2 *>(pp + r * LDP + i) = make_float2(s0 ? pr[t][j][2] : 0.f, s1 ? pr[t][j][3] : 0.f);
+            }
+        }
+    }
+
+    // The nodes' rows times the state.  Column group j's MMA column gq is S's column 4 gq + j of
+    // the warp's 32.  The MMA wants channel c4 of four, columns 4 gq .. in lane 4 gq + c4;
+    // the lanes load them as 8 c4 + gq, so that eight lanes read a line of 128 bytes (four
+    // lines by two sectors each take four times the wavefronts of the L1), and exchange.
+    constexpr int MT = NT / 8 / SPLIT;
+    const int part = warp % SPLIT;                       // this warp's tiles of 8 nodes: part, part + SPLIT, ...
+    const int from = 8 * c4 + gq;
+    const float *Sl = S + (lane >> 3) * D + cols + 4 * (lane & 7);
+    float acc[MT][4][4] = {};
+#pragma unroll(MT > 2 ? 2 : 4)
+    for (int s = 0; s < D / 16; ++s) {
+        float4 y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = load4(Sl + (16 * s + 4 * j) * D);
+        float f[4][4];                                   // [channel 16 s + 4 j + c4][column]
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f[j][0] = to_tf32(__shfl_sync(0xffffffffu, y[j].x, from));
+            f[j][1] = to_tf32(__shfl_sync(0xffffffffu, y[j].y, from));
+            f[j][2] = to_tf32(__shfl_sync(0xffffffffu, y[j].z, from));
+            f[j][3] = to_tf32(__shfl_sync(0xffffffffu, y[j].w, from));
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const int at = (8 * (mt * SPLIT + part) + gq) * LD + 16 * s + c4;
+            const float *a = kg + at, *c = qg + at;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mma_tf32(acc[mt][j], a[8 * t], c[8 * t], a[8 * t + 4], c[8 * t + 4], f[2 * t][j], f[2 * t + 1][j]);
+        }
+    }
+    // row gq of a tile: columns 8 c4 + j (from registers 0 and 2 of group j) and 8 c4 + 4 + j
+    const int n0 = cols + 8 * c4;
+    uint4 vr[MT];                                        // the values, while M is worked out
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        const int r = 8 * (mt * SPLIT + part) + gq;
+        vr[mt] = make_uint4(0, 0, 0, 0);
+        if (mask[r]) vr[mt] = *reinterpret_cast<const uint4 *>(v + r * step + n0);
+    }
+    __syncthreads();
+    // o_r = (q_r e^gamma_r) S + sum_j M_rj d_j with d_j = beta_j (v_j - (k_j e^gamma_j) S) and
+    // M (I + A) = P: along r's path M_rj = P_rj - sum_{i below j} M_ri A_ij, nearest first.
+    // A warp a node, a lane the nodes `lane` and `lane + 32`.  M replaces P.
+    constexpr int AT_ONCE = MINE < 4 ? MINE : 4;         // nodes whose chains run side by side
+#pragma unroll
+    for (int n0_ = 0; n0_ < MINE; n0_ += AT_ONCE) {
+        int at[AT_ONCE];
+        float m0[AT_ONCE], m1[AT_ONCE];
+        bool any = false;
+#pragma unroll
+        for (int n = 0; n < AT_ONCE; ++n) {
+            const int r = warp + (n0_ + n) * WARPS;
+            at[n] = mask[r] ? r : -1;
+            any |= at[n] >= 0;
+            m0[n] = lane < NT ? pp[r * LDP + lane] : 0.f;
+            m1[n] = NT > 32 ? pp[r * LDP + lane + 32] : 0.f;
+        }
+        while (any) {
+            any = false;
+#pragma unroll
+            for (int n = 0; n < AT_ONCE; ++n) {
+                const int i = at[n];
+                if (i < 0) continue;
+                const float x = __shfl_sync(0xffffffffu, NT > 32 && i >= 32 ? m1[n] : m0[n], i & 31);
+                at[n] = *rounds ? ups[i] : -1;           // A's row i is 0 but for i's ancestors, and at i
+                any |= at[n] >= 0;
+                if (lane < NT && lane != i) m0[n] -= x * pa[i * LDP + lane];
+                if (NT > 32 && lane + 32 != i) m1[n] -= x * pa[i * LDP + lane + 32];
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < AT_ONCE; ++n) {
+            const int r = warp + (n0_ + n) * WARPS;
+            if (lane < NT) pp[r * LDP + lane] = mask[r] ? to_tf32(m0[n]) : 0.f;
+            if (NT > 32) pp[r * LDP + lane + 32] = mask[r] ? to_tf32(m1[n]) : 0.f;
+        }
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        const int r = 8 * (mt * SPLIT + part) + gq;
+        const __nv_bfloat162 *vv = reinterpret_cast<const __nv_bfloat162 *>(&vr[mt]);
+        const float2 v0 = __bfloat1622float2(vv[0]), v1 = __bfloat1622float2(vv[1]), v2 = __bfloat1622float2(vv[2]), v3 = __bfloat1622float2(vv[3]);
+        const float br = mask[r] ? beta[r] : 0.f;        // padding: values and products are 0
+        const float4 x = make_float4(br * (v0.x - acc[mt][0][0]), br * (v0.y - acc[mt][1][0]), br * (v1.x - acc[mt][2][0]), br * (v1.y - acc[mt][3][0]));
+        const float4 y = make_float4(br * (v2.x - acc[mt][0][1]), br * (v2.y - acc[mt][1][1]), br * (v3.x - acc[mt][2][1]), br * (v3.y - acc[mt][3][1]));
+        store4(kg + r * LDU + n0, make_float4(to_tf32(x.x), to_tf32(x.y), to_tf32(x.z), to_tf32(x.w)));
+        store4(kg + r * LDU + n0 + 4, make_float4(to_tf32(y.x), to_tf32(y.y), to_tf32(y.z), to_tf32(y.w)));
+    }
+    __syncthreads();
+    // M d on top of the q rows' products (registers 2 and 3); the k rows' are done with
+#pragma unroll
+    for (int ks = 0; ks < NT / 8; ++ks) {
+        const float4 x = load4(kg + (8 * ks + c4) * LDU + cols + 4 * gq), y = load4(kg + (8 * ks + c4 + 4) * LDU + cols + 4 * gq);
+        const float xv[4] = {x.x, x.y, x.z, x.w}, yv[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const int tile = mt * SPLIT + part;
+            if (mt * SPLIT + SPLIT - 1 < ks || tile < ks) continue;      // nodes see earlier ones only
+            const float a1 = pp[(8 * tile + gq) * LDP + 8 * ks + c4], a3 = pp[(8 * tile + gq) * LDP + 8 * ks + c4 + 4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mma_tf32(acc[mt][j], 0.f, a1, 0.f, a3, xv[j], yv[j]);
+        }
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        const int r = 8 * (mt * SPLIT + part) + gq;
+        if (r < T) {
+            __nv_bfloat162 y[4] = {__floats2bfloat162_rn(acc[mt][0][2], acc[mt][1][2]), __floats2bfloat162_rn(acc[mt][2][2], acc[mt][3][2]),
+                                   __floats2bfloat162_rn(acc[mt][0][3], acc[mt][1][3]), __floats2bfloat162_rn(acc[mt][2][3], acc[mt][3][3])};
+            *reinterpret_cast<uint4 *>(o + r * step + n0) = *reinterpret_cast<const uint4 *>(y);
+        }
+    }
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(32 * Warps<D, NT>::ALL) step_simt_kernel(const StepArgs p) {
+    using L = Smem<D, NT>;
+    using Tin = float;
+    constexpr int LD = L::LDS, LDP = L::LDP;
+    constexpr int SPLIT = Warps<D, NT>::SPLIT, WARPS = Warps<D, NT>::ALL, THREADS = 32 * WARPS;
+    extern __shared__ __align__(16) uint8_t sm[];
+    float *kg = reinterpret_cast<float *>(sm), *qg = reinterpret_cast<float *>(sm + L::SQG);
+    float *pa = reinterpret_cast<float *>(sm + L::SAP), *pp = pa + NT * LDP;
+    uint64_t *mask = reinterpret_cast<uint64_t *>(sm + L::SMASK);
+    float *beta = reinterpret_cast<float *>(sm + L::SBETA);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int b = blockIdx.x / p.H, h = blockIdx.x % p.H, T = p.T;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    const int64_t step = (int64_t)p.H * D;                              // between a head's nodes
+    const int64_t at0 = (int64_t)b * T * step + (int64_t)h * D;         // of node 0
+    const int64_t bt0 = (int64_t)b * T * p.H + h;
+    const float *q = (const float *)p.q + at0, *k = (const float *)p.k + at0, *v = (const float *)p.v + at0;
+    const float *g = p.scalar_gate ? p.g + bt0 : p.g + at0;
+    int64_t in = step, gs = p.scalar_gate ? p.H : step;                 // between nodes of the inputs, of the gates
+    float *o = (float *)p.o + at0;
+    int64_t slot = b;
+    if (p.slots) {
+        slot = p.slots[b];
+        if (slot < 0 || slot >= p.P) {
+            for (int e = tid; e < T * D; e += THREADS) o[e / D * step + e % D] = 0.f;
+            return;
+        }
+    }
+    if constexpr (L::STAGED) {                           // all inputs to shared memory at once
+        float *rows = reinterpret_cast<float *>(sm + L::ROWS), *gates = rows + 3 * NT * D;
+        for (int e = tid; e < T * (D / 4); e += THREADS) {
+            const int r = e / (D / 4), c = e % (D / 4) * 4;
+            copy16(rows + r * D + c, q + r * step + c);
+            copy16(rows + (NT + r) * D + c, k + r * step + c);
+            copy16(rows + (2 * NT + r) * D + c, v + r * step + c);
+            if (!p.scalar_gate) copy16(gates + r * D + c, g + r * step + c);
+        }
+        if (p.scalar_gate && tid < T) gates[tid] = g[tid * gs];
+        q = rows; k = rows + NT * D; v = rows + 2 * NT * D; g = gates;
+        in = D;
+        gs = p.scalar_gate ? 1 : D;
+    }
+    const float *S = p.S + (slot * p.H + h) * (D * D);
+    if (tid == 0) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" :: "l"(S), "r"(D * D * 4) : "memory");
+    if (warp == 0) {
+        uint64_t x, y;
+        all_ancestors(p.parents + (int64_t)b * T, T, lane, x, y);
+        if (lane < NT) mask[lane] = x;
+        if (NT > 32) mask[lane + 32] = y;
+    }
+    if (tid < T) beta[tid] = p.beta[bt0 + (int64_t)tid * p.H];
+    if constexpr (L::STAGED) asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    pair_by_pair<D, NT, LD, WARPS>(q, k, g, in, gs, p.scalar_gate, mask, beta, kg, qg, pa, pp);
     __syncthreads();
 
     const int gq = lane >> 2, c4 = lane & 3, cols = 32 * (warp / SPLIT);
     const float *Sw = S + cols + 4 * gq;                 // this thread's 4 columns
-    if constexpr (TC) {
-        // o_r = (q_r e^gamma_r) S + sum_j M_rj d_j with d_j = beta_j (v_j - (k_j e^gamma_j) S) and
-        // M (I + A) = P: along r's path M_rj = P_rj - sum_{i below j} M_ri A_ij, nearest first.
-        // A warp a node, a lane the nodes `lane` and `lane + 32`.  M replaces P.
-        for (int r = warp; r < NT; r += WARPS) {
-            const uint64_t all = mask[r];
-            float m0 = 0.f, m1 = 0.f;
-            if (lane < NT && (all >> lane & 1)) m0 = ap[r * LDP + lane].y;
-            if (NT > 32 && (all >> (lane + 32) & 1)) m1 = ap[r * LDP + lane + 32].y;
-            uint64_t m = all;
-            while (m) {
-                const int i = 63 - __clzll((long long)m);
-                m ^= 1ull << i;                          // what is left is above i on the path
-                const float x = __shfl_sync(0xffffffffu, NT > 32 && i >= 32 ? m1 : m0, i & 31);
-                if (lane < NT && (m >> lane & 1)) m0 -= x * ap[i * LDP + lane].x;
-                if (NT > 32 && (m >> (lane + 32) & 1)) m1 -= x * ap[i * LDP + lane + 32].x;
-            }
-            if (lane < NT) ap[r * LDP + lane].y = to_tf32(m0);
-            if (NT > 32) ap[r * LDP + lane + 32].y = to_tf32(m1);
-        }
-        // K step (s, t): MMA column c4 is channel 16 s + 4 c4 + 2 t, column c4 + 4 the next
-        // one; column group j's MMA column gq is S's column 4 gq + j of the warp's 32.
-        constexpr int MT = NT / 8 / SPLIT;
-        const int part = warp % SPLIT;                   // this warp's tiles of 8 nodes: part, part + SPLIT, ...
-        float acc[MT][4][4] = {};
-#pragma unroll(MT > 2 ? 2 : 4)
+    // up to four groups of 4 nodes in one pass over the state; the four lanes of a
+    // column hold every fourth group of 4 channels
+    constexpr int GROUPS = NT / 4 / SPLIT, PASS = GROUPS < 4 ? GROUPS : 4;
+    float4 keep[GROUPS][2];                          // node 4 t + c4: products with k, with q
+#pragma unroll
+    for (int x0 = 0; x0 < GROUPS; x0 += PASS) {
+        if (4 * (x0 * SPLIT + warp % SPLIT) >= T) break;
+        float w[PASS][4][4] = {}, z[PASS][4][4] = {};
+#pragma unroll(D == 64 ? 4 : 2)
         for (int s = 0; s < D / 16; ++s) {
             float4 y[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) y[j] = load4(Sw + (16 * s + 4 * c4 + j) * D);
-            float f[4][4];                               // [channel][column]
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                f[j][0] = to_tf32(y[j].x); f[j][1] = to_tf32(y[j].y); f[j][2] = to_tf32(y[j].z); f[j][3] = to_tf32(y[j].w);
-            }
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                const int row = 8 * (mt * SPLIT + part) + gq;
-                const float4 a = load4(kg + row * LD + 16 * s + 4 * c4);
-                const float4 c = load4(qg + row * LD + 16 * s + 4 * c4);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    mma_tf32(acc[mt][j], a.x, c.x, a.y, c.y, f[0][j], f[1][j]);
-                    mma_tf32(acc[mt][j], a.z, c.z, a.w, c.w, f[2][j], f[3][j]);
-                }
-            }
-        }
-        // row gq of a tile: columns 8 c4 + j (from registers 0 and 2 of group j) and 8 c4 + 4 + j
-        const int n0 = cols + 8 * c4;
-        __syncthreads();
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            const int r = 8 * (mt * SPLIT + part) + gq;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-            if (mask[r]) {
-                x = load4(v + r * in + n0);
-                y = load4(v + r * in + n0 + 4);
-                const float br = beta[r];
-                x = make_float4(br * (x.x - acc[mt][0][0]), br * (x.y - acc[mt][1][0]), br * (x.z - acc[mt][2][0]), br * (x.w - acc[mt][3][0]));
-                y = make_float4(br * (y.x - acc[mt][0][1]), br * (y.y - acc[mt][1][1]), br * (y.z - acc[mt][2][1]), br * (y.w - acc[mt][3][1]));
-            }
-            store4(kg + r * LDU + n0, make_float4(to_tf32(x.x), to_tf32(x.y), to_tf32(x.z), to_tf32(x.w)));
-            store4(kg + r * LDU + n0 + 4, make_float4(to_tf32(y.x), to_tf32(y.y), to_tf32(y.z), to_tf32(y.w)));
-        }
-        __syncthreads();
-        // M d on top of the q rows' products (registers 2 and 3); the k rows' are done with
-#pragma unroll
-        for (int ks = 0; ks < NT / 8; ++ks) {
-            const float4 x = load4(kg + (8 * ks + c4) * LDU + cols + 4 * gq), y = load4(kg + (8 * ks + c4 + 4) * LDU + cols + 4 * gq);
-            const float xv[4] = {x.x, x.y, x.z, x.w}, yv[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                const int tile = mt * SPLIT + part;
-                if (mt * SPLIT + SPLIT - 1 < ks || tile < ks) continue;      // nodes see earlier ones only
-                const float a1 = ap[(8 * tile + gq) * LDP + 8 * ks + c4].y, a3 = ap[(8 * tile + gq) * LDP + 8 * ks + c4 + 4].y;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) mma_tf32(acc[mt][j], 0.f, a1, 0.f, a3, xv[j], yv[j]);
-            }
-        }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            const int r = 8 * (mt * SPLIT + part) + gq;
-            if (r < T) {
-                __nv_bfloat162 y[4] = {__floats2bfloat162_rn(acc[mt][0][2], acc[mt][1][2]), __floats2bfloat162_rn(acc[mt][2][2], acc[mt][3][2]),
-                                       __floats2bfloat162_rn(acc[mt][0][3], acc[mt][1][3]), __floats2bfloat162_rn(acc[mt][2][3], acc[mt][3][3])};
-                *reinterpret_cast<uint4 *>(o + r * step + n0) = *reinterpret_cast<const uint4 *>(y);
-            }
-        }
-    } else {
-        // 4 nodes at a time; the four lanes of a column hold every fourth group of 4 channels
-        constexpr int GROUPS = NT / 4 / SPLIT;
-        float4 keep[GROUPS][2];                          // node 4 t + c4: products with k, with q
-#pragma unroll
-        for (int x = 0; x < GROUPS; ++x) {
-            const int t = x * SPLIT + warp % SPLIT;
-            if (4 * t >= T) break;
-            float w[4][4] = {}, z[4][4] = {};
-#pragma unroll 2
-            for (int s = 0; s < D / 16; ++s) {
-                float4 y[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) y[j] = load4(Sw + (16 * s + 4 * c4 + j) * D);
+            for (int x = 0; x < PASS; ++x) {
+                const int t = (x0 + x) * SPLIT + warp % SPLIT;
+                if (4 * t >= T) break;
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
                     const float4 a = load4(kg + (4 * t + n) * LD + 16 * s + 4 * c4);
@@ -332,70 +568,72 @@ __launch_bounds__(32 * Warps<D, NT>::ALL, resident<D, NT>(sizeof(Tin) == 2)) ste
                     const float av[4] = {a.x, a.y, a.z, a.w}, cv[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        w[n][0] += av[j] * y[j].x; w[n][1] += av[j] * y[j].y; w[n][2] += av[j] * y[j].z; w[n][3] += av[j] * y[j].w;
-                        z[n][0] += cv[j] * y[j].x; z[n][1] += cv[j] * y[j].y; z[n][2] += cv[j] * y[j].z; z[n][3] += cv[j] * y[j].w;
+                        w[x][n][0] += av[j] * y[j].x; w[x][n][1] += av[j] * y[j].y; w[x][n][2] += av[j] * y[j].z; w[x][n][3] += av[j] * y[j].w;
+                        z[x][n][0] += cv[j] * y[j].x; z[x][n][1] += cv[j] * y[j].y; z[x][n][2] += cv[j] * y[j].z; z[x][n][3] += cv[j] * y[j].w;
                     }
                 }
             }
+        }
+#pragma unroll
+        for (int x = 0; x < PASS; ++x)
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    w[n][e] += __shfl_xor_sync(0xffffffffu, w[n][e], 1);
-                    w[n][e] += __shfl_xor_sync(0xffffffffu, w[n][e], 2);
-                    z[n][e] += __shfl_xor_sync(0xffffffffu, z[n][e], 1);
-                    z[n][e] += __shfl_xor_sync(0xffffffffu, z[n][e], 2);
+                    w[x][n][e] += __shfl_xor_sync(0xffffffffu, w[x][n][e], 1);
+                    w[x][n][e] += __shfl_xor_sync(0xffffffffu, w[x][n][e], 2);
+                    z[x][n][e] += __shfl_xor_sync(0xffffffffu, z[x][n][e], 1);
+                    z[x][n][e] += __shfl_xor_sync(0xffffffffu, z[x][n][e], 2);
                 }
                 if (n == c4) {
-                    keep[x][0] = make_float4(w[n][0], w[n][1], w[n][2], w[n][3]);
-                    keep[x][1] = make_float4(z[n][0], z[n][1], z[n][2], z[n][3]);
+                    keep[x0 + x][0] = make_float4(w[x][n][0], w[x][n][1], w[x][n][2], w[x][n][3]);
+                    keep[x0 + x][1] = make_float4(z[x][n][0], z[x][n][1], z[x][n][2], z[x][n][3]);
                 }
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int x = 0; x < GROUPS; ++x) {
-            const int t = x * SPLIT + warp % SPLIT, r = 4 * t + c4, n = cols + 4 * gq;
-            if (4 * t >= T) break;
-            float4 y = make_float4(0.f, 0.f, 0.f, 0.f), z = y;
-            if (mask[r]) {
-                const float4 vv = load4(v + r * in + n), w = keep[x][0];
-                const float br = beta[r];
-                y = make_float4(br * (vv.x - w.x), br * (vv.y - w.y), br * (vv.z - w.z), br * (vv.w - w.w));
-                z = keep[x][1];
-            }
-            store4(kg + r * LD + n, y);
-            store4(qg + r * LD + n, z);
-        }
-        __syncthreads();
-        // the deltas, parents first; thread = column
-        if (tid < D)
-            for (int r = 0; r < T; ++r) {
-                uint64_t m = mask[r];
-                float u = kg[r * LD + tid], z = qg[r * LD + tid];
-                if (m) {
-                    m &= ~(1ull << r);
-                    while (m) {
-                        const int i = __ffsll((long long)m) - 1;
-                        m &= m - 1;
-                        const float2 x = ap[r * LDP + i];
-                        const float ui = kg[i * LD + tid];
-                        u -= x.x * ui;
-                        z += x.y * ui;
-                    }
-                    z += ap[r * LDP + r].y * u;
-                    kg[r * LD + tid] = u;
-                }
-                o[r * step + tid] = from_f32<Tin>(z);
             }
     }
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < GROUPS; ++x) {
+        const int t = x * SPLIT + warp % SPLIT, r = 4 * t + c4, n = cols + 4 * gq;
+        if (4 * t >= T) break;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f), z = y;
+        if (mask[r]) {
+            const float4 vv = load4(v + r * in + n), w = keep[x][0];
+            const float br = beta[r];
+            y = make_float4(br * (vv.x - w.x), br * (vv.y - w.y), br * (vv.z - w.z), br * (vv.w - w.w));
+            z = keep[x][1];
+        }
+        store4(kg + r * LD + n, y);
+        store4(qg + r * LD + n, z);
+    }
+    __syncthreads();
+    // the deltas, parents first; thread = column
+    if (tid < D)
+        for (int r = 0; r < T; ++r) {
+            uint64_t m = mask[r];
+            float u = kg[r * LD + tid], z = qg[r * LD + tid];
+            if (m) {
+                m &= ~(1ull << r);
+                while (m) {
+                    const int i = __ffsll((long long)m) - 1;
+                    m &= m - 1;
+                    const float ui = kg[i * LD + tid];
+                    u -= pa[r * LDP + i] * ui;
+                    z += pp[r * LDP + i] * ui;
+                }
+                z += pp[r * LDP + r] * u;
+                kg[r * LD + tid] = u;
+            }
+            o[r * step + tid] = from_f32<Tin>(z);
+        }
 }
 
-template <int D, int NT, typename Tin>
+template <int D, int NT, bool TC>
 cudaError_t run(const StepArgs &a, cudaStream_t st) {
-    constexpr uint32_t bytes = Smem<D, NT>::bytes(sizeof(Tin));
+    constexpr uint32_t bytes = TC ? Smem<D, NT>::TC_BYTES : Smem<D, NT>::SIMT_BYTES;
+    void (*kernel)(StepArgs) = TC ? step_tc_kernel<D, NT> : step_simt_kernel<D, NT>;
     if (bytes > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(step_kernel<D, NT, Tin>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
@@ -408,22 +646,22 @@ cudaError_t run(const StepArgs &a, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, step_kernel<D, NT, Tin>, a);
+    return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-template <int D, typename Tin>
+template <int D, bool TC>
 cudaError_t by_nodes(const StepArgs &a, cudaStream_t st) {
-    if (a.T <= 8) return run<D, 8, Tin>(a, st);
-    if (a.T <= 16) return run<D, 16, Tin>(a, st);
-    if (a.T <= 32) return run<D, 32, Tin>(a, st);
-    return run<D, 64, Tin>(a, st);
+    if (a.T <= 8) return run<D, 8, TC>(a, st);
+    if (a.T <= 16) return run<D, 16, TC>(a, st);
+    if (a.T <= 32) return run<D, 32, TC>(a, st);
+    return run<D, 64, TC>(a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_step(const StepArgs &a, cudaStream_t st) {
-    if (a.d == 128) return a.dtype == 0 ? by_nodes<128, __nv_bfloat16>(a, st) : by_nodes<128, float>(a, st);
-    return a.dtype == 0 ? by_nodes<64, __nv_bfloat16>(a, st) : by_nodes<64, float>(a, st);
+    if (a.d == 128) return a.dtype == 0 ? by_nodes<128, true>(a, st) : by_nodes<128, false>(a, st);
+    return a.dtype == 0 ? by_nodes<64, true>(a, st) : by_nodes<64, false>(a, st);
 }
 
 }  // namespace tree
