@@ -279,18 +279,22 @@ __global__ void __launch_bounds__(32 * Warps<D, NT>::ALL, resident<D, NT>()) ste
     // gamma: every round adds up twice as far a stretch of the paths, from one buffer to
     // the other; a warp its rows
     float *was = kg, *now = ki;
-    for (int k = 0; k < *rounds; ++k) {
+    const int n_rounds = *rounds;
+    for (int k = 0; k < n_rounds; ++k) {
+        int above[MINE];
+        Row<D> x[MINE];
+#pragma unroll
+        for (int n = 0; n < MINE; ++n) above[n] = ups[k * NT + warp + n * WARPS];
 #pragma unroll
         for (int n = 0; n < MINE; ++n) {
-            const int r = warp + n * WARPS, up = ups[k * NT + r];
-            Row<D> x = load_row<D>(was + r * LD, lane);
-            if (up >= 0) {
-                const Row<D> y = load_row<D>(was + up * LD, lane);
+            const int r = warp + n * WARPS;
+            x[n] = load_row<D>(was + r * LD, lane);
+            const Row<D> y = load_row<D>(was + (above[n] < 0 ? r : above[n]) * LD, lane);
 #pragma unroll
-                for (int c = 0; c < C; ++c) x.x[c] += y.x[c];
-            }
-            store_row<D>(now + r * LD, lane, x);
+            for (int c = 0; c < C; ++c) x[n].x[c] += above[n] < 0 ? 0.f : y.x[c];
         }
+#pragma unroll
+        for (int n = 0; n < MINE; ++n) store_row<D>(now + (warp + n * WARPS) * LD, lane, x[n]);
         __syncthreads();
         float *z = was;
         was = now;
@@ -367,6 +371,43 @@ __global__ void __launch_bounds__(32 * Warps<D, NT>::ALL, resident<D, NT>()) ste
         }
     }
 
+    // o_r = (q_r e^gamma_r) S + sum_j M_rj d_j with d_j = beta_j (v_j - (k_j e^gamma_j) S) and
+    // M (I + A) = P: along r's path M_rj = P_rj - sum_{i below j} M_ri A_ij, nearest first.
+    // A warp a node, a lane the nodes `lane` and `lane + 32`.  M replaces P.
+    __syncthreads();
+    {
+        int at[MINE];                                    // all of the warp's chains side by side
+        float m0[MINE], m1[MINE];
+        bool any = false;
+#pragma unroll
+        for (int n = 0; n < MINE; ++n) {
+            const int r = warp + n * WARPS;
+            at[n] = mask[r] ? r : -1;
+            any |= at[n] >= 0;
+            m0[n] = lane < NT ? pp[r * LDP + lane] : 0.f;
+            m1[n] = NT > 32 ? pp[r * LDP + lane + 32] : 0.f;
+        }
+        while (any) {
+            any = false;
+#pragma unroll
+            for (int n = 0; n < MINE; ++n) {
+                const int i = at[n] < 0 ? 0 : at[n];
+                float x = __shfl_sync(0xffffffffu, NT > 32 && i >= 32 ? m1[n] : m0[n], i & 31);
+                if (at[n] < 0) x = 0.f;                  // at its end
+                at[n] = at[n] < 0 || !n_rounds ? -1 : ups[i];
+                any |= at[n] >= 0;
+                // A's row i is 0 but for i's ancestors, and i
+                if (lane < NT) m0[n] -= lane == i ? 0.f : x * pa[i * LDP + lane];
+                if (NT > 32) m1[n] -= lane + 32 == i ? 0.f : x * pa[i * LDP + lane + 32];
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < MINE; ++n) {
+            const int r = warp + n * WARPS;
+            if (lane < NT) pp[r * LDP + lane] = mask[r] ? to_tf32(m0[n]) : 0.f;
+            if (NT > 32) pp[r * LDP + lane + 32] = mask[r] ? to_tf32(m1[n]) : 0.f;
+        }
+    }
     // The nodes' rows times the state.  Column group j's MMA column gq is S's column 4 gq + j of
     // the warp's 32.  The MMA wants channel c4 of four, columns 4 gq .. in lane 4 gq + c4;
     // the lanes load them as 8 c4 + gq, so that eight lanes read a line of 128 bytes (four
@@ -409,43 +450,6 @@ __global__ void __launch_bounds__(32 * Warps<D, NT>::ALL, resident<D, NT>()) ste
         if (mask[r]) vr[mt] = *reinterpret_cast<const uint4 *>(v + r * step + n0);
     }
     __syncthreads();
-    // o_r = (q_r e^gamma_r) S + sum_j M_rj d_j with d_j = beta_j (v_j - (k_j e^gamma_j) S) and
-    // M (I + A) = P: along r's path M_rj = P_rj - sum_{i below j} M_ri A_ij, nearest first.
-    // A warp a node, a lane the nodes `lane` and `lane + 32`.  M replaces P.
-    constexpr int AT_ONCE = MINE < 4 ? MINE : 4;         // nodes whose chains run side by side
-#pragma unroll
-    for (int n0_ = 0; n0_ < MINE; n0_ += AT_ONCE) {
-        int at[AT_ONCE];
-        float m0[AT_ONCE], m1[AT_ONCE];
-        bool any = false;
-#pragma unroll
-        for (int n = 0; n < AT_ONCE; ++n) {
-            const int r = warp + (n0_ + n) * WARPS;
-            at[n] = mask[r] ? r : -1;
-            any |= at[n] >= 0;
-            m0[n] = lane < NT ? pp[r * LDP + lane] : 0.f;
-            m1[n] = NT > 32 ? pp[r * LDP + lane + 32] : 0.f;
-        }
-        while (any) {
-            any = false;
-#pragma unroll
-            for (int n = 0; n < AT_ONCE; ++n) {
-                const int i = at[n];
-                if (i < 0) continue;
-                const float x = __shfl_sync(0xffffffffu, NT > 32 && i >= 32 ? m1[n] : m0[n], i & 31);
-                at[n] = *rounds ? ups[i] : -1;           // A's row i is 0 but for i's ancestors, and at i
-                any |= at[n] >= 0;
-                if (lane < NT && lane != i) m0[n] -= x * pa[i * LDP + lane];
-                if (NT > 32 && lane + 32 != i) m1[n] -= x * pa[i * LDP + lane + 32];
-            }
-        }
-#pragma unroll
-        for (int n = 0; n < AT_ONCE; ++n) {
-            const int r = warp + (n0_ + n) * WARPS;
-            if (lane < NT) pp[r * LDP + lane] = mask[r] ? to_tf32(m0[n]) : 0.f;
-            if (NT > 32) pp[r * LDP + lane + 32] = mask[r] ? to_tf32(m1[n]) : 0.f;
-        }
-    }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
         const int r = 8 * (mt * SPLIT + part) + gq;
