@@ -426,8 +426,8 @@ kda_status kda_mla_prefill(const void *q, const void *kv, const void *k_r, const
 
 uint64_t kda_mla_decode_workspace_size(int32_t B, int32_t H, int32_t dtype) {
     if (B <= 0 || H <= 0 || (dtype != KDA_BF16 && dtype != KDA_FP32)) return 0;
-    return dtype == KDA_BF16 ? kda::mla::decode_tc_workspace_bytes(H)
-                             : kda::mla::decode_simt_workspace_bytes(H);
+    return dtype == KDA_BF16 ? kda::mla::decode_tc_workspace_bytes(H, false)
+                             : kda::mla::decode_simt_workspace_bytes(H, false);
 }
 
 kda_status kda_mla_decode(const void *q, const void *cache, const int32_t *table,
@@ -462,8 +462,10 @@ kda_status kda_mla_decode(const void *q, const void *cache, const int32_t *table
 }
 
 uint64_t kda_mla_tree_decode_workspace_size(int32_t B, int32_t T, int32_t H, int32_t dtype) {
-    if (T <= 0 || T > kda::tree::MAX_NODES || H <= 0 || H > 65535) return 0;
-    return kda_mla_decode_workspace_size(B, T * H, dtype);
+    if (B <= 0 || T <= 0 || T > kda::tree::MAX_NODES || H <= 0 || H > 65535 || (dtype != KDA_BF16 && dtype != KDA_FP32))
+        return 0;
+    return dtype == KDA_BF16 ? kda::mla::decode_tc_workspace_bytes(T * H, true)
+                             : kda::mla::decode_simt_workspace_bytes(T * H, true);
 }
 
 kda_status kda_mla_tree_decode(const void *q, const void *cache, const int32_t *table,

@@ -50,9 +50,9 @@ cudaError_t launch_append(const AppendArgs &a, cudaStream_t st);
 cudaError_t launch_prefill_simt(const PrefillArgs &a, cudaStream_t st);
 cudaError_t launch_decode_simt(const DecodeArgs &a, cudaStream_t st);
 uint64_t prefill_simt_workspace_bytes(int32_t N, int64_t Tq, int32_t H);
-uint64_t decode_simt_workspace_bytes(int32_t H);
+uint64_t decode_simt_workspace_bytes(int32_t H, bool tree);
 cudaError_t launch_decode_tc(const DecodeArgs &a, cudaStream_t st);
-uint64_t decode_tc_workspace_bytes(int32_t H);
+uint64_t decode_tc_workspace_bytes(int32_t H, bool tree);
 cudaError_t launch_prefill_tc(const PrefillArgs &a, cudaStream_t st);
 uint64_t prefill_tc_workspace_bytes(int32_t N, int64_t Tq);
 

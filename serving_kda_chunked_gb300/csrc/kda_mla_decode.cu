@@ -112,7 +112,6 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-    const int h0 = blockIdx.x % p.groups * N, nh = min(N, p.H - h0);
 
     if (tid == 0) {
         for (int i = 0; i < 12; ++i) mbar_init(&full[i], i == 6 || i == 10 ? 8 : 1);
@@ -125,7 +124,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     fence_before_sync();
-    const Share share = find_share<TOK, OVER, THREADS, N, __nv_bfloat16>(p, *scratch);
+    const Share share = find_share<TOK, OVER, THREADS, N, __nv_bfloat16, TREE>(p, *scratch);
     fence_after_sync();
     const uint32_t tmem = warp_uniform(*tmem_slot);
     const uint32_t smb = warp_uniform(smem_addr(sm));
@@ -136,7 +135,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
     }
 
     if (share.busy && !forced) {
-        Walk<TOK, OVER> w;
+        Walk<TOK, OVER, N, TREE> w;
         w.start(p, share);
         if (warp == W_LOAD) {
             // ---- loads: the table is read 32 entries at a time; what a tile
@@ -152,18 +151,19 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
             do {
                 if (seg > 0) ok = wait_or_fail(q_empty, (seg - 1) & 1, fail);
                 if (!ok) break;
+                const Item it = item_of<N>(share.o, w.b);
                 if (elect_one()) {
                     mbar_arrive_expect_tx(q_full, CHUNKS * N * 128);
-                    tma4(smb + L::Q, &p.tm_q, 0, h0, 0, w.b, q_full);
+                    tma4(smb + L::Q, &p.tm_q, 0, it.h0, 0, it.b, q_full);
                 }
                 __syncwarp();
                 ++seg;
-                const int32_t *tab = p.table + (int64_t)w.b * p.max_pages;
+                const int32_t *tab = p.table + (int64_t)it.b * p.max_pages;
                 uint64_t nodes = 0;                                        // that are not padding
                 int64_t front = 0;
                 if constexpr (TREE) {
-                    front = seq_front(p, w.b);
-                    const int32_t *par = p.parents + (int64_t)w.b * p.T;
+                    front = seq_len(p, it.b);
+                    const int32_t *par = p.parents + (int64_t)it.b * p.T;
                     uint64_t a, c;
                     tree::all_ancestors(par, p.T, lane, a, c);
                     const uint32_t lo = __ballot_sync(0xffffffffu, a != 0), hi = __ballot_sync(0xffffffffu, c != 0);
@@ -311,9 +311,11 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                 uint64_t sees = 0, sees32 = 0;
                 uint32_t pad = 0;
                 int64_t front = 0;
+                const Item it = item_of<N>(share.o, w.b);
+                const int h0 = it.h0, nh = min(N, p.H - h0);
                 if constexpr (TREE) {
-                    const int32_t *par = p.parents + (int64_t)w.b * p.T;
-                    front = seq_front(p, w.b);
+                    const int32_t *par = p.parents + (int64_t)it.b * p.T;
+                    front = seq_len(p, it.b);
                     tree::all_ancestors(par, p.T, lane, sees, sees32);
                     const uint32_t lo = __ballot_sync(0xffffffffu, sees != 0), hi = __ballot_sync(0xffffffffu, sees32 != 0);
                     const int t = min((h0 + n0 + lane) / p.heads, p.T - 1);
@@ -495,7 +497,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                     ca[wt] = whole ? inverse_of(sum) : 1.f;
                     if (whole) {
                         if (p.lse && n0 + wt < nh)
-                            p.lse[(int64_t)w.b * p.H + h0 + n0 + wt] = lse_of(top, sum);
+                            p.lse[(int64_t)it.b * p.H + h0 + n0 + wt] = lse_of(top, sum);
                     } else {
                         float2 *to = reinterpret_cast<float2 *>(p.stat + slot * N * 2) + n0 + wt;
                         *to = make_float2(top, sum);
@@ -520,7 +522,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                                 if (pad >> (c + e) & 1) y[e] = 0.f;
                         }
                         if (whole) {
-                            __nv_bfloat16 *to = (__nv_bfloat16 *)p.o + ((int64_t)w.b * p.H + h0 + n) * LATENT + ch;
+                            __nv_bfloat16 *to = (__nv_bfloat16 *)p.o + ((int64_t)it.b * p.H + h0 + n) * LATENT + ch;
 #pragma unroll
                             for (int e = 0; e < EC; ++e)
                                 if (n + e < nh) to[e * LATENT] = __float2bfloat16_rn(y[e] * ca[c + e]);
@@ -545,7 +547,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
 }
 
 // Heads a CTA: the fewest that hold all H, else 64 a group.
-SplitPlan plan_of(int32_t H, int nsm) { return split_plan(H, H <= 16 ? 16 : (H <= 32 ? 32 : 64), nsm); }
+SplitPlan plan_of(int32_t H, int nsm, bool tree) { return split_plan(H, H <= 16 ? 16 : (H <= 32 ? 32 : 64), nsm, tree); }
 
 template <int N, bool TREE>
 cudaError_t run(const DecodeArgs &a, const SplitPlan &pl, cudaStream_t st) {
@@ -580,8 +582,8 @@ cudaError_t run(const DecodeArgs &a, const SplitPlan &pl, cudaStream_t st) {
 
 }  // namespace
 
-uint64_t decode_tc_workspace_bytes(int32_t H) {
-    return ws_bytes(plan_of(H, MAX_CTAS));     // the most any device takes
+uint64_t decode_tc_workspace_bytes(int32_t H, bool tree) {
+    return ws_bytes(plan_of(H, MAX_CTAS, tree));     // the most any device takes
 }
 
 cudaError_t launch_decode_tc(const DecodeArgs &a, cudaStream_t st) {
@@ -589,7 +591,7 @@ cudaError_t launch_decode_tc(const DecodeArgs &a, cudaStream_t st) {
     const cudaError_t e = sm_count(&nsm);
     if (e != cudaSuccess) return e;
     if (nsm > MAX_CTAS) nsm = MAX_CTAS;
-    const SplitPlan pl = plan_of(a.H, nsm);
+    const SplitPlan pl = plan_of(a.H, nsm, a.parents != nullptr);
     if (a.parents) switch (pl.N) {
     case 16: return run<16, true>(a, pl, st);
     case 32: return run<32, true>(a, pl, st);

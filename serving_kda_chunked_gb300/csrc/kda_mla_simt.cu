@@ -346,26 +346,27 @@ __global__ void __launch_bounds__(DTHREADS, 2) decode_simt_kernel(const SplitPar
     float *fs = ps + TT * HG;               // rescale factor per head
     __shared__ ShareScratch<DTHREADS> scratch;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int h0 = blockIdx.x % p.groups * HG, nh = min(HG, p.H - h0);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Share share = find_share<TT, OVER, DTHREADS, HG, float>(p, scratch);
+    const Share share = find_share<TT, OVER, DTHREADS, HG, float, TREE>(p, scratch);
     if (tid == 0) p.status[blockIdx.x] = 0;
     if (!share.busy) return;
-    Walk<TT, OVER> w;
+    Walk<TT, OVER, HG, TREE> w;
     w.start(p, share);
     const int shift = 31 - __clz(p.page);
     do {
-        const int32_t *tab = p.table + (int64_t)w.b * p.max_pages;
+        const Item it = item_of<HG>(share.o, w.b);
+        const int h0 = it.h0, nh = min(HG, p.H - h0);
+        const int32_t *tab = p.table + (int64_t)it.b * p.max_pages;
         __syncthreads();
         for (int e = tid; e < HG * ROW / 4; e += DTHREADS) {
             const int r = e / (ROW / 4), c = e % (ROW / 4) * 4;
-            store4(qs + r * LDR + c, r < nh ? load4(q + ((int64_t)w.b * p.H + h0 + r) * ROW + c)
+            store4(qs + r * LDR + c, r < nh ? load4(q + ((int64_t)it.b * p.H + h0 + r) * ROW + c)
                                             : make_float4(0.f, 0.f, 0.f, 0.f));
         }
         float m = -CUDART_INF_F, l = 0.f;   // of head `warp`, this lane's tokens
-        const int32_t *par = TREE ? p.parents + (int64_t)w.b * p.T : nullptr;
-        const int64_t front = TREE ? seq_front(p, w.b) : 0;
+        const int32_t *par = TREE ? p.parents + (int64_t)it.b * p.T : nullptr;
+        const int64_t front = TREE ? seq_len(p, it.b) : 0;
         const int node = TREE ? (h0 + warp) / p.heads : 0;
         const uint64_t sees = TREE && node < p.T ? tree::ancestors(par, node) : 0;
         float2 acc[HG][2] = {};             // channels 4 (tid % 128) .., tokens of half tid / 128
@@ -467,7 +468,7 @@ __global__ void __launch_bounds__(DTHREADS, 2) decode_simt_kernel(const SplitPar
         const int64_t slot = w.slot();
         if (lane == 0 && warp < nh) {
             if (whole) {
-                if (p.lse) p.lse[(int64_t)w.b * p.H + h0 + warp] = lse_of(m, l);
+                if (p.lse) p.lse[(int64_t)it.b * p.H + h0 + warp] = lse_of(m, l);
             } else {
                 *reinterpret_cast<float2 *>(p.stat + (slot * HG + warp) * 2) = make_float2(m, l);
             }
@@ -482,7 +483,7 @@ __global__ void __launch_bounds__(DTHREADS, 2) decode_simt_kernel(const SplitPar
 #pragma unroll
         for (int h = 0; h < HG; ++h)
             if (h / 4 == half && h < nh) {
-                float *to = whole ? (float *)p.o + ((int64_t)w.b * p.H + h0 + h) * LATENT
+                float *to = whole ? (float *)p.o + ((int64_t)it.b * p.H + h0 + h) * LATENT
                                   : p.part + (slot * HG + h) * LATENT;
                 const float4 x = load4(rows + h * LDR + ch);
                 const float f = fs[h];
@@ -494,7 +495,7 @@ __global__ void __launch_bounds__(DTHREADS, 2) decode_simt_kernel(const SplitPar
 
 }  // namespace
 
-uint64_t decode_simt_workspace_bytes(int32_t H) { return ws_bytes(split_plan(H, HG, DEC_CTAS)); }
+uint64_t decode_simt_workspace_bytes(int32_t H, bool tree) { return ws_bytes(split_plan(H, HG, DEC_CTAS, tree)); }
 
 uint64_t prefill_simt_workspace_bytes(int32_t N, int64_t Tq, int32_t H) {
     const int parts = prefill_parts(N, Tq, H);
@@ -535,7 +536,7 @@ cudaError_t launch_decode_simt(const DecodeArgs &a, cudaStream_t st) {
         e = cudaFuncSetAttribute(a.parents ? decode_simt_kernel<true> : decode_simt_kernel<false>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, DEC_FLOATS * (int)sizeof(float));
     if (e != cudaSuccess) return e;
-    const SplitPlan pl = split_plan(a.H, HG, 2 * nsm < DEC_CTAS ? 2 * nsm : DEC_CTAS);
+    const SplitPlan pl = split_plan(a.H, HG, 2 * nsm < DEC_CTAS ? 2 * nsm : DEC_CTAS, a.parents != nullptr);
     SplitParams p;
     split_params(p, a, pl);
     return launch_split<HG, float>(a.parents ? decode_simt_kernel<true> : decode_simt_kernel<false>, p, pl, DTHREADS, DEC_FLOATS * sizeof(float), a.ws, st,

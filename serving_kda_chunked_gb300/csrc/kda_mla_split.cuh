@@ -8,6 +8,14 @@
 // join_kernel adds those up in order of the shares.  Heads come in groups of N;
 // CTA x works for group x % groups on share x / groups, so that the CTAs that
 // read the same tokens for different heads do so at about the same time.
+//
+// Drafted trees (TREE): nothing is computed for groups of rows that are padding.  Where there
+// are such, the groups differ in work, and every (sequence, group) is an item of its own in one
+// list, in that order; what is said of sequences holds for items then, and groups of
+// padding alone are items of length 0.  Where there are none, all is as above: the groups
+// stay in step, and read a tile from L2 at the same time.  32 heads, each way in us:
+//   64 trees of 8 nodes over up to 8192 tokens, full 192 (as items 223), ragged 201 (as items 152)
+//   8 trees of 48 over up to 32,768, full 537 (597), ragged 530 (464)
 #pragma once
 
 #include "kda_mla.cuh"
@@ -33,9 +41,9 @@ __device__ __forceinline__ float lse_of(float top, float sum) {
     return sum == 0.f ? -CUDART_INF_F : (top + log2f(sum)) * CUDART_LN2_F;
 }
 
-// What the share of a CTA starts in: sequence b, which the starts of the shares
-// first .. last cut; b < 0 marks an idle CTA.
-struct Meta { int32_t b, first, last; };
+// What the share of a CTA starts in: sequence (or item) b, which the starts of the shares
+// first .. last cut; b < 0 marks an idle CTA.  groups: of the call's order.
+struct Meta { int32_t b, first, last, groups; };
 
 struct SplitParams {
     const int32_t *table, *seq_lens;
@@ -46,19 +54,50 @@ struct SplitParams {
     float *part, *stat;        // two slots per CTA: [N][512], and [N][2] (maximum in log2 units, sum)
     int32_t B, H, n_pages, page, max_pages, groups;
     float scale_log2;
-    const int32_t *parents;    // drafted trees: [B, T], and the heads of a node (else NULL, 0, 0)
+    const int32_t *parents;    // drafted trees: [sequences, T], the heads of a node
     int32_t T, heads;
 };
 
-// Tokens in front of a sequence's tree, and all of its tokens (without trees the same).
-__device__ __forceinline__ int64_t seq_front(const SplitParams &p, int b) {
+// Tokens of a sequence; with a tree, in front of it.
+__device__ __forceinline__ int64_t seq_len(const SplitParams &p, int b) {
     const int64_t cap = (int64_t)p.max_pages * p.page, n = p.seq_lens[b];
     return n < 0 ? 0 : (n > cap ? cap : n);
 }
-__device__ __forceinline__ int64_t seq_len(const SplitParams &p, int b) {
-    const int64_t cap = (int64_t)p.max_pages * p.page, n = seq_front(p, b) + p.T;
-    return n > cap ? cap : n;
+// How the work is listed: CTA x works for group x % groups; a sequence is `items` items.
+struct Order { int groups, items; };
+// Item i: which sequence, and its first row of H.
+struct Item { int b, h0; };
+template <int N> __device__ __forceinline__ Item item_of(Order o, int i) {
+    return {i / o.items, (i % o.items + (int)blockIdx.x % o.groups) * N};
 }
+// Nodes of a tree up to the last that may not be padding.
+__device__ __forceinline__ int tree_nodes(const SplitParams &p, int b) {
+    const int32_t *par = p.parents + (int64_t)b * p.T;
+    int n = p.T;
+    for (; n > 0; --n) {
+        const int up = par[n - 1];
+        if (up >= -1 && up < n - 1) break;
+    }
+    return n;
+}
+// Tokens that items read; what is known of the sequence of the last one is kept.
+template <bool TREE, int N> struct Lengths {
+    int b = -1, rows = 0;
+    int64_t len = 0;
+    __device__ __forceinline__ int64_t of(const SplitParams &p, Order o, int i) {
+        if (!TREE) return seq_len(p, i);
+        const Item it = item_of<N>(o, i);
+        if (it.b != b) {
+            const int64_t cap = (int64_t)p.max_pages * p.page;
+            const int n = tree_nodes(p, it.b);
+            b = it.b;
+            rows = n * p.heads;
+            len = seq_len(p, b) + n;
+            len = len > cap ? cap : len;
+        }
+        return it.h0 < rows ? len : 0;
+    }
+};
 template <int TOK> __device__ __forceinline__ int64_t tiles_of(int64_t len) { return (len + TOK - 1) / TOK; }
 template <int TOK, int OVER> __device__ __forceinline__ int64_t units_of(int64_t len) {
     return len > 0 ? tiles_of<TOK>(len) + OVER : 0;
@@ -94,20 +133,27 @@ struct Shares {
 // end one, and then a unit a tile: without them the CTA with the most sequences
 // ended 9 us after the others (48 sequences of up to 9001, 128 heads: 93 us in
 // all, with one, two and three units 88, 86 and 86).
-struct Share { int64_t g0, g1, t00; int b0; bool busy; };
-template <int THREADS> struct ShareScratch { int64_t sums[THREADS / 32], t0, t1; int b; };
+struct Share { int64_t g0, g1, t00, len0; Order o; int b0, items; bool busy; };
+template <int THREADS> struct ShareScratch { int64_t sums[THREADS / 32], t0, t1, len; int b; };
 
 // Finds the share (all THREADS threads; ends with a barrier), records it for
 // the join, and writes the outputs of sequences with nothing cached.
-template <int TOK, int OVER, int THREADS, int N, typename To>
+template <int TOK, int OVER, int THREADS, int N, typename To, bool TREE>
 __device__ __forceinline__ Share find_share(const SplitParams &p, ShareScratch<THREADS> &sh) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int group = blockIdx.x % p.groups, c = blockIdx.x / p.groups, C0 = gridDim.x / p.groups;
-    const int h0 = group * N, nh = min(N, p.H - h0);
-    const int per = (p.B + THREADS - 1) / THREADS;
-    const int b_lo = min(p.B, tid * per), b_hi = min(p.B, b_lo + per);
+    Order o = {p.groups, 1};
+    if (TREE && p.groups > 1) {                // any group that some sequence has only padding for?
+        bool even = true;
+        for (int b = tid; b < p.B; b += THREADS) even &= tree_nodes(p, b) * p.heads > (p.groups - 1) * N;
+        const int order = __shfl_sync(0xffffffffu, __syncthreads_and(even) ? 0 : 1, 0);
+        if (order) o = {1, p.groups};
+    }
+    const int c = blockIdx.x / o.groups, C0 = gridDim.x / o.groups, items = p.B * o.items;
+    const int per = (items + THREADS - 1) / THREADS;
+    const int b_lo = min(items, tid * per), b_hi = min(items, b_lo + per);
     int64_t mine = 0;
-    for (int b = b_lo; b < b_hi; ++b) mine += units_of<TOK, OVER>(seq_len(p, b));
+    Lengths<TREE, N> lens;
+    for (int b = b_lo; b < b_hi; ++b) mine += units_of<TOK, OVER>(lens.of(p, o, b));
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -124,7 +170,13 @@ __device__ __forceinline__ Share find_share(const SplitParams &p, ShareScratch<T
         T += sh.sums[w];
     }
     Share s;
-    const int C = (int)(T < C0 ? T : C0);
+    s.o = o;
+    s.items = items;
+    // the shares of several groups of 64 have two units at least: with one the partial results of 64 rows each
+    // cost more than the second tile (one tree of 16 nodes, 32 heads, over 700 tokens: 23.3 us,
+    // here 18.3, with three units 17.9, four 19.4; four trees of 8 25.7, 20.3, 20.8, 21.8)
+    const int64_t cap = TREE && N == 64 && p.groups > 1 ? (T + 1) / 2 : T;
+    const int C = (int)(cap < C0 ? cap : C0);
     s.busy = c < C;
     const Shares cuts(T, C > 0 ? C : 1);
     s.g0 = s.busy ? cuts.start(c) : 0;
@@ -133,8 +185,9 @@ __device__ __forceinline__ Share find_share(const SplitParams &p, ShareScratch<T
         int64_t at = excl;
         int b = b_lo;
         for (; b < b_hi; ++b) {
-            const int64_t n = units_of<TOK, OVER>(seq_len(p, b));
+            const int64_t len = lens.of(p, o, b), n = units_of<TOK, OVER>(len);
             if (s.g0 < at + n) {
+                sh.len = len;
                 sh.t0 = at + OVER;
                 sh.t1 = at + n;
                 sh.b = b;
@@ -143,9 +196,11 @@ __device__ __forceinline__ Share find_share(const SplitParams &p, ShareScratch<T
             at += n;
         }
     }
-    for (int b = c; b < p.B; b += C0) {
-        if (seq_len(p, b) > 0) continue;
-        const int64_t at = (int64_t)b * p.H + h0;
+    for (int b = c; b < items && c < C0; b += C0) {
+        if (lens.of(p, o, b) > 0) continue;
+        const Item it = item_of<N>(o, b);
+        const int nh = min(N, p.H - it.h0);
+        const int64_t at = (int64_t)it.b * p.H + it.h0;
         for (int e = tid; e < nh * (LATENT / 4); e += THREADS)
             store4((To *)p.o + at * LATENT + 4 * e, make_float4(0.f, 0.f, 0.f, 0.f));
         if (p.lse && tid < nh) p.lse[at + tid] = -CUDART_INF_F;
@@ -153,9 +208,10 @@ __device__ __forceinline__ Share find_share(const SplitParams &p, ShareScratch<T
     __syncthreads();
     s.b0 = sh.b;
     s.t00 = sh.t0;
+    s.len0 = sh.len;
     if (tid == THREADS - 64) {                 // of a warp that has nothing to do yet
-        Meta m = {-1, 0, 0};
-        if (s.busy && s.b0 >= 0) m = {s.b0, cuts.after(s.t00), cuts.after(sh.t1 - 1) - 1};
+        Meta m = {-1, 0, 0, o.groups};
+        if (s.busy && s.b0 >= 0) m = {s.b0, cuts.after(s.t00), cuts.after(sh.t1 - 1) - 1, o.groups};
         p.meta[blockIdx.x] = m;
     }
     // no tile: the share lies in a sequence's OVER (or lengths changed under the kernel)
@@ -165,24 +221,26 @@ __device__ __forceinline__ Share find_share(const SplitParams &p, ShareScratch<T
 
 // The share as segments: sequence b, its tiles [lo, hi); `at` is the unit of
 // the sequence's first tile.  Every warp walks them with the same arithmetic.
-template <int TOK, int OVER> struct Walk {
+template <int TOK, int OVER, int N, bool TREE> struct Walk {
     int64_t at, len, lo, hi;
     int b;
-    __device__ __forceinline__ void open(const SplitParams &p, const Share &s, int b_, int64_t at_, int64_t g) {
-        len = seq_len(p, b_);
+    Lengths<TREE, N> lens;
+    __device__ __forceinline__ void open(const Share &s, int b_, int64_t len_, int64_t at_, int64_t g) {
+        len = len_;
         b = b_; at = at_;
         lo = g > at ? g - at : 0;
         const int64_t n = tiles_of<TOK>(len);
         hi = s.g1 - at < n ? s.g1 - at : n;
     }
-    __device__ __forceinline__ void start(const SplitParams &p, const Share &s) { open(p, s, s.b0, s.t00, s.g0); }
+    __device__ __forceinline__ void start(const SplitParams &p, const Share &s) { open(s, s.b0, s.len0, s.t00, s.g0); }
     __device__ __forceinline__ bool next(const SplitParams &p, const Share &s) {
         const int64_t to = at + tiles_of<TOK>(len);
         if (to + OVER >= s.g1) return false;
         int n = b + 1;
-        while (n < p.B && seq_len(p, n) == 0) ++n;
-        if (n >= p.B) return false;            // lengths changed under the kernel
-        open(p, s, n, to + OVER, to + OVER);
+        int64_t more = 0;
+        while (n < s.items && (more = lens.of(p, s.o, n)) == 0) ++n;
+        if (n >= s.items) return false;            // lengths changed under the kernel
+        open(s, n, more, to + OVER, to + OVER);
         return true;
     }
     __device__ __forceinline__ bool whole() const { return lo == 0 && hi == tiles_of<TOK>(len); }
@@ -209,20 +267,21 @@ __global__ void __launch_bounds__(256, 4) join_kernel(const SplitParams p, int c
         st = __syncthreads_or(st);
         if (tid == 0) *header = st ? FAIL_TIMEOUT : 0;
     }
-    const int cta = blockIdx.y + p.groups;                  // shares 1 .. of every group
+    const int cta = blockIdx.y + (p.parents ? 1 : p.groups);   // shares 1 .. of every group
     if (cta >= ctas) return;
-    const int group = cta % p.groups, c = cta / p.groups;
     const Meta m = p.meta[cta];
+    const int groups = m.groups, group = cta % groups, c = cta / groups;
     if (m.b < 0 || c < m.first || c > m.last) return;
     const int pieces = m.last - m.first + 2;                // of shares first - 1 .. last
-    const int nh = min(N, p.H - group * N);
-    const int slot0 = 2 * ((m.first - 1) * p.groups + group);   // of piece i: slot0 + 2 groups i, + 1 for the first
-    auto slot_of = [&](int i) { return slot0 + 2 * p.groups * i + (i == 0); };
+    const int items = groups == p.groups ? 1 : p.groups, seq = m.b / items, h0 = (m.b % items + group) * N;
+    const int nh = min(N, p.H - h0);
+    const int slot0 = 2 * ((m.first - 1) * groups + group);     // of piece i: slot0 + 2 groups i, + 1 for the first
+    auto slot_of = [&](int i) { return slot0 + 2 * groups * i + (i == 0); };
     const int block = (c - m.first) * gridDim.x + blockIdx.x, blocks = (pieces - 1) * gridDim.x;
     auto write = [&](int item, float4 acc, float top, float sum, int bad) {
         if (__any_sync(0xffffffffu, bad)) return;           // a share that gave up: o stays as it is
         const float r = inverse_of(sum);
-        const int64_t at = (int64_t)m.b * p.H + group * N + (item >> 2);
+        const int64_t at = (int64_t)seq * p.H + h0 + (item >> 2);
         store4((To *)p.o + at * LATENT + (item & 3) * 128 + 4 * lane,
                make_float4(acc.x * r, acc.y * r, acc.z * r, acc.w * r));
         if (p.lse && (item & 3) == 0 && lane == 0) p.lse[at] = lse_of(top, sum);
@@ -315,11 +374,12 @@ inline uint64_t ws_stat(const SplitPlan &s) { return ws_meta(s) + ((uint64_t)s.c
 inline uint64_t ws_part(const SplitPlan &s) { return ws_stat(s) + (uint64_t)s.ctas * 2 * s.N * 8; }
 inline uint64_t ws_bytes(const SplitPlan &s) { return ws_part(s) + (uint64_t)s.ctas * 2 * s.N * LATENT * 4; }
 
-inline SplitPlan split_plan(int32_t H, int N, int ctas) {
+inline SplitPlan split_plan(int32_t H, int N, int ctas, bool tree) {
     SplitPlan s;
     s.N = N;
     s.groups = (H + N - 1) / N;
     s.ctas = s.groups * (ctas / s.groups > 0 ? ctas / s.groups : 1);
+    if (tree && s.ctas < ctas) s.ctas = ctas;   // as items, all work
     return s;
 }
 
@@ -354,7 +414,7 @@ cudaError_t launch_split(void (*kernel)(Params, More...), const Params &p, const
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p, more...);
     if (e != cudaSuccess) return e;
-    const int joins = s.ctas - s.groups;
+    const int joins = s.ctas - (p.parents ? 1 : s.groups);
     // two items a warp where one boundary cuts a sequence: with one, twice the
     // blocks come in more waves (48 sequences of up to 9001, 128 heads: 86 us, 84)
     cfg.gridDim = dim3(N / 4, (unsigned)(joins > 0 ? joins : 1));
