@@ -8,8 +8,8 @@
 // HBM.  A CTA owns 64 columns of a head, 16 rows x 4 columns a thread in registers; two
 // warps share 32 columns and exchange one partial sum of S^T k a token.  All that a token
 // needs comes to shared memory eight tokens at a time, so that no load stands in the chain
-// from token to token.  Measured, 256 sequences, 32 heads, D = 128: 157 us for one token a
-// sequence, 164 for two, 215 for four, 271 for eight (6.9, 6.5, 5.0, 4.0 TB/s; a decode
+// from token to token.  Measured, 256 sequences, 32 heads, D = 128: 158 us for one token a
+// sequence, 167 for two, 193 for four, 248 for eight (6.8, 6.5, 5.7, 4.5 TB/s; a decode
 // step 157 each); with every token's loads a token ahead of it 161, 181, 258, 390.
 #include "kda_tree.cuh"
 
@@ -18,6 +18,7 @@ namespace tree {
 namespace {
 
 constexpr int THREADS = 128;                 // 64 columns
+constexpr int AHEAD = 304;                   // CTAs
 constexpr int BLOCK = 8;                     // tokens whose inputs are in shared memory at a time
 static_assert(THREADS == 16 * BLOCK, "a thread brings in four of a token's 64 values");
 
@@ -43,6 +44,18 @@ __global__ void __launch_bounds__(THREADS, 4) commit_kernel(const CommitArgs p) 
     const int n = end0 ? __ffs((int)end0) - 1 : (end1 ? 31 + __ffs((int)end1) : 64);
     if (n == 0) return;                                     // nothing accepted: the state stays as it is
 
+    // a state that half a round of CTAs later will want, to L2: the memory goes on while
+    // these here compute (batch of 256 166 us, here 159; a round ahead 158, two 164)
+    if (tid == 0 && blockIdx.x % PARTS == 0) {
+        const int64_t later = (int64_t)bh + AHEAD / PARTS;
+        if (later < (int64_t)p.B * p.H) {
+            const int b2 = (int)(later / p.H), h2 = (int)(later % p.H);
+            const int64_t slot2 = p.slots ? p.slots[b2] : b2;
+            const int next = p.path[(int64_t)b2 * p.T];
+            if (next >= 0 && next < p.T && slot2 >= 0 && slot2 < p.P)
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" :: "l"(p.S + (slot2 * p.H + h2) * (D * D)), "r"(D * D * 4) : "memory");
+        }
+    }
     // two warps share 32 columns, half the rows each
     const int half = warp & 1, rg = lane >> 3, cl = lane & 7;
     const int col = blockIdx.x % PARTS * 64 + 32 * (warp >> 1) + 4 * cl, row0 = half * (D / 2) + 4 * rg;
