@@ -507,7 +507,8 @@ uint64_t kda_mla_decode_workspace_size(int32_t B, int32_t H, int32_t dtype);
  *     committed tokens; any other value makes it a padding node, and so are
  *     the nodes behind one.  Several nodes may have -1.  A node's path is itself and its
  *     ancestors, in the order of their index.
- *   - Padding nodes' inputs may hold anything; their outputs are 0 (lse -inf).
+ *   - Padding nodes' inputs may hold anything; their outputs are 0 (lse -inf).  Those of
+ *     other nodes are finite: a NaN in one may reach other nodes of its sequence.
  *   - Neither parents nor slots nor lengths are read on the host, and no value
  *     in them leads outside the buffers.  Equal inputs give equal bits.
  */
@@ -526,9 +527,10 @@ uint64_t kda_mla_decode_workspace_size(int32_t B, int32_t H, int32_t dtype);
  *   dk, dv     64 or 128, dk == dv
  *
  * Row (b, i) of o is what kda_decode_step gives for node i after the decode
- * steps of its ancestors, started from the state.  bf16: the product of the nodes'
- * rows with the state takes both rounded to tf32 (11 bits), sums are float32;
- * fp32: float32 throughout.  B = 0 is a valid no-op.
+ * steps of its ancestors, started from the state.  bf16: products take their
+ * factors (the nodes' rows, the state, the deltas) rounded to tf32, 11 bits; sums and
+ * gates are float32.  fp32: float32 throughout.  o must not overlap the other
+ * tensors.  B = 0 is a valid no-op.
  */
 kda_status kda_tree_step(const void *q, const void *k, const void *v,
                          const float *g, const float *beta, const float *S,

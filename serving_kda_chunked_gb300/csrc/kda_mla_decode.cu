@@ -25,6 +25,17 @@
 //
 // Work split and join: kda_mla_split.cuh, one share per SM.
 //
+// Trees of drafted tokens (TREE) are the same with more rows, in groups of 64, and a mask
+// in the tiles that hold nodes.  Each group reads every tile for itself, and shared memory bounds
+// that: the MMAs of a tile read 147 KB for the scores (rows and queries) and 96 KB for the
+// output, and 74 KB come in, 2480 cycles at 128 bytes of the 2750 that a tile takes (the
+// issuing thread waits for 600 of them, for data or weights).  More rows a tile, or 128
+// tokens at a time, would read less, but 64 rows of queries and two stages fill shared memory.
+// Tried: the halves of a stage loaded and released apart (198 us for the 64 trees below, 204),
+// a tile brought in once for two and four groups by TMA multicast (204, 216).  Measured, 32
+// heads: 64 ragged trees of up to 8 nodes over up to 8192 tokens 164 us, 8 trees of 48 nodes
+// over up to 32,768 tokens 740 us = 0.9 PFLOP/s.
+//
 // Warps 0-3 and 4-7: softmax and epilogue of half the heads each; warp 8: MMA
 // issue; warp 9: loads.
 #include "kda_mla_split.cuh"

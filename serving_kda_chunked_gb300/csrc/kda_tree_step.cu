@@ -8,19 +8,32 @@
 //   u_r  = beta_r (v_r - (k_r e^gamma_r) S) - sum_i A_ri u_i
 //   o_r  = (q_r e^gamma_r) S + sum_i P_ri u_i
 // so that S meets all 2 T rows k_r e^gamma_r and q_r e^gamma_r in one product, is
-// read once and not written; siblings share what is above them.  No exponent is
-// above 0, however strong the gates are.
+// read once and not written; siblings share what is above them.
 //
-// What bounds it: S is 64 KB a head (D = 128) and is read once, HBM.  One CTA of
-// D threads per (sequence, head); a warp owns 32 of S's columns.  bf16 inputs:
-// the product runs as m16n8k8 tf32 MMAs whose 16 rows are 8 nodes' k and q rows
-// (S and the rows are rounded to 11 bits there, as the prefill's fp16 operands are;
-// sums are float32, and the committed state never passes through it).  The MMA's
-// columns and K steps are permuted so that a thread's S fragments are 16-byte
-// loads straight from global memory.  With T <= 16 that is 16 or 32 rows: too few
-// for a 128-row tcgen05.mma, which would want S in shared memory first.  float32
-// inputs: the same loads, FMAs.
+// What bounds it: S is 64 KB a head (D = 128) and is read once: HBM.  One CTA per (sequence,
+// head), all of whose products are m16n8k8 tf32 MMAs (bf16 inputs).  With T nodes those
+// have 2 T rows at most, 16 for the usual eight nodes: an eighth of a 128-row tcgen05.mma,
+// which would want S in shared memory first, where two CTAs an SM would fit in place of six.
+//   1. gamma by doubling: every round adds up twice as far a stretch of the paths;
+//   2. A and P as one product of the rows k e^gamma, q e^gamma with k e^-gamma.  Where gamma
+//      falls below -100 (log2), pair by pair in float32 instead, no exponent above 0;
+//   3. M with M (I + A) = P, along each node's path;
+//   4. the 2 T rows times S; d_j = beta_j (v_j - (k_j e^gamma_j) S);  o = (q e^gamma) S + M d.
+// Operands are rounded to tf32's 11 bits, as many as the prefill's fp16 operands have;
+// gates, sums and the state are float32, and what a commit writes never passes through here.
+//
+// Measured, 32 heads, D = 128: 256 sequences with 8 nodes 109 us, with one 96 (5.6 TB/s; L1
+// wavefronts, then latency, take over before HBM does); with chains of up to 8 in a pool 105;
+// 32 sequences with 64 nodes 89 us, where two CTAs an SM spend 45,000 cycles each in
+// phases 1 to 4 and in the loads before them, a quarter of it in 4.
+// On the way, both cases: gates and A, P by FMAs and shuffles 127 and 137; the state's lines
+// read by four lanes each of eight rows (L1 wavefronts at 67%) 118 and 110; M's chains four
+// at a time 105 and 103.
+//
+// float32 inputs: pair by pair, FMAs, and the deltas one node after the other.
 #include "kda_tree.cuh"
+
+#include <mutex>
 
 namespace kda {
 namespace tree {
@@ -98,7 +111,7 @@ template <int D> __device__ __forceinline__ Row<D> unpack(const Raw<D> &a) {
 constexpr float LOG2E = 1.4426950408889634f;
 
 // Shared memory.  bf16: rows k e^gamma, q e^gamma and k e^-gamma (before them gamma, after the
-// product the deltas d); A and P, then M; masks, betas, parents.  With 64 nodes A and P take
+// product the deltas d); A and P, then M; masks, betas, who is above whom.  With 64 nodes A and P take
 // the place of k e^-gamma, so that two CTAs fit an SM.  fp32: rows k e^gamma and q e^gamma,
 // after the product deltas and outputs; A and P; masks, betas; up to 16 nodes the inputs.
 template <int D, int NT> struct Smem {       // NT: nodes, a multiple of 8
@@ -109,11 +122,11 @@ template <int D, int NT> struct Smem {       // NT: nodes, a multiple of 8
     static constexpr bool OVER = NT == 64, STAGED = NT <= 16;
     static constexpr uint32_t AP_BYTES = NT * LDP * 8;
     // bf16 (the deltas' rows are longer, and may reach into those of q)
-    static constexpr uint32_t KG = 0, QG = NT * LD * 4, KI = 2 * QG, AP = OVER ? KI : 3 * QG, MASK = AP + (OVER && AP_BYTES < QG ? QG : AP_BYTES), BETA = MASK + NT * 8,
-                              UPS = BETA + NT * 4, TC_BYTES = UPS + 6 * NT + 16;
+    static constexpr uint32_t KG = 0, QG = NT * LD * 4, KI = 2 * QG, AP = OVER ? KI : 3 * QG, MASK = AP + (OVER && AP_BYTES < QG ? QG : AP_BYTES),
+                              BETA = MASK + NT * 8, UPS = BETA + NT * 4, TC_BYTES = UPS + 6 * NT + 16;
     // fp32
-    static constexpr uint32_t SQG = NT * LDS * 4, SAP = 2 * SQG, SMASK = SAP + AP_BYTES, SBETA = SMASK + NT * 8, ROWS = SBETA + NT * 4,
-                              SIMT_BYTES = ROWS + (STAGED ? NT * D * 16 : 0);
+    static constexpr uint32_t SQG = NT * LDS * 4, SAP = 2 * SQG, SMASK = SAP + AP_BYTES, SBETA = SMASK + NT * 8,
+                              ROWS = SBETA + NT * 4, SIMT_BYTES = ROWS + (STAGED ? NT * D * 16 : 0);
 };
 // Warps a CTA: one for every 32 columns; from 32 nodes on (D = 64: 16) two, which share the nodes.
 template <int D, int NT> struct Warps { static constexpr int COLS = D / 32, SPLIT = NT >= 32 || (D == 64 && NT == 16) ? 2 : 1, ALL = COLS * SPLIT; };
@@ -637,8 +650,18 @@ cudaError_t run(const StepArgs &a, cudaStream_t st) {
     constexpr uint32_t bytes = TC ? Smem<D, NT>::TC_BYTES : Smem<D, NT>::SIMT_BYTES;
     void (*kernel)(StepArgs) = TC ? step_tc_kernel<D, NT> : step_simt_kernel<D, NT>;
     if (bytes > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        static std::mutex mu;
+        static bool ready[64] = {false};
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
         if (e != cudaSuccess) return e;
+        if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+        std::lock_guard<std::mutex> lock(mu);
+        if (!ready[dev]) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+            if (e != cudaSuccess) return e;
+            ready[dev] = true;
+        }
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((int64_t)a.B * a.H));

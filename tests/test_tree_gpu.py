@@ -5,10 +5,11 @@ Tolerances.  Step, with unit keys and queries and w = the largest norm of a colu
 state: a product of a row with a column is a sum of at most 128 terms whose magnitudes add
 up to w or less.  bf16: both factors are rounded to 11 bits, 2^-11 each at most,
 so a product is off by d = 2^-10 w; an output takes one such product and the errors of its
-path's deltas, each d and what it takes over from those above it, times the weights P and A
-between them, which for unit vectors of random directions in 64 or 128 dimensions stay
-below 1/2 or so (a path of n nodes: below d (1 + n) in all); its rounding is 2^-8 of its
-value at most.  Pair sums and their exponentials are float32.
+path's deltas, each d and what it takes over from those above it, times the weights between
+them, which for unit vectors of random directions in 64 or 128 dimensions stay below 1/2
+or so (a path of n nodes: below d (1 + n) in all); its rounding is 2^-8 of its value at
+most.  The weights and the deltas are rounded to 11 bits in their product as well: 2^-10 of
+a delta (below w or so, as it goes into the state) times a weight below 1/2, which n d holds.
     |o - ref| <= 2^-8 |ref| + 2^-10 w (1 + n)
 fp32: a float32 sum of 128 terms is off by about sqrt(128) 2^-24 of their magnitude, 12 2^-24;
 exponentials, the other sums and the path's deltas as above:
