@@ -170,16 +170,9 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                 __syncwarp();
                 ++seg;
                 const int32_t *tab = p.table + (int64_t)it.b * p.max_pages;
-                uint64_t nodes = 0;                                        // that are not padding
-                int64_t front = 0;
-                if constexpr (TREE) {
-                    front = seq_len(p, it.b);
-                    const int32_t *par = p.parents + (int64_t)it.b * p.T;
-                    uint64_t a, c;
-                    tree::all_ancestors(par, p.T, lane, a, c);
-                    const uint32_t lo = __ballot_sync(0xffffffffu, a != 0), hi = __ballot_sync(0xffffffffu, c != 0);
-                    nodes = (uint64_t)hi << 32 | lo;
-                }
+                uint64_t nodes = 0;                                        // that are not padding, once known
+                bool known = false;
+                const int64_t front = TREE ? seq_len(p, it.b) : 0;
                 // first row / 8 of this lane's box of 32, and of the next 32
                 auto boxes = [&](int64_t i) {
                     const int64_t t = i * TOK + ((int64_t)lane << psh);
@@ -206,6 +199,12 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                     if (left < TOK) mask &= (1ull << left) - 1;
                     if constexpr (TREE) {
                         const int64_t d = i * TOK - front;                 // node of the tile's first token
+                        if (d > -64 && !known) {
+                            uint64_t a, c;
+                            tree::all_ancestors(p.parents + (int64_t)it.b * p.T, p.T, lane, a, c);
+                            nodes = (uint64_t)__ballot_sync(0xffffffffu, c != 0) << 32 | __ballot_sync(0xffffffffu, a != 0);
+                            known = true;
+                        }
                         if (d >= 0) mask &= d < 64 ? nodes >> d : 0ull;
                         else if (d > -64) mask &= nodes << -d | ((1ull << -d) - 1);
                     }
