@@ -43,7 +43,7 @@ __device__ __forceinline__ float lse_of(float top, float sum) {
 
 // What the share of a CTA starts in: sequence (or item) b, which the starts of the shares
 // first .. last cut; b < 0 marks an idle CTA.  groups: of the call's order.
-struct Meta { int32_t b, first, last, groups; };
+struct __align__(16) Meta { int32_t b, first, last, groups; };
 
 struct SplitParams {
     const int32_t *table, *seq_lens;
@@ -67,7 +67,8 @@ __device__ __forceinline__ int64_t seq_len(const SplitParams &p, int b) {
 struct Order { int groups, items; };
 // Item i: which sequence, and its first row of H.
 struct Item { int b, h0; };
-template <int N> __device__ __forceinline__ Item item_of(Order o, int i) {
+template <bool TREE, int N> __device__ __forceinline__ Item item_of(Order o, int i) {
+    if (!TREE) return {i, (int)blockIdx.x % o.groups * N};
     return {i / o.items, (i % o.items + (int)blockIdx.x % o.groups) * N};
 }
 // Nodes of a tree up to the last that may not be padding.
@@ -86,7 +87,7 @@ template <bool TREE, int N> struct Lengths {
     int64_t len = 0;
     __device__ __forceinline__ int64_t of(const SplitParams &p, Order o, int i) {
         if (!TREE) return seq_len(p, i);
-        const Item it = item_of<N>(o, i);
+        const Item it = item_of<TREE, N>(o, i);
         if (it.b != b) {
             const int64_t cap = (int64_t)p.max_pages * p.page;
             const int n = tree_nodes(p, it.b);
@@ -144,7 +145,10 @@ __device__ __forceinline__ Share find_share(const SplitParams &p, ShareScratch<T
     Order o = {p.groups, 1};
     if (TREE && p.groups > 1) {                // any group that some sequence has only padding for?
         bool even = true;
-        for (int b = tid; b < p.B; b += THREADS) even &= tree_nodes(p, b) * p.heads > (p.groups - 1) * N;
+        for (int b = tid; b < p.B; b += THREADS) {
+            asm volatile("prefetch.global.L1 [%0];" :: "l"(p.seq_lens + b));
+            even &= tree_nodes(p, b) * p.heads > (p.groups - 1) * N;
+        }
         const int order = __shfl_sync(0xffffffffu, __syncthreads_and(even) ? 0 : 1, 0);
         if (order) o = {1, p.groups};
     }
@@ -152,8 +156,13 @@ __device__ __forceinline__ Share find_share(const SplitParams &p, ShareScratch<T
     const int per = (items + THREADS - 1) / THREADS;
     const int b_lo = min(items, tid * per), b_hi = min(items, b_lo + per);
     int64_t mine = 0;
+    bool empty = false;
     Lengths<TREE, N> lens;
-    for (int b = b_lo; b < b_hi; ++b) mine += units_of<TOK, OVER>(lens.of(p, o, b));
+    for (int b = b_lo; b < b_hi; ++b) {
+        const int64_t n = units_of<TOK, OVER>(lens.of(p, o, b));
+        mine += n;
+        empty |= n == 0;
+    }
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -162,7 +171,9 @@ __device__ __forceinline__ Share find_share(const SplitParams &p, ShareScratch<T
     }
     if (lane == 31) sh.sums[warp] = incl;
     if (tid == 0) sh.b = -1;
-    __syncthreads();
+    bool empties = true;
+    if (TREE) empties = __syncthreads_or(empty);             // the loop below reads much for nothing
+    else __syncthreads();
     int64_t T = 0, excl = incl - mine;
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) {
@@ -196,9 +207,9 @@ __device__ __forceinline__ Share find_share(const SplitParams &p, ShareScratch<T
             at += n;
         }
     }
-    for (int b = c; b < items && c < C0; b += C0) {
+    for (int b = c; empties && b < items && c < C0; b += C0) {
         if (lens.of(p, o, b) > 0) continue;
-        const Item it = item_of<N>(o, b);
+        const Item it = item_of<TREE, N>(o, b);
         const int nh = min(N, p.H - it.h0);
         const int64_t at = (int64_t)it.b * p.H + it.h0;
         for (int e = tid; e < nh * (LATENT / 4); e += THREADS)
@@ -256,7 +267,7 @@ template <int TOK, int OVER, int N, bool TREE> struct Walk {
 // every eighth piece a warp.  Pieces are added in a fixed order.  What counts is
 // how many blocks fit beside one another: with 102 registers a thread instead of
 // 64 one sequence takes 1% less, 48 sequences 6% more.
-template <int N, typename To>
+template <int N, typename To, bool TREE>
 __global__ void __launch_bounds__(256, 4) join_kernel(const SplitParams p, int ctas, int32_t *header) {
     __shared__ float4 buf[8][32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -267,13 +278,14 @@ __global__ void __launch_bounds__(256, 4) join_kernel(const SplitParams p, int c
         st = __syncthreads_or(st);
         if (tid == 0) *header = st ? FAIL_TIMEOUT : 0;
     }
-    const int cta = blockIdx.y + (p.parents ? 1 : p.groups);   // shares 1 .. of every group
+    const int cta = blockIdx.y + (TREE ? 1 : p.groups);     // shares 1 .. of every group
     if (cta >= ctas) return;
     const Meta m = p.meta[cta];
-    const int groups = m.groups, group = cta % groups, c = cta / groups;
+    const int groups = TREE ? m.groups : p.groups, group = cta % groups, c = cta / groups;
     if (m.b < 0 || c < m.first || c > m.last) return;
     const int pieces = m.last - m.first + 2;                // of shares first - 1 .. last
-    const int items = groups == p.groups ? 1 : p.groups, seq = m.b / items, h0 = (m.b % items + group) * N;
+    const int items = TREE && groups != p.groups ? p.groups : 1;
+    const int seq = TREE ? m.b / items : m.b, h0 = ((TREE ? m.b % items : 0) + group) * N;
     const int nh = min(N, p.H - h0);
     const int slot0 = 2 * ((m.first - 1) * groups + group);     // of piece i: slot0 + 2 groups i, + 1 for the first
     auto slot_of = [&](int i) { return slot0 + 2 * groups * i + (i == 0); };
@@ -420,8 +432,8 @@ cudaError_t launch_split(void (*kernel)(Params, More...), const Params &p, const
     cfg.gridDim = dim3(N / 4, (unsigned)(joins > 0 ? joins : 1));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, join_kernel<N, To>, (const SplitParams &)p, s.ctas,
-                              static_cast<int32_t *>(ws));
+    return cudaLaunchKernelEx(&cfg, p.parents ? join_kernel<N, To, true> : join_kernel<N, To, false>,
+                              (const SplitParams &)p, s.ctas, static_cast<int32_t *>(ws));
 }
 
 }  // namespace mla
