@@ -17,18 +17,20 @@
 //   1. gamma by doubling: every round adds up twice as far a stretch of the paths;
 //   2. A and P as one product of the rows k e^gamma, q e^gamma with k e^-gamma.  Where gamma
 //      falls below -100 (log2), pair by pair in float32 instead, no exponent above 0;
-//   3. M with M (I + A) = P, along each node's path;
+//   3. M with M (I + A) = P by tiles of 8 nodes, from the last to the first;
 //   4. the 2 T rows times S; d_j = beta_j (v_j - (k_j e^gamma_j) S);  o = (q e^gamma) S + M d.
 // Operands are rounded to tf32's 11 bits, as many as the prefill's fp16 operands have;
 // gates, sums and the state are float32, and what a commit writes never passes through here.
 //
-// Measured, 32 heads, D = 128: 256 sequences with 8 nodes 109 us, with one 96 (5.6 TB/s; L1
-// wavefronts, then latency, take over before HBM does); with chains of up to 8 in a pool 105;
-// 32 sequences with 64 nodes 89 us, where two CTAs an SM spend 45,000 cycles each in
-// phases 1 to 4 and in the loads before them, a quarter of it in 4.
-// On the way, both cases: gates and A, P by FMAs and shuffles 127 and 137; the state's lines
-// read by four lanes each of eight rows (L1 wavefronts at 67%) 118 and 110; M's chains four
-// at a time 105 and 103.
+// Measured, 32 heads, D = 128: 256 sequences with chains of 8 nodes 102 us, with one 91 (5.9 TB/s;
+// L1 wavefronts, then latency, take over before HBM does); with up to 8 in a pool 105; 32
+// sequences with 64 nodes 82 us in trees three wide, 91 in chains, where two CTAs an SM spend
+// 40,000 cycles each: loads 7,000, phase 1 5,500, 2 9,000, 3 4,000, 4 14,000, issuing half the time.
+// On the way, with 8 and with 64 nodes: gates and A, P by FMAs and shuffles 127 and 137; the
+// state's lines read by four lanes each of eight rows (L1 wavefronts at 67%) 118 and 110; M node
+// by node along the paths 105 and 89, and 108 and 185 for chains (a third of all instructions).
+// Tried: what a later CTA reads asked into L2, 64 nodes 87 to 89; 1, 2 or 8 unrolled steps of 4 with
+// 4 to 9 CTAs an SM in phase 4, 8 nodes: 106 to 112.
 //
 // float32 inputs: pair by pair, FMAs, and the deltas one node after the other.
 #include "kda_tree.cuh"
@@ -56,10 +58,14 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], float a0, float a1, floa
                    "r"(__float_as_uint(a3)), "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
 }
 
+__device__ __forceinline__ float2 load2(const float *p) { return *reinterpret_cast<const float2 *>(p); }
 __device__ __forceinline__ void copy16(void *dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" :: "l"(p)); }
+__device__ __forceinline__ void prefetch_bulk(const void *p, int bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" :: "l"(p), "r"(bytes) : "memory");
+}
 
 // A row of bf16 as a lane loads it.
 template <int D> struct Raw { uint32_t x[D / 64]; };
@@ -115,13 +121,13 @@ constexpr float LOG2E = 1.4426950408889634f;
 // the place of k e^-gamma, so that two CTAs fit an SM.  fp32: rows k e^gamma and q e^gamma,
 // after the product deltas and outputs; A and P; masks, betas; up to 16 nodes the inputs.
 template <int D, int NT> struct Smem {       // NT: nodes, a multiple of 8
-    static constexpr int LD = D + 4;         // eight rows' reads of four channels meet different banks
-    static constexpr int LDU = D + 8;        // the deltas' rows: four rows' reads of 32 columns do
+    static constexpr int LD = D + 8;         // four rows' reads of eight channels meet different banks
+    static constexpr int LDU = D + 4;        // the deltas' rows: every other of eight rows' reads of 32 columns do
     static constexpr int LDS = D + 16;       // fp32: two rows' reads of 16 channels do
-    static constexpr int LDP = NT + 4;       // A and P of node r: pa[r * LDP + i], pp[r * LDP + i]
+    static constexpr int LDA = NT + 4, LDP = NT + 8;   // A and P of node r: pa[r * LDA + i], pp[r * LDP + i]
     static constexpr bool OVER = NT == 64, STAGED = NT <= 16;
-    static constexpr uint32_t AP_BYTES = NT * LDP * 8;
-    // bf16 (the deltas' rows are longer, and may reach into those of q)
+    static constexpr uint32_t AP_BYTES = NT * (LDA + LDP) * 4;
+    // bf16
     static constexpr uint32_t KG = 0, QG = NT * LD * 4, KI = 2 * QG, AP = OVER ? KI : 3 * QG, MASK = AP + (OVER && AP_BYTES < QG ? QG : AP_BYTES),
                               BETA = MASK + NT * 8, UPS = BETA + NT * 4, TC_BYTES = UPS + 6 * NT + 16;
     // fp32
@@ -139,7 +145,7 @@ template <int D, int NT> struct Warps { static constexpr int COLS = D / 32, SPLI
 template <int D, int NT, int LD, int WARPS, typename Tin>
 __device__ __forceinline__ void pair_by_pair(const Tin *q, const Tin *k, const float *g, int64_t in, int64_t gs, bool scalar_gate,
                                              const uint64_t *mask, const float *beta, float *kg, float *qg, float *pa, float *pp) {
-    constexpr int LDP = Smem<D, NT>::LDP, C = D / 32;
+    constexpr int LDA = Smem<D, NT>::LDA, LDP = Smem<D, NT>::LDP, C = D / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int r = warp; r < NT; r += WARPS) {
         uint64_t m = mask[r];
@@ -149,7 +155,7 @@ __device__ __forceinline__ void pair_by_pair(const Tin *q, const Tin *k, const f
             kr = load_row<D>(k + r * in, lane);
             qr = load_row<D>(q + r * in, lane);
         }
-        for (int i = lane; i < NT; i += 32) pa[r * LDP + i] = pp[r * LDP + i] = 0.f;
+        for (int i = lane; i < NT; i += 32) pa[r * LDA + i] = pp[r * LDP + i] = 0.f;
         __syncwarp();
         while (m) {
             int at[4];
@@ -194,8 +200,10 @@ __device__ __forceinline__ void pair_by_pair(const Tin *q, const Tin *k, const f
             sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 2);
             sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 1);
             const int u = lane >> 3, i = u == 0 ? at[0] : (u == 1 ? at[1] : (u == 2 ? at[2] : at[3]));
-            if ((lane & 3) == 0 && i >= 0)
-                (lane & 4 ? pp : pa)[r * LDP + i] = lane & 4 ? sum[0] : beta[r] * sum[0];
+            if ((lane & 3) == 0 && i >= 0) {
+                if (lane & 4) pp[r * LDP + i] = sum[0];
+                else pa[r * LDA + i] = beta[r] * sum[0];
+            }
         }
 #pragma unroll
         for (int c = 0; c < C; ++c) {
@@ -216,11 +224,11 @@ template <int D, int NT>
 __global__ void __launch_bounds__(32 * Warps<D, NT>::ALL, resident<D, NT>()) step_tc_kernel(const StepArgs p) {
     using L = Smem<D, NT>;
     using Tin = __nv_bfloat16;
-    constexpr int LD = L::LD, LDU = L::LDU, LDP = L::LDP, C = D / 32;
+    constexpr int LD = L::LD, LDU = L::LDU, LDA = L::LDA, LDP = L::LDP, C = D / 32;
     constexpr int SPLIT = Warps<D, NT>::SPLIT, WARPS = Warps<D, NT>::ALL, THREADS = 32 * WARPS;
     extern __shared__ __align__(16) uint8_t sm[];
     float *kg = reinterpret_cast<float *>(sm + L::KG), *qg = reinterpret_cast<float *>(sm + L::QG), *ki = reinterpret_cast<float *>(sm + L::KI);
-    float *pa = reinterpret_cast<float *>(sm + L::AP), *pp = pa + NT * LDP;
+    float *pa = reinterpret_cast<float *>(sm + L::AP), *pp = pa + NT * LDA;
     uint64_t *mask = reinterpret_cast<uint64_t *>(sm + L::MASK);
     float *beta = reinterpret_cast<float *>(sm + L::BETA);
     int8_t *ups = reinterpret_cast<int8_t *>(sm + L::UPS);  // [round][node]: the node 2^round above
@@ -286,49 +294,70 @@ __global__ void __launch_bounds__(32 * Warps<D, NT>::ALL, resident<D, NT>()) ste
         if (lane == 0) *rounds = n;
     }
     if (tid < T) beta[tid] = p.beta[bt0 + (int64_t)tid * p.H];
-    if (tid == 0) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" :: "l"(S), "r"(D * D * 4) : "memory");
+    if (tid == 0) prefetch_bulk(S, D * D * 4);
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     // gamma: every round adds up twice as far a stretch of the paths, from one buffer to
-    // the other; a warp its rows
+    // the other; a warp its rows.  A row that stood still for two rounds is in both.
     float *was = kg, *now = ki;
     const int n_rounds = *rounds;
-    for (int k = 0; k < n_rounds; ++k) {
-        int above[MINE];
-        Row<D> x[MINE];
+    Row<D> gm[MINE];
+    int above[MINE];
 #pragma unroll
-        for (int n = 0; n < MINE; ++n) above[n] = ups[k * NT + warp + n * WARPS];
+    for (int n = 0; n < MINE; ++n) {
+        gm[n] = load_row<D>(kg + (warp + n * WARPS) * LD, lane);
+        above[n] = 0;
+    }
+    for (int k = 0; k < n_rounds; ++k) {
+        bool moved[MINE];
+        Row<D> y[MINE];
 #pragma unroll
         for (int n = 0; n < MINE; ++n) {
-            const int r = warp + n * WARPS;
-            x[n] = load_row<D>(was + r * LD, lane);
-            const Row<D> y = load_row<D>(was + (above[n] < 0 ? r : above[n]) * LD, lane);
-#pragma unroll
-            for (int c = 0; c < C; ++c) x[n].x[c] += above[n] < 0 ? 0.f : y.x[c];
+            moved[n] = above[n] >= 0;
+            if (moved[n]) above[n] = ups[k * NT + warp + n * WARPS];
         }
 #pragma unroll
-        for (int n = 0; n < MINE; ++n) store_row<D>(now + (warp + n * WARPS) * LD, lane, x[n]);
-        __syncthreads();
+        for (int n = 0; n < MINE; ++n)
+            y[n] = above[n] >= 0 ? load_row<D>(was + above[n] * LD, lane) : Row<D>{};
+#pragma unroll
+        for (int n = 0; n < MINE; ++n) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) gm[n].x[c] += y[n].x[c];
+            if (moved[n] && k + 1 < n_rounds) store_row<D>(now + (warp + n * WARPS) * LD, lane, gm[n]);
+        }
+        if (k + 1 < n_rounds) __syncthreads();
         float *z = was;
         was = now;
         now = z;
     }
-    Row<D> gm[MINE];                                     // in log2 units
     bool far = false;
 #pragma unroll
     for (int n = 0; n < MINE; ++n) {
         const int r = warp + n * WARPS;
-        gm[n] = load_row<D>(was + r * LD, lane);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            gm[n].x[c] = mask[r] ? gm[n].x[c] * LOG2E : 0.f;
-            far |= !(gm[n].x[c] >= -RANGE);              // (or a gate that is not a number)
+            gm[n].x[c] = mask[r] ? gm[n].x[c] * LOG2E : 0.f; // in log2 units
+            far |= !(fabsf(gm[n].x[c]) <= RANGE);       // (or a gate that is not a number)
         }
     }
     const int gq = lane >> 2, c4 = lane & 3, cols = 32 * (warp / SPLIT);
+    // A warp's tiles of 8 nodes.  With one each, the two warps of a scheduler (w, w + 4) have
+    // 9 of the 36 products of two tiles.
+    constexpr int TILES = (NT / 8 + WARPS - 1) / WARPS;
+    const auto tile_of = [&](int t) { return NT == 64 && WARPS == 8 && warp >= 4 ? 11 - warp : warp + t * WARPS; };
+    float pr[TILES][NT / 8][4] = {};                     // A and P; then in 0 and 1 row gq, columns 8 j + 2 c4 and the next
     if (__syncthreads_or(far)) {
         pair_by_pair<D, NT, LD, WARPS>(q, k, g, step, gs, p.scalar_gate, mask, beta, kg, qg, pa, pp);
         __syncthreads();
+#pragma unroll
+        for (int t = 0; t < TILES; ++t)
+#pragma unroll
+            for (int j = 0; j < NT / 8; ++j)
+                if (tile_of(t) < NT / 8) {
+                    const float2 x = load2(pp + (8 * tile_of(t) + gq) * LDP + 8 * j + 2 * c4);
+                    pr[t][j][0] = x.x;
+                    pr[t][j][1] = x.y;
+                }
     } else {
 #pragma unroll
         for (int n = 0; n < MINE; ++n) {
@@ -348,28 +377,26 @@ __global__ void __launch_bounds__(32 * Warps<D, NT>::ALL, resident<D, NT>()) ste
         }
         __syncthreads();
         // A and P of 8 nodes a warp: e^(gamma_r - gamma_i) is the product of the two rows' factors.
-        constexpr int TILES = (NT / 8 + WARPS - 1) / WARPS;
-        float pr[TILES][NT / 8][4] = {};
+        // Channels 8 s + 2 c4 and the next one are the MMA's c4 and c4 + 4, so that one load has both.
 #pragma unroll
         for (int t = 0; t < TILES; ++t) {
-            const int tile = warp + t * WARPS;
+            const int tile = tile_of(t);
             if (tile >= NT / 8) break;
 #pragma unroll 4
             for (int s = 0; s < D / 8; ++s) {
-                const float *a = kg + (8 * tile + gq) * LD + 8 * s + c4, *c = qg + (8 * tile + gq) * LD + 8 * s + c4;
-                const float a0 = a[0], a1 = c[0], a2 = a[4], a3 = c[4];
+                const float2 a = load2(kg + (8 * tile + gq) * LD + 8 * s + 2 * c4), c = load2(qg + (8 * tile + gq) * LD + 8 * s + 2 * c4);
 #pragma unroll
                 for (int j = 0; j < NT / 8; ++j)
                     if (j <= tile) {                     // nodes see earlier ones only
-                        const float *x = ki + (8 * j + gq) * LD + 8 * s + c4;
-                        mma_tf32(pr[t][j], a0, a1, a2, a3, x[0], x[4]);
+                        const float2 x = load2(ki + (8 * j + gq) * LD + 8 * s + 2 * c4);
+                        mma_tf32(pr[t][j], a.x, c.x, a.y, c.y, x.x, x.y);
                     }
             }
         }
         if constexpr (L::OVER) __syncthreads();
 #pragma unroll
         for (int t = 0; t < TILES; ++t) {
-            const int tile = warp + t * WARPS;
+            const int tile = tile_of(t);
             if (tile >= NT / 8) break;
             const int r = 8 * tile + gq;
             const uint64_t m = mask[r];
@@ -378,49 +405,14 @@ __global__ void __launch_bounds__(32 * Warps<D, NT>::ALL, resident<D, NT>()) ste
             for (int j = 0; j < NT / 8; ++j) {           // zeros where r does not see a node
                 const int i = 8 * j + 2 * c4;
                 const bool s0 = m >> i & 1, s1 = m >> (i + 1) & 1;
-                *reinterpret_cast<float2 *>(pa + r * LDP + i) = make_float2(s0 ? br * pr[t][j][0] : 0.f, s1 ? br * pr[t][j][1] : 0.f);
-                *reinterpret_cast<float2 *>(pp + r * LDP + i) = make_float2(s0 ? pr[t][j][2] : 0.f, s1 ? pr[t][j][3] : 0.f);
+                *reinterpret_cast<float2 *>(pa + r * LDA + i) = make_float2(s0 ? br * pr[t][j][0] : 0.f, s1 ? br * pr[t][j][1] : 0.f);
+                pr[t][j][0] = s0 ? pr[t][j][2] : 0.f;
+                pr[t][j][1] = s1 ? pr[t][j][3] : 0.f;
+                pr[t][j][2] = pr[t][j][3] = 0.f;
             }
         }
     }
 
-    // o_r = (q_r e^gamma_r) S + sum_j M_rj d_j with d_j = beta_j (v_j - (k_j e^gamma_j) S) and
-    // M (I + A) = P: along r's path M_rj = P_rj - sum_{i below j} M_ri A_ij, nearest first.
-    // A warp a node, a lane the nodes `lane` and `lane + 32`.  M replaces P.
-    __syncthreads();
-    {
-        int at[MINE];                                    // all of the warp's chains side by side
-        float m0[MINE], m1[MINE];
-        bool any = false;
-#pragma unroll
-        for (int n = 0; n < MINE; ++n) {
-            const int r = warp + n * WARPS;
-            at[n] = mask[r] ? r : -1;
-            any |= at[n] >= 0;
-            m0[n] = lane < NT ? pp[r * LDP + lane] : 0.f;
-            m1[n] = NT > 32 ? pp[r * LDP + lane + 32] : 0.f;
-        }
-        while (any) {
-            any = false;
-#pragma unroll
-            for (int n = 0; n < MINE; ++n) {
-                const int i = at[n] < 0 ? 0 : at[n];
-                float x = __shfl_sync(0xffffffffu, NT > 32 && i >= 32 ? m1[n] : m0[n], i & 31);
-                if (at[n] < 0) x = 0.f;                  // at its end
-                at[n] = at[n] < 0 || !n_rounds ? -1 : ups[i];
-                any |= at[n] >= 0;
-                // A's row i is 0 but for i's ancestors, and i
-                if (lane < NT) m0[n] -= lane == i ? 0.f : x * pa[i * LDP + lane];
-                if (NT > 32) m1[n] -= lane + 32 == i ? 0.f : x * pa[i * LDP + lane + 32];
-            }
-        }
-#pragma unroll
-        for (int n = 0; n < MINE; ++n) {
-            const int r = warp + n * WARPS;
-            if (lane < NT) pp[r * LDP + lane] = mask[r] ? to_tf32(m0[n]) : 0.f;
-            if (NT > 32) pp[r * LDP + lane + 32] = mask[r] ? to_tf32(m1[n]) : 0.f;
-        }
-    }
     // The nodes' rows times the state.  Column group j's MMA column gq is S's column 4 gq + j of
     // the warp's 32.  The MMA wants channel c4 of four, columns 4 gq .. in lane 4 gq + c4;
     // the lanes load them as 8 c4 + gq, so that eight lanes read a line of 128 bytes (four
@@ -428,14 +420,85 @@ __global__ void __launch_bounds__(32 * Warps<D, NT>::ALL, resident<D, NT>()) ste
     constexpr int MT = NT / 8 / SPLIT;
     const int part = warp % SPLIT;                       // this warp's tiles of 8 nodes: part, part + SPLIT, ...
     const int from = 8 * c4 + gq;
-    const float *Sl = S + (lane >> 3) * D + cols + 4 * (lane & 7);
-    float acc[MT][4][4] = {};
-#pragma unroll(MT > 2 ? 2 : 4)
-    for (int s = 0; s < D / 16; ++s) {
-        float4 y[4];
+    const float *Sl = S + 2 * (lane >> 3) * D + cols + 4 * (lane & 7);
+    constexpr bool PIPE = MT > 2;                        // enough products to load the next lines behind
+    float4 y[4];
+    if constexpr (PIPE) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = load4(Sl + (16 * s + 4 * j) * D);
-        float f[4][4];                                   // [channel 16 s + 4 j + c4][column]
+        for (int j = 0; j < 4; ++j) y[j] = load4(Sl + (j / 2 * 8 + j % 2) * D);
+    }
+
+    // o_r = (q_r e^gamma_r) S + sum_j M_rj d_j with d_j = beta_j (v_j - (k_j e^gamma_j) S) and
+    // M (I + A) = P.  Within a tile of 8 nodes one column comes after the other: one tile alone is
+    // solved so, of several the inverses of I + A (in place of A's), with which P's columns are
+    // multiplied from the last tile to the first; M A's other tiles come off P on the way.  All
+    // factors are taken as two tf32 numbers (P's and M's two fill the MMA's 16 rows), which keeps
+    // what float32 has.
+    __syncthreads();
+    const auto solve = [&](int J, float &x0, float &x1) {        // row gq, columns 2 c4 and the next: X (I + A_JJ)^-1
+        float2 a[8];
+#pragma unroll
+        for (int c = 1; c < 8; ++c) a[c] = load2(pa + (8 * J + c) * LDA + 8 * J + 2 * c4);
+#pragma unroll
+        for (int c = 7; c > 0; --c) {
+            const float m = __shfl_sync(0xffffffffu, c & 1 ? x1 : x0, (lane & 28) + c / 2);
+            if (2 * c4 < c) x0 -= m * a[c].x;
+            if (2 * c4 + 1 < c) x1 -= m * a[c].y;
+        }
+    };
+    const auto times = [&](float (&y)[4], float (&z)[4], float h0, float h1, float l0, float l1, int J, int j) {      // y + z += rows times A_Jj
+        const float *b = pa + (8 * J + 2 * c4) * LDA + 8 * j + gq;
+        const float b0 = b[0], b1 = b[LDA], y0 = to_tf32(b0), y1 = to_tf32(b1);
+        mma_tf32(y, h0, l0, h1, l1, y0, y1);
+        mma_tf32(z, h0, l0, h1, l1, to_tf32(b0 - y0), to_tf32(b1 - y1));
+    };
+    if constexpr (NT > 8) {
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) {
+            const int tile = tile_of(t);
+            if (tile >= NT / 8) break;
+            float x0 = gq == 2 * c4 ? 1.f : 0.f, x1 = gq == 2 * c4 + 1 ? 1.f : 0.f;
+            solve(tile, x0, x1);
+            __syncwarp();
+            *reinterpret_cast<float2 *>(pa + (8 * tile + gq) * LDA + 8 * tile + 2 * c4) = make_float2(x0, x1);
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) {
+        const int tile = tile_of(t);
+        if (tile >= NT / 8) break;
+        const int r = 8 * tile + gq;
+        const bool on = mask[r] != 0;
+#pragma unroll
+        for (int J = NT / 8 - 1; J >= 0; --J) {
+            if (J > tile) continue;
+            float x0 = pr[t][J][0] + pr[t][J][2], x1 = pr[t][J][1] + pr[t][J][3];
+            float h0, h1, l0, l1;
+            if constexpr (NT == 8) {
+                if (n_rounds) solve(J, x0, x1);          // a node has a parent
+            } else {
+                h0 = to_tf32(x0); h1 = to_tf32(x1); l0 = to_tf32(x0 - h0); l1 = to_tf32(x1 - h1);
+                float y[4] = {}, z[4] = {};
+                times(y, z, h0, h1, l0, l1, J, J);
+                x0 = (y[0] + y[2]) + (z[0] + z[2]);
+                x1 = (y[1] + y[3]) + (z[1] + z[3]);
+            }
+            h0 = on ? to_tf32(x0) : 0.f; h1 = on ? to_tf32(x1) : 0.f;
+            *reinterpret_cast<float2 *>(pp + r * LDP + 8 * J + 2 * c4) = make_float2(h0, h1);
+            l0 = to_tf32(x0 - h0); l1 = to_tf32(x1 - h1);
+#pragma unroll
+            for (int j = J - 1; j >= 0; --j) times(pr[t][j], pr[t][j], -h0, -h1, -l0, -l1, J, j);
+        }
+    }
+    float acc[MT][4][4] = {};
+#pragma unroll(MT > 2 ? 1 : 4)
+    for (int s = 0; s < D / 16; ++s) {
+        if constexpr (!PIPE) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = load4(Sl + (16 * s + j / 2 * 8 + j % 2) * D);
+        }
+        float f[4][4];                                   // [channel 16 s + 8 (j / 2) + 2 c4 + j % 2][column]
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             f[j][0] = to_tf32(__shfl_sync(0xffffffffu, y[j].x, from));
@@ -443,14 +506,19 @@ __global__ void __launch_bounds__(32 * Warps<D, NT>::ALL, resident<D, NT>()) ste
             f[j][2] = to_tf32(__shfl_sync(0xffffffffu, y[j].z, from));
             f[j][3] = to_tf32(__shfl_sync(0xffffffffu, y[j].w, from));
         }
+        if (PIPE && s + 1 < D / 16) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = load4(Sl + (16 * (s + 1) + j / 2 * 8 + j % 2) * D);
+        }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            const int at = (8 * (mt * SPLIT + part) + gq) * LD + 16 * s + c4;
-            const float *a = kg + at, *c = qg + at;
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < 2; ++t) {
+                const int at = (8 * (mt * SPLIT + part) + gq) * LD + 16 * s + 8 * t + 2 * c4;
+                const float2 a = load2(kg + at), c = load2(qg + at);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) mma_tf32(acc[mt][j], a[8 * t], c[8 * t], a[8 * t + 4], c[8 * t + 4], f[2 * t][j], f[2 * t + 1][j]);
+                for (int j = 0; j < 4; ++j) mma_tf32(acc[mt][j], a.x, c.x, a.y, c.y, f[2 * t][j], f[2 * t + 1][j]);
+            }
         }
     }
     // row gq of a tile: columns 8 c4 + j (from registers 0 and 2 of group j) and 8 c4 + 4 + j
@@ -478,15 +546,15 @@ __global__ void __launch_bounds__(32 * Warps<D, NT>::ALL, resident<D, NT>()) ste
     // M d on top of the q rows' products (registers 2 and 3); the k rows' are done with
 #pragma unroll
     for (int ks = 0; ks < NT / 8; ++ks) {
-        const float4 x = load4(kg + (8 * ks + c4) * LDU + cols + 4 * gq), y = load4(kg + (8 * ks + c4 + 4) * LDU + cols + 4 * gq);
+        const float4 x = load4(kg + (8 * ks + 2 * c4) * LDU + cols + 4 * gq), y = load4(kg + (8 * ks + 2 * c4 + 1) * LDU + cols + 4 * gq);
         const float xv[4] = {x.x, x.y, x.z, x.w}, yv[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             const int tile = mt * SPLIT + part;
             if (mt * SPLIT + SPLIT - 1 < ks || tile < ks) continue;      // nodes see earlier ones only
-            const float a1 = pp[(8 * tile + gq) * LDP + 8 * ks + c4], a3 = pp[(8 * tile + gq) * LDP + 8 * ks + c4 + 4];
+            const float2 a = load2(pp + (8 * tile + gq) * LDP + 8 * ks + 2 * c4);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) mma_tf32(acc[mt][j], 0.f, a1, 0.f, a3, xv[j], yv[j]);
+            for (int j = 0; j < 4; ++j) mma_tf32(acc[mt][j], 0.f, a.x, 0.f, a.y, xv[j], yv[j]);
         }
     }
 #pragma unroll
@@ -504,11 +572,11 @@ template <int D, int NT>
 __global__ void __launch_bounds__(32 * Warps<D, NT>::ALL) step_simt_kernel(const StepArgs p) {
     using L = Smem<D, NT>;
     using Tin = float;
-    constexpr int LD = L::LDS, LDP = L::LDP;
+    constexpr int LD = L::LDS, LDA = L::LDA, LDP = L::LDP;
     constexpr int SPLIT = Warps<D, NT>::SPLIT, WARPS = Warps<D, NT>::ALL, THREADS = 32 * WARPS;
     extern __shared__ __align__(16) uint8_t sm[];
     float *kg = reinterpret_cast<float *>(sm), *qg = reinterpret_cast<float *>(sm + L::SQG);
-    float *pa = reinterpret_cast<float *>(sm + L::SAP), *pp = pa + NT * LDP;
+    float *pa = reinterpret_cast<float *>(sm + L::SAP), *pp = pa + NT * LDA;
     uint64_t *mask = reinterpret_cast<uint64_t *>(sm + L::SMASK);
     float *beta = reinterpret_cast<float *>(sm + L::SBETA);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -546,7 +614,7 @@ __global__ void __launch_bounds__(32 * Warps<D, NT>::ALL) step_simt_kernel(const
         gs = p.scalar_gate ? 1 : D;
     }
     const float *S = p.S + (slot * p.H + h) * (D * D);
-    if (tid == 0) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" :: "l"(S), "r"(D * D * 4) : "memory");
+    if (tid == 0) prefetch_bulk(S, D * D * 4);
     if (warp == 0) {
         uint64_t x, y;
         all_ancestors(p.parents + (int64_t)b * T, T, lane, x, y);
@@ -635,7 +703,7 @@ __global__ void __launch_bounds__(32 * Warps<D, NT>::ALL) step_simt_kernel(const
                     const int i = __ffsll((long long)m) - 1;
                     m &= m - 1;
                     const float ui = kg[i * LD + tid];
-                    u -= pa[r * LDP + i] * ui;
+                    u -= pa[r * LDA + i] * ui;
                     z += pp[r * LDP + i] * ui;
                 }
                 z += pp[r * LDP + r] * u;
