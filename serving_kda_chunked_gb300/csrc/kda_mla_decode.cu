@@ -33,8 +33,8 @@
 // tokens at a time, would read less, but 64 rows of queries and two stages fill shared memory.
 // Tried: the halves of a stage loaded and released apart (198 us for the 64 trees below, 204),
 // a tile brought in once for two and four groups by TMA multicast (204, 216).  Measured, 32
-// heads: 64 ragged trees of up to 8 nodes over up to 8192 tokens 164 us, 8 trees of 48 nodes
-// over up to 32,768 tokens 740 us = 0.9 PFLOP/s.
+// heads: 64 ragged trees of up to 8 nodes over up to 8192 tokens 151 us, 8 trees of 48 nodes
+// over up to 32,768 tokens 738 us = 0.9 PFLOP/s.
 //
 // Warps 0-3 and 4-7: softmax and epilogue of half the heads each; warp 8: MMA
 // issue; warp 9: loads.
@@ -51,7 +51,6 @@ namespace {
 constexpr int TOK = 64, CHUNKS = ROW / 64;                  // tokens a tile, 128-byte chunks a row
 constexpr uint32_t GROUP = CHUNKS * 1024;                   // 8 tokens
 constexpr uint32_t STAGE = 8 * GROUP;
-constexpr int OVER = 2;                                     // tiles' time to begin and end a sequence
 constexpr int THREADS = 320, W_MMA = 8, W_LOAD = 9;
 constexpr int MAX_CTAS = 160;                               // per launch, up to one wave
 constexpr float RESCALE = 8.f;                              // see the softmax below
@@ -105,6 +104,8 @@ __device__ __forceinline__ void st_cols(uint32_t a, const float (&v)[16]) { tmem
 template <int N, bool TREE>
 __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constant__ DecParams p) {
     using L = Smem<N>;
+    // tiles' time to begin and end a sequence (64 trees of 8 nodes: 2 154 us, 3 152, 4 151, 6 150; one: 17.3, 15.9, 17.2, 17.2)
+    constexpr int OVER = TREE && N == 64 ? 4 : 2;
     constexpr uint32_t TCOLS = N == 64 ? 512 : 256;
     constexpr uint32_t S_COL = 0, O_COL = 2 * N;            // S^T twice, O^T in 4 blocks of 128 channels
     extern __shared__ __align__(1024) uint8_t sm[];
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     fence_before_sync();
-    const Share share = find_share<TOK, OVER, THREADS, N, __nv_bfloat16, TREE>(p, *scratch);
+    const Share share = find_share<TOK, OVER, THREADS, N, __nv_bfloat16, TREE>(p, *scratch, reinterpret_cast<int64_t *>(sm + L::RED));
     fence_after_sync();
     const uint32_t tmem = warp_uniform(*tmem_slot);
     const uint32_t smb = warp_uniform(smem_addr(sm));

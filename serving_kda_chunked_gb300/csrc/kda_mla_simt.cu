@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(DTHREADS, 2) decode_simt_kernel(const SplitPar
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Share share = find_share<TT, OVER, DTHREADS, HG, float, TREE>(p, scratch);
+    const Share share = find_share<TT, OVER, DTHREADS, HG, float, TREE>(p, scratch, nullptr);
     if (tid == 0) p.status[blockIdx.x] = 0;
     if (!share.busy) return;
     Walk<TT, OVER, HG, TREE> w;

@@ -9,13 +9,19 @@
 // CTA x works for group x % groups on share x / groups, so that the CTAs that
 // read the same tokens for different heads do so at about the same time.
 //
-// Drafted trees (TREE): nothing is computed for groups of rows that are padding.  Where there
-// are such, the groups differ in work, and every (sequence, group) is an item of its own in one
-// list, in that order; what is said of sequences holds for items then, and groups of
-// padding alone are items of length 0.  Where there are none, all is as above: the groups
-// stay in step, and read a tile from L2 at the same time.  32 heads, each way in us:
-//   64 trees of 8 nodes over up to 8192 tokens, full 192 (as items 223), ragged 201 (as items 152)
-//   8 trees of 48 over up to 32,768, full 537 (597), ragged 530 (464)
+// Drafted trees (TREE): nothing is computed for groups of rows that are padding.  Where there are
+// none, all is as above: the groups stay in step, and read a tile from L2 at the same time.
+// Else sequences differ in groups, and every (sequence, group) is an item of its own in one list, in
+// that order; what is said of sequences holds for items then, and groups of padding alone are
+// items of length 0.  An item's tokens come from HBM, though, where L2 cannot hold them until
+// the next group wants them: sequences with the same number of groups then have CTAs of their own, in
+// step (alike_order).  32 heads, each way in us:
+//   64 trees of 8 nodes over up to 8192 tokens, full: in step 192, items 223;
+//     ragged: in step 201, items 162 (812 MB from HBM of 360), alike 151
+//   128 and 256 ragged trees of 8, 560,000 tokens in all: items 279 and 273, alike 255 and 259
+//   64 ragged trees of 8, 120,000 tokens: items 91, alike 90; 90,000: 77, 80; 66,000: 61, 64
+//   64 and 256 ragged trees of 16 (8 groups): items 233 and 544, alike 238 and 580
+//   8 trees of 48 over up to 32,768, full: in step 533, items 597; ragged: 530 and 457
 #pragma once
 
 #include "kda_mla.cuh"
@@ -42,8 +48,10 @@ __device__ __forceinline__ float lse_of(float top, float sum) {
 }
 
 // What the share of a CTA starts in: sequence (or item) b, which the starts of the shares
-// first .. last cut; b < 0 marks an idle CTA.  groups: of the call's order.
-struct __align__(16) Meta { int32_t b, first, last, groups; };
+// first .. last cut; b < 0 marks an idle CTA.  order: Order's groups (at most 1024), base (beside
+// 32 groups at most) from bit 16 on, and whether a sequence's groups are items.
+struct __align__(16) Meta { int32_t b, first, last, order; };
+constexpr int32_t LISTED = 1 << 15;
 
 struct SplitParams {
     const int32_t *table, *seq_lens;
@@ -63,13 +71,14 @@ __device__ __forceinline__ int64_t seq_len(const SplitParams &p, int b) {
     const int64_t cap = (int64_t)p.max_pages * p.page, n = p.seq_lens[b];
     return n < 0 ? 0 : (n > cap ? cap : n);
 }
-// How the work is listed: CTA x works for group x % groups; a sequence is `items` items.
-struct Order { int groups, items; };
+// How the work is listed: CTA base + x works for group x % groups on share x / groups of
+// `shares`; a sequence is `items` items.  alike: only sequences of that many groups.
+struct Order { int groups, items, base, shares; bool alike; };
 // Item i: which sequence, and its first row of H.
 struct Item { int b, h0; };
 template <bool TREE, int N> __device__ __forceinline__ Item item_of(Order o, int i) {
     if (!TREE) return {i, (int)blockIdx.x % o.groups * N};
-    return {i / o.items, (i % o.items + (int)blockIdx.x % o.groups) * N};
+    return {i / o.items, (i % o.items + ((int)blockIdx.x - o.base) % o.groups) * N};
 }
 // Nodes of a tree up to the last that may not be padding.
 __device__ __forceinline__ int tree_nodes(const SplitParams &p, int b) {
@@ -96,7 +105,7 @@ template <bool TREE, int N> struct Lengths {
             len = seq_len(p, b) + n;
             len = len > cap ? cap : len;
         }
-        return it.h0 < rows ? len : 0;
+        return it.h0 < rows && (!o.alike || rows > (o.groups - 1) * N && rows <= o.groups * N) ? len : 0;
     }
 };
 template <int TOK> __device__ __forceinline__ int64_t tiles_of(int64_t len) { return (len + TOK - 1) / TOK; }
@@ -137,22 +146,76 @@ struct Shares {
 struct Share { int64_t g0, g1, t00, len0; Order o; int b0, items; bool busy; };
 template <int THREADS> struct ShareScratch { int64_t sums[THREADS / 32], t0, t1, len; int b; };
 
+// Groups in step for trees with different numbers of groups (up to ALIKE), where the tokens exceed what
+// L2 holds, so that items would bring them in once for every group: sequences with g groups get
+// g k_g CTAs of their own, with k_g the fewest whose shares are w units at most.  w is
+// the least of 32 up to a quarter above an even share for which there are CTAs enough, and
+// where there is none, `o` (items) stays.  units: ALIKE words of shared memory, 0.
+// Not inlined, or the main loop spills.
+constexpr int ALIKE = 4;
+constexpr int64_t PAST_L2 = 2048;              // tiles of 73,728 bytes
+template <int TOK, int OVER, int THREADS, int N> __device__ __noinline__ Order alike_order(const SplitParams &p, int64_t *units, Order o) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    const Order first = {1, 1, 0, 0, false};   // a sequence's first group
+    Lengths<true, N> lens;
+    for (int b = tid; b < p.B; b += THREADS) {
+        const int64_t n = units_of<TOK, OVER>(lens.of(p, first, b));
+        if (n) atomicAdd(reinterpret_cast<unsigned long long *>(units + (lens.rows - 1) / N), (unsigned long long)n);
+    }
+    __syncthreads();
+    int64_t sum = 0, once = 0;
+#pragma unroll
+    for (int g = 1; g <= ALIKE; ++g) {
+        sum += g * units[g - 1];
+        once += units[g - 1];
+    }
+    if (once < PAST_L2) return o;
+    int64_t w = quotient(sum + gridDim.x - 1, gridDim.x);
+    w += w * lane / 128;                       // every lane tries another one
+    int need = 0;
+#pragma unroll 1
+    for (int g = 1; g <= ALIKE; ++g) need += g * (int)quotient(units[g - 1] + w - 1, w);
+    const uint32_t fits = __ballot_sync(0xffffffffu, need <= (int)gridDim.x);
+    if (!fits) return o;
+    w = __shfl_sync(0xffffffffu, w, __ffs(fits) - 1);
+    o = {1, 1, 0, 0, true};                    // CTAs that are left over
+    int base = 0;
+#pragma unroll 1
+    for (int g = 1; g <= ALIKE; ++g) {
+        const int k = (int)quotient(units[g - 1] + w - 1, w);
+        if ((int)blockIdx.x >= base && (int)blockIdx.x < base + g * k) o = {g, 1, base, k, true};
+        base += g * k;
+    }
+    return o;
+}
+// The order of the work of trees with several groups (all THREADS threads).
+template <int TOK, int OVER, int THREADS, int N> __device__ __forceinline__ Order tree_order(const SplitParams &p, int64_t *units) {
+    const int tid = threadIdx.x;
+    bool even = true;                          // or has some sequence only padding for a group?
+    for (int b = tid; b < p.B; b += THREADS) {
+        asm volatile("prefetch.global.L1 [%0];" :: "l"(p.seq_lens + b));
+        even &= tree_nodes(p, b) * p.heads > (p.groups - 1) * N;
+    }
+    if (N == 64 && tid < ALIKE) units[tid] = 0;
+    Order o = {p.groups, 1, 0, (int)gridDim.x / p.groups, false};
+    if (!__syncthreads_and(even)) {
+        o = {1, p.groups, 0, (int)gridDim.x, false};
+        if (N == 64 && p.groups <= ALIKE && (int64_t)p.max_pages * p.page * p.B >= PAST_L2 * TOK)      // could be as many
+            o = alike_order<TOK, OVER, THREADS, N>(p, units, o);
+    }
+    // one lane's numbers for all, so that the compiler knows them to be a warp's (or the main loop spills)
+    return {__shfl_sync(0xffffffffu, o.groups, 0), __shfl_sync(0xffffffffu, o.items, 0), __shfl_sync(0xffffffffu, o.base, 0),
+            __shfl_sync(0xffffffffu, o.shares, 0), __shfl_sync(0xffffffffu, (int)o.alike, 0) != 0};
+}
+
 // Finds the share (all THREADS threads; ends with a barrier), records it for
 // the join, and writes the outputs of sequences with nothing cached.
 template <int TOK, int OVER, int THREADS, int N, typename To, bool TREE>
-__device__ __forceinline__ Share find_share(const SplitParams &p, ShareScratch<THREADS> &sh) {
+__device__ __forceinline__ Share find_share(const SplitParams &p, ShareScratch<THREADS> &sh, int64_t *units) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    Order o = {p.groups, 1};
-    if (TREE && p.groups > 1) {                // any group that some sequence has only padding for?
-        bool even = true;
-        for (int b = tid; b < p.B; b += THREADS) {
-            asm volatile("prefetch.global.L1 [%0];" :: "l"(p.seq_lens + b));
-            even &= tree_nodes(p, b) * p.heads > (p.groups - 1) * N;
-        }
-        const int order = __shfl_sync(0xffffffffu, __syncthreads_and(even) ? 0 : 1, 0);
-        if (order) o = {1, p.groups};
-    }
-    const int c = blockIdx.x / o.groups, C0 = gridDim.x / o.groups, items = p.B * o.items;
+    Order o = {p.groups, 1, 0, (int)gridDim.x / p.groups, false};
+    if (TREE && p.groups > 1) o = tree_order<TOK, OVER, THREADS, N>(p, units);
+    const int c = ((int)blockIdx.x - o.base) / o.groups, C0 = o.shares, items = p.B * o.items;
     const int per = (items + THREADS - 1) / THREADS;
     const int b_lo = min(items, tid * per), b_hi = min(items, b_lo + per);
     int64_t mine = 0;
@@ -207,9 +270,12 @@ __device__ __forceinline__ Share find_share(const SplitParams &p, ShareScratch<T
             at += n;
         }
     }
-    for (int b = c; empties && b < items && c < C0; b += C0) {
-        if (lens.of(p, o, b) > 0) continue;
-        const Item it = item_of<TREE, N>(o, b);
+    const Order e = {1, p.groups, 0, (int)gridDim.x, false};     // with sequences of a kind, of all there are
+    const bool alike = TREE && o.alike;
+    const int ec = alike ? blockIdx.x : c, eC = alike ? gridDim.x : C0, many = alike ? p.B * p.groups : items;
+    for (int b = ec; (empties || alike) && b < many && ec < eC; b += eC) {
+        if (lens.of(p, alike ? e : o, b) > 0) continue;
+        const Item it = item_of<TREE, N>(alike ? e : o, b);
         const int nh = min(N, p.H - it.h0);
         const int64_t at = (int64_t)it.b * p.H + it.h0;
         for (int e = tid; e < nh * (LATENT / 4); e += THREADS)
@@ -221,8 +287,9 @@ __device__ __forceinline__ Share find_share(const SplitParams &p, ShareScratch<T
     s.t00 = sh.t0;
     s.len0 = sh.len;
     if (tid == THREADS - 64) {                 // of a warp that has nothing to do yet
-        Meta m = {-1, 0, 0, o.groups};
-        if (s.busy && s.b0 >= 0) m = {s.b0, cuts.after(s.t00), cuts.after(sh.t1 - 1) - 1, o.groups};
+        Meta m = {-1, 0, 0, 0};
+        if (s.busy && s.b0 >= 0)
+            m = {s.b0, cuts.after(s.t00), cuts.after(sh.t1 - 1) - 1, o.groups | (o.items > 1 ? LISTED : 0) | o.base << 16};
         p.meta[blockIdx.x] = m;
     }
     // no tile: the share lies in a sequence's OVER (or lengths changed under the kernel)
@@ -281,13 +348,15 @@ __global__ void __launch_bounds__(256, 4) join_kernel(const SplitParams p, int c
     const int cta = blockIdx.y + (TREE ? 1 : p.groups);     // shares 1 .. of every group
     if (cta >= ctas) return;
     const Meta m = p.meta[cta];
-    const int groups = TREE ? m.groups : p.groups, group = cta % groups, c = cta / groups;
-    if (m.b < 0 || c < m.first || c > m.last) return;
+    if (m.b < 0) return;
+    const int groups = TREE ? m.order & (LISTED - 1) : p.groups, base = TREE ? m.order >> 16 : 0;
+    const int group = (cta - base) % groups, c = (cta - base) / groups;
+    if (c < m.first || c > m.last) return;
     const int pieces = m.last - m.first + 2;                // of shares first - 1 .. last
-    const int items = TREE && groups != p.groups ? p.groups : 1;
+    const int items = TREE && m.order & LISTED ? p.groups : 1;
     const int seq = TREE ? m.b / items : m.b, h0 = ((TREE ? m.b % items : 0) + group) * N;
     const int nh = min(N, p.H - h0);
-    const int slot0 = 2 * ((m.first - 1) * groups + group);     // of piece i: slot0 + 2 groups i, + 1 for the first
+    const int slot0 = 2 * (base + (m.first - 1) * groups + group);     // of piece i: slot0 + 2 groups i, + 1 for the first
     auto slot_of = [&](int i) { return slot0 + 2 * groups * i + (i == 0); };
     const int block = (c - m.first) * gridDim.x + blockIdx.x, blocks = (pieces - 1) * gridDim.x;
     auto write = [&](int item, float4 acc, float top, float sum, int bad) {

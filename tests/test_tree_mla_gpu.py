@@ -116,6 +116,24 @@ def test_many_sequences_and_a_long_one(dtype):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("nodes, ctx", [
+    # 16 heads: four nodes a group of 64 rows; tokens beyond what L2 holds, so that sequences with as many
+    # groups are worked on together
+    ([1, 16, 5, 9, 4, 13, 2, 8, 0, 12, 16, 3, 7, 11, 15, 1, 6, 10, 14, 16, 8, 5, 0, 2], [5000 + 97 * i for i in range(24)]),
+    ([16] + [3] * 11, [9000, 64] + [14000 + 63 * i for i in range(10)]),
+    ([7, 13, 13, 1, 16], [140000, 0, 1, 64, 200]),
+    ([10, 12, 9, 0, 11, 12], [40000, 1, 40001, 50000, 39999, 20000]),
+])
+def test_sequences_with_different_numbers_of_groups(nodes, ctx):
+    rng = np.random.default_rng(len(nodes))
+    parents = [[int(rng.integers(-1, i)) if i < n else -2 for i in range(16)] for n in nodes]
+    q, cache, table, n, rows = _inputs(ctx, parents, 16, 64, "bf16", 260 + len(nodes))
+    o, lse = _call(q, cache, table, n, parents)
+    _check(q, rows, ctx, parents, "bf16", o, lse)
+    o2, lse2 = _call(q, cache, table, n, parents)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_padding_and_odd_parents(dtype):
     """Sequences of padding alone, odd parents, padding between valid nodes."""
