@@ -46,9 +46,10 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// To nearest, ties to even: one instruction, where ties away from 0 take four (64 nodes: RN_US us, RNA_US).
 __device__ __forceinline__ float to_tf32(float x) {
     uint32_t y;
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(y) : "f"(x));
+    asm("cvt.rn.tf32.f32 %0, %1;" : "=r"(y) : "f"(x));
     return __uint_as_float(y);
 }
 __device__ __forceinline__ void mma_tf32(float (&c)[4], float a0, float a1, float a2, float a3, float b0, float b1) {
@@ -116,20 +117,22 @@ template <int D> __device__ __forceinline__ Row<D> unpack(const Raw<D> &a) {
 
 constexpr float LOG2E = 1.4426950408889634f;
 
-// Shared memory.  bf16: rows k e^gamma, q e^gamma and k e^-gamma (before them gamma, after the
-// product the deltas d); A and P, then M; masks, betas, who is above whom.  With 64 nodes A and P take
+// Shared memory.  bf16: rows of (k e^gamma, q e^gamma) channel by channel, as an MMA wants
+// them in a thread's registers (before them gamma, after the product the deltas d), and k e^-gamma;
+// A and P, then M; masks, betas, who is above whom.  With 64 nodes A and P take
 // the place of k e^-gamma, so that two CTAs fit an SM.  fp32: rows k e^gamma and q e^gamma,
 // after the product deltas and outputs; A and P; masks, betas; up to 16 nodes the inputs.
 template <int D, int NT> struct Smem {       // NT: nodes, a multiple of 8
     static constexpr int LD = D + 8;         // four rows' reads of eight channels meet different banks
+    static constexpr int LDK = 2 * D + 16;   // two rows' reads of eight channels of both do
     static constexpr int LDU = D + 4;        // the deltas' rows: every other of eight rows' reads of 32 columns do
     static constexpr int LDS = D + 16;       // fp32: two rows' reads of 16 channels do
     static constexpr int LDA = NT + 4, LDP = NT + 8;   // A and P of node r: pa[r * LDA + i], pp[r * LDP + i]
     static constexpr bool OVER = NT == 64, STAGED = NT <= 16;
     static constexpr uint32_t AP_BYTES = NT * (LDA + LDP) * 4;
     // bf16
-    static constexpr uint32_t KG = 0, QG = NT * LD * 4, KI = 2 * QG, AP = OVER ? KI : 3 * QG, MASK = AP + (OVER && AP_BYTES < QG ? QG : AP_BYTES),
-                              BETA = MASK + NT * 8, UPS = BETA + NT * 4, TC_BYTES = UPS + 6 * NT + 16;
+    static constexpr uint32_t KI = NT * LDK * 4, KI_BYTES = NT * LD * 4, AP = OVER ? KI : KI + KI_BYTES,
+                              MASK = AP + (OVER && AP_BYTES < KI_BYTES ? KI_BYTES : AP_BYTES), BETA = MASK + NT * 8, UPS = BETA + NT * 4, TC_BYTES = UPS + 6 * NT + 16;
     // fp32
     static constexpr uint32_t SQG = NT * LDS * 4, SAP = 2 * SQG, SMASK = SAP + AP_BYTES, SBETA = SMASK + NT * 8,
                               ROWS = SBETA + NT * 4, SIMT_BYTES = ROWS + (STAGED ? NT * D * 16 : 0);
@@ -142,7 +145,8 @@ template <int D, int NT> struct Warps { static constexpr int COLS = D / 32, SPLI
 // (differences of sums from the root would cancel); what the sum is at the end fades the
 // rows.  Four ancestors at a time, so that their loads are under way together and the sums
 // over the lanes share exchanges.  in, gs: elements between nodes of k and q, of the gates.
-template <int D, int NT, int LD, int WARPS, typename Tin>
+// EACH: floats between a row's channels.
+template <int D, int NT, int LD, int EACH, int WARPS, typename Tin>
 __device__ __forceinline__ void pair_by_pair(const Tin *q, const Tin *k, const float *g, int64_t in, int64_t gs, bool scalar_gate,
                                              const uint64_t *mask, const float *beta, float *kg, float *qg, float *pa, float *pp) {
     constexpr int LDA = Smem<D, NT>::LDA, LDP = Smem<D, NT>::LDP, C = D / 32;
@@ -209,8 +213,8 @@ __device__ __forceinline__ void pair_by_pair(const Tin *q, const Tin *k, const f
         for (int c = 0; c < C; ++c) {
             const float f = on ? ex2(run.x[c]) : 0.f;
             const float a = kr.x[c] * f, z = qr.x[c] * f;
-            kg[r * LD + C * lane + c] = sizeof(Tin) == 2 ? to_tf32(a) : a;
-            qg[r * LD + C * lane + c] = sizeof(Tin) == 2 ? to_tf32(z) : z;
+            kg[r * LD + EACH * (C * lane + c)] = sizeof(Tin) == 2 ? to_tf32(a) : a;
+            qg[r * LD + EACH * (C * lane + c)] = sizeof(Tin) == 2 ? to_tf32(z) : z;
         }
     }
 }
@@ -224,10 +228,10 @@ template <int D, int NT>
 __global__ void __launch_bounds__(32 * Warps<D, NT>::ALL, resident<D, NT>()) step_tc_kernel(const StepArgs p) {
     using L = Smem<D, NT>;
     using Tin = __nv_bfloat16;
-    constexpr int LD = L::LD, LDU = L::LDU, LDA = L::LDA, LDP = L::LDP, C = D / 32;
+    constexpr int LD = L::LD, LDK = L::LDK, LDU = L::LDU, LDA = L::LDA, LDP = L::LDP, C = D / 32;
     constexpr int SPLIT = Warps<D, NT>::SPLIT, WARPS = Warps<D, NT>::ALL, THREADS = 32 * WARPS;
     extern __shared__ __align__(16) uint8_t sm[];
-    float *kg = reinterpret_cast<float *>(sm + L::KG), *qg = reinterpret_cast<float *>(sm + L::QG), *ki = reinterpret_cast<float *>(sm + L::KI);
+    float *kq = reinterpret_cast<float *>(sm), *ki = reinterpret_cast<float *>(sm + L::KI);
     float *pa = reinterpret_cast<float *>(sm + L::AP), *pp = pa + NT * LDA;
     uint64_t *mask = reinterpret_cast<uint64_t *>(sm + L::MASK);
     float *beta = reinterpret_cast<float *>(sm + L::BETA);
@@ -276,12 +280,12 @@ __global__ void __launch_bounds__(32 * Warps<D, NT>::ALL, resident<D, NT>()) ste
             const int r = warp + n * WARPS;
             if (r < T) {
                 const float x = g[r * gs];
-                store_row<D>(kg + r * LD, lane, spread<D>(x));
+                store_row<D>(kq + r * LD, lane, spread<D>(x));
             }
         }
     } else {
         for (int e = tid; e < T * (D / 4); e += THREADS)
-            copy16(kg + e / (D / 4) * LD + e % (D / 4) * 4, g + e / (D / 4) * step + e % (D / 4) * 4);
+            copy16(kq + e / (D / 4) * LD + e % (D / 4) * 4, g + e / (D / 4) * step + e % (D / 4) * 4);
     }
     if (warp == 0) {
         uint64_t x, y;
@@ -299,13 +303,13 @@ __global__ void __launch_bounds__(32 * Warps<D, NT>::ALL, resident<D, NT>()) ste
     __syncthreads();
     // gamma: every round adds up twice as far a stretch of the paths, from one buffer to
     // the other; a warp its rows.  A row that stood still for two rounds is in both.
-    float *was = kg, *now = ki;
+    float *was = kq, *now = ki;
     const int n_rounds = *rounds;
     Row<D> gm[MINE];
     int above[MINE];
 #pragma unroll
     for (int n = 0; n < MINE; ++n) {
-        gm[n] = load_row<D>(kg + (warp + n * WARPS) * LD, lane);
+        gm[n] = load_row<D>(kq + (warp + n * WARPS) * LD, lane);
         above[n] = 0;
     }
     for (int k = 0; k < n_rounds; ++k) {
@@ -347,7 +351,7 @@ __global__ void __launch_bounds__(32 * Warps<D, NT>::ALL, resident<D, NT>()) ste
     const auto tile_of = [&](int t) { return NT == 64 && WARPS == 8 && warp >= 4 ? 11 - warp : warp + t * WARPS; };
     float pr[TILES][NT / 8][4] = {};                     // A and P; then in 0 and 1 row gq, columns 8 j + 2 c4 and the next
     if (__syncthreads_or(far)) {
-        pair_by_pair<D, NT, LD, WARPS>(q, k, g, step, gs, p.scalar_gate, mask, beta, kg, qg, pa, pp);
+        pair_by_pair<D, NT, LDK, 2, WARPS>(q, k, g, step, gs, p.scalar_gate, mask, beta, kq, kq + 1, pa, pp);
         __syncthreads();
 #pragma unroll
         for (int t = 0; t < TILES; ++t)
@@ -362,17 +366,18 @@ __global__ void __launch_bounds__(32 * Warps<D, NT>::ALL, resident<D, NT>()) ste
 #pragma unroll
         for (int n = 0; n < MINE; ++n) {
             const int r = warp + n * WARPS;
-            const bool on = mask[r] != 0;
+            if (!mask[r]) kr[n] = qr[n] = {};
             Row<D> a = unpack<D>(kr[n]), z = unpack<D>(qr[n]), i;
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 const float f = ex2(gm[n].x[c]);
-                i.x[c] = on ? to_tf32(a.x[c] * ex2(-gm[n].x[c])) : 0.f;
-                a.x[c] = on ? to_tf32(a.x[c] * f) : 0.f;
-                z.x[c] = on ? to_tf32(z.x[c] * f) : 0.f;
+                i.x[c] = to_tf32(a.x[c] * ex2(-gm[n].x[c]));
+                a.x[c] = to_tf32(a.x[c] * f);
+                z.x[c] = to_tf32(z.x[c] * f);
             }
-            store_row<D>(kg + r * LD, lane, a);
-            store_row<D>(qg + r * LD, lane, z);
+#pragma unroll
+            for (int c = 0; c < C; c += 2)
+                store4(kq + r * LDK + 2 * (C * lane + c), make_float4(a.x[c], z.x[c], a.x[c + 1], z.x[c + 1]));
             store_row<D>(ki + r * LD, lane, i);
         }
         __syncthreads();
@@ -384,12 +389,12 @@ __global__ void __launch_bounds__(32 * Warps<D, NT>::ALL, resident<D, NT>()) ste
             if (tile >= NT / 8) break;
 #pragma unroll 4
             for (int s = 0; s < D / 8; ++s) {
-                const float2 a = load2(kg + (8 * tile + gq) * LD + 8 * s + 2 * c4), c = load2(qg + (8 * tile + gq) * LD + 8 * s + 2 * c4);
+                const float4 a = load4(kq + (8 * tile + gq) * LDK + 16 * s + 4 * c4);
 #pragma unroll
                 for (int j = 0; j < NT / 8; ++j)
-                    if (j <= tile) {                     // nodes see earlier ones only
+                    if (j / 2 * 2 <= tile) {             // nodes see earlier ones only
                         const float2 x = load2(ki + (8 * j + gq) * LD + 8 * s + 2 * c4);
-                        mma_tf32(pr[t][j], a.x, c.x, a.y, c.y, x.x, x.y);
+                        mma_tf32(pr[t][j], a.x, a.y, a.z, a.w, x.x, x.y);
                     }
             }
         }
@@ -401,10 +406,12 @@ __global__ void __launch_bounds__(32 * Warps<D, NT>::ALL, resident<D, NT>()) ste
             const int r = 8 * tile + gq;
             const uint64_t m = mask[r];
             const float br = m ? beta[r] : 0.f;
+            const uint32_t lo = (uint32_t)m >> 2 * c4, hi = (uint32_t)(m >> 32) >> 2 * c4;
 #pragma unroll
             for (int j = 0; j < NT / 8; ++j) {           // zeros where r does not see a node
                 const int i = 8 * j + 2 * c4;
-                const bool s0 = m >> i & 1, s1 = m >> (i + 1) & 1;
+                const uint32_t sees = j < 4 ? lo : hi;
+                const bool s0 = sees >> 8 * (j % 4) & 1, s1 = sees >> 8 * (j % 4) & 2;
                 *reinterpret_cast<float2 *>(pa + r * LDA + i) = make_float2(s0 ? br * pr[t][j][0] : 0.f, s1 ? br * pr[t][j][1] : 0.f);
                 pr[t][j][0] = s0 ? pr[t][j][2] : 0.f;
                 pr[t][j][1] = s1 ? pr[t][j][3] : 0.f;
@@ -514,10 +521,9 @@ __global__ void __launch_bounds__(32 * Warps<D, NT>::ALL, resident<D, NT>()) ste
         for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const int at = (8 * (mt * SPLIT + part) + gq) * LD + 16 * s + 8 * t + 2 * c4;
-                const float2 a = load2(kg + at), c = load2(qg + at);
+                const float4 a = load4(kq + (8 * (mt * SPLIT + part) + gq) * LDK + 32 * s + 16 * t + 4 * c4);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) mma_tf32(acc[mt][j], a.x, c.x, a.y, c.y, f[2 * t][j], f[2 * t + 1][j]);
+                for (int j = 0; j < 4; ++j) mma_tf32(acc[mt][j], a.x, a.y, a.z, a.w, f[2 * t][j], f[2 * t + 1][j]);
             }
         }
     }
@@ -539,14 +545,14 @@ __global__ void __launch_bounds__(32 * Warps<D, NT>::ALL, resident<D, NT>()) ste
         const float br = mask[r] ? beta[r] : 0.f;        // padding: values and products are 0
         const float4 x = make_float4(br * (v0.x - acc[mt][0][0]), br * (v0.y - acc[mt][1][0]), br * (v1.x - acc[mt][2][0]), br * (v1.y - acc[mt][3][0]));
         const float4 y = make_float4(br * (v2.x - acc[mt][0][1]), br * (v2.y - acc[mt][1][1]), br * (v3.x - acc[mt][2][1]), br * (v3.y - acc[mt][3][1]));
-        store4(kg + r * LDU + n0, make_float4(to_tf32(x.x), to_tf32(x.y), to_tf32(x.z), to_tf32(x.w)));
-        store4(kg + r * LDU + n0 + 4, make_float4(to_tf32(y.x), to_tf32(y.y), to_tf32(y.z), to_tf32(y.w)));
+        store4(kq + r * LDU + n0, make_float4(to_tf32(x.x), to_tf32(x.y), to_tf32(x.z), to_tf32(x.w)));
+        store4(kq + r * LDU + n0 + 4, make_float4(to_tf32(y.x), to_tf32(y.y), to_tf32(y.z), to_tf32(y.w)));
     }
     __syncthreads();
     // M d on top of the q rows' products (registers 2 and 3); the k rows' are done with
 #pragma unroll
     for (int ks = 0; ks < NT / 8; ++ks) {
-        const float4 x = load4(kg + (8 * ks + 2 * c4) * LDU + cols + 4 * gq), y = load4(kg + (8 * ks + 2 * c4 + 1) * LDU + cols + 4 * gq);
+        const float4 x = load4(kq + (8 * ks + 2 * c4) * LDU + cols + 4 * gq), y = load4(kq + (8 * ks + 2 * c4 + 1) * LDU + cols + 4 * gq);
         const float xv[4] = {x.x, x.y, x.z, x.w}, yv[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -624,7 +630,7 @@ __global__ void __launch_bounds__(32 * Warps<D, NT>::ALL) step_simt_kernel(const
     if (tid < T) beta[tid] = p.beta[bt0 + (int64_t)tid * p.H];
     if constexpr (L::STAGED) asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
-    pair_by_pair<D, NT, LD, WARPS>(q, k, g, in, gs, p.scalar_gate, mask, beta, kg, qg, pa, pp);
+    pair_by_pair<D, NT, LD, 1, WARPS>(q, k, g, in, gs, p.scalar_gate, mask, beta, kg, qg, pa, pp);
     __syncthreads();
 
     const int gq = lane >> 2, c4 = lane & 3, cols = 32 * (warp / SPLIT);
