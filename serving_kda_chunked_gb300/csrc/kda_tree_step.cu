@@ -22,15 +22,18 @@
 // Operands are rounded to tf32's 11 bits, as many as the prefill's fp16 operands have;
 // gates, sums and the state are float32, and what a commit writes never passes through here.
 //
-// Measured, 32 heads, D = 128: 256 sequences with chains of 8 nodes 102 us, with one 91 (5.9 TB/s;
-// L1 wavefronts, then latency, take over before HBM does); with up to 8 in a pool 105; 32
-// sequences with 64 nodes 82 us in trees three wide, 91 in chains, where two CTAs an SM spend
-// 40,000 cycles each: loads 7,000, phase 1 5,500, 2 9,000, 3 4,000, 4 14,000, issuing half the time.
+// Measured, 32 heads, D = 128: 256 sequences with chains of 8 nodes 99 us, with one 88 (6.2 TB/s;
+// the latency of phases and L1 stand beside HBM); with up to 8 in a pool 102; 32 sequences with
+// 64 nodes 73 us in trees three wide, 76 in chains: two CTAs an SM take 1,024 in 3.4 rounds,
+// of which loads and phases 1 and 2 up to the rows are 27 us, A and P 12, M 6, the state's product 18
+// (its MMAs alone, at 8 cycles, 14) and the rest 10.
 // On the way, with 8 and with 64 nodes: gates and A, P by FMAs and shuffles 127 and 137; the
 // state's lines read by four lanes each of eight rows (L1 wavefronts at 67%) 118 and 110; M node
-// by node along the paths 105 and 89, and 108 and 185 for chains (a third of all instructions).
-// Tried: what a later CTA reads asked into L2, 64 nodes 87 to 89; 1, 2 or 8 unrolled steps of 4 with
-// 4 to 9 CTAs an SM in phase 4, 8 nodes: 106 to 112.
+// by node along the paths 105 and 89, and 108 and 185 for chains (a third of all instructions);
+// k e^gamma and q e^gamma in rows of their own, whose loads are not in the order of an MMA's registers,
+// 103 and 76.
+// Tried: what a later CTA reads asked into L2, 64 nodes 87 to 89 (of 82); 1, 2 or 8 unrolled steps of 4
+// with 4 to 9 CTAs an SM in phase 4, 8 nodes 106 to 112 (of 105); values loaded before phase 4 103 (of 102).
 //
 // float32 inputs: pair by pair, FMAs, and the deltas one node after the other.
 #include "kda_tree.cuh"
@@ -46,7 +49,7 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// To nearest, ties to even: one instruction, where ties away from 0 take four (64 nodes: RN_US us, RNA_US).
+// To nearest, ties to even: one instruction, where ties away from 0 take four (64 nodes: 76 us, 82).
 __device__ __forceinline__ float to_tf32(float x) {
     uint32_t y;
     asm("cvt.rn.tf32.f32 %0, %1;" : "=r"(y) : "f"(x));
@@ -219,8 +222,12 @@ __device__ __forceinline__ void pair_by_pair(const Tin *q, const Tin *k, const f
     }
 }
 
-// CTAs an SM that registers are shared out for (bf16, D = 128).
-template <int D, int NT> constexpr int resident() { return D != 128 ? 1 : (NT == 8 ? 6 : (NT == 16 ? 5 : (NT == 32 ? 3 : 2))); }
+// CTAs an SM that registers are shared out for (bf16).  One more or fewer, 32 heads, D = 128: 8
+// nodes 99 us, 5 102, 8 102; 16 nodes 67, 4 72, 6 69; 32 nodes 71, 2 81.  D = 64: 8 nodes 32, 9 35,
+// 20 34; 16 nodes 35, 4 41; 32 nodes 29, 4 30, 6 33; 64 nodes 40, 2 48.
+template <int D, int NT> constexpr int resident() {
+    return D == 128 ? (NT == 8 ? 6 : (NT == 16 ? 5 : (NT == 32 ? 3 : 2))) : (NT == 8 ? 16 : (NT == 16 ? 6 : (NT == 32 ? 5 : 3)));
+}
 // Beyond 2^-RANGE of decay from the root, e^-gamma and the products with it could leave float32.
 constexpr float RANGE = 100.f;
 
@@ -498,6 +505,14 @@ __global__ void __launch_bounds__(32 * Warps<D, NT>::ALL, resident<D, NT>()) ste
             for (int j = J - 1; j >= 0; --j) times(pr[t][j], pr[t][j], -h0, -h1, -l0, -l1, J, j);
         }
     }
+    // row gq of a tile: columns 8 c4 + j (from registers 0 and 2 of group j) and 8 c4 + 4 + j
+    const int n0 = cols + 8 * c4;
+    const auto values_of = [&](int mt) -> float4 {
+        const int r = 8 * (mt * SPLIT + part) + gq;
+        return mask[r] ? *reinterpret_cast<const float4 *>(v + r * step + n0) : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    static_assert(!PIPE || MT == 4, "y holds a row's values of every tile");
+    float4 vr[PIPE ? 1 : MT];
     float acc[MT][4][4] = {};
 #pragma unroll(MT > 2 ? 1 : 4)
     for (int s = 0; s < D / 16; ++s) {
@@ -513,7 +528,10 @@ __global__ void __launch_bounds__(32 * Warps<D, NT>::ALL, resident<D, NT>()) ste
             f[j][2] = to_tf32(__shfl_sync(0xffffffffu, y[j].z, from));
             f[j][3] = to_tf32(__shfl_sync(0xffffffffu, y[j].w, from));
         }
-        if (PIPE && s + 1 < D / 16) {
+        if (PIPE && s + 1 == D / 16) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) y[mt] = values_of(mt);
+        } else if (PIPE) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) y[j] = load4(Sl + (16 * (s + 1) + j / 2 * 8 + j % 2) * D);
         }
@@ -527,26 +545,21 @@ __global__ void __launch_bounds__(32 * Warps<D, NT>::ALL, resident<D, NT>()) ste
             }
         }
     }
-    // row gq of a tile: columns 8 c4 + j (from registers 0 and 2 of group j) and 8 c4 + 4 + j
-    const int n0 = cols + 8 * c4;
-    uint4 vr[MT];                                        // the values, while M is worked out
+    if constexpr (!PIPE) {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        const int r = 8 * (mt * SPLIT + part) + gq;
-        vr[mt] = make_uint4(0, 0, 0, 0);
-        if (mask[r]) vr[mt] = *reinterpret_cast<const uint4 *>(v + r * step + n0);
+        for (int mt = 0; mt < MT; ++mt) vr[mt] = values_of(mt);
     }
     __syncthreads();
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
         const int r = 8 * (mt * SPLIT + part) + gq;
-        const __nv_bfloat162 *vv = reinterpret_cast<const __nv_bfloat162 *>(&vr[mt]);
+        const __nv_bfloat162 *vv = reinterpret_cast<const __nv_bfloat162 *>(PIPE ? &y[mt] : &vr[PIPE ? 0 : mt]);
         const float2 v0 = __bfloat1622float2(vv[0]), v1 = __bfloat1622float2(vv[1]), v2 = __bfloat1622float2(vv[2]), v3 = __bfloat1622float2(vv[3]);
         const float br = mask[r] ? beta[r] : 0.f;        // padding: values and products are 0
-        const float4 x = make_float4(br * (v0.x - acc[mt][0][0]), br * (v0.y - acc[mt][1][0]), br * (v1.x - acc[mt][2][0]), br * (v1.y - acc[mt][3][0]));
-        const float4 y = make_float4(br * (v2.x - acc[mt][0][1]), br * (v2.y - acc[mt][1][1]), br * (v3.x - acc[mt][2][1]), br * (v3.y - acc[mt][3][1]));
-        store4(kq + r * LDU + n0, make_float4(to_tf32(x.x), to_tf32(x.y), to_tf32(x.z), to_tf32(x.w)));
-        store4(kq + r * LDU + n0 + 4, make_float4(to_tf32(y.x), to_tf32(y.y), to_tf32(y.z), to_tf32(y.w)));
+        const float4 d0 = make_float4(br * (v0.x - acc[mt][0][0]), br * (v0.y - acc[mt][1][0]), br * (v1.x - acc[mt][2][0]), br * (v1.y - acc[mt][3][0]));
+        const float4 d1 = make_float4(br * (v2.x - acc[mt][0][1]), br * (v2.y - acc[mt][1][1]), br * (v3.x - acc[mt][2][1]), br * (v3.y - acc[mt][3][1]));
+        store4(kq + r * LDU + n0, make_float4(to_tf32(d0.x), to_tf32(d0.y), to_tf32(d0.z), to_tf32(d0.w)));
+        store4(kq + r * LDU + n0 + 4, make_float4(to_tf32(d1.x), to_tf32(d1.y), to_tf32(d1.z), to_tf32(d1.w)));
     }
     __syncthreads();
     // M d on top of the q rows' products (registers 2 and 3); the k rows' are done with
