@@ -35,7 +35,9 @@
 // Tried: what a later CTA reads asked into L2, 64 nodes 87 to 89 (of 82); 1, 2 or 8 unrolled steps of 4
 // with 4 to 9 CTAs an SM in phase 4, 8 nodes 106 to 112 (of 105); values loaded before phase 4 103 (of 102).
 //
-// float32 inputs: pair by pair, FMAs, and the deltas one node after the other.
+// float32 inputs: FMAs, A and P pair by pair, M node by node along the paths (the deltas one node after
+// the other, each from its ancestors': 32 sequences with chains of 64 1350 us, here 637; in trees
+// three wide 623 and 352).
 #include "kda_tree.cuh"
 
 #include <mutex>
@@ -587,8 +589,17 @@ __global__ void __launch_bounds__(32 * Warps<D, NT>::ALL, resident<D, NT>()) ste
     }
 }
 
+// fp32: groups of 4 nodes that meet the state in one pass over it, and CTAs an SM that registers are
+// shared out for.  32 heads, D = 128, trees three wide, with twice or half as many groups in a pass and
+// the CTAs that leaves room for: 256 sequences of 8 nodes 203 us, 251; 128 of 16 213, 220; 64 of 32
+// 255, 351 and 289; 32 of 64 352, 436 and 393.
+template <int D, int NT> constexpr int simt_pass() { return D == 64 && NT == 8 ? 1 : (NT == 64 && D == 64 ? 4 : (NT == 16 && D == 128 ? 4 : 2)); }
+template <int D, int NT> constexpr int simt_resident() {
+    return D == 128 ? (NT == 8 ? 4 : (NT == 16 ? 3 : 2)) : (NT == 8 ? 8 : (NT == 16 ? 4 : (NT == 32 ? 3 : 1)));
+}
+
 template <int D, int NT>
-__global__ void __launch_bounds__(32 * Warps<D, NT>::ALL) step_simt_kernel(const StepArgs p) {
+__global__ void __launch_bounds__(32 * Warps<D, NT>::ALL, simt_resident<D, NT>()) step_simt_kernel(const StepArgs p) {
     using L = Smem<D, NT>;
     using Tin = float;
     constexpr int LD = L::LDS, LDA = L::LDA, LDP = L::LDP;
@@ -645,18 +656,56 @@ __global__ void __launch_bounds__(32 * Warps<D, NT>::ALL) step_simt_kernel(const
     __syncthreads();
     pair_by_pair<D, NT, LD, 1, WARPS>(q, k, g, in, gs, p.scalar_gate, mask, beta, kg, qg, pa, pp);
     __syncthreads();
+    // M with M (I + A) = P, node by node along each node's path, nearest first (a warp a node, eight
+    // chains side by side; a lane the nodes `lane` and `lane + 32`).  M replaces P.
+    constexpr int MINE = NT / WARPS, CHAINS = MINE < 8 ? MINE : 8;
+#pragma unroll 1
+    for (int r0 = warp; r0 < T; r0 += CHAINS * WARPS) {
+        int at[CHAINS];
+        float m0[CHAINS], m1[CHAINS];
+        bool any = false;
+#pragma unroll
+        for (int n = 0; n < CHAINS; ++n) {
+            const int r = r0 + n * WARPS;
+            at[n] = mask[r] ? r : -1;
+            any |= at[n] >= 0;
+            m0[n] = lane < NT ? pp[r * LDP + lane] : 0.f;
+            m1[n] = NT > 32 ? pp[r * LDP + lane + 32] : 0.f;
+        }
+        while (any) {
+            any = false;
+#pragma unroll
+            for (int n = 0; n < CHAINS; ++n) {
+                const int i = at[n] < 0 ? 0 : at[n];
+                float x = __shfl_sync(0xffffffffu, NT > 32 && i >= 32 ? m1[n] : m0[n], i & 31);
+                const uint64_t above = mask[i] & ~(1ull << i);
+                if (at[n] < 0) x = 0.f;                  // at its end
+                at[n] = at[n] < 0 || !above ? -1 : 63 - __clzll((long long)above);
+                any |= at[n] >= 0;
+                // A's row i is 0 but for i's ancestors, and i
+                if (lane < NT) m0[n] -= lane == i ? 0.f : x * pa[i * LDA + lane];
+                if (NT > 32) m1[n] -= lane + 32 == i ? 0.f : x * pa[i * LDA + lane + 32];
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < CHAINS; ++n) {
+            const int r = r0 + n * WARPS;
+            if (lane < NT) pp[r * LDP + lane] = mask[r] ? m0[n] : 0.f;
+            if (NT > 32) pp[r * LDP + lane + 32] = mask[r] ? m1[n] : 0.f;
+        }
+    }
 
     const int gq = lane >> 2, c4 = lane & 3, cols = 32 * (warp / SPLIT);
     const float *Sw = S + cols + 4 * gq;                 // this thread's 4 columns
-    // up to four groups of 4 nodes in one pass over the state; the four lanes of a
-    // column hold every fourth group of 4 channels
-    constexpr int GROUPS = NT / 4 / SPLIT, PASS = GROUPS < 4 ? GROUPS : 4;
+    // PASS groups of 4 nodes in one pass over the state; the four lanes of a column hold every
+    // fourth group of 4 channels
+    constexpr int GROUPS = NT / 4 / SPLIT, PASS = GROUPS < simt_pass<D, NT>() ? GROUPS : simt_pass<D, NT>();
     float4 keep[GROUPS][2];                          // node 4 t + c4: products with k, with q
 #pragma unroll
     for (int x0 = 0; x0 < GROUPS; x0 += PASS) {
         if (4 * (x0 * SPLIT + warp % SPLIT) >= T) break;
         float w[PASS][4][4] = {}, z[PASS][4][4] = {};
-#pragma unroll(D == 64 ? 4 : 2)
+#pragma unroll(D == 64 || NT == 8 ? 4 : 2)
         for (int s = 0; s < D / 16; ++s) {
             float4 y[4];
 #pragma unroll
@@ -700,36 +749,40 @@ __global__ void __launch_bounds__(32 * Warps<D, NT>::ALL) step_simt_kernel(const
     for (int x = 0; x < GROUPS; ++x) {
         const int t = x * SPLIT + warp % SPLIT, r = 4 * t + c4, n = cols + 4 * gq;
         if (4 * t >= T) break;
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f), z = y;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
         if (mask[r]) {
             const float4 vv = load4(v + r * in + n), w = keep[x][0];
             const float br = beta[r];
             y = make_float4(br * (vv.x - w.x), br * (vv.y - w.y), br * (vv.z - w.z), br * (vv.w - w.w));
-            z = keep[x][1];
         }
-        store4(kg + r * LD + n, y);
-        store4(qg + r * LD + n, z);
+        store4(kg + r * LD + n, y);                      // the delta
     }
     __syncthreads();
-    // the deltas, parents first; thread = column
-    if (tid < D)
-        for (int r = 0; r < T; ++r) {
-            uint64_t m = mask[r];
-            float u = kg[r * LD + tid], z = qg[r * LD + tid];
-            if (m) {
-                m &= ~(1ull << r);
-                while (m) {
-                    const int i = __ffsll((long long)m) - 1;
-                    m &= m - 1;
-                    const float ui = kg[i * LD + tid];
-                    u -= pa[r * LDA + i] * ui;
-                    z += pp[r * LDP + i] * ui;
-                }
-                z += pp[r * LDP + r] * u;
-                kg[r * LD + tid] = u;
+    // o = (q e^gamma) S + M d, four earlier nodes at a time
+#pragma unroll 1
+    for (int j = 0; j < T; j += 4) {
+        float4 d[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = load4(kg + (j + i) * LD + cols + 4 * gq);
+#pragma unroll
+        for (int x = 0; x < GROUPS; ++x) {
+            const int t = x * SPLIT + warp % SPLIT;
+            if (4 * t >= T || 4 * t < j) continue;
+            const float4 a = load4(pp + (4 * t + c4) * LDP + j);
+            const float av[4] = {a.x, a.y, a.z, a.w};
+            float4 &z = keep[x][1];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                z.x += av[i] * d[i].x; z.y += av[i] * d[i].y; z.z += av[i] * d[i].z; z.w += av[i] * d[i].w;
             }
-            o[r * step + tid] = from_f32<Tin>(z);
         }
+    }
+#pragma unroll
+    for (int x = 0; x < GROUPS; ++x) {
+        const int t = x * SPLIT + warp % SPLIT, r = 4 * t + c4;
+        if (4 * t >= T) break;
+        if (r < T) store4(o + r * step + cols + 4 * gq, mask[r] ? keep[x][1] : make_float4(0.f, 0.f, 0.f, 0.f));
+    }
 }
 
 template <int D, int NT, bool TC>
