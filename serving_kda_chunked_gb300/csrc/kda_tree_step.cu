@@ -125,8 +125,8 @@ constexpr float LOG2E = 1.4426950408889634f;
 // Shared memory.  bf16: rows of (k e^gamma, q e^gamma) channel by channel, as an MMA wants
 // them in a thread's registers (before them gamma, after the product the deltas d), and k e^-gamma;
 // A and P, then M; masks, betas, who is above whom.  With 64 nodes A and P take
-// the place of k e^-gamma, so that two CTAs fit an SM.  fp32: rows k e^gamma and q e^gamma,
-// after the product deltas and outputs; A and P; masks, betas; up to 16 nodes the inputs.
+// the place of k e^-gamma, so that two CTAs fit an SM.  fp32: rows k e^gamma, after the product the
+// deltas, and q e^gamma; A and P, then M; masks, betas; up to 16 nodes the inputs.
 template <int D, int NT> struct Smem {       // NT: nodes, a multiple of 8
     static constexpr int LD = D + 8;         // four rows' reads of eight channels meet different banks
     static constexpr int LDK = 2 * D + 16;   // two rows' reads of eight channels of both do
