@@ -38,6 +38,7 @@ constexpr int PER_LANE = MAX_CLUSTER * WARPS / 32;          // pieces a lane add
 
 // A number as the sum of two floats, lo below half a unit of hi's last place.
 struct Pair { float hi, lo; };
+struct bool2 { bool x, y; };
 
 __device__ __forceinline__ Pair two_sum(float a, float b) {                  // a + b, exact
     const float s = __fadd_rn(a, b), z = __fsub_rn(s, a);
@@ -85,6 +86,19 @@ struct Sums {
         return d;
     }
 };
+
+// Which of two values p exceed c q.  c's hi alone would drop a value whose p / q lies within half of its
+// last place of c, and that may be all that is left of R after some 25 rejections.  p - hi q is rounded
+// once, so its sign is right, and against lo q it errs for what lies within 2^-46 of c only.
+__device__ __forceinline__ bool2 exceeds(float2 p, float2 q, Pair c) {
+    const float2 hi = make_float2(-c.hi, -c.hi), lo = make_float2(c.lo, c.lo);
+    float2 d, e;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(reinterpret_cast<uint64_t &>(d))
+        : "l"(reinterpret_cast<const uint64_t &>(hi)), "l"(reinterpret_cast<uint64_t &>(q)), "l"(reinterpret_cast<uint64_t &>(p)));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<uint64_t &>(e))
+        : "l"(reinterpret_cast<const uint64_t &>(lo)), "l"(reinterpret_cast<uint64_t &>(q)));
+    return {d.x > e.x, d.y > e.y};
+}
 
 __device__ __forceinline__ Pair shfl(Pair x, int from) {
     return {__shfl_sync(0xffffffffu, x.hi, from), __shfl_sync(0xffffffffu, x.lo, from)};
@@ -278,7 +292,6 @@ __global__ void __launch_bounds__(THREADS, MIN_CTAS) verify_kernel(const VerifyA
         __syncthreads();
         if (!st.pass) break;
         const Rows<Tp> w(p, st, b);
-        const float cf = w.c.hi;
         const int64_t e0 = ((int64_t)rank * WARPS + warp) * piece - w.lead;
         const int64_t size = min(piece, (int64_t)V - e0);   // none or less where the row ends before
         Pair s = {0.f, 0.f};
@@ -302,12 +315,12 @@ __global__ void __launch_bounds__(THREADS, MIN_CTAS) verify_kernel(const VerifyA
                 }
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    // a value that this rounding puts on the other side counts for nothing
-                    const bool i0 = y[x].x > cf * z[x].x, i1 = y[x].y > cf * z[x].y, i2 = y[x].z > cf * z[x].z, i3 = y[x].w > cf * z[x].w;
-                    sp.add(make_float2(i0 ? y[x].x : 0.f, i1 ? y[x].y : 0.f));
-                    sq.add(make_float2(i0 ? z[x].x : 0.f, i1 ? z[x].y : 0.f));
-                    sp.add(make_float2(i2 ? y[x].z : 0.f, i3 ? y[x].w : 0.f));
-                    sq.add(make_float2(i2 ? z[x].z : 0.f, i3 ? z[x].w : 0.f));
+                    const bool2 a = exceeds(make_float2(y[x].x, y[x].y), make_float2(z[x].x, z[x].y), w.c);
+                    const bool2 o = exceeds(make_float2(y[x].z, y[x].w), make_float2(z[x].z, z[x].w), w.c);
+                    sp.add(make_float2(a.x ? y[x].x : 0.f, a.y ? y[x].y : 0.f));
+                    sq.add(make_float2(a.x ? z[x].x : 0.f, a.y ? z[x].y : 0.f));
+                    sp.add(make_float2(o.x ? y[x].z : 0.f, o.y ? y[x].w : 0.f));
+                    sq.add(make_float2(o.x ? z[x].z : 0.f, o.y ? z[x].w : 0.f));
                 }
             }
             s = sp.value() - w.c * sq.value();
