@@ -627,8 +627,10 @@ uint64_t kda_mla_tree_decode_workspace_size(int32_t B, int32_t T, int32_t H,
  * nothing is left of R, R = p.  Skipped sequences have path -1, count 0 and next -1;
  * a target row without a positive value gives next = -1.
  *
- * Probabilities are finite and >= 0.  Sums over V and comparisons are held in pairs
- * of floats and float64, so that results do not depend on the order of a sum.
+ * Probabilities are finite and >= 0.  Sums over V, S and comparisons are held in pairs of
+ * floats, to about 2^-40 of the row's sum.  The order of a sum goes by B and V: equal calls
+ * give equal results, and a sequence in another batch the same ones unless a comparison
+ * is closer than that.
  */
 kda_status kda_tree_verify(const void *target, int64_t target_stride,
                            const void *draft, int64_t draft_stride,
