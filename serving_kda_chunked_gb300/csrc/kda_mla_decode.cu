@@ -32,9 +32,11 @@
 // issuing thread waits for 600 of them, for data or weights).  More rows a tile, or 128
 // tokens at a time, would read less, but 64 rows of queries and two stages fill shared memory.
 // Tried: the halves of a stage loaded and released apart (198 us for the 64 trees below, 204),
-// a tile brought in once for two and four groups by TMA multicast (204, 216).  Measured, 32
-// heads: 64 ragged trees of up to 8 nodes over up to 8192 tokens 151 us, 8 trees of 48 nodes
-// over up to 32,768 tokens 738 us = 0.9 PFLOP/s.
+// a tile brought in once for two and four groups (204, 216).  Measured, 32 heads: 64 ragged trees
+// of up to 8 nodes over up to 8192 tokens 151 us, of which tiles are 101, beginnings and ends of
+// sequences some 10 and the join 4 (the rest has not been found: the order's arithmetic in front of
+// the first load, shares of up to a quarter more than even, or L2 misses of CTAs that fall out of
+// step); 8 trees of 48 nodes over up to 32,768 tokens 738 us = 0.9 PFLOP/s.
 //
 // Warps 0-3 and 4-7: softmax and epilogue of half the heads each; warp 8: MMA
 // issue; warp 9: loads.

@@ -48,10 +48,12 @@ __device__ __forceinline__ float lse_of(float top, float sum) {
 }
 
 // What the share of a CTA starts in: sequence (or item) b, which the starts of the shares
-// first .. last cut; b < 0 marks an idle CTA.  order: Order's groups (at most 1024), base (beside
-// 32 groups at most) from bit 16 on, and whether a sequence's groups are items.
+// first .. last cut; b < 0 marks an idle CTA.  order: Order's groups, base (a CTA's
+// number, 0 but for groups of 64 rows) from bit 16 on, and whether a sequence's groups are items.
 struct __align__(16) Meta { int32_t b, first, last, order; };
 constexpr int32_t LISTED = 1 << 15;
+constexpr int MAX_ROWS = 65535, MIN_N = 8;     // rows of H that the calls take, of a group (fp32)
+static_assert((MAX_ROWS + MIN_N - 1) / MIN_N < LISTED, "a group's number lies below the mark");
 
 struct SplitParams {
     const int32_t *table, *seq_lens;
@@ -336,6 +338,7 @@ template <int TOK, int OVER, int N, bool TREE> struct Walk {
 // 64 one sequence takes 1% less, 48 sequences 6% more.
 template <int N, typename To, bool TREE>
 __global__ void __launch_bounds__(256, 4) join_kernel(const SplitParams p, int ctas, int32_t *header) {
+    static_assert(N >= MIN_N, "more groups than Meta's order holds");
     __shared__ float4 buf[8][32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
