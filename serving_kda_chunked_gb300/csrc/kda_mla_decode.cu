@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
             do {
                 if (seg > 0) ok = wait_or_fail(q_empty, (seg - 1) & 1, fail);
                 if (!ok) break;
-                const Item it = item_of<TREE, N>(share.o, w.b);
+                const Item it = share.item<TREE, N>(w.b);
                 if (elect_one()) {
                     mbar_arrive_expect_tx(q_full, CHUNKS * N * 128);
                     tma4(smb + L::Q, &p.tm_q, 0, it.h0, 0, it.b, q_full);
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(THREADS, 1) decode_kernel(const __grid_constan
                 uint64_t sees = 0, sees32 = 0;
                 uint32_t pad = 0;
                 int64_t front = 0;
-                const Item it = item_of<TREE, N>(share.o, w.b);
+                const Item it = share.item<TREE, N>(w.b);
                 const int h0 = it.h0, nh = min(N, p.H - h0);
                 if constexpr (TREE) {
                     const int32_t *par = p.parents + (int64_t)it.b * p.T;

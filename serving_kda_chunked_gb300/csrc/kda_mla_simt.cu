@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(DTHREADS, 2) decode_simt_kernel(const SplitPar
     w.start(p, share);
     const int shift = 31 - __clz(p.page);
     do {
-        const Item it = item_of<TREE, HG>(share.o, w.b);
+        const Item it = share.item<TREE, HG>(w.b);
         const int h0 = it.h0, nh = min(HG, p.H - h0);
         const int32_t *tab = p.table + (int64_t)it.b * p.max_pages;
         __syncthreads();

@@ -145,7 +145,16 @@ struct Shares {
 // end one, and then a unit a tile: without them the CTA with the most sequences
 // ended 9 us after the others (48 sequences of up to 9001, 128 heads: 93 us in
 // all, with one, two and three units 88, 86 and 86).
-struct Share { int64_t g0, g1, t00, len0; Order o; int b0, items; bool busy; };
+struct Share {
+    int64_t g0, g1, t00, len0;
+    Order o;
+    int b0, items, h0;                         // h0: of all sequences, without trees
+    bool busy;
+    template <bool TREE, int N> __device__ __forceinline__ Item item(int i) const {
+        if (!TREE) return {i, h0};             // (the modulus taken at every sequence: a short one 8.93 us, here 8.83)
+        return item_of<TREE, N>(o, i);
+    }
+};
 template <int THREADS> struct ShareScratch { int64_t sums[THREADS / 32], t0, t1, len; int b; };
 
 // Groups in step for trees with different numbers of groups (up to ALIKE), where the tokens exceed what
@@ -248,6 +257,7 @@ __device__ __forceinline__ Share find_share(const SplitParams &p, ShareScratch<T
     Share s;
     s.o = o;
     s.items = items;
+    s.h0 = (int)blockIdx.x % o.groups * N;
     // the shares of several groups of 64 have two units at least: with one the partial results of 64 rows each
     // cost more than the second tile (one tree of 16 nodes, 32 heads, over 700 tokens: 23.3 us,
     // here 18.3, with three units 17.9, four 19.4; four trees of 8 25.7, 20.3, 20.8, 21.8)
@@ -351,10 +361,10 @@ __global__ void __launch_bounds__(256, 4) join_kernel(const SplitParams p, int c
     const int cta = blockIdx.y + (TREE ? 1 : p.groups);     // shares 1 .. of every group
     if (cta >= ctas) return;
     const Meta m = p.meta[cta];
-    if (m.b < 0) return;
+    if (TREE && m.b < 0) return;                            // before its order is made sense of
     const int groups = TREE ? m.order & (LISTED - 1) : p.groups, base = TREE ? m.order >> 16 : 0;
     const int group = (cta - base) % groups, c = (cta - base) / groups;
-    if (c < m.first || c > m.last) return;
+    if (m.b < 0 || c < m.first || c > m.last) return;
     const int pieces = m.last - m.first + 2;                // of shares first - 1 .. last
     const int items = TREE && m.order & LISTED ? p.groups : 1;
     const int seq = TREE ? m.b / items : m.b, h0 = ((TREE ? m.b % items : 0) + group) * N;
