@@ -528,9 +528,10 @@ uint64_t kda_mla_decode_workspace_size(int32_t B, int32_t H, int32_t dtype);
  *
  * Row (b, i) of o is what kda_decode_step gives for node i after the decode
  * steps of its ancestors, started from the state.  bf16: products take their
- * factors (the nodes' rows, the state, the deltas) rounded to tf32, 11 bits; sums and
- * gates are float32.  fp32: float32 throughout.  o must not overlap the other
- * tensors.  B = 0 is a valid no-op.
+ * factors (the nodes' rows, the state, the deltas and their weights) rounded to tf32, 11 bits;
+ * sums and gates are float32, and so is what kda_tree_commit writes.  Where the gates on some path add up to less than -69 in a channel,
+ * that head of that sequence takes longer (up to four times with 64 nodes).  fp32: float32
+ * throughout.  o must not overlap the other tensors.  B = 0 is a valid no-op.
  */
 kda_status kda_tree_step(const void *q, const void *k, const void *v,
                          const float *g, const float *beta, const float *S,

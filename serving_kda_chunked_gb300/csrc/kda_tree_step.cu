@@ -32,6 +32,11 @@
 // by node along the paths 105 and 89, and 108 and 185 for chains (a third of all instructions);
 // k e^gamma and q e^gamma in rows of their own, whose loads are not in the order of an MMA's registers,
 // 103 and 76.
+// Pair by pair, where one channel of one node of a head falls below the range: 256 sequences of 8 nodes
+// 102 -> 114 us, of 16 127 -> 221, 64 of 32 71 -> 168, 32 of 64 79 -> 310 (a node's path four ancestors
+// at a time, each four with sums over the lanes; all of the CTA's nodes, whichever of them is far).
+// Gated DeltaNet reads fewer gates and gains nothing by it, the phases being what they are: 256 sequences of
+// 8 nodes 102 us, of 16 129, 32 of 64 80; D = 64: 32, 65 and 48 us (KDA 33, 62 and 43).
 // Tried: what a later CTA reads asked into L2, 64 nodes 87 to 89 (of 82); 1, 2 or 8 unrolled steps of 4
 // with 4 to 9 CTAs an SM in phase 4, 8 nodes 106 to 112 (of 105); values loaded before phase 4 103 (of 102).
 //

@@ -20,10 +20,12 @@
 //
 // What bounds it: HBM, a row of p and one of q a sequence.  A cluster of CTAs takes a
 // sequence; all of its CTAs walk the tree alike and share each pass.  Measured, 256
-// sequences over 131,072 tokens: one rejection each 51 us (5.3 TB/s), trees of 16 nodes with
-// 1.9 passes on average and up to seven 92 us (the sequences with many passes end last), no
-// drafted token 42 us; one sequence 10 us, of which the pass is 4 and the rest its chain:
-// parents, probabilities, walk, sums, the piece.  The next loads under way beside a block's sums: 2% off.
+// sequences over 131,072 tokens: one rejection each 50 us (5.4 TB/s), trees of 16 nodes with
+// 1.9 passes on average and up to seven 96 us (the sequences with many passes end last), without
+// draft rows 61, no drafted token 40; one sequence over 50,021 tokens 8.3 us, a chain of passes with
+// a cluster barrier each.  The next loads under way beside a block's sums: 2% off.
+// bf16 rows, half the bytes: 52, 103, 62, 39 and 10.7 us, so that HBM bounds none of them (the
+// pairs' arithmetic is the same for a value of two bytes; how far it or the chain does has not been measured).
 #include "kda_tree.cuh"
 
 
@@ -32,7 +34,7 @@ namespace tree {
 namespace {
 
 // With 512 threads and two CTAs an SM a batch of 256 trees over 131,072 tokens takes 100 us
-// (here 94), with 128 and eight 92, but single sequences 11 (here 8).
+// (here 96), with 128 and eight 92, but single sequences 11 (here 8).
 constexpr int THREADS = 256, MIN_CTAS = 4, WARPS = THREADS / 32, MAX_CLUSTER = 8;
 constexpr int PER_LANE = MAX_CLUSTER * WARPS / 32;          // pieces a lane adds up
 
